@@ -24,7 +24,9 @@ EXPORTS = ("mla_qcache_page_bytes", "mla_qcache_config_check", "mla_qcache_works
            "mla_qcache_write_advance", "mla_qcache_decode_attn_bf16", "mla_qcache_bf16_workspace_bytes",
            "mla_qcache_write_transformed", "mla_qcache_row_transform", "mla_qcache_absorb_query",
            "mla_qcache_up_project", "mla_qcache_decode_attn_multi", "mla_qcache_decode_plan",
-           "mla_qcache_selftest_wait_timeout", "mla_qcache_decode_attn_pending", "mla_qcache_decode_launches")
+           "mla_qcache_selftest_wait_timeout", "mla_qcache_decode_attn_pending", "mla_qcache_decode_launches",
+           "mla_qcache_kv4_config_check", "mla_qcache_kv4_page_bytes", "mla_qcache_kv4_append",
+           "mla_qcache_kv4_workspace_bytes", "mla_qcache_kv4_attn", "mla_qcache_append_bf16")
 
 
 class Config(ctypes.Structure):
@@ -42,6 +44,30 @@ def make_config(bits_c=4, page_size=128, n_sink=4, n_recent=128, clip_q=None, bi
     if clip_q is None:
         clip_q = 0.94 if bits_c == 2 else 0.0
     return Config(bits_c, bits_r, page_size, n_sink, n_recent, clip_q)
+
+
+class KV4Config(ctypes.Structure):
+    """mla_qcache_kv4_config."""
+    _fields_ = [("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
+
+    def __repr__(self):
+        return (f"KV4Config(n_kv_heads={self.n_kv_heads}, head_dim={self.head_dim}, group={self.group}, "
+                f"page_size={self.page_size})")
+
+
+def make_kv4_config(n_kv_heads, head_dim=128, group=None, page_size=64) -> KV4Config:
+    """Grouped-query cache in 4 bits; one scale and minimum per head unless a smaller group is given."""
+    return KV4Config(n_kv_heads, head_dim, head_dim if group is None else group, page_size)
+
+
+class _View(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _Rotation(ctypes.Structure):
+    _fields_ = [("cos_tab", ctypes.c_void_p), ("sin_tab", ctypes.c_void_p), ("n_pos", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 class QCacheError(RuntimeError):
@@ -106,6 +132,22 @@ def lib() -> ctypes.CDLL:
                                                   vp, sz, vp, vp]
         L.mla_qcache_advance.restype = ctypes.c_int
         L.mla_qcache_advance.argtypes = [vp, vp, i32, vp]
+        KC, V, R = P(KV4Config), P(_View), P(_Rotation)
+        L.mla_qcache_kv4_config_check.restype = ctypes.c_int
+        L.mla_qcache_kv4_config_check.argtypes = [KC]
+        L.mla_qcache_kv4_page_bytes.restype = sz
+        L.mla_qcache_kv4_page_bytes.argtypes = [KC]
+        L.mla_qcache_kv4_append.restype = ctypes.c_int
+        L.mla_qcache_kv4_append.argtypes = [KC, i32, i32, i32, V, V, vp, vp, vp, i32, R, V, i32, vp, vp, vp, vp, i32, vp,
+                                            i64, vp, vp]
+        L.mla_qcache_kv4_workspace_bytes.restype = sz
+        L.mla_qcache_kv4_workspace_bytes.argtypes = [KC, i32, i32, i32, i32]
+        L.mla_qcache_kv4_attn.restype = ctypes.c_int
+        L.mla_qcache_kv4_attn.argtypes = [KC, i32, i32, i32, i32, V, vp, i32, vp, i32, vp, vp, i64, i32, i32,
+                                          ctypes.c_float, vp, vp, vp, sz, vp, vp]
+        L.mla_qcache_append_bf16.restype = ctypes.c_int
+        L.mla_qcache_append_bf16.argtypes = [i32, i32, vp, i64, vp, vp, vp, i32, vp, ctypes.c_float, R, V, i32, vp, vp, vp,
+                                             vp, i32, i32, vp, i64, vp, vp]
         L.mla_qcache_strerror.restype = ctypes.c_char_p
         L.mla_qcache_strerror.argtypes = [i32]
         _lib = L
@@ -388,3 +430,159 @@ def mla_qcache_decode_attn_noalloc(cfg: Config, q_lat, q_rope, page_table, seq_l
         ctypes.c_float(softmax_scale), _ptr(out, "out", dtype=torch.float32), _ptr(lse, "lse", dtype=torch.float32),
         _ptr(err_word, "err_word", dtype=torch.int32), _stream(stream))
     _raise(st, "mla_qcache_decode_attn_noalloc")
+
+
+# ---------------------------------------------------------------- grouped-query cache in 4 bits, BF16 latent append
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def kv4_page_bytes(cfg: KV4Config) -> int:
+    return int(lib().mla_qcache_kv4_page_bytes(ctypes.byref(cfg)))
+
+
+def kv4_workspace_bytes(cfg: KV4Config, B: int, n_heads: int, max_q: int, max_pages: int) -> int:
+    return int(lib().mla_qcache_kv4_workspace_bytes(ctypes.byref(cfg), B, n_heads, max_q, max_pages))
+
+
+def _dev_ptr(t, name, device, dtype, shape):
+    """Pointer of a contiguous tensor of this type, shape (None: any extent) and device."""
+    if t is None:
+        raise QCacheError(f"{name} is required")
+    if t.device != device:
+        raise QCacheError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise QCacheError(f"{name} must be {dtype}, got {t.dtype}")
+    got = t.shape
+    if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
+        raise ValueError(f"{name} must be {[x if x is not None else 'any' for x in shape]}, got {tuple(got)}")
+    if not t.is_contiguous():
+        raise QCacheError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _call_device(t, name):
+    """Device of a call's tensors: CUDA, and the current one (the launch goes to its stream)."""
+    if t is None or not t.is_cuda:
+        raise QCacheError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise QCacheError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _head_view(t, name, device, dtype, rows, heads, dim):
+    """View [rows, heads, dim] with contiguous channels; rows and heads may be strided."""
+    if t is None:
+        raise QCacheError(f"{name} is required")
+    if t.device != device or t.dtype != dtype:
+        raise QCacheError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [{rows}, {heads if heads is not None else 'heads'}, {dim}], got {tuple(t.shape)}")
+    s = t.stride()
+    if s[2] != 1:
+        raise QCacheError(f"{name}: the channels of a head must be contiguous")
+    return _View(t.data_ptr(), s[0] if rows > 1 else 0, s[1] if t.shape[1] > 1 else 0)
+
+
+def _rotation(cos, sin, interleaved, device):
+    if cos is None and sin is None:
+        return None
+    if cos is None or sin is None or cos.dim() != 2:
+        raise ValueError("cos and sin must both be [positions, rot_dim / 2] tables")
+    n, half = cos.shape
+    return ctypes.byref(_Rotation(_dev_ptr(cos, "cos", device, torch.float32, (n, half)),
+                                  _dev_ptr(sin, "sin", device, torch.float32, (n, half)), n, 2 * half, int(interleaved)))
+
+
+def mla_qcache_kv4_append(cfg: KV4Config, k_new, v_new, cu_new, seq_lens, max_new: int, page_table, pool, err_word,
+                          cos=None, sin=None, interleaved=False, q=None, q_out=None, k_deq=None, v_deq=None,
+                          seq_lens_next=None, stream=None) -> None:
+    """Append K/V rows to the grouped-query cache in 4 bits, keys and queries rotated on the way (see
+    include/mla_qcache.h). k_new, v_new [rows, kv heads, D] and q [rows, heads, D] may be views of one
+    projection's output."""
+    dev = _call_device(k_new, "k_new")
+    dtype = k_new.dtype
+    if dtype not in _DTYPES:
+        raise QCacheError(f"k_new must be bfloat16 or float16, got {dtype}")
+    rows, Hkv, D = k_new.shape[0], cfg.n_kv_heads, cfg.head_dim
+    i32 = torch.int32
+    lens = _dev_ptr(seq_lens, "seq_lens", dev, i32, (None,))
+    B = seq_lens.shape[0]
+    if page_table is None or page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    heads = q.shape[1] if q is not None and q.dim() == 3 else 0
+    if (q is None) != (q_out is None):
+        raise QCacheError("q and q_out go together")
+    st = lib().mla_qcache_kv4_append(
+        ctypes.byref(cfg), _DTYPES[dtype], B, rows, ctypes.byref(_head_view(k_new, "k_new", dev, dtype, rows, Hkv, D)),
+        ctypes.byref(_head_view(v_new, "v_new", dev, dtype, rows, Hkv, D)), _dev_ptr(cu_new, "cu_new", dev, i32, (B + 1,)),
+        lens, None if seq_lens_next is None else _dev_ptr(seq_lens_next, "seq_lens_next", dev, i32, (B,)), int(max_new),
+        _rotation(cos, sin, interleaved, dev),
+        None if q is None else ctypes.byref(_head_view(q, "q", dev, dtype, rows, None, D)), heads,
+        None if q is None else _dev_ptr(q_out, "q_out", dev, dtype, (rows, heads, D)),
+        None if k_deq is None else _dev_ptr(k_deq, "k_deq", dev, dtype, (rows, Hkv, D)),
+        None if v_deq is None else _dev_ptr(v_deq, "v_deq", dev, dtype, (rows, Hkv, D)),
+        _dev_ptr(page_table, "page_table", dev, i32, (B, None)), page_table.shape[1],
+        _dev_ptr(pool, "pool", dev, torch.uint8, (None, kv4_page_bytes(cfg))), pool.shape[0],
+        _dev_ptr(err_word, "err_word", dev, i32, (1,)), _stream(stream))
+    _raise(st, "mla_qcache_kv4_append")
+
+
+def mla_qcache_kv4_attn(cfg: KV4Config, q, page_table, seq_lens, pool, softmax_scale: float, out, workspace, err_word,
+                        cu_q=None, max_q: int = 1, lse=None, causal=True, window: int = 0, stream=None) -> None:
+    """Attention of query rows q [rows, heads, D] over the cache in 4 bits (see include/mla_qcache.h);
+    without cu_q one row per sequence."""
+    dev = _call_device(q, "q")
+    dtype = q.dtype
+    if dtype not in _DTYPES:
+        raise QCacheError(f"q must be bfloat16 or float16, got {dtype}")
+    if q.dim() != 3:
+        raise ValueError(f"q must be [rows, heads, D], got {tuple(q.shape)}")
+    rows, heads, D = q.shape[0], q.shape[1], cfg.head_dim
+    i32 = torch.int32
+    lens = _dev_ptr(seq_lens, "seq_lens", dev, i32, (None,))
+    B = seq_lens.shape[0]
+    if page_table is None or page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    st = lib().mla_qcache_kv4_attn(
+        ctypes.byref(cfg), _DTYPES[dtype], B, heads, rows, ctypes.byref(_head_view(q, "q", dev, dtype, rows, heads, D)),
+        None if cu_q is None else _dev_ptr(cu_q, "cu_q", dev, i32, (B + 1,)), int(max_q),
+        _dev_ptr(page_table, "page_table", dev, i32, (B, None)), page_table.shape[1], lens,
+        _dev_ptr(pool, "pool", dev, torch.uint8, (None, kv4_page_bytes(cfg))), pool.shape[0], int(causal), int(window),
+        softmax_scale, _dev_ptr(out, "out", dev, dtype, (rows, heads, D)),
+        None if lse is None else _dev_ptr(lse, "lse", dev, torch.float32, (rows, heads)),
+        _dev_ptr(workspace, "workspace", dev, torch.uint8, (None,)), workspace.shape[0],
+        _dev_ptr(err_word, "err_word", dev, i32, (1,)), _stream(stream))
+    _raise(st, "mla_qcache_kv4_attn")
+
+
+def mla_qcache_append_bf16(kv_new, cu_new, seq_lens, max_new: int, page_table, kv_pool, err_word, norm_weight=None,
+                           eps: float = 1e-6, cos=None, sin=None, interleaved=False, q_rope=None, q_out=None, c_out=None,
+                           kr_out=None, seq_lens_next=None, stream=None) -> None:
+    """Append raw latent rows kv_new [rows, 576] (BF16; rows may be strided) to the paged BF16 cache
+    kv_pool [pages, page_size, 576] with RMS norm and rotation on the way (see include/mla_qcache.h).
+    kv_pool (and page_table) may be None when only c_out / kr_out, the rows as cached, are wanted."""
+    dev = _call_device(kv_new, "kv_new")
+    bf, i32 = torch.bfloat16, torch.int32
+    if kv_new.dtype != bf or kv_new.dim() != 2 or kv_new.shape[1] != 576 or kv_new.stride(1) != 1:
+        raise ValueError(f"kv_new must be bfloat16 [rows, 576] with contiguous rows, got {kv_new.dtype} {tuple(kv_new.shape)}")
+    rows = kv_new.shape[0]
+    lens = _dev_ptr(seq_lens, "seq_lens", dev, i32, (None,))
+    B = seq_lens.shape[0]
+    P, table, pages, pool, n_pages = 64, None, 1, None, 0
+    if kv_pool is not None:
+        pool = _dev_ptr(kv_pool, "kv_pool", dev, bf, (None, None, 576))
+        n_pages, P = kv_pool.shape[0], kv_pool.shape[1]
+        table = _dev_ptr(page_table, "page_table", dev, i32, (B, None))
+        pages = page_table.shape[1]
+    heads = q_rope.shape[1] if q_rope is not None and q_rope.dim() == 3 else 0
+    if (q_rope is None) != (q_out is None):
+        raise QCacheError("q_rope and q_out go together")
+    opt = lambda t, name, shape: None if t is None else _dev_ptr(t, name, dev, bf, shape)  # noqa: E731
+    st = lib().mla_qcache_append_bf16(
+        B, rows, kv_new.data_ptr(), kv_new.stride(0) if rows > 1 else 0, _dev_ptr(cu_new, "cu_new", dev, i32, (B + 1,)), lens,
+        None if seq_lens_next is None else _dev_ptr(seq_lens_next, "seq_lens_next", dev, i32, (B,)), int(max_new),
+        opt(norm_weight, "norm_weight", (512,)), eps, _rotation(cos, sin, interleaved, dev),
+        None if q_rope is None else ctypes.byref(_head_view(q_rope, "q_rope", dev, bf, rows, None, 64)), heads,
+        opt(q_out, "q_out", (rows, heads, 64)), opt(c_out, "c_out", (rows, 512)), opt(kr_out, "kr_out", (rows, 64)), table,
+        pages, P, pool, n_pages, _dev_ptr(err_word, "err_word", dev, i32, (1,)), _stream(stream))
+    _raise(st, "mla_qcache_append_bf16")

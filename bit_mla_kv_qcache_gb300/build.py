@@ -19,6 +19,10 @@ SOURCES = {  # file -> extra flags
     "decode_tc.cu": [],
     "proj.cu": [],
     "diag.cu": [],
+    "abi_kv4.cu": [],
+    "kv4_append.cu": ["-fmad=false"],  # as the writer
+    "kv4_attn.cu": [],
+    "latent_append.cu": [],
 }
 
 

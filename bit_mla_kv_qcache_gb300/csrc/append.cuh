@@ -1,0 +1,164 @@
+// What the appending kernels share: where a new row goes, and the rotation of channel pairs.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kernels.cuh"
+#include "kv4.cuh"
+
+namespace mlaq {
+
+// The largest b in [0, B) with cu[b] <= r, found by a whole warp: each round 32 lanes probe 32
+// evenly spread entries of the remaining range (one round for B <= 32, two for B <= 1024).
+__device__ __forceinline__ int warp_find_seq(const int32_t* cu, int B, int r) {
+  int lo = 0, n = B;  // the answer lies in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) >> 5, i = static_cast<int>(threadIdx.x & 31) * step;
+    const bool le = i < n && __ldg(cu + lo + i) <= r;
+    const unsigned m = __ballot_sync(0xffffffffu, le);
+    const int hit = m ? 31 - __clz(m) : 0;
+    lo += hit * step;
+    n = min(step, n - hit * step);
+  }
+  return lo;
+}
+
+struct RowPlace {
+  int64_t t;    // position, or -1: the row is skipped
+  int32_t pid;  // page
+  int tp;       // token within the page
+  int flags;    // device error bits
+};
+
+// Where row r of the call goes. Rows at and behind cu_new[B] belong to no sequence and are skipped
+// without an error (a padded batch). Called by whole warps.
+__device__ __forceinline__ RowPlace place_row(const int32_t* cu, const int32_t* lens, const int32_t* table, int B, int r,
+                                              int max_new, int max_pages, int p_shift, int64_t n_pages, bool paged,
+                                              int n_pos) {
+  RowPlace z{-1, 0, 0, 0};
+  int b = -1, r0 = 0, r1 = 0;
+  if (r < B) {  // decode steps: one row per sequence
+    r0 = __ldg(cu + r);
+    r1 = __ldg(cu + r + 1);
+    if (r0 == r && r1 == r + 1) b = r;
+  }
+  if (b < 0) {
+    if (r >= __ldg(cu + B)) return z;
+    b = warp_find_seq(cu, B, r);
+    r0 = __ldg(cu + b);
+    r1 = __ldg(cu + b + 1);
+  }
+  if (r < r0 || r >= r1 || r1 - r0 > max_new) {
+    z.flags = kErrRows;
+    return z;
+  }
+  const int s0 = __ldg(lens + b);
+  const int64_t t = static_cast<int64_t>(s0) + (r - r0);
+  const int64_t pg = t >> p_shift;
+  if (s0 < 0 || pg >= max_pages || t >= n_pos) {
+    z.flags = kErrSeqOverflow;
+    return z;
+  }
+  if (paged) {
+    z.pid = __ldg(table + static_cast<size_t>(b) * max_pages + pg);
+    if (z.pid < 0 || z.pid >= n_pages) {
+      z.flags = kErrBadPage;
+      return z;
+    }
+  }
+  z.tp = static_cast<int>(t & ((1 << p_shift) - 1));
+  z.t = t;
+  return z;
+}
+
+__device__ __forceinline__ float elem_lo(uint32_t w, bool f16) {
+  return f16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(w))) : __uint_as_float(w << 16);
+}
+__device__ __forceinline__ float elem_hi(uint32_t w, bool f16) {
+  return f16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(w >> 16))) : __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack8(const uint4& w, bool f16, float (&x)[8]) {
+  x[0] = elem_lo(w.x, f16), x[1] = elem_hi(w.x, f16), x[2] = elem_lo(w.y, f16), x[3] = elem_hi(w.y, f16);
+  x[4] = elem_lo(w.z, f16), x[5] = elem_hi(w.z, f16), x[6] = elem_lo(w.w, f16), x[7] = elem_hi(w.w, f16);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, bool f16) {
+  if (f16) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint4 pack8(const float (&x)[8], bool f16) {
+  return make_uint4(pack2(x[0], x[1], f16), pack2(x[2], x[3], f16), pack2(x[4], x[5], f16), pack2(x[6], x[7], f16));
+}
+
+// The angles of one thread's eight channels 8 i .. 8 i + 7 at position t: with neighbouring pairs
+// four (c, s), with pairs half a rotation apart eight; rows of the tables are 16-byte aligned
+// (rot_dim / 2 is a multiple of 8).
+struct Angles {
+  float c[8], s[8];
+};
+__device__ __forceinline__ Angles load_angles(const Rotation& rot, int64_t t, int i) {
+  Angles a;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) a.c[k] = 1.f, a.s[k] = 0.f;
+  if (8 * i >= rot.rot_dim) return a;
+  const int half = rot.rot_dim >> 1;
+  const size_t row = static_cast<size_t>(t) * half;
+  if (rot.interleaved) {
+    const float4 c = __ldg(reinterpret_cast<const float4*>(rot.cos_tab + row + 4 * i));
+    const float4 s = __ldg(reinterpret_cast<const float4*>(rot.sin_tab + row + 4 * i));
+    a.c[0] = c.x, a.c[1] = c.y, a.c[2] = c.z, a.c[3] = c.w;
+    a.s[0] = s.x, a.s[1] = s.y, a.s[2] = s.z, a.s[3] = s.w;
+  } else {
+    const int f = 8 * i < half ? 8 * i : 8 * i - half;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float4 c = __ldg(reinterpret_cast<const float4*>(rot.cos_tab + row + f) + k);
+      const float4 s = __ldg(reinterpret_cast<const float4*>(rot.sin_tab + row + f) + k);
+      a.c[4 * k] = c.x, a.c[4 * k + 1] = c.y, a.c[4 * k + 2] = c.z, a.c[4 * k + 3] = c.w;
+      a.s[4 * k] = s.x, a.s[4 * k + 1] = s.y, a.s[4 * k + 2] = s.z, a.s[4 * k + 3] = s.w;
+    }
+  }
+  return a;
+}
+
+// (a, b) -> (a cos - b sin, b cos + a sin) on the thread's eight channels (thread i of the head, in
+// lane order); every product and sum is rounded by itself, so the keys' codes are reproducible.
+// The partner of a pair half a rotation away sits in the lane rot_dim / 16 further up or down; the
+// whole warp takes part.
+__device__ __forceinline__ void rotate8(const Rotation& rot, const Angles& a, int i, const uint4& raw, bool f16,
+                                        float (&x)[8]) {
+  unpack8(raw, f16, x);
+  if (rot.rot_dim == 0) return;
+  if (rot.interleaved) {
+    if (8 * i < rot.rot_dim) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float u = x[2 * k], w = x[2 * k + 1];
+        x[2 * k] = __fsub_rn(__fmul_rn(u, a.c[k]), __fmul_rn(w, a.s[k]));
+        x[2 * k + 1] = __fadd_rn(__fmul_rn(w, a.c[k]), __fmul_rn(u, a.s[k]));
+      }
+    }
+    return;
+  }
+  const int d = rot.rot_dim >> 4, lane = threadIdx.x & 31;
+  const bool first = i < d, in = i < 2 * d;
+  const int src = !in ? lane : first ? lane + d : lane - d;
+  uint4 o;
+  o.x = __shfl_sync(0xffffffffu, raw.x, src);
+  o.y = __shfl_sync(0xffffffffu, raw.y, src);
+  o.z = __shfl_sync(0xffffffffu, raw.z, src);
+  o.w = __shfl_sync(0xffffffffu, raw.w, src);
+  if (!in) return;
+  float y[8];
+  unpack8(o, f16, y);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float xc = __fmul_rn(x[k], a.c[k]), ys = __fmul_rn(y[k], a.s[k]);
+    x[k] = first ? __fsub_rn(xc, ys) : __fadd_rn(xc, ys);
+  }
+}
+
+}  // namespace mlaq

@@ -1,0 +1,90 @@
+// Append of new latent rows to the paged BF16 cache (the one the unquantized decode reads): RMS
+// norm of the latent, rotation of the positional key and of the queries' positional part.
+//
+// CTA r serves row r. Warp 0 normalizes the latent (sixteen channels per lane, sum of squares in
+// float32 over the warp); the other warps rotate the positional key and the queries, eight lanes
+// per head of 64 channels. Bound: the bytes of the rows, read and written once.
+#include "append.cuh"
+
+namespace mlaq {
+namespace {
+
+constexpr int kLatThreads = 128;
+
+__global__ void __launch_bounds__(kLatThreads) latent_append_kernel(const LatentAppendParams p) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r = blockIdx.x;
+  if (r >= p.n_rows) {  // the blocks behind the rows: the new lengths
+    const int b = (r - p.n_rows) * kLatThreads + tid;
+    if (b < p.B) p.seq_next[b] = __ldg(p.seq_lens + b) + __ldg(p.cu_new + b + 1) - __ldg(p.cu_new + b);
+    return;
+  }
+  const uint16_t* row = p.kv.data + r * p.kv.row_stride;
+  const RowPlace at = place_row(p.cu_new, p.seq_lens, p.page_table, p.B, r, p.max_new, p.max_pages, p.p_shift, p.n_pages,
+                                p.pool != nullptr, p.rot.rot_dim ? p.rot.n_pos : 0x7fffffff);
+  if (at.t < 0) {
+    if (tid == 0 && at.flags) atomicOr(p.err, at.flags);
+    return;
+  }
+  uint16_t* dst = p.pool ? p.pool + (static_cast<size_t>(at.pid) * p.P + at.tp) * kRow : nullptr;
+  if (warp == 0) {
+    uint4 w[2];
+    float x[2][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      w[k] = __ldg(reinterpret_cast<const uint4*>(row) + lane + 32 * k);
+      unpack8(w[k], false, x[k]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss += x[k][j] * x[k][j];
+    }
+    if (p.weight) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float inv = 1.f / sqrtf(ss * (1.f / kLatent) + p.eps);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float g[8];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(p.weight) + lane + 32 * k), false, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[k][j] = x[k][j] * inv * g[j];
+        w[k] = pack8(x[k], false);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (dst) reinterpret_cast<uint4*>(dst)[lane + 32 * k] = w[k];
+      if (p.c_out) reinterpret_cast<uint4*>(p.c_out + static_cast<size_t>(r) * kLatent)[lane + 32 * k] = w[k];
+    }
+    return;
+  }
+  const int i = tid & 7;
+  const Angles ang = load_angles(p.rot, at.t, i);
+  const int heads = 1 + (p.q.data ? p.H : 0);  // the positional key, then the queries
+  for (int h0 = 0; h0 < heads; h0 += (kLatThreads - 32) / 8) {
+    const int h = h0 + (tid - 32) / 8;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (h < heads)
+      raw = __ldg(reinterpret_cast<const uint4*>(h == 0 ? row + kLatent
+                                                        : p.q.data + r * p.q.row_stride + (h - 1) * p.q.head_stride) + i);
+    float x[8];
+    rotate8(p.rot, ang, i, raw, false, x);
+    const uint4 y = pack8(x, false);
+    if (h == 0) {
+      if (dst) reinterpret_cast<uint4*>(dst + kLatent)[i] = y;
+      if (p.kr_out) reinterpret_cast<uint4*>(p.kr_out + static_cast<size_t>(r) * kRope)[i] = y;
+    } else if (h < heads) {
+      reinterpret_cast<uint4*>(p.q_out + (static_cast<size_t>(r) * p.H + h - 1) * kRope)[i] = y;
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_latent_append(const LatentAppendParams& p, cudaStream_t stream) {
+  const int tail = p.seq_next ? (p.B + kLatThreads - 1) / kLatThreads : 0;
+  latent_append_kernel<<<p.n_rows + tail, kLatThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace mlaq

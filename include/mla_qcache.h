@@ -480,6 +480,152 @@ int mla_qcache_decode_attn_noalloc(const mla_qcache_config* cfg, int32_t B, int3
 /* Size in bytes of the built-in scratch used by mla_qcache_decode_attn_noalloc. */
 size_t mla_qcache_noalloc_scratch_bytes(void);
 
+/*
+ * ---------------------------------------------------------------------------------------------
+ * Grouped-query K/V cache in 4 bits
+ *
+ * For models beside the latent ones that keep key and value heads: the small drafting model whose
+ * tokens mla_qcache_decode_attn_multi verifies, or the other models of a served fleet. The
+ * quantizer is the one of this header (RAQ-MLA page, appendix Table 5: FP16 scale and minimum),
+ * per token, kv head and group of channels, for keys (after their rotation) and values alike.
+ *   n_kv_heads 1..256.   head_dim D: 64 or 128.
+ *   group      channels per scale and minimum: 32, 64 or 128, at most D.
+ *   page_size  P, tokens per page: 16, 32, 64, 128 or 256.
+ *
+ * Page layout: one region per kv head, P * (D + 8 * D / group) bytes each, heads in order. Token
+ * t of the page has in its head's region
+ *   key codes    D/2 bytes at t*D/2. Channel c is nibble 8*((c%32/8)*(D/32) + c/32) + c%8,
+ *   value codes  D/2 bytes at P*D/2 + t*D/2. Channel c is nibble
+ *                8*((c%8)*(D/64) + c/64) + 4*(c/8%2) + c/16%4
+ *                (nibble i: byte i/2, the low half first),
+ *   numbers      for each group four FP16 at P*D + (t*D/group + g)*8: key scale, key minimum,
+ *                value scale, value minimum.
+ * (The orders are those in which one lane of the attention kernel reads its 16 or 8 contiguous
+ * bytes as a tensor-core operand.)
+ */
+typedef struct {
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t group;
+  int32_t page_size;
+} mla_qcache_kv4_config;
+
+/* Element type of the rows (keys, values, queries, outputs). */
+#define MLA_QCACHE_BF16 0
+#define MLA_QCACHE_FP16 1
+
+/* Rows of heads in device memory: element (r, h, c) at data[r*row_stride + h*head_stride + c].
+ * Strides are in elements, >= 0 and multiples of 8; data is 16-byte aligned. (The struct itself is
+ * in host memory.) */
+typedef struct {
+  const void* data;
+  int64_t row_stride;
+  int64_t head_stride;
+} mla_qcache_view;
+
+/* Position rotation: at position t the pair (a, b) number i becomes
+ * (a cos[t][i] - b sin[t][i], b cos[t][i] + a sin[t][i]), each product and sum rounded to float32.
+ * Pairs are channels (i, i + rot_dim/2), or (2i, 2i+1) when `interleaved`; channels from rot_dim on
+ * pass unchanged. cos_tab, sin_tab: device float32 [n_pos][rot_dim/2], 16-byte aligned; rot_dim a
+ * multiple of 16. A position >= n_pos is an error (MLA_QCACHE_DEV_SEQ_OVERFLOW, the row is skipped). */
+typedef struct {
+  const float* cos_tab;
+  const float* sin_tab;
+  int32_t n_pos;
+  int32_t rot_dim;
+  int32_t interleaved;
+} mla_qcache_rotation;
+
+/* MLA_QCACHE_OK if the configuration is supported, else MLA_QCACHE_ERR_CONFIG/NULL. */
+int mla_qcache_kv4_config_check(const mla_qcache_kv4_config* cfg);
+
+/* Bytes of one page, or 0 for an invalid configuration. */
+size_t mla_qcache_kv4_page_bytes(const mla_qcache_kv4_config* cfg);
+
+/*
+ * Append: rows cu_new[b] .. cu_new[b+1]-1 of k_new / v_new [n_rows][n_kv_heads][D] are sequence b's
+ * tokens at positions seq_lens[b], seq_lens[b]+1, ... Keys are rotated in float32 and quantized from
+ * there (no rounding in between), values as they are; both go to page page_table[b][t / P]. In the
+ * same launch, each optional:
+ *   q, q_out       the rows' queries [n_rows][n_heads][D], rotated, rounded to the rows' type
+ *                  (contiguous);
+ *   k_deq, v_deq   [n_rows][n_kv_heads][D] contiguous: the values that the cache now holds for the
+ *                  new rows (min + code * scale, rounded to the rows' type), for a prompt's own
+ *                  dense attention that is to agree with what later steps read;
+ *   seq_lens_next  [B]: seq_lens[b] + cu_new[b+1] - cu_new[b]; must not overlap seq_lens.
+ * Rows from cu_new[B] on (a padded batch) are left alone, in every output. max_new: bound on the rows
+ * per sequence; a sequence with more has its rows skipped (MLA_QCACHE_DEV_ROWS).
+ * rotation NULL: none. Outputs must not overlap inputs or one another.
+ * A group with a NaN or an infinity sets MLA_QCACHE_DEV_NONFINITE, one beyond the FP16 range
+ * MLA_QCACHE_DEV_RANGE (what the cache then holds for it is not specified).
+ * Errors: bad config or dtype -> MLA_QCACHE_ERR_CONFIG; B < 1 or > 2^20, n_rows < 0, max_new < 1,
+ * max_pages < 1, n_pages < 1, n_heads < 1 or > 4096 (with q), bad rotation, negative strides,
+ * overlapping buffers -> MLA_QCACHE_ERR_SHAPE; missing pointers, q without q_out -> MLA_QCACHE_ERR_NULL;
+ * misaligned -> MLA_QCACHE_ERR_ALIGN.
+ */
+int mla_qcache_kv4_append(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t n_rows,
+                          const mla_qcache_view* k_new, const mla_qcache_view* v_new, const int32_t* cu_new,
+                          const int32_t* seq_lens, int32_t* seq_lens_next, int32_t max_new,
+                          const mla_qcache_rotation* rotation, const mla_qcache_view* q, int32_t n_heads,
+                          void* q_out, void* k_deq, void* v_deq, const int32_t* page_table, int32_t max_pages,
+                          uint8_t* pool, int64_t n_pages, int32_t* err_word, void* stream);
+
+/*
+ * Bytes of device workspace for mla_qcache_kv4_attn. The caller zeroes the first 8192 bytes once
+ * (counters, left zero by every call); calls that share a workspace must not overlap in time, and a
+ * workspace of another operator is not one of these. Returns 0 on invalid arguments.
+ */
+size_t mla_qcache_kv4_workspace_bytes(const mla_qcache_kv4_config* cfg, int32_t B, int32_t n_heads, int32_t max_q,
+                                      int32_t max_pages);
+
+/*
+ * Attention over the cache in 4 bits. Query rows cu_q[b] .. cu_q[b+1]-1 of q [n_rows][n_heads][D]
+ * belong to sequence b, which holds seq_lens[b] tokens (the rows' own tokens among them); n_heads is a
+ * multiple of n_kv_heads, query head h reads kv head h / (n_heads / n_kv_heads). The n rows of a
+ * sequence are its last positions: row i is at pos = seq_lens[b] - n + i.
+ *   causal != 0: row i sees tokens t <= pos, and with window > 0 only those with t > pos - window.
+ *   causal == 0: every row sees all seq_lens[b] tokens (window must be 0).
+ * cu_q NULL: one row per sequence (n_rows = B, max_q = 1). Rows from cu_q[B] on are left alone.
+ *   out [n_rows][n_heads][D] in the queries' type, lse [n_rows][n_heads] float32, natural log
+ *   (optional). A row that sees no token gets out = 0, lse = -inf.
+ * Scores are products of the exact codes with the queries (prescaled by a power of two to FP16: every
+ * value within 2^-14 of the row's largest enters exactly, smaller ones are off by at most 2^-39 of it),
+ * summed in float32; weights enter the readout in FP16.
+ * max_q: bound on the rows per sequence; a sequence with more sets MLA_QCACHE_DEV_ROWS, a length
+ * outside [0, max_pages * P] MLA_QCACHE_DEV_SEQ_OVERFLOW (read as 0), a page id outside [0, n_pages)
+ * MLA_QCACHE_DEV_BAD_PAGE (its tokens are left out).
+ * Errors: as for mla_qcache_kv4_append; n_heads no multiple of n_kv_heads, n_rows * n_heads > 2^31 - 1,
+ * a window without causal, a scale that is not finite -> MLA_QCACHE_ERR_SHAPE; too small a workspace ->
+ * MLA_QCACHE_ERR_WORKSPACE.
+ */
+int mla_qcache_kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t n_heads, int32_t n_rows,
+                        const mla_qcache_view* q, const int32_t* cu_q, int32_t max_q, const int32_t* page_table,
+                        int32_t max_pages, const int32_t* seq_lens, const uint8_t* pool, int64_t n_pages,
+                        int32_t causal, int32_t window, float softmax_scale, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, int32_t* err_word, void* stream);
+
+/*
+ * Append to the paged BF16 latent cache that mla_qcache_decode_attn_bf16 reads, from the raw output
+ * of the down-projection (RAQ-MLA page, Figure 4: RMSNorm -> latent, rotation -> k_R). Row r of kv_new
+ * is 576 BF16 values at kv_new + r*kv_row_stride: the latent (512), then the positional key (64).
+ *   norm_weight   BF16 [512]: latent * rsqrt(mean(latent^2) + norm_eps) * weight, in float32, rounded
+ *                 once; NULL: the latent is stored as it is.
+ *   rotation      of the positional key and of q_rope (rot_dim at most 64); NULL: none.
+ *   q_rope, q_out the positional part of the queries [n_rows][n_heads][64] (strided), rotated into
+ *                 q_out (contiguous), the q_rope input of the decode entry points; optional.
+ *   c_out, kr_out [n_rows][512] and [n_rows][64] contiguous: the rows as cached, the inputs of
+ *                 mla_qcache_write and mla_qcache_decode_attn_pending; optional.
+ *   kv_pool       [n_pages][page_size][576], or NULL (then page_table is not read) when only c_out /
+ *                 kr_out are wanted; page_size 32, 64 or 128.
+ * Other arguments, padded rows and errors as for mla_qcache_kv4_append.
+ */
+int mla_qcache_append_bf16(int32_t B, int32_t n_rows, const uint16_t* kv_new, int64_t kv_row_stride,
+                           const int32_t* cu_new, const int32_t* seq_lens, int32_t* seq_lens_next, int32_t max_new,
+                           const uint16_t* norm_weight, float norm_eps, const mla_qcache_rotation* rotation,
+                           const mla_qcache_view* q_rope, int32_t n_heads, uint16_t* q_out, uint16_t* c_out,
+                           uint16_t* kr_out, const int32_t* page_table, int32_t max_pages, int32_t page_size,
+                           uint16_t* kv_pool, int64_t n_pages, int32_t* err_word, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* mla_qcache_strerror(int32_t status);
 
