@@ -210,7 +210,7 @@ int mla_qcache_kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t
   if ((st = sm_count(&sms)) != MLA_QCACHE_OK) return st;
   const int rows = mlaq::kv4_decode_rows(max_q, G);
   if (workspace_bytes < mlaq::kv4_decode_workspace_bytes(rows, D, sms)) return MLA_QCACHE_ERR_WORKSPACE;
-  const size_t ctas = mlaq::kv4_decode_ctas(rows, sms);
+  const size_t ctas = mlaq::kv4_decode_ctas(sms);
   p.cu_q = cu_q;
   p.page_table = page_table;
   p.seq_lens = seq_lens;

@@ -76,7 +76,7 @@ struct Kv4AttnParams {
 constexpr size_t kKv4CounterBytes = 8192;
 // Rows of one work item of the decode kernel (8 or 16) and the CTAs that it launches.
 int kv4_decode_rows(int max_q, int G);
-int kv4_decode_ctas(int rows, int num_sms);
+int kv4_decode_ctas(int num_sms);
 size_t kv4_decode_workspace_bytes(int rows, int D, int num_sms);
 cudaError_t launch_kv4_decode(const Kv4AttnParams& p, int D, int n_groups, int num_sms, cudaStream_t stream);
 

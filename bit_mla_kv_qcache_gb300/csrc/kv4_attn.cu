@@ -10,12 +10,13 @@
 // scaled by a power of two that follows the largest vs seen; sum p vm stays in float32.
 //
 // A warp owns 16 tokens at a time: S^T[16 tokens x rows] = K q^T with the key codes as the A operand
-// (each lane loads its fragment's 16 contiguous bytes straight from the page), softmax on the
-// accumulators, movmatrix turns the weights into the B operand, O^T += V^T w^T with the value codes
-// as A (token pairs joined by byte permutes). No shared memory and no barrier inside the loop; the
-// next tile is in registers before this one is multiplied. Warps of a CTA meet once per work item.
+// (a lane's fragment is 16 contiguous bytes of the page), softmax on the accumulators, movmatrix
+// turns the weights into the B operand, O^T += V^T w^T with the value codes as A (token pairs joined
+// by byte permutes). Codes go from the page straight to registers, one or two tiles ahead of their
+// use and the page id one tile before that; no shared memory and no barrier inside the loop. The warps of a CTA meet
+// once per work item.
 //
-// Work: (sequence, kv head, row block) x its 16-token tiles, laid on one line; CTA i takes tiles
+// Work: (sequence, kv head, row block) x its 32-token steps, laid on one line; CTA i takes steps
 // [i S, (i + 1) S). An item cut by CTA borders is joined by the CTA that arrives last (partials in
 // CTA order, so the result does not depend on who that is).
 #include <algorithm>
@@ -31,10 +32,27 @@
 namespace mlaq {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kTok = 16;           // tokens per warp tile
-constexpr int kMinTiles = 8;       // tiles per CTA at least: two per warp
+constexpr int kTile = 16;      // tokens of a tensor-core tile
+constexpr int kTok = 32;       // tokens of a step: two tiles
+constexpr int kMaxParts = 64;  // CTAs that one item is cut into, at most
+
+template <int D, int NG, int NT>
+struct Geom {
+  static constexpr int kWarps = NT == 1 ? 8 : 6;  // two CTAs per SM: 16 warps of 128 registers, or 12 of 168
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kMinTiles = kWarps;        // steps per CTA at least
+  static constexpr int kR = 8 * NT;
+  static constexpr int kCodes = kTok * D / 2;     // bytes of a step's key codes, and of its value codes
+  static constexpr int kStage = 2 * kCodes + kTok * 8 * NG;
+  static constexpr int kStages = 3 * kStage * 16 <= 210 * 1024 ? 3 : 2;
+  static constexpr int kRowPad = D + 4;
+  // a warp's ring, later its sums when the warps meet
+  static constexpr int kRing = kStages * kStage > kR * kRowPad * 4 ? kStages * kStage : kR * kRowPad * 4;
+  static constexpr int kSmem = kWarps * kRing;
+};
+
 constexpr float kSlack = 8.f;      // the running max is raised when a score exceeds it by more than this
+constexpr float kNoMax = -1e30f;  // the running max before the first score
 constexpr float kWeightRoom = 64.f;  // w / p stays at or below this: w <= 2^14 in FP16
 
 __device__ __forceinline__ float ex2(float x) {
@@ -53,30 +71,88 @@ __device__ __forceinline__ uint32_t float2_to_half2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// What one lane holds of a tile: key words of tokens g and g + 8, value words of tokens 2q, 2q + 1,
-// 2q + 8, 2q + 9, and the numbers of tokens g and g + 8 (per group: scale | min of key, of value).
-template <int D, int NG>
-struct Tile {
-  uint32_t k[2][D / 32];
-  uint32_t v[4][D / 64];
-  uint2 meta[2][NG];
-};
-
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t* p) {
   if constexpr (N == 4) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
     w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
   } else if constexpr (N == 2) {
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
     w[0] = x.x, w[1] = x.y;
   } else {
-    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
   }
 }
 
-struct Item {
-  int b, h, rb;  // sequence, kv head, row block
+// Copies one tile (16 tokens from `tp` of the page region `base`) to its place in a ring stage: keys at
+// `ks`, values at `vs`, numbers at `ms`. Key rows keep their order. The value row of token
+// t = 8f + 2q + e goes to row 8f + 4e + q, at D = 128 with its 16-byte chunks exchanged by pairs for
+// q >= 2, so that the 8-byte reads of a half warp (four q, four g) fall in distinct banks.
+template <int D, int NG>
+__device__ __forceinline__ void copy_tile(uint8_t* ks, uint8_t* vs, uint8_t* ms, const uint8_t* base, int tp, int P,
+                                          int lane) {
+  constexpr int CPR = D / 32;  // 16-byte chunks per row
+  const int t = lane / CPR, c = lane % CPR, q = (t >> 1) & 3;
+  const uint8_t* kp = base + (tp * (D / 2) + 16 * lane);
+  uint8_t* vd = vs + ((t & 8) + 4 * (t & 1) + q) * (D / 2) + 16 * (D == 128 ? c ^ (q & 2) : c);
+#pragma unroll
+  for (int i = 0; i < CPR / 2; ++i) {  // 32 chunks cover eight rows (D = 128) or sixteen
+    cp_async_cg16(ks + 16 * lane + 512 * i, kp + 512 * i);
+    cp_async_cg16(vd + 512 * i, kp + P * (D / 2) + 512 * i);
+  }
+  if (lane < 8 * NG) cp_async_cg16(ms + 16 * lane, base + (P * D + tp * 8 * NG + 16 * lane));
+}
+
+// This lane's key words of tokens g and g + 8, channels 8 q4 .. 8 q4 + 7 of each block of 32.
+template <int D>
+__device__ __forceinline__ void read_keys(uint32_t (&k)[2][D / 32], const uint8_t* ks, int g, int q4) {
+  load_words<D / 32>(k[0], ks + g * (D / 2) + q4 * (D / 8));
+  load_words<D / 32>(k[1], ks + (g + 8) * (D / 2) + q4 * (D / 8));
+}
+// Its value words of tokens 2 q4, 2 q4 + 1, 2 q4 + 8, 2 q4 + 9.
+template <int D>
+__device__ __forceinline__ void read_values(uint32_t (&v)[4][D / 64], const uint8_t* vs, int g, int q4) {
+  const int at = D == 128 ? 16 * ((g >> 1) ^ (q4 & 2)) + 8 * (g & 1) : 4 * g;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) load_words<D / 64>(v[i], vs + q4 * (D / 2) + at + 4 * i * (D / 2));
+}
+// The numbers of tokens g and g + 8, per group: scale | min of the key, then of the value.
+template <int NG>
+__device__ __forceinline__ void read_numbers(uint2 (&m)[2][NG], const uint8_t* ms, int g) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if constexpr (NG == 1) {
+      m[e][0] = *reinterpret_cast<const uint2*>(ms + (g + 8 * e) * 8);
+    } else {
+#pragma unroll
+      for (int k = 0; k < NG / 2; ++k) {
+        const uint4 x = *reinterpret_cast<const uint4*>(ms + (g + 8 * e) * 8 * NG + 16 * k);
+        m[e][2 * k] = make_uint2(x.x, x.y);
+        m[e][2 * k + 1] = make_uint2(x.z, x.w);
+      }
+    }
+  }
+}
+// Keeps the loads that follow behind the work that came before (their registers are not needed yet).
+__device__ __forceinline__ void no_loads_across() { asm volatile("" ::: "memory"); }
+
+__device__ __forceinline__ float sum_over_g(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 4);
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  return v + __shfl_xor_sync(0xffffffffu, v, 16);
+}
+__device__ __forceinline__ float max_over_g(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+
+// The part of the line that a CTA works on and the item it is in. Kept in shared memory: the loop
+// over tiles needs the registers.
+struct Place {
+  long long at, end, item0, share;  // line position, end of the CTA's stretch, item's first tile, CTA stretch
+  int b, h, rb;                     // the item: sequence, kv head, row block
+  int T, n, r0, tiles, blocks;      // of the sequence: length, query rows, first row, tiles of an item, row blocks
 };
 
 // The length, rows and tiles per row block of sequence b.
@@ -111,26 +187,99 @@ __device__ __forceinline__ int2 visible(const Kv4AttnParams& p, int T, int n, in
   return make_int2(lo, hi);
 }
 
+// Channels 4 c4 .. 4 c4 + 3 of row `row` of the item: sums v under the max M (log2 units) and sum L.
+template <int D, int R>
+__device__ __forceinline__ void store_out(const Kv4AttnParams& p, const Place& at, int row, int c4, float4 v, float M, float L) {
+  const int rr = at.rb * R + row;
+  if (rr >= at.n * p.G) return;
+  const size_t orow = static_cast<size_t>(at.r0 + rr / p.G) * p.Hq + at.h * p.G + rr % p.G;
+  const float y = L == 0.f ? 0.f : 1.f / L;
+  reinterpret_cast<uint2*>(p.out + orow * D)[c4] = make_uint2(pack2(v.x * y, v.y * y, p.f16), pack2(v.z * y, v.w * y, p.f16));
+  if (c4 == 0 && p.lse) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+}
+
+// The CTA that came last joins the item's parts, those of CTAs c0 .. c0 + parts - 1 in this order:
+// first the parts' weights, then the outputs, which each thread copies to shared memory (`room`
+// bytes) for as many parts as fit there at once, all in flight and none in registers.
+template <int D, int R, int kThreads>
+__device__ __forceinline__ void merge_parts(const Kv4AttnParams& p, const Place& at, int c0, int parts, uint8_t* smem,
+                                            int room, float (&s_f)[kMaxParts + 1][R], float (&s_ml)[R][2]) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto slot_of = [&](int i) { return static_cast<uint32_t>(2 * (c0 + i) + (i == 0 ? 1 : 0)); };
+  constexpr int kPer = (kMaxParts + 31) / 32;
+  for (int row = warp; row < R; row += kThreads / 32) {
+    float M = kNoMax, L = 0.f;
+    float2 ml[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int i = lane + 32 * k;
+      ml[k] = i < parts ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(i) * R + row) : make_float2(kNoMax, 0.f);
+      M = fmaxf(M, ml[k].x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int i = lane + 32 * k;
+      const float f = ex2(ml[k].x - M);
+      if (i < parts) s_f[i][row] = f;
+      L += f * ml[k].y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (lane == 0) s_ml[row][0] = M, s_ml[row][1] = L;
+  }
+  __syncthreads();
+  constexpr int kPart = R * D * 4;
+  for (int e = tid; e < R * D / 4; e += kThreads) {
+    const int row = e / (D / 4), c4 = e % (D / 4);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int batch = room / kPart;
+    for (int i0 = 0; i0 < parts; i0 += batch) {
+      const int n = min(batch, parts - i0);
+      for (int i = 0; i < n; ++i)
+        cp_async_cg16(smem + i * kPart + e * 16, p.part_o + static_cast<size_t>(slot_of(i0 + i)) * (R * D) + 4 * e);
+      cp_async_wait_all();  // a thread reads what it copied itself
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float4 x = *reinterpret_cast<const float4*>(smem + i * kPart + e * 16);
+        const float f = s_f[i0 + i][row];
+        v.x += f * x.x, v.y += f * x.y, v.z += f * x.z, v.w += f * x.w;
+      }
+    }
+    store_out<D, R>(p, at, row, c4, v, s_ml[row][0], s_ml[row][1]);
+  }
+}
+
 template <int D, int NG, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(const Kv4AttnParams p) {
+__global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kernel(const Kv4AttnParams p) {
+  using Ge = Geom<D, NG, NT>;
   constexpr int R = 8 * NT, KW = D / 32, VW = D / 64, MT = D / 16;
-  constexpr int kRowPad = D + 4;
-  __shared__ __align__(16) float s_o[kWarps][R][kRowPad];
+  constexpr int kWarps = Ge::kWarps, kThreads = Ge::kThreads, kRowPad = Ge::kRowPad;
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][R], s_l[kWarps][R];
   __shared__ long long s_sum[kThreads + 1];
-  __shared__ int s_last;
+  __shared__ float s_f[kMaxParts + 1][R];  // weights of the parts of a cut item; then the rows' (M, L)
+  __shared__ float s_ml[R][2];
+  __shared__ int s_last, s_most[kWarps];
+  __shared__ Place s_at;
+  __shared__ int s_full[kWarps][3];  // steps that every row sees whole: from, to; tokens seen by any
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
   int flags = 0;
 
   // ---- this CTA's stretch of the line of tiles: thread i sums sequences [i c, (i + 1) c)
   const int chunk = (p.B + kThreads - 1) / kThreads;
   long long mine = 0;
+  int most = 0;
   for (int b = tid * chunk; b < min(p.B, (tid + 1) * chunk); ++b) {
     int T, n, r0, tiles, blocks;
     sequence<R>(p, b, T, n, r0, tiles, blocks, flags);
     mine += static_cast<long long>(tiles) * blocks * p.Hkv;
+    if (blocks > 0) most = max(most, tiles);
   }
   {
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) s_most[warp] = most;
     long long x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -141,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
     __syncthreads();
     long long base = 0;
     for (int w = 0; w < warp; ++w) base += s_sum[w];
+    for (int w = 0; w < kWarps; ++w) most = max(most, s_most[w]);
     __syncthreads();
     s_sum[tid + 1] = base + x;
     if (tid == 0) s_sum[0] = 0;
@@ -153,62 +303,117 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
   flags = 0;
   const long long total = s_sum[kThreads];
   long long share = (total + gridDim.x - 1) / gridDim.x;
-  if (share < kMinTiles) share = kMinTiles;
-  long long at = share * blockIdx.x;
+  share = max(share, static_cast<long long>(max(min(Ge::kMinTiles, most), (most + kMaxParts - 2) / (kMaxParts - 1))));
+  const long long at = share * blockIdx.x;
   const long long end = min(total, at + share);
   if (at >= end) return;
 
   // ---- the first item: the thread whose sequences hold tile `at`, then the sequence
-  Item it;
-  long long item0;  // line position of the item's first tile
-  int T, n, r0, tiles, blocks;
-  {
+  if (tid == 0) {
     int lo = 0, hi = kThreads - 1;  // s_sum[lo] <= at < s_sum[lo + 1]
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if (s_sum[mid + 1] > at) hi = mid;
       else lo = mid + 1;
     }
+    Place& s = s_at;
+    s.at = at;
+    s.end = end;
+    s.share = share;
     long long pos = s_sum[lo];
-    it.b = lo * chunk;
     int ignore = 0;
-    for (;; ++it.b) {
-      if (it.b >= p.B) return;  // lengths that changed under the call
-      sequence<R>(p, it.b, T, n, r0, tiles, blocks, ignore);
-      const long long w = static_cast<long long>(tiles) * blocks * p.Hkv;
+    for (s.b = lo * chunk; s.b < p.B; ++s.b) {
+      sequence<R>(p, s.b, s.T, s.n, s.r0, s.tiles, s.blocks, ignore);
+      const long long w = static_cast<long long>(s.tiles) * s.blocks * p.Hkv;
       if (at < pos + w) break;
       pos += w;
     }
-    const long long k = (at - pos) / tiles;
-    it.h = static_cast<int>(k / blocks);
-    it.rb = static_cast<int>(k % blocks);
-    item0 = pos + k * tiles;
+    if (s.b < p.B) {
+      const long long k = (at - pos) / s.tiles;
+      s.h = static_cast<int>(k / s.blocks);
+      s.rb = static_cast<int>(k % s.blocks);
+      s.item0 = pos + k * s.tiles;
+    } else {
+      s.at = s.end;  // lengths that changed under the call
+    }
   }
+  __syncthreads();
 
-  while (at < end) {
+  while (s_at.at < s_at.end) {
     // ---- the item's tokens
-    const int i0 = it.rb * R / p.G, i1 = min(n - 1, (it.rb * R + R - 1) / p.G);
-    const int t_lo = visible(p, T, n, i0).x, t_hi = visible(p, T, n, i1).y;
-    const int tile0 = t_lo / kTok;
-    const int a0 = static_cast<int>(at - item0);                                  // this CTA's tiles of the item
-    const int a1 = static_cast<int>(min(end - item0, static_cast<long long>(tiles)));
-    const int tile_end = min(tile0 + a1, (t_hi + kTok - 1) / kTok);
+    int tile, tile_end;
+    {
+      const int i0 = s_at.rb * R / p.G, i1 = min(s_at.n - 1, (s_at.rb * R + R - 1) / p.G);
+      const int2 first = visible(p, s_at.T, s_at.n, i0), last = visible(p, s_at.T, s_at.n, i1);
+      const int tile0 = first.x / kTok;
+      const int a0 = static_cast<int>(s_at.at - s_at.item0);  // this CTA's tiles of the item
+      const int a1 = static_cast<int>(min(s_at.end - s_at.item0, static_cast<long long>(s_at.tiles)));
+      tile = tile0 + a0 + warp;
+      tile_end = min(tile0 + a1, (last.y + kTok - 1) / kTok);
+      // steps in [full_lo, full_hi) are seen whole by every row of the block
+      if (lane == 0) {
+        s_full[warp][0] = (last.x + kTok - 1) / kTok;
+        s_full[warp][1] = first.y / kTok;
+        s_full[warp][2] = last.y;
+      }
+      __syncwarp();
+    }
+    const volatile int* const full = s_full[warp];  // read where needed: the loop has no registers to spare
+
+    // ---- this warp's steps tile, tile + kWarps, ...: the first ones are on their way before the
+    // queries are read. Lane i holds the page id of tile i & 1 of the next step to be copied; a bad one
+    // drops its tile.
+    constexpr int kStages = Ge::kStages;
+    uint8_t* const ring = smem + warp * Ge::kRing;
+    int next = tile;
+    uint32_t next_st = 0, present = 0;  // two bits per stage
+    auto page_id = [&](int t) {
+      const int tok = t * kTok + kTile * (lane & 1);
+      return tok < full[2] ? __ldg(p.page_table + static_cast<size_t>(s_at.b) * p.max_pages + (tok >> p.p_shift)) : -2;
+    };
+    int32_t pid = page_id(next);
+    auto issue = [&]() {
+      if (next < tile_end) {
+        uint8_t* const st = ring + next_st * Ge::kStage;
+        const int h = *const_cast<const volatile int*>(&s_at.h);
+        present &= ~(3u << (2 * next_st));
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int32_t id = __shfl_sync(0xffffffffu, pid, r);
+          if (static_cast<uint32_t>(id) < static_cast<uint32_t>(p.n_pages)) {
+            const uint8_t* base = p.pool + static_cast<uint64_t>(static_cast<uint32_t>(id)) * static_cast<uint32_t>(p.page_bytes) +
+                                  static_cast<uint32_t>(h * kv4_head_bytes(D, NG, p.P));
+            copy_tile<D, NG>(st + r * (Ge::kCodes / 2), st + Ge::kCodes + r * (Ge::kCodes / 2),
+                             st + 2 * Ge::kCodes + r * (kTile * 8 * NG), base, (next * kTok + r * kTile) & (p.P - 1), p.P, lane);
+            present |= 1u << (2 * next_st + r);
+          } else if (id != -2) {
+            flags |= kErrBadPage;
+          }
+        }
+        next += kWarps;
+        next_st = next_st + 1 == kStages ? 0 : next_st + 1;
+        if (next < tile_end) pid = page_id(next);
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue();
 
     // ---- queries: B fragments of rows g (+ 8), channels 32 j + 8 q4 + (0 .. 7)
     uint32_t bq[NT][KW][4];
     float fr[NT][2], qs[NT][2][NG];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int rr = it.rb * R + 8 * nt + g;  // row = (query token rr / G, head rr % G)
-      const bool live = rr < n * p.G;
+      const int rr = s_at.rb * R + 8 * nt + g;  // row = (query token rr / G, head rr % G)
+      const bool live = rr < s_at.n * p.G;
       float x[KW][8];
       float mx = 0.f;
 #pragma unroll
       for (int j = 0; j < KW; ++j) {
         uint4 w = make_uint4(0, 0, 0, 0);
         if (live)
-          w = __ldg(reinterpret_cast<const uint4*>(p.q.data + static_cast<int64_t>(r0 + rr / p.G) * p.q.row_stride +
-                                                   (it.h * p.G + rr % p.G) * p.q.head_stride + 32 * j) + q4);
+          w = __ldg(reinterpret_cast<const uint4*>(p.q.data + static_cast<int64_t>(s_at.r0 + rr / p.G) * p.q.row_stride +
+                                                   (s_at.h * p.G + rr % p.G) * p.q.head_stride + 32 * j) + q4);
         unpack8(w, p.f16, x[j]);
 #pragma unroll
         for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(x[j][k]));
@@ -247,18 +452,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
         for (int k = 0; k < NG; ++k) qs[nt][c][k] = __shfl_sync(0xffffffffu, sum[k], 4 * (2 * q4 + c));
       }
     }
-    int2 vis[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int rr = it.rb * R + 8 * nt + 2 * q4 + c;
-        vis[nt][c] = rr < n * p.G ? visible(p, T, n, rr / p.G) : make_int2(0, 0);
-      }
-    // tiles in [full_lo, full_hi) are seen whole by every row of the block
-    const int full_lo = (visible(p, T, n, i1).x + kTok - 1) / kTok;
-    const int full_hi = visible(p, T, n, i0).y / kTok;
-
     float o[NT][MT][4], m[NT][2], l[NT][2], om[NT][2][NG];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -266,340 +459,312 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
       for (int j = 0; j < MT; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.f;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        m[nt][c] = -INFINITY;
+        m[nt][c] = kNoMax;
         l[nt][c] = 0.f;
 #pragma unroll
         for (int k = 0; k < NG; ++k) om[nt][c][k] = 0.f;
       }
     }
-    float wf = 0.f, vs_most = -1.f;  // weight factor 2^Ev, and the scale above which it is lowered
+    float wf = 0.f;  // weight factor 2^Ev, lowered when a scale times it exceeds kWeightRoom; 0: none yet
 
-    const size_t region = static_cast<size_t>(it.h) * kv4_head_bytes(D, NG, p.P);
-    const int32_t* table = p.page_table + static_cast<size_t>(it.b) * p.max_pages;
-    // a bad page id drops the tile: its numbers read as zero and its tokens are hidden
-    auto load = [&](int tile, Tile<D, NG>& t) -> bool {
-      const int tok = tile * kTok, tp = tok & (p.P - 1);
-      const int32_t pid = __ldg(table + (tok >> p.p_shift));
-      if (pid < 0 || pid >= p.n_pages) {
-        flags |= kErrBadPage;
-        return false;
-      }
-      const uint8_t* base = p.pool + static_cast<size_t>(pid) * p.page_bytes + region;
-      const uint8_t* kp = base + (tp + g) * (D / 2) + q4 * (D / 8);
-      load_words<KW>(t.k[0], kp);
-      load_words<KW>(t.k[1], kp + 8 * (D / 2));
-      const uint8_t* vp = base + p.P * (D / 2) + (tp + 2 * q4) * (D / 2) + g * (D / 16);
-      load_words<VW>(t.v[0], vp);
-      load_words<VW>(t.v[1], vp + D / 2);
-      load_words<VW>(t.v[2], vp + 8 * (D / 2));
-      load_words<VW>(t.v[3], vp + 9 * (D / 2));
-      const uint8_t* mp = base + p.P * D + (tp + g) * (8 * NG);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if constexpr (NG == 1) {
-          t.meta[e][0] = __ldg(reinterpret_cast<const uint2*>(mp + e * 64));
-        } else {
-#pragma unroll
-          for (int k = 0; k < NG / 2; ++k) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(mp + e * 64 * NG) + k);
-            t.meta[e][2 * k] = make_uint2(x.x, x.y);
-            t.meta[e][2 * k + 1] = make_uint2(x.z, x.w);
-          }
-        }
-      }
-      return true;
-    };
-
-    Tile<D, NG> nxt;
-    int tile = tile0 + a0 + warp;
-    bool ok = false;
-    if (tile < tile_end) ok = load(tile, nxt);
+    uint32_t stage = 0;
     for (; tile < tile_end; tile += kWarps) {
-      Tile<D, NG> cur = nxt;
-      const bool cur_ok = ok;
-      if (tile + kWarps < tile_end) ok = load(tile + kWarps, nxt);
-      if (!cur_ok) continue;  // the same for all lanes
-
-      const int tok = tile * kTok;
-      if (tok + kTok > T) {  // numbers of tokens behind the sequence are not read as such
+      cp_async_wait_group<kStages - 2>();
+      __syncwarp();  // this step's copies of every lane have landed, and the stage before it is read
+      issue();
+      const uint8_t* const st = ring + stage * Ge::kStage;
+      const uint32_t here = present >> (2 * stage);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      const bool edge = tile < full[0] || tile >= full[1];
+#pragma unroll 1
+      for (int r = 0; r < 2; ++r) {
+        if (!((here >> r) & 1)) continue;  // the same for all lanes
+        uint2 num[2][NG];
+        read_numbers<NG>(num, st + 2 * Ge::kCodes + r * (kTile * 8 * NG), g);
+        const int tok = tile * kTok + r * kTile;
+        if (edge) {  // numbers of tokens behind the sequence are not read as such
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (tok + 8 * e + g >= T)
+          for (int e = 0; e < 2; ++e)
+            if (tok + 8 * e + g >= s_at.T)
 #pragma unroll
-            for (int k = 0; k < NG; ++k) cur.meta[e][k] = make_uint2(0, 0);
-      }
-      // ---- scores
-      float x[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
-#pragma unroll
-      for (int k = 0; k < NG; ++k) {
-        float s[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-#pragma unroll
-        for (int j = k * (KW / NG); j < (k + 1) * (KW / NG); ++j) {
-          const uint32_t u0 = cur.k[0][j], u1 = cur.k[1][j], v0 = u0 >> 8, v1 = u1 >> 8;
-          const uint32_t a01[4] = {u0 & 0x000F000Fu, u1 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x00F000F0u};
-          const uint32_t a23[4] = {v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_f16_16816(s[nt], a01, bq[nt][j][0], bq[nt][j][1]);
-            mma_f16_16816(s[nt], a23, bq[nt][j][2], bq[nt][j][3]);
-          }
+              for (int k = 0; k < NG; ++k) num[e][k] = make_uint2(0, 0);
         }
-        const float2 k0 = half2_to_float2(cur.meta[0][k].x), k1 = half2_to_float2(cur.meta[1][k].x);
+        // ---- scores
+        uint32_t kw[2][KW];
+        read_keys<D>(kw, st + r * (Ge::kCodes / 2), g, q4);
+        float x[NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            x[nt][c] += k0.x * (fr[nt][c] * s[nt][c]) + k0.y * qs[nt][c][k];
-            x[nt][2 + c] += k1.x * (fr[nt][c] * s[nt][2 + c]) + k1.y * qs[nt][c][k];
-          }
-      }
-      if (tile < full_lo || tile >= full_hi) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int t = tok + 8 * e + g;
-              if (t < vis[nt][c].x || t >= vis[nt][c].y) x[nt][2 * e + c] = -INFINITY;
-            }
-      }
-      // ---- running max and weight factor, raised rarely
-      float2 v0[NG], v1[NG];
-      float vs = 0.f;
-      bool raise = false;
-#pragma unroll
-      for (int k = 0; k < NG; ++k) {
-        v0[k] = half2_to_float2(cur.meta[0][k].y);
-        v1[k] = half2_to_float2(cur.meta[1][k].y);
-        vs = fmaxf(vs, fmaxf(v0[k].x, v1[k].x));
-      }
-      raise = vs > vs_most;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) raise |= fmaxf(x[nt][c], x[nt][2 + c]) > m[nt][c] + kSlack;
-      if (__any_sync(0xffffffffu, raise)) {
-        float wr = 1.f;
-        vs = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, 4));
-        vs = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, 8));
-        vs = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, 16));
-        if (vs > vs_most) {  // 2^Ev vs in [1, 2)
-          const int e = vs > 0.f ? max(-24, static_cast<int>(__float_as_uint(vs) >> 23) - 127) : -24;
-          const float f = pow2_int(-e);
-          wr = wf > 0.f ? f / wf : 1.f;
-          wf = f;
-          vs_most = kWeightRoom * pow2_int(e);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float sc[2];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float t = fmaxf(x[nt][c], x[nt][2 + c]);
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-            const float mn = fmaxf(m[nt][c], t);
-            sc[c] = mn > m[nt][c] ? ex2(m[nt][c] - mn) : 1.f;
-            m[nt][c] = mn;
-            l[nt][c] *= sc[c];
-#pragma unroll
-            for (int k = 0; k < NG; ++k) om[nt][c][k] *= sc[c];
-            sc[c] *= wr;
-          }
-#pragma unroll
-          for (int j = 0; j < MT; ++j) {
-            o[nt][j][0] *= sc[0], o[nt][j][2] *= sc[0];
-            o[nt][j][1] *= sc[1], o[nt][j][3] *= sc[1];
-          }
-        }
-      }
-      // ---- weights
-      uint32_t bw[NT][NG][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float mm = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
-          w[c] = ex2(x[nt][c] - mm);
-          w[2 + c] = ex2(x[nt][2 + c] - mm);
-          l[nt][c] += w[c] + w[2 + c];
-#pragma unroll
-          for (int k = 0; k < NG; ++k) om[nt][c][k] += w[c] * v0[k].y + w[2 + c] * v1[k].y;
-        }
+        for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
-          const float s0 = v0[k].x * wf, s1 = v1[k].x * wf;
-          bw[nt][k][0] = movmatrix_t(float2_to_half2(w[0] * s0, w[1] * s0));
-          bw[nt][k][1] = movmatrix_t(float2_to_half2(w[2] * s1, w[3] * s1));
+          float s[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+          for (int j = k * (KW / NG); j < (k + 1) * (KW / NG); ++j) {
+            const uint32_t u0 = kw[0][j], u1 = kw[1][j], v0 = u0 >> 8, v1 = u1 >> 8;
+            const uint32_t a01[4] = {u0 & 0x000F000Fu, u1 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x00F000F0u};
+            const uint32_t a23[4] = {v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16_16816(s[nt], a01, bq[nt][j][0], bq[nt][j][1]);
+              mma_f16_16816(s[nt], a23, bq[nt][j][2], bq[nt][j][3]);
+            }
+          }
+          const float2 k0 = half2_to_float2(num[0][k].x), k1 = half2_to_float2(num[1][k].x);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              x[nt][c] += k0.x * (fr[nt][c] * s[nt][c]) + k0.y * qs[nt][c][k];
+              x[nt][2 + c] += k1.x * (fr[nt][c] * s[nt][2 + c]) + k1.y * qs[nt][c][k];
+            }
         }
-      }
-      // ---- readout
+        if (edge) {
 #pragma unroll
-      for (int u = 0; u < VW; ++u) {
-        const uint32_t p0 = prmt(cur.v[0][u], cur.v[1][u], 0x5410), p1 = prmt(cur.v[0][u], cur.v[1][u], 0x7632);
-        const uint32_t p2 = prmt(cur.v[2][u], cur.v[3][u], 0x5410), p3 = prmt(cur.v[2][u], cur.v[3][u], 0x7632);
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int hi = 0; hi < 2; ++hi) {
-          const int sh = 8 * hi;
-          const uint32_t r0w = p0 >> sh, r1w = p1 >> sh, r2w = p2 >> sh, r3w = p3 >> sh;
-          const uint32_t a0w[4] = {r0w & 0x000F000Fu, r1w & 0x000F000Fu, r2w & 0x000F000Fu, r3w & 0x000F000Fu};
-          const uint32_t a1w[4] = {r0w & 0x00F000F0u, r1w & 0x00F000F0u, r2w & 0x00F000F0u, r3w & 0x00F000F0u};
-          const int j = 4 * u + 2 * hi;
-          constexpr int kPer = MT / NG;  // 16-channel blocks per group
+            for (int c = 0; c < 2; ++c) {
+              const int rr = s_at.rb * R + 8 * nt + 2 * q4 + c;
+              const int2 v = rr < s_at.n * p.G ? visible(p, s_at.T, s_at.n, rr / p.G) : make_int2(0, 0);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int t = tok + 8 * e + g;
+                if (t < v.x || t >= v.y) x[nt][2 * e + c] = -INFINITY;
+              }
+            }
+        }
+        // ---- running max and weight factor, raised rarely
+        float2 v0[NG], v1[NG];
+        float vs = 0.f;
+        bool raise = false;
+#pragma unroll
+        for (int k = 0; k < NG; ++k) {
+          v0[k] = half2_to_float2(num[0][k].y);
+          v1[k] = half2_to_float2(num[1][k].y);
+          vs = fmaxf(vs, fmaxf(v0[k].x, v1[k].x));
+        }
+        raise = vs * wf > kWeightRoom;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) raise |= fmaxf(x[nt][c], x[nt][2 + c]) > m[nt][c] + kSlack;
+        if (__any_sync(0xffffffffu, raise)) {
+          float wr = 1.f;
+          vs = max_over_g(vs);
+          if (wf == 0.f || vs * wf > kWeightRoom) {  // 2^Ev vs in [1, 2)
+            const int e = vs > 0.f ? max(-24, static_cast<int>(__float_as_uint(vs) >> 23) - 127) : -24;
+            const float f = pow2_int(-e);
+            wr = wf > 0.f ? f / wf : 1.f;
+            wf = f;
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma_f16_16816(o[nt][j], a0w, bw[nt][j / kPer][0], bw[nt][j / kPer][1]);
-            mma_f16_16816(o[nt][j + 1], a1w, bw[nt][(j + 1) / kPer][0], bw[nt][(j + 1) / kPer][1]);
+            float sc[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float mn = fmaxf(m[nt][c], max_over_g(fmaxf(x[nt][c], x[nt][2 + c])));
+              sc[c] = ex2(m[nt][c] - mn);
+              m[nt][c] = mn;
+              l[nt][c] *= sc[c];
+#pragma unroll
+              for (int k = 0; k < NG; ++k) om[nt][c][k] *= sc[c];
+              sc[c] *= wr;
+            }
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+              o[nt][j][0] *= sc[0], o[nt][j][2] *= sc[0];
+              o[nt][j][1] *= sc[1], o[nt][j][3] *= sc[1];
+            }
+          }
+        }
+        // ---- weights
+        uint32_t bw[NT][NG][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            w[c] = ex2(x[nt][c] - m[nt][c]);
+            w[2 + c] = ex2(x[nt][2 + c] - m[nt][c]);
+            l[nt][c] += w[c] + w[2 + c];
+#pragma unroll
+            for (int k = 0; k < NG; ++k) om[nt][c][k] += w[c] * v0[k].y + w[2 + c] * v1[k].y;
+          }
+#pragma unroll
+          for (int k = 0; k < NG; ++k) {
+            const float s0 = v0[k].x * wf, s1 = v1[k].x * wf;
+            bw[nt][k][0] = movmatrix_t(float2_to_half2(w[0] * s0, w[1] * s0));
+            bw[nt][k][1] = movmatrix_t(float2_to_half2(w[2] * s1, w[3] * s1));
+          }
+        }
+        // ---- readout
+        no_loads_across();
+        uint32_t vw[4][VW];
+        read_values<D>(vw, st + Ge::kCodes + r * (Ge::kCodes / 2), g, q4);
+#pragma unroll
+        for (int u = 0; u < VW; ++u) {
+          const uint32_t p0 = prmt(vw[0][u], vw[1][u], 0x5410), p1 = prmt(vw[0][u], vw[1][u], 0x7632);
+          const uint32_t p2 = prmt(vw[2][u], vw[3][u], 0x5410), p3 = prmt(vw[2][u], vw[3][u], 0x7632);
+#pragma unroll
+          for (int hi = 0; hi < 2; ++hi) {
+            const int sh = 8 * hi;
+            const uint32_t r0w = p0 >> sh, r1w = p1 >> sh, r2w = p2 >> sh, r3w = p3 >> sh;
+            const uint32_t a0w[4] = {r0w & 0x000F000Fu, r1w & 0x000F000Fu, r2w & 0x000F000Fu, r3w & 0x000F000Fu};
+            const uint32_t a1w[4] = {r0w & 0x00F000F0u, r1w & 0x00F000F0u, r2w & 0x00F000F0u, r3w & 0x00F000F0u};
+            const int j = 4 * u + 2 * hi;
+            constexpr int kPer = MT / NG;  // 16-channel blocks per group
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16_16816(o[nt][j], a0w, bw[nt][j / kPer][0], bw[nt][j / kPer][1]);
+              mma_f16_16816(o[nt][j + 1], a1w, bw[nt][(j + 1) / kPer][0], bw[nt][(j + 1) / kPer][1]);
+            }
           }
         }
       }
     }
+    cp_async_wait_group<0>();
+    __syncwarp();
 
-    // ---- the warps of the CTA meet
+    // ---- the warps of the CTA meet: a common max per row, then each leaves its scaled sums
     const float undo = wf > 0.f ? 16777216.f / wf : 0.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float v = l[nt][c];
-        v += __shfl_xor_sync(0xffffffffu, v, 4);
-        v += __shfl_xor_sync(0xffffffffu, v, 8);
-        v += __shfl_xor_sync(0xffffffffu, v, 16);
-        const int row = 8 * nt + 2 * q4 + c;
-        if (g == 0) s_m[warp][row] = m[nt][c], s_l[warp][row] = v;
+        l[nt][c] = sum_over_g(l[nt][c]);
 #pragma unroll
-        for (int k = 0; k < NG; ++k) {
-          float z = om[nt][c][k];
-          z += __shfl_xor_sync(0xffffffffu, z, 4);
-          z += __shfl_xor_sync(0xffffffffu, z, 8);
-          z += __shfl_xor_sync(0xffffffffu, z, 16);
-          om[nt][c][k] = z;
-        }
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-          const float f = (j & 1) ? undo * 0.0625f : undo;
-          const float z = om[nt][c][j / (MT / NG)];
-          s_o[warp][row][16 * j + g] = o[nt][j][c] * f + z;
-          s_o[warp][row][16 * j + 8 + g] = o[nt][j][2 + c] * f + z;
-        }
+        for (int k = 0; k < NG; ++k) om[nt][c][k] = sum_over_g(om[nt][c][k]);
+        if (g == 0) s_m[warp][8 * nt + 2 * q4 + c] = m[nt][c], s_l[warp][8 * nt + 2 * q4 + c] = l[nt][c];
       }
     __syncthreads();
-    const long long item_end = item0 + tiles;
-    const bool whole = at == item0 && end >= item_end;
-    const long long c0 = item0 / share, c1 = (item_end - 1) / share;  // CTAs of the item
-    // partial slots: 2 c for the item that CTA c continues, 2 c + 1 for the one that it begins
-    const int slot = 2 * static_cast<int>(blockIdx.x) + (at == item0 ? 1 : 0);
-    auto store_row = [&](int row, int ch, float v, float M, float L) {  // M in log2 units
-      const int rr = it.rb * R + row;
-      if (rr >= n * p.G) return;
-      const size_t orow = static_cast<size_t>(r0 + rr / p.G) * p.Hq + it.h * p.G + rr % p.G;
-      const float y = L > 0.f ? v / L : (L == 0.f ? 0.f : v);
-      p.out[orow * D + ch] = p.f16 ? __half_as_ushort(__float2half_rn(y)) : __bfloat16_as_ushort(__float2bfloat16_rn(y));
-      if (ch == 0 && p.lse) p.lse[orow] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : (L == 0.f ? -INFINITY : L);
-    };
-    for (int e = tid; e < R * D; e += kThreads) {
-      const int row = e / D, ch = e % D;
-      float M = -INFINITY;
+    float(*const mine_o)[kRowPad] = reinterpret_cast<float(*)[kRowPad]>(ring);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][row]);
-      float v = 0.f, L = 0.f;
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int row = 8 * nt + 2 * q4 + c;
+        float M = m[nt][c];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][row]);
+        const float f = ex2(m[nt][c] - M), fo = f * undo;
+#pragma unroll
+        for (int k = 0; k < NG; ++k) om[nt][c][k] *= f;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          const float fj = (j & 1) ? fo * 0.0625f : fo;
+          mine_o[row][16 * j + g] = o[nt][j][c] * fj + om[nt][c][j / (MT / NG)];
+          mine_o[row][16 * j + 8 + g] = o[nt][j][2 + c] * fj + om[nt][c][j / (MT / NG)];
+        }
+      }
+    if (tid < R) {
+      float M = kNoMax, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][tid]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) L += ex2(s_m[w][tid] - M) * s_l[w][tid];
+      s_ml[tid][0] = M, s_ml[tid][1] = L;
+    }
+    __syncthreads();
+    const long long item_end = s_at.item0 + s_at.tiles;
+    const bool whole = s_at.at == s_at.item0 && s_at.end >= item_end;
+    const int c0 = static_cast<int>(s_at.item0 / s_at.share);  // first CTA of the item
+    // partial slots: 2 c for the item that CTA c continues, 2 c + 1 for the one that it begins
+    const int slot = 2 * static_cast<int>(blockIdx.x) + (s_at.at == s_at.item0 ? 1 : 0);
+    for (int e = tid; e < R * D / 4; e += kThreads) {
+      const int row = e / (D / 4), c4 = e % (D / 4);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = s_m[w][row] == -INFINITY ? (s_l[w][row] == 0.f ? 0.f : 1.f) : ex2(s_m[w][row] - M);
-        if (f != 0.f) v += f * s_o[w][row][ch], L += f * s_l[w][row];
+        const float4 x = *reinterpret_cast<const float4*>(smem + w * Ge::kRing + (row * kRowPad + 4 * c4) * 4);
+        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
       }
       if (whole) {
-        store_row(row, ch, v, M, L);
+        store_out<D, R>(p, s_at, row, c4, v, s_ml[row][0], s_ml[row][1]);
       } else {
-        p.part_o[(static_cast<size_t>(slot) * R + row) * D + ch] = v;
-        if (ch == 0) {
-          float* ml = p.part_ml + (static_cast<size_t>(slot) * R + row) * 2;
-          ml[0] = M;
-          ml[1] = L;
-        }
+        reinterpret_cast<float4*>(p.part_o + (static_cast<size_t>(slot) * R + row) * D)[c4] = v;
+        if (c4 == 0)
+          reinterpret_cast<float2*>(p.part_ml)[static_cast<size_t>(slot) * R + row] = make_float2(s_ml[row][0], s_ml[row][1]);
       }
     }
     if (!whole) {
       __threadfence();
       __syncthreads();
       if (tid == 0) {
-        const uint32_t parts = static_cast<uint32_t>(c1 - c0 + 1);
-        const uint32_t before = atomicAdd(p.arrive + c0, 1u);
-        s_last = before == parts - 1;
-        if (s_last) {
+        const int parts = static_cast<int>((item_end - 1) / s_at.share) - c0 + 1;  // CTAs of the item
+        const bool last = atomicAdd(p.arrive + c0, 1u) == static_cast<uint32_t>(parts - 1);
+        s_last = last ? parts : 0;
+        if (last) {
           p.arrive[c0] = 0;
           __threadfence();
         }
       }
       __syncthreads();
-      if (s_last) {
-        for (int e = tid; e < R * D; e += kThreads) {
-          const int row = e / D, ch = e % D;
-          float M = -INFINITY, L = 0.f, v = 0.f;
-          for (long long c = c0; c <= c1; ++c) {
-            const size_t sl = 2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0);
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + sl * R + row);
-            if (ml.y == 0.f) continue;
-            const float x = __ldcg(p.part_o + (sl * R + row) * D + ch);
-            const float mn = fmaxf(M, ml.x);
-            const float fa = M == -INFINITY ? 0.f : ex2(M - mn), fb = ml.x == -INFINITY ? 1.f : ex2(ml.x - mn);
-            v = v * fa + x * fb;
-            L = L * fa + ml.y * fb;
-            M = mn;
-          }
-          store_row(row, ch, v, M, L);
-        }
-      }
+      if (s_last) merge_parts<D, R, kThreads>(p, s_at, c0, s_last, smem, Ge::kSmem, s_f, s_ml);
     }
     __syncthreads();
 
     // ---- the next item
-    at = min(end, item_end);
-    if (at >= end) break;
-    item0 = at;
-    if (++it.rb == blocks) {
-      it.rb = 0;
-      if (++it.h == p.Hkv) {
-        it.h = 0;
-        int ignore = 0;
-        do {
-          if (++it.b >= p.B) return;
-          sequence<R>(p, it.b, T, n, r0, tiles, blocks, ignore);
-        } while (blocks == 0);
+    if (tid == 0) {
+      Place& s = s_at;
+      s.at = min(s.end, item_end);
+      if (s.at < s.end) {
+        s.item0 = s.at;
+        if (++s.rb == s.blocks) {
+          s.rb = 0;
+          if (++s.h == p.Hkv) {
+            s.h = 0;
+            int ignore = 0;
+            do {
+              if (++s.b >= p.B) {  // lengths that changed under the call
+                s.at = s.end;
+                break;
+              }
+              sequence<R>(p, s.b, s.T, s.n, s.r0, s.tiles, s.blocks, ignore);
+            } while (s.blocks == 0);
+          }
+        }
       }
     }
+    __syncthreads();
   }
   flags = __reduce_or_sync(0xffffffffu, flags);
   if (lane == 0 && flags) atomicOr(p.err, flags);
 }
 
+template <int D, int NG, int NT>
+cudaError_t launch_rows(const Kv4AttnParams& p, int ctas, cudaStream_t stream) {
+  using Ge = Geom<D, NG, NT>;
+  static bool attr_done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_done[dev]) {
+    e = cudaFuncSetAttribute(kv4_decode_kernel<D, NG, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ge::kSmem);
+    if (e != cudaSuccess) return e;
+    attr_done[dev] = true;
+  }
+  kv4_decode_kernel<D, NG, NT><<<ctas, Ge::kThreads, Ge::kSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
 template <int D, int NG>
 cudaError_t launch(const Kv4AttnParams& p, int rows, int ctas, cudaStream_t stream) {
-  if (rows == 8) kv4_decode_kernel<D, NG, 1><<<ctas, kThreads, 0, stream>>>(p);
-  else kv4_decode_kernel<D, NG, 2><<<ctas, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return rows == 8 ? launch_rows<D, NG, 1>(p, ctas, stream) : launch_rows<D, NG, 2>(p, ctas, stream);
 }
 
 }  // namespace
 
 int kv4_decode_rows(int max_q, int G) { return static_cast<int64_t>(max_q) * G <= 8 ? 8 : 16; }
-int kv4_decode_ctas(int rows, int num_sms) {
-  return std::min(num_sms * (rows == 8 ? 4 : 3), static_cast<int>(kKv4CounterBytes / 4));
-}
+int kv4_decode_ctas(int num_sms) { return std::min(2 * num_sms, static_cast<int>(kKv4CounterBytes / 4)); }
 size_t kv4_decode_workspace_bytes(int rows, int D, int num_sms) {
-  const size_t ctas = kv4_decode_ctas(rows, num_sms);
+  const size_t ctas = kv4_decode_ctas(num_sms);
   return kKv4CounterBytes + 2 * ctas * rows * (static_cast<size_t>(D) + 2) * sizeof(float);
 }
 
 cudaError_t launch_kv4_decode(const Kv4AttnParams& p, int D, int n_groups, int num_sms, cudaStream_t stream) {
-  const int rows = kv4_decode_rows(p.max_q, p.G), ctas = kv4_decode_ctas(rows, num_sms);
+  const int rows = kv4_decode_rows(p.max_q, p.G), ctas = kv4_decode_ctas(num_sms);
   if (D == 128) {
     if (n_groups == 1) return launch<128, 1>(p, rows, ctas, stream);
     if (n_groups == 2) return launch<128, 2>(p, rows, ctas, stream);
