@@ -22,6 +22,7 @@ SOURCES = {  # file -> extra flags
     "abi_kv4.cu": [],
     "kv4_append.cu": ["-fmad=false"],  # as the writer
     "kv4_attn.cu": [],
+    "kv4_prompt.cu": [],
     "latent_append.cu": [],
 }
 

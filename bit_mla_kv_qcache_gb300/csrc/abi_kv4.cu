@@ -178,7 +178,17 @@ size_t mla_qcache_kv4_workspace_bytes(const mla_qcache_kv4_config* cfg, int32_t 
     return 0;
   int sms = 0;
   if (sm_count(&sms) != MLA_QCACHE_OK) return 0;
-  return mlaq::kv4_decode_workspace_bytes(mlaq::kv4_decode_rows(max_q, n_heads / cfg->n_kv_heads), cfg->head_dim, sms);
+  const int G = n_heads / cfg->n_kv_heads, D = cfg->head_dim;
+  const size_t few = mlaq::kv4_decode_workspace_bytes(mlaq::kv4_decode_rows(max_q, G), D, sms);
+  if (!mlaq::kv4_uses_prompt(max_q, G)) return few;
+  // the rows of a call, below max_q per sequence, decide how it is cut: the most that any needs
+  size_t most = few;
+  for (int64_t rows = 1; rows <= max_q; rows = rows < max_q && 2 * rows > max_q ? max_q : 2 * rows) {
+    const size_t w = mlaq::kv4_prompt_workspace_bytes(
+        mlaq::kv4_prompt_plan(B, cfg->n_kv_heads, static_cast<int>(rows), max_q, G, sms), D);
+    most = most > w ? most : w;
+  }
+  return most;
 }
 
 int mla_qcache_kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t n_heads, int32_t n_rows,
@@ -208,9 +218,14 @@ int mla_qcache_kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t
     return MLA_QCACHE_ERR_SHAPE;
   int sms = 0;
   if ((st = sm_count(&sms)) != MLA_QCACHE_OK) return st;
-  const int rows = mlaq::kv4_decode_rows(max_q, G);
-  if (workspace_bytes < mlaq::kv4_decode_workspace_bytes(rows, D, sms)) return MLA_QCACHE_ERR_WORKSPACE;
-  const size_t ctas = mlaq::kv4_decode_ctas(sms);
+  const bool prompt = mlaq::kv4_uses_prompt(max_q, G);
+  const mlaq::Kv4PromptPlan plan = mlaq::kv4_prompt_plan(B, cfg->n_kv_heads, n_rows, max_q, G, sms);
+  const size_t rows = prompt ? plan.rows : mlaq::kv4_decode_rows(max_q, G);
+  const size_t need = prompt ? mlaq::kv4_prompt_workspace_bytes(plan, D)
+                             : mlaq::kv4_decode_workspace_bytes(static_cast<int>(rows), D, sms);
+  if (workspace_bytes < need) return MLA_QCACHE_ERR_WORKSPACE;
+  if (prompt && plan.ctas > 0x7fffffff) return MLA_QCACHE_ERR_SHAPE;
+  const size_t ctas = prompt ? (plan.line ? plan.ctas : 0) : mlaq::kv4_decode_ctas(sms);
   p.cu_q = cu_q;
   p.page_table = page_table;
   p.seq_lens = seq_lens;
@@ -236,7 +251,9 @@ int mla_qcache_kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t
   p.window = window;
   p.causal = causal != 0;
   p.f16 = dtype == MLA_QCACHE_FP16;
-  const cudaError_t e = mlaq::launch_kv4_decode(p, D, D / cfg->group, sms, static_cast<cudaStream_t>(stream));
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = prompt ? mlaq::launch_kv4_prompt(p, plan, D, D / cfg->group, cs)
+                               : mlaq::launch_kv4_decode(p, D, D / cfg->group, sms, cs);
   return e == cudaSuccess ? MLA_QCACHE_OK : MLA_QCACHE_ERR_CUDA;
 }
 

@@ -80,4 +80,16 @@ int kv4_decode_ctas(int num_sms);
 size_t kv4_decode_workspace_bytes(int rows, int D, int num_sms);
 cudaError_t launch_kv4_decode(const Kv4AttnParams& p, int D, int n_groups, int num_sms, cudaStream_t stream);
 
+// More rows than the decode kernel holds go to the fifth-generation tensor cores: 128 rows of
+// queries (or two tiles of 128), one CTA per item or, with few items, the items cut over the SMs.
+struct Kv4PromptPlan {
+  bool two, line;
+  int rows;      // rows of one item
+  int64_t ctas;
+};
+bool kv4_uses_prompt(int max_q, int G);
+Kv4PromptPlan kv4_prompt_plan(int B, int Hkv, int n_rows, int max_q, int G, int num_sms);
+size_t kv4_prompt_workspace_bytes(const Kv4PromptPlan& z, int D);
+cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, const Kv4PromptPlan& z, int D, int n_groups, cudaStream_t stream);
+
 }  // namespace mlaq

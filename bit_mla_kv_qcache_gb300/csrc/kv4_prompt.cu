@@ -1,0 +1,756 @@
+// Attention over the grouped-query cache in 4 bits for many query rows per kv head (chunks of a
+// prompt, several drafted tokens of many heads), on the fifth-generation tensor cores. Rows = (query
+// token, head of the group), 128 to a tile of queries.
+//
+// One CTA per SM, 13 warps. Per tile of 128 cached tokens:
+//   warps 8-11   one token per thread: the token's codes become FP16 values min + code * scale (one
+//                rounding) in shared memory, keys and values, two stages each;
+//   warp 12      one thread issues S = Q K^T (128 rows x 128 tokens, both operands in shared memory)
+//                and O += P V (P from tensor memory);
+//   warps 0-3, 4-7  two softmax groups, one row per thread: S is read from tensor memory (its
+//                maximum, then the weights), P replaces it there as FP16. The running max is raised,
+//                and O rescaled in place, only when a score exceeds it by more than 2^8.
+// The groups alternate so that the tensor cores work for one while the other takes its softmax:
+// with more than 128 rows they hold two tiles of queries and see every token tile, with at most 128
+// they hold the same queries, take the even and the odd token tiles and join at the end.
+// Tensor memory: S0, S1 (128 columns each), O0, O1 (D each). A step's S overwrites the P of the same
+// group two steps before; products of one thread run in the order of their issue.
+//
+// Channels keep the order in which a code word unpacks: eight channels of a word in the order 0 4 1 5
+// 2 6 3 7, for keys matched by the queries, for values undone when a row is stored.
+//
+// Work: with many items (sequence, kv head, row block) one CTA per item, those that see the most
+// tokens first; with few, the items' token tiles are laid on one line and cut evenly over the SMs
+// (as in the kernel for few rows).
+#include <algorithm>
+
+#include <cuda_fp16.h>
+
+#include "append.cuh"
+#include "kernels.cuh"
+#include "kv4.cuh"
+#include "ptx.cuh"
+#include "tcgen05.cuh"
+
+namespace mlaq {
+namespace {
+
+constexpr int kThreads = 416;
+constexpr int kTok = 128;         // tokens per tile
+constexpr int kMaxParts = 32;     // CTAs that one item is cut into, at most
+constexpr float kSlack = 8.f;     // the running max is raised when a score exceeds it by more than this
+constexpr float kNoMax = -1e30f;  // the running max before the first score
+constexpr long long kBudget = 4ll << 30;  // cycles of a wait before it is given up
+
+template <int D>
+struct Geom {
+  static constexpr int kTile = 128 * D * 2;  // bytes of a tile of queries, keys or values
+  static constexpr int kQ = 0, kK = 2 * kTile, kV = 4 * kTile;
+  static constexpr int kSmem = 6 * kTile + 1024;  // slack to align the start
+  static constexpr uint32_t kColS = 0, kColO = 256;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint32_t h2(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The two codes at bits 0-3 (kHigh: 4-7) of the halves of w as min + code * scale: 1024 + n (1024 + 16 n)
+// is put together by bits, n comes out exactly, then one rounding.
+template <bool kHigh>
+__device__ __forceinline__ uint32_t dequant2(uint32_t w, __half2 s, __half2 m) {
+  const uint32_t b = and_or(w, kHigh ? 0x00F000F0u : 0x000F000Fu, 0x64006400u);
+  const __half2 x = *reinterpret_cast<const __half2*>(&b);
+  const __half2 n = kHigh ? __hfma2(x, __float2half2_rn(0.0625f), __float2half2_rn(-64.f))
+                          : __hadd2(x, __float2half2_rn(-1024.f));
+  const __half2 v = __hfma2(n, s, m);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The part of an item that the CTA works on.
+struct Seg {
+  int b, h, rb;          // sequence, kv head, row block
+  int T, n, r0;          // of the sequence: length, query rows, first row
+  int tile, tiles;       // first token tile here, and how many
+  int part, c0, parts;   // slot of the partial result, or -1 (the item is whole here); CTAs of the item
+  int valid;
+  // line mode: position, end of the CTA's stretch, the item's first tile and its tiles, CTA stretch
+  long long at, end, item0, share;
+  int item_tiles;
+};
+
+__device__ __forceinline__ void load_sequence(const Kv4AttnParams& p, int b, int& T, int& n, int& r0, int& flags) {
+  T = __ldg(p.seq_lens + b);
+  r0 = b, n = 1;
+  if (p.cu_q) {
+    r0 = __ldg(p.cu_q + b);
+    n = __ldg(p.cu_q + b + 1) - r0;
+  }
+  if (n < 0 || n > p.max_q || r0 < 0 || r0 > p.n_rows - n) {
+    flags |= kErrRows;
+    n = 0;
+  }
+  if (T < 0 || T > static_cast<int64_t>(p.max_pages) * p.P) {
+    flags |= kErrSeqOverflow;
+    T = 0;
+  }
+}
+
+// Tokens that query row i of the sequence sees: [lo, hi).
+__device__ __forceinline__ int2 visible(const Kv4AttnParams& p, int T, int n, int i) {
+  const int pos = T - n + i;
+  const int hi = p.causal ? max(0, min(T, pos + 1)) : T;
+  const int lo = p.window ? max(0, pos - p.window + 1) : 0;
+  return make_int2(lo, hi);
+}
+
+// First token tile of row block rb and the number of tiles (at least one, to store rows that see nothing).
+__device__ __forceinline__ int2 block_tiles(const Kv4AttnParams& p, int T, int n, int rb, int R) {
+  const int i0 = static_cast<int>(static_cast<int64_t>(rb) * R / p.G);
+  const int i1 = min(n - 1, static_cast<int>((static_cast<int64_t>(rb) * R + R - 1) / p.G));
+  const int t0 = visible(p, T, n, i0).x / kTok, t1 = (visible(p, T, n, i1).y + kTok - 1) / kTok;
+  return make_int2(t0, max(1, t1 - t0));
+}
+__device__ __forceinline__ int row_blocks(const Kv4AttnParams& p, int n, int R) { return (n * p.G + R - 1) / R; }
+
+// Line mode: the segment that starts at s.at (b, h, rb and the sequence are set).
+__device__ __forceinline__ void line_segment(const Kv4AttnParams& p, Seg& s, int R) {
+  const int2 t = block_tiles(p, s.T, s.n, s.rb, R);
+  s.item_tiles = t.y;
+  const int a0 = static_cast<int>(s.at - s.item0);
+  const int a1 = static_cast<int>(min(s.end - s.item0, static_cast<long long>(t.y)));
+  s.tile = t.x + a0;
+  s.tiles = a1 - a0;
+  s.c0 = static_cast<int>(s.item0 / s.share);
+  s.parts = static_cast<int>((s.item0 + t.y - 1) / s.share) - s.c0 + 1;
+  s.part = s.parts == 1 ? -1 : 2 * static_cast<int>(blockIdx.x) + (a0 == 0 ? 1 : 0);
+  s.valid = 1;
+}
+
+template <int D, int NG>
+__global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnParams p, const int two, const int line) {
+  using Ge = Geom<D>;
+  constexpr int KW = D / 32, VW = D / 64, CB = D / 8;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t bars[13];  // k_full[2] k_free[2] v_full[2] v_free[2] s_full[2] p_ready[2] o_done
+  __shared__ uint32_t s_tmem;
+  __shared__ Seg s_seg;
+  __shared__ long long s_sum[kThreads + 1];
+  __shared__ int s_most[kThreads / 32], s_last;
+  __shared__ volatile int s_abort;
+  __shared__ float s_ml[2][128][2];
+  uint64_t *const k_full = bars, *const k_free = bars + 2, *const v_full = bars + 4, *const v_free = bars + 6,
+           *const s_full = bars + 8, *const p_ready = bars + 10, *const o_done = bars + 12;
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (base - smem_addr(smem_raw));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int R = two ? 256 : 128;
+  int flags = 0;
+
+  // ---- which part of which item
+  if (!line) {
+    if (tid == 0) {
+      Seg& s = s_seg;
+      const int per = p.B * p.Hkv, blocks = static_cast<int>(gridDim.x) / per;
+      const int bh = static_cast<int>(blockIdx.x) % per;
+      s.rb = blocks - 1 - static_cast<int>(blockIdx.x) / per;
+      s.b = bh / p.Hkv;
+      s.h = bh % p.Hkv;
+      int f = 0;
+      load_sequence(p, s.b, s.T, s.n, s.r0, f);
+      flags |= f;
+      s.valid = s.rb < row_blocks(p, s.n, R);
+      s.part = -1;
+      s.parts = 1;
+      if (s.valid) {
+        const int2 t = block_tiles(p, s.T, s.n, s.rb, R);
+        s.tile = t.x;
+        s.tiles = t.y;
+      }
+    }
+  } else {
+    // thread i sums the tiles of sequences [i c, (i + 1) c)
+    const int chunk = (p.B + kThreads - 1) / kThreads;
+    long long x = 0;
+    int most = 0;
+    for (int b = tid * chunk; b < min(p.B, (tid + 1) * chunk); ++b) {
+      int T, n, r0, f = 0;
+      load_sequence(p, b, T, n, r0, f);
+      if (blockIdx.x == 0) flags |= f;
+      const int blocks = row_blocks(p, n, R);
+      for (int rb = 0; rb < blocks; ++rb) {
+        const int t = block_tiles(p, T, n, rb, R).y;
+        x += static_cast<long long>(t) * p.Hkv;
+        most = max(most, t);
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 31) s_sum[warp] = x;
+    if (lane == 0) s_most[warp] = most;
+    __syncthreads();
+    long long before = 0;
+    for (int w = 0; w < warp; ++w) before += s_sum[w];
+    for (int w = 0; w < kThreads / 32; ++w) most = max(most, s_most[w]);
+    __syncthreads();
+    s_sum[tid + 1] = before + x;
+    if (tid == 0) s_sum[0] = 0;
+    __syncthreads();
+    if (tid == 0) {
+      Seg& s = s_seg;
+      const long long total = s_sum[kThreads];
+      s.share = max((total + gridDim.x - 1) / gridDim.x,
+                    static_cast<long long>(max(min(4, most), (most + kMaxParts - 2) / (kMaxParts - 1))));
+      s.at = s.share * blockIdx.x;
+      s.end = min(total, s.at + s.share);
+      s.valid = 0;
+      if (s.at < s.end) {
+        int lo = 0, hi = kThreads - 1;  // s_sum[lo] <= at < s_sum[lo + 1]
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (s_sum[mid + 1] > s.at) hi = mid;
+          else lo = mid + 1;
+        }
+        long long pos = s_sum[lo];
+        int f = 0;
+        for (s.b = lo * chunk; s.b < p.B && !s.valid; ++s.b) {
+          load_sequence(p, s.b, s.T, s.n, s.r0, f);
+          const int blocks = row_blocks(p, s.n, R);
+          long long per = 0;  // tiles of one kv head
+          for (int rb = 0; rb < blocks; ++rb) per += block_tiles(p, s.T, s.n, rb, R).y;
+          if (s.at < pos + per * p.Hkv) {
+            s.h = static_cast<int>((s.at - pos) / per);
+            pos += s.h * per;
+            for (s.rb = 0; s.rb < blocks - 1; ++s.rb) {
+              const int t = block_tiles(p, s.T, s.n, s.rb, R).y;
+              if (s.at < pos + t) break;
+              pos += t;
+            }
+            s.item0 = pos;
+            line_segment(p, s, R);
+            break;
+          }
+          pos += per * p.Hkv;
+        }
+      }
+    }
+  }
+  if (tid == 0) {
+    s_abort = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full + i, 128);
+      mbar_init(v_full + i, 128);
+      mbar_init(p_ready + i, 128);
+      mbar_init(k_free + i, 1);
+      mbar_init(v_free + i, 1);
+      mbar_init(s_full + i, 1);
+    }
+    mbar_init(o_done, 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (!s_seg.valid) {
+    flags = __reduce_or_sync(0xffffffffu, flags);
+    if (lane == 0 && flags) atomicOr(p.err, flags);
+    return;
+  }
+  if (warp == 12) tc5::alloc512(&s_tmem);
+  tc5::fence_before();
+  __syncthreads();
+  tc5::fence_after();
+  const uint32_t tmem = s_tmem;
+
+  // A wait that runs out raises the abort flag, which ends every other wait too.
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+      if (s_abort) return false;
+      if (clock64() - t0 > kBudget) {
+        s_abort = 1;
+        flags |= kErrTimeout;
+        return false;
+      }
+    }
+    return true;
+  };
+
+  uint32_t tiles_done = 0;                  // token tiles of earlier segments (stages and their phases go on)
+  uint32_t steps_done[2] = {0, 0};          // steps of each group in earlier segments
+  uint32_t segs = 0;
+  const int group = warp >> 2;              // 0, 1: softmax groups; 2: unpacking; 3: products
+  const int lane_row = tid & 127;
+  const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+
+  while (true) {
+    const Seg& sg = s_seg;
+    const int n_tiles = sg.tiles, tile0 = sg.tile;
+    const int steps = two ? 2 * n_tiles : n_tiles;  // step s: group s & 1, token tile two ? s / 2 : s
+    const int rows_left = sg.n * p.G - sg.rb * R;   // live rows of the block
+
+    float m = kNoMax, l = 0.f, fr = 0.f;
+    int2 vis = make_int2(0, 0);
+    if (group < 2) {
+      // ---- queries: this thread's row, prescaled by a power of two, in the keys' channel order
+      const int row = (two ? 128 * group : 0) + lane_row;
+      const bool live = row < rows_left;
+      const int rr = sg.rb * R + row;
+      if (live) vis = visible(p, sg.T, sg.n, rr / p.G);
+      const uint16_t* src = p.q.data + static_cast<int64_t>(sg.r0 + rr / p.G) * p.q.row_stride +
+                            static_cast<int64_t>(sg.h * p.G + rr % p.G) * p.q.head_stride;
+      uint4 w[CB];
+      float mx = 0.f;
+#pragma unroll
+      for (int c = 0; c < CB; ++c) w[c] = live ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < CB; ++c) {
+        float x[8];
+        unpack8(w[c], p.f16, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(x[k]));
+      }
+      bool range = false;
+      const int E = prescale_exponent(mx, range);
+      const float up = p.scale_log2 < 0.f ? -pow2_int(E) : pow2_int(E);
+      fr = pow2_int(-E) * fabsf(p.scale_log2);
+      if (two || group == 0) {
+        const uint32_t dst = base + Ge::kQ + (two ? group * Ge::kTile : 0) + 16 * lane_row;
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {  // channels 8 c .. 8 c + 7 = 32 j + 8 q ..: chunk (D / 32) q + j
+          float x[8];
+          unpack8(w[c], p.f16, x);
+          st_shared_v4(dst + ((c & 3) * KW + (c >> 2)) * 2048, h2(x[0] * up, x[4] * up), h2(x[1] * up, x[5] * up),
+                       h2(x[2] * up, x[6] * up), h2(x[3] * up, x[7] * up));
+        }
+        fence_proxy_async_smem();
+      }
+    }
+    __syncthreads();
+
+    if (group == 2) {
+      // ---- unpacking: thread = token of the tile
+      const int t_end = visible(p, sg.T, sg.n, min(sg.n - 1, (sg.rb * R + R - 1) / p.G)).y;
+      const int32_t* table = p.page_table + static_cast<size_t>(sg.b) * p.max_pages;
+      const size_t region = static_cast<size_t>(sg.h) * kv4_head_bytes(D, NG, p.P);
+      uint32_t kw[D / 8], vw[D / 8];
+      uint2 num[NG], vnum[NG];
+      auto page_of = [&](int j) -> int32_t {
+        const int tok = (tile0 + j) * kTok + lane_row;
+        return j < n_tiles && tok < t_end ? __ldg(table + (tok >> p.p_shift)) : -2;
+      };
+      auto token_base = [&](int32_t id) -> const uint8_t* {
+        if (static_cast<uint32_t>(id) < static_cast<uint32_t>(p.n_pages))
+          return p.pool + static_cast<size_t>(static_cast<uint32_t>(id)) * p.page_bytes + region;
+        if (id != -2) flags |= kErrBadPage;
+        return nullptr;
+      };
+      auto load_codes = [&](uint32_t (&w)[D / 8], const uint8_t* src) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const uint4 x = src ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+          w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+        }
+      };
+      auto load_nums = [&](const uint8_t* src) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) num[g] = src ? __ldg(reinterpret_cast<const uint2*>(src) + g) : make_uint2(0, 0);
+      };
+      auto scale_of = [](uint32_t w) { return __half2half2(__ushort_as_half(static_cast<unsigned short>(w))); };
+      auto min_of = [](uint32_t w) { return __half2half2(__ushort_as_half(static_cast<unsigned short>(w >> 16))); };
+      int32_t id = page_of(0);
+      {
+        const uint8_t* src = token_base(id);
+        const int tp = (tile0 * kTok + lane_row) & (p.P - 1);
+        load_nums(src ? src + p.P * D + tp * 8 * NG : nullptr);
+        load_codes(kw, src ? src + tp * (D / 2) : nullptr);
+        load_codes(vw, src ? src + p.P * (D / 2) + tp * (D / 2) : nullptr);
+      }
+      id = page_of(1);
+      for (int j = 0; j < n_tiles; ++j) {
+        const uint32_t J = tiles_done + j, st = J & 1, ph = (J >> 1) & 1;
+        const uint8_t* next = token_base(id);
+        const int tp = ((tile0 + j + 1) * kTok + lane_row) & (p.P - 1);
+        id = page_of(j + 2);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) vnum[g] = num[g];
+        if (!wait(k_free + st, ph ^ 1)) break;
+        const uint32_t kd = base + Ge::kK + st * Ge::kTile + 16 * lane_row;
+#pragma unroll
+        for (int wi = 0; wi < D / 8; ++wi) {
+          const uint32_t nm = vnum[(wi % KW) / (KW / NG)].x;
+          const __half2 s = scale_of(nm), mn = min_of(nm);
+          const uint32_t w = kw[wi], w8 = w >> 8;
+          st_shared_v4(kd + wi * 2048, dequant2<false>(w, s, mn), dequant2<true>(w, s, mn), dequant2<false>(w8, s, mn),
+                       dequant2<true>(w8, s, mn));
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(k_full + st);
+        load_nums(next ? next + p.P * D + tp * 8 * NG : nullptr);
+        load_codes(kw, next ? next + tp * (D / 2) : nullptr);
+        if (!wait(v_free + st, ph ^ 1)) break;
+        const uint32_t vd = base + Ge::kV + st * Ge::kTile + 16 * lane_row;
+#pragma unroll
+        for (int wi = 0; wi < D / 8; ++wi) {  // pair i: channels 64 (wi % VW) + 16 i + {0, 8} + wi / VW
+          uint32_t y[4];
+          const uint32_t w = vw[wi], w8 = w >> 8;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t nm = vnum[(64 * (wi % VW) + 16 * i) / (D / NG)].y;
+            const __half2 s = scale_of(nm), mn = min_of(nm);
+            const uint32_t src = i < 2 ? w : w8;
+            y[i] = (i & 1) ? dequant2<true>(src, s, mn) : dequant2<false>(src, s, mn);
+          }
+          st_shared_v4(vd + wi * 2048, y[0], y[1], y[2], y[3]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(v_full + st);
+        load_codes(vw, next ? next + p.P * (D / 2) + tp * (D / 2) : nullptr);
+      }
+    } else if (group == 3) {
+      // ---- products
+      if (lane == 0) {
+        constexpr uint32_t kDescS = tc5::instr_desc(kTok, false), kDescO = tc5::instr_desc(D, true);
+        auto tile_of = [&](int s) { return two ? s >> 1 : s; };
+        auto scores = [&](int s) -> bool {
+          const int u = s & 1, j = tile_of(s);
+          const uint32_t J = tiles_done + j, st = J & 1;
+          if ((!two || u == 0) && !wait(k_full + st, (J >> 1) & 1)) return false;
+          tc5::fence_after();
+          const uint32_t qa = base + Ge::kQ + (two ? u * Ge::kTile : 0), ka = base + Ge::kK + st * Ge::kTile;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            tc5::mma_ss(tmem + Ge::kColS + 128 * u, tc5::smem_desc(qa + 4096 * k, 2048, 128),
+                        tc5::smem_desc(ka + 4096 * k, 2048, 128), kDescS, k > 0);
+          tc5::commit(s_full + u);
+          if (!two || u == 1) tc5::commit(k_free + st);
+          return true;
+        };
+        bool ok = scores(0) && (steps < 2 || scores(1));
+        for (int s = 0; ok && s < steps; ++s) {
+          const int u = s & 1, j = tile_of(s);
+          const uint32_t J = tiles_done + j, st = J & 1;
+          ok = wait(p_ready + u, (steps_done[u] + (s >> 1)) & 1) && ((two && u == 1) || wait(v_full + st, (J >> 1) & 1));
+          if (!ok) break;
+          tc5::fence_after();
+          const uint32_t va = base + Ge::kV + st * Ge::kTile;
+#pragma unroll
+          for (int k = 0; k < kTok / 16; ++k)
+            tc5::mma_ts(tmem + Ge::kColO + D * u, tmem + Ge::kColS + 128 * u + 8 * k, tc5::smem_desc(va + 256 * k, 128, 2048),
+                        kDescO, s >= 2 || k > 0);
+          if (!two || u == 1) tc5::commit(v_free + st);
+          if (s + 2 < steps) ok = scores(s + 2);
+        }
+        tc5::commit(o_done);  // the products in flight end before anyone goes on, whatever happened
+        if (!mbar_wait_bounded(o_done, segs & 1, ok ? kBudget : kBudget >> 4)) {
+          s_abort = 1;
+          flags |= kErrTimeout;
+        }
+      }
+      __syncwarp();
+    } else {
+      // ---- softmax: thread = row
+      const uint32_t sc = tmem + lane_base + Ge::kColS + 128 * group, oc = tmem + lane_base + Ge::kColO + D * group;
+      int full_lo, full_hi;  // tiles that every live row of the block sees whole
+      {
+        const int i0 = sg.rb * R / p.G, i1 = min(sg.n - 1, (sg.rb * R + R - 1) / p.G);
+        full_lo = (visible(p, sg.T, sg.n, i1).x + kTok - 1) / kTok;
+        full_hi = visible(p, sg.T, sg.n, i0).y / kTok;
+      }
+      const int mine = (steps - group + 1) >> 1;
+      for (int k = 0; k < mine; ++k) {
+        const int t = tile0 + (two ? k : 2 * k + group);
+        const bool edge = t < full_lo || t >= full_hi;
+        const int lo = vis.x - t * kTok, hi = vis.y - t * kTok;  // columns that this row sees: [lo, hi)
+        if (!wait(s_full + group, (steps_done[group] + k) & 1)) break;
+        tc5::fence_after();
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tc5::ld32(sc + 32 * c, v);
+          tc5::wait_ld(v);
+          if (edge) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i >= lo && 32 * c + i < hi) mx = fmaxf(mx, __uint_as_float(v[i]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+          }
+        }
+        mx *= fr;
+        if (__any_sync(0xffffffffu, mx > m + kSlack)) {
+          const float mn = fmaxf(m, mx), a = ex2(m - mn);
+          m = mn;
+          l *= a;
+          if (k > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t v[32];
+              tc5::ld32(oc + 32 * c, v);
+              tc5::wait_ld(v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a);
+              tc5::st32(oc + 32 * c, v);
+            }
+            tc5::wait_st();
+          }
+        }
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32], w[16];
+          tc5::ld32(sc + 32 * c, v);
+          tc5::wait_ld(v);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float a = ex2(__fmaf_rn(__uint_as_float(v[i]), fr, -m)), b = ex2(__fmaf_rn(__uint_as_float(v[i + 1]), fr, -m));
+            if (edge) {
+              if (32 * c + i < lo || 32 * c + i >= hi) a = 0.f;
+              if (32 * c + i + 1 < lo || 32 * c + i + 1 >= hi) b = 0.f;
+            }
+            l0 += a;
+            l1 += b;
+            w[i >> 1] = h2(a, b);
+          }
+          tc5::st16(sc + 16 * c, w);
+        }
+        l += l0 + l1;
+        tc5::wait_st();
+        tc5::fence_before();
+        mbar_arrive(p_ready + group);
+      }
+    }
+    __syncthreads();
+    tc5::fence_after();
+    if (s_abort) break;
+    tiles_done += n_tiles;
+    steps_done[0] += (steps + 1) >> 1;
+    steps_done[1] += steps >> 1;
+    ++segs;
+
+    // ---- results: thread = row; with one tile of queries the second group hands its sums over
+    // (tile region of the keys and values, column by column: distinct banks)
+    float* const xo = reinterpret_cast<float*>(smem + Ge::kK);
+    if (!two) {
+      if (group == 1) {
+        s_ml[1][lane_row][0] = m;
+        s_ml[1][lane_row][1] = l;
+        if (steps > 1) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            tc5::ld32(tmem + lane_base + Ge::kColO + D + 32 * c, v);
+            tc5::wait_ld(v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) xo[(32 * c + i) * 128 + lane_row] = __uint_as_float(v[i]);
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (group == 0 || (two && group == 1)) {
+      const int row = (two ? 128 * group : 0) + lane_row;
+      const bool live = row < rows_left;
+      const uint32_t oc = tmem + lane_base + Ge::kColO + D * group;
+      float f0 = 1.f, f1 = 0.f;
+      if (!two && steps > 1) {
+        const float m1 = s_ml[1][lane_row][0], l1 = s_ml[1][lane_row][1], M = fmaxf(m, m1);
+        f0 = ex2(m - M);
+        f1 = ex2(m1 - M);
+        m = M;
+        l = l * f0 + l1 * f1;
+      }
+      const int rr = sg.rb * R + row;
+      const size_t orow = static_cast<size_t>(sg.r0 + rr / p.G) * p.Hq + sg.h * p.G + rr % p.G;
+      const float y = l == 0.f ? 0.f : 1.f / l;
+      uint32_t res[D / 2];
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        tc5::ld32(oc + 32 * c, v);
+        tc5::wait_ld(v);
+        float x[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]) * f0;
+        if (!two && steps > 1) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] += f1 * xo[(32 * c + i) * 128 + lane_row];
+        }
+        if (sg.part >= 0) {
+          if (live) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + (static_cast<size_t>(sg.part) * R + row) * D + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          }
+        } else {
+          // column 8 wi + 2 i + e is channel 64 (wi % VW) + 16 i + 8 e + wi / VW: neighbouring channels are
+          // columns VW * 8 apart, in the same 32
+#pragma unroll
+          for (int i = 0; i < 8 * VW; ++i) {  // i = 8 w + 2 pair + e
+            constexpr int kPairs = 32 / (16 * VW);  // channel pairs per 32 columns
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k) {
+              const int col = (2 * k) * 8 * VW + i;
+              res[i * (4) + c * kPairs + k] = pack2(x[col] * y, x[col + 8 * VW] * y, p.f16);
+            }
+          }
+        }
+      }
+      if (sg.part >= 0) {
+        if (live)
+          reinterpret_cast<float2*>(p.part_ml)[static_cast<size_t>(sg.part) * R + row] = make_float2(m, l);
+      } else if (live) {
+        uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D);
+#pragma unroll
+        for (int i = 0; i < 8 * VW; ++i)  // channels 64 w + 8 (2 pair + e) .. + 7
+          dst[i] = make_uint4(res[4 * i], res[4 * i + 1], res[4 * i + 2], res[4 * i + 3]);
+        if (p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+      }
+    }
+    if (sg.part >= 0) {
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const bool last = atomicAdd(p.arrive + sg.c0, 1u) == static_cast<uint32_t>(sg.parts - 1);
+        s_last = last;
+        if (last) {
+          p.arrive[sg.c0] = 0;
+          __threadfence();
+        }
+      }
+      __syncthreads();
+      if (s_last) {
+        // this CTA came last: the item's parts in CTA order, a warp per row
+        const int rows = min(R, rows_left);
+        for (int row = warp; row < rows; row += kThreads / 32) {
+          const int rr = sg.rb * R + row;
+          const size_t orow = static_cast<size_t>(sg.r0 + rr / p.G) * p.Hq + sg.h * p.G + rr % p.G;
+          const int slot = 2 * (sg.c0 + lane) + (lane == 0 ? 1 : 0);  // part `lane`
+          const float2 ml = lane < sg.parts ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + static_cast<size_t>(slot) * R + row)
+                                            : make_float2(kNoMax, 0.f);
+          float M = ml.x;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+          const float f = ex2(ml.x - M);
+          float L = f * ml.y;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+          const float y = L == 0.f ? 0.f : 1.f / L;
+          constexpr int kPer = D / 32;  // columns per lane
+          float v[kPer];
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) v[k] = 0.f;
+#pragma unroll 8
+          for (int i = 0; i < sg.parts; ++i) {
+            const float fi = __shfl_sync(0xffffffffu, f, i);
+            const float* src = p.part_o + (static_cast<size_t>(2 * (sg.c0 + i) + (i == 0 ? 1 : 0)) * R + row) * D + lane;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) v[k] += fi * __ldcg(src + 32 * k);
+          }
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            const int col = 32 * k + lane, wi = col >> 3;
+            const int ch = 64 * (wi % VW) + 8 * (col & 7) + wi / VW;
+            p.out[orow * D + ch] = static_cast<uint16_t>(pack2(v[k] * y, 0.f, p.f16));
+          }
+          if (lane == 0 && p.lse) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+        }
+      }
+    }
+    tc5::fence_before();
+    __syncthreads();
+    tc5::fence_after();
+    if (!line) break;
+    if (tid == 0) {  // the next segment of the CTA's stretch
+      Seg& s = s_seg;
+      s.at = min(s.end, s.item0 + s.item_tiles);
+      s.valid = 0;
+      if (s.at < s.end) {
+        s.item0 = s.at;
+        bool found = true;
+        if (++s.rb == row_blocks(p, s.n, R)) {
+          s.rb = 0;
+          if (++s.h == p.Hkv) {
+            s.h = 0;
+            int f = 0;
+            do {
+              if (++s.b >= p.B) {  // lengths that changed under the call
+                found = false;
+                break;
+              }
+              load_sequence(p, s.b, s.T, s.n, s.r0, f);
+            } while (s.n == 0);
+          }
+        }
+        if (found) line_segment(p, s, R);
+      }
+    }
+    __syncthreads();
+    if (!s_seg.valid) break;
+  }
+  tc5::fence_before();
+  __syncthreads();
+  if (warp == 12) tc5::dealloc512(tmem);
+  flags = __reduce_or_sync(0xffffffffu, flags);
+  if (lane == 0 && flags) atomicOr(p.err, flags);
+}
+
+template <int D, int NG>
+cudaError_t launch(const Kv4AttnParams& p, int two, int line, int ctas, cudaStream_t stream) {
+  static bool attr_done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_done[dev]) {
+    e = cudaFuncSetAttribute(kv4_prompt_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geom<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    attr_done[dev] = true;
+  }
+  kv4_prompt_kernel<D, NG><<<ctas, kThreads, Geom<D>::kSmem, stream>>>(p, two, line);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool kv4_uses_prompt(int max_q, int G) { return static_cast<int64_t>(max_q) * G > 16; }
+
+Kv4PromptPlan kv4_prompt_plan(int B, int Hkv, int n_rows, int max_q, int G, int num_sms) {
+  Kv4PromptPlan z;
+  const int64_t rows = static_cast<int64_t>(std::min(max_q, n_rows)) * G;
+  z.two = rows > 128;
+  z.rows = z.two ? 256 : 128;
+  const int64_t items = static_cast<int64_t>(B) * Hkv * ((rows + z.rows - 1) / z.rows);
+  z.line = items < 2 * static_cast<int64_t>(num_sms);
+  z.ctas = z.line ? std::min(num_sms, static_cast<int>(kKv4CounterBytes / 4)) : items;
+  return z;
+}
+
+size_t kv4_prompt_workspace_bytes(const Kv4PromptPlan& z, int D) {
+  return kKv4CounterBytes + (z.line ? 2 * static_cast<size_t>(z.ctas) * z.rows * (static_cast<size_t>(D) + 2) * sizeof(float) : 0);
+}
+
+cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, const Kv4PromptPlan& z, int D, int n_groups, cudaStream_t stream) {
+  const int ctas = static_cast<int>(z.ctas);
+  if (D == 128) {
+    if (n_groups == 1) return launch<128, 1>(p, z.two, z.line, ctas, stream);
+    if (n_groups == 2) return launch<128, 2>(p, z.two, z.line, ctas, stream);
+    return launch<128, 4>(p, z.two, z.line, ctas, stream);
+  }
+  return n_groups == 1 ? launch<64, 1>(p, z.two, z.line, ctas, stream) : launch<64, 2>(p, z.two, z.line, ctas, stream);
+}
+
+}  // namespace mlaq
