@@ -2,14 +2,17 @@
 // prompt, several drafted tokens of many heads), on the fifth-generation tensor cores. Rows = (query
 // token, head of the group), 128 to a tile of queries.
 //
-// One CTA per SM, 13 warps. Per tile of 128 cached tokens:
+// One CTA per SM, 16 warps. Per tile of 128 cached tokens:
 //   warps 8-11   one token per thread: the token's codes become FP16 values min + code * scale (one
 //                rounding) in shared memory, keys and values, two stages each;
 //   warp 12      one thread issues S = Q K^T (128 rows x 128 tokens, both operands in shared memory)
 //                and O += P V (P from tensor memory);
-//   warps 0-3, 4-7  two softmax groups, one row per thread: S is read from tensor memory (its
+//   warp 13      asks for the codes of later tiles, so that they are in L2 when warps 8-11 read them;
+//   warps 0-3, 4-7  two softmax groups, one row per thread: S is read from tensor memory once (its
 //                maximum, then the weights), P replaces it there as FP16. The running max is raised,
 //                and O rescaled in place, only when a score exceeds it by more than 2^8.
+// The softmax groups take the registers that the others give up (setmaxnreg), so every role has its own
+// loop over the CTA's work.
 // The groups alternate so that the tensor cores work for one while the other takes its softmax:
 // with more than 128 rows they hold two tiles of queries and see every token tile, with at most 128
 // they hold the same queries, take the even and the odd token tiles and join at the end.
@@ -18,6 +21,10 @@
 //
 // Channels keep the order in which a code word unpacks: eight channels of a word in the order 0 4 1 5
 // 2 6 3 7, for keys matched by the queries, for values undone when a row is stored.
+//
+// kExact (when the log-sum-exp is asked for): keys as a high and a low FP16 part (together 2^-22 of the
+// value), two products per score and one stage, since the rounding of one part, 2^-12 of a key, shows
+// in a log-sum-exp as ~1e-4.
 //
 // Work: with many items (sequence, kv head, row block) one CTA per item, those that see the most
 // tokens first; with few, the items' token tiles are laid on one line and cut evenly over the SMs
@@ -35,7 +42,9 @@
 namespace mlaq {
 namespace {
 
-constexpr int kThreads = 416;
+constexpr int kThreads = 512;
+constexpr int kRegsSoftmax = 184, kRegsUnpack = 96, kRegsIssue = 48;  // x 256, 128, 128 threads: all 64 K
+constexpr int kAhead = 3;         // tiles that warp 13 runs ahead
 constexpr int kTok = 128;         // tokens per tile
 constexpr int kMaxParts = 32;     // CTAs that one item is cut into, at most
 constexpr float kSlack = 8.f;     // the running max is raised when a score exceeds it by more than this
@@ -63,6 +72,26 @@ __device__ __forceinline__ uint32_t h2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// (a, b) * (f, f) + (c, c) in one instruction
+__device__ __forceinline__ void fma_pair(float& a, float& b, float f, float c) {
+  asm("{ .reg .b64 x, f, c; mov.b64 x, {%0, %1}; mov.b64 f, {%2, %2}; mov.b64 c, {%3, %3}; fma.rn.f32x2 x, x, f, c;"
+      " mov.b64 {%0, %1}, x; }"
+      : "+f"(a), "+f"(b)
+      : "f"(f), "f"(c));
+}
+__device__ __forceinline__ void add_pair(float& a, float& b, float x, float y) {
+  asm("{ .reg .b64 u, v; mov.b64 u, {%0, %1}; mov.b64 v, {%2, %3}; add.rn.f32x2 u, u, v; mov.b64 {%0, %1}, u; }"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y));
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+__device__ __forceinline__ void softmax_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
 // The two codes at bits 0-3 (kHigh: 4-7) of the halves of w as min + code * scale: 1024 + n (1024 + 16 n)
 // is put together by bits, n comes out exactly, then one rounding.
 template <bool kHigh>
@@ -73,6 +102,15 @@ __device__ __forceinline__ uint32_t dequant2(uint32_t w, __half2 s, __half2 m) {
                           : __hadd2(x, __float2half2_rn(-1024.f));
   const __half2 v = __hfma2(n, s, m);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The same pair as a high part and the rest (both FP16).
+template <bool kHigh>
+__device__ __forceinline__ uint32_t dequant2_low(uint32_t w, uint32_t high, float s, float m) {
+  const uint32_t sh = kHigh ? w >> 4 : w;
+  const float n0 = static_cast<float>(sh & 15u), n1 = static_cast<float>((sh >> 16) & 15u);
+  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&high));
+  return h2(__fmaf_rn(n0, s, m) - h.x, __fmaf_rn(n1, s, m) - h.y);
 }
 
 // The part of an item that the CTA works on.
@@ -114,8 +152,7 @@ __device__ __forceinline__ int2 visible(const Kv4AttnParams& p, int T, int n, in
 
 // First token tile of row block rb and the number of tiles (at least one, to store rows that see nothing).
 __device__ __forceinline__ int2 block_tiles(const Kv4AttnParams& p, int T, int n, int rb, int R) {
-  const int i0 = static_cast<int>(static_cast<int64_t>(rb) * R / p.G);
-  const int i1 = min(n - 1, static_cast<int>((static_cast<int64_t>(rb) * R + R - 1) / p.G));
+  const int i0 = rb * R / p.G, i1 = min(n - 1, (rb * R + R - 1) / p.G);  // rows * G < 2^31
   const int t0 = visible(p, T, n, i0).x / kTok, t1 = (visible(p, T, n, i1).y + kTok - 1) / kTok;
   return make_int2(t0, max(1, t1 - t0));
 }
@@ -135,7 +172,7 @@ __device__ __forceinline__ void line_segment(const Kv4AttnParams& p, Seg& s, int
   s.valid = 1;
 }
 
-template <int D, int NG>
+template <int D, int NG, bool kExact>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnParams p, const int two, const int line) {
   using Ge = Geom<D>;
   constexpr int KW = D / 32, VW = D / 64, CB = D / 8;
@@ -146,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   __shared__ long long s_sum[kThreads + 1];
   __shared__ int s_most[kThreads / 32], s_last;
   __shared__ volatile int s_abort;
-  __shared__ float s_ml[2][128][2];
+  __shared__ float s_ml[128][2];
   uint64_t *const k_full = bars, *const k_free = bars + 2, *const v_full = bars + 4, *const v_free = bars + 6,
            *const s_full = bars + 8, *const p_ready = bars + 10, *const o_done = bars + 12;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -250,9 +287,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < 2; ++i) {
-      mbar_init(k_full + i, 128);
-      mbar_init(v_full + i, 128);
-      mbar_init(p_ready + i, 128);
+      mbar_init(k_full + i, 4);  // one arrival per warp
+      mbar_init(v_full + i, 4);
+      mbar_init(p_ready + i, 4);
       mbar_init(k_free + i, 1);
       mbar_init(v_free + i, 1);
       mbar_init(s_full + i, 1);
@@ -286,68 +323,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     }
     return true;
   };
-
-  uint32_t tiles_done = 0;                  // token tiles of earlier segments (stages and their phases go on)
-  uint32_t steps_done[2] = {0, 0};          // steps of each group in earlier segments
-  uint32_t segs = 0;
-  const int group = warp >> 2;              // 0, 1: softmax groups; 2: unpacking; 3: products
-  const int lane_row = tid & 127;
-  const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-
-  while (true) {
-    const Seg& sg = s_seg;
-    const int n_tiles = sg.tiles, tile0 = sg.tile;
-    const int steps = two ? 2 * n_tiles : n_tiles;  // step s: group s & 1, token tile two ? s / 2 : s
-    const int rows_left = sg.n * p.G - sg.rb * R;   // live rows of the block
-
-    float m = kNoMax, l = 0.f, fr = 0.f;
-    int2 vis = make_int2(0, 0);
-    if (group < 2) {
-      // ---- queries: this thread's row, prescaled by a power of two, in the keys' channel order
-      const int row = (two ? 128 * group : 0) + lane_row;
-      const bool live = row < rows_left;
-      const int rr = sg.rb * R + row;
-      if (live) vis = visible(p, sg.T, sg.n, rr / p.G);
-      const uint16_t* src = p.q.data + static_cast<int64_t>(sg.r0 + rr / p.G) * p.q.row_stride +
-                            static_cast<int64_t>(sg.h * p.G + rr % p.G) * p.q.head_stride;
-      uint4 w[CB];
-      float mx = 0.f;
-#pragma unroll
-      for (int c = 0; c < CB; ++c) w[c] = live ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int c = 0; c < CB; ++c) {
-        float x[8];
-        unpack8(w[c], p.f16, x);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(x[k]));
-      }
-      bool range = false;
-      const int E = prescale_exponent(mx, range);
-      const float up = p.scale_log2 < 0.f ? -pow2_int(E) : pow2_int(E);
-      fr = pow2_int(-E) * fabsf(p.scale_log2);
-      if (two || group == 0) {
-        const uint32_t dst = base + Ge::kQ + (two ? group * Ge::kTile : 0) + 16 * lane_row;
-#pragma unroll
-        for (int c = 0; c < CB; ++c) {  // channels 8 c .. 8 c + 7 = 32 j + 8 q ..: chunk (D / 32) q + j
-          float x[8];
-          unpack8(w[c], p.f16, x);
-          st_shared_v4(dst + ((c & 3) * KW + (c >> 2)) * 2048, h2(x[0] * up, x[4] * up), h2(x[1] * up, x[5] * up),
-                       h2(x[2] * up, x[6] * up), h2(x[3] * up, x[7] * up));
-        }
-        fence_proxy_async_smem();
-      }
-    }
+  // Stages and barrier phases go on from segment to segment: token tiles and steps of the earlier ones.
+  uint32_t tiles_done = 0, steps_done[2] = {0, 0}, segs = 0;
+  const int group = warp >> 2;  // 0, 1: softmax; 2: unpacking; 3: products, prefetch
+  const Seg& sg = s_seg;
+  auto steps_of = [&]() { return two ? 2 * sg.tiles : sg.tiles; };  // step s: group s & 1, token tile two ? s / 2 : s
+  // Two barriers of all warps frame a segment: queries in place; results stored and the next segment set.
+  auto leave_segment = [&](int n_tiles, int steps) -> bool {
     __syncthreads();
+    tiles_done += n_tiles;
+    steps_done[0] += (steps + 1) >> 1;
+    steps_done[1] += steps >> 1;
+    ++segs;
+    return !s_abort && sg.valid;
+  };
+  constexpr int kKStages = kExact ? 1 : 2;
 
-    if (group == 2) {
-      // ---- unpacking: thread = token of the tile
+  if (group == 2) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
+    // ---- unpacking: thread = token of the tile
+    const int tok_row = tid & 127;
+    int n_tiles, steps;
+    do {
+      n_tiles = sg.tiles, steps = steps_of();
+      const int tile0 = sg.tile;
       const int t_end = visible(p, sg.T, sg.n, min(sg.n - 1, (sg.rb * R + R - 1) / p.G)).y;
       const int32_t* table = p.page_table + static_cast<size_t>(sg.b) * p.max_pages;
       const size_t region = static_cast<size_t>(sg.h) * kv4_head_bytes(D, NG, p.P);
       uint32_t kw[D / 8], vw[D / 8];
-      uint2 num[NG], vnum[NG];
+      uint2 num[NG], cur[NG];
       auto page_of = [&](int j) -> int32_t {
-        const int tok = (tile0 + j) * kTok + lane_row;
+        const int tok = (tile0 + j) * kTok + tok_row;
         return j < n_tiles && tok < t_end ? __ldg(table + (tok >> p.p_shift)) : -2;
       };
       auto token_base = [&](int32_t id) -> const uint8_t* {
@@ -367,88 +373,133 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
 #pragma unroll
         for (int g = 0; g < NG; ++g) num[g] = src ? __ldg(reinterpret_cast<const uint2*>(src) + g) : make_uint2(0, 0);
       };
-      auto scale_of = [](uint32_t w) { return __half2half2(__ushort_as_half(static_cast<unsigned short>(w))); };
-      auto min_of = [](uint32_t w) { return __half2half2(__ushort_as_half(static_cast<unsigned short>(w >> 16))); };
+      auto scale_of = [](uint32_t w) { return __ushort_as_half(static_cast<unsigned short>(w)); };
+      auto min_of = [](uint32_t w) { return __ushort_as_half(static_cast<unsigned short>(w >> 16)); };
       int32_t id = page_of(0);
       {
         const uint8_t* src = token_base(id);
-        const int tp = (tile0 * kTok + lane_row) & (p.P - 1);
+        const int tp = (tile0 * kTok + tok_row) & (p.P - 1);
         load_nums(src ? src + p.P * D + tp * 8 * NG : nullptr);
         load_codes(kw, src ? src + tp * (D / 2) : nullptr);
         load_codes(vw, src ? src + p.P * (D / 2) + tp * (D / 2) : nullptr);
       }
       id = page_of(1);
+      __syncthreads();
       for (int j = 0; j < n_tiles; ++j) {
         const uint32_t J = tiles_done + j, st = J & 1, ph = (J >> 1) & 1;
+        const uint32_t ks = kExact ? 0 : st, kph = kExact ? J & 1 : ph;
         const uint8_t* next = token_base(id);
-        const int tp = ((tile0 + j + 1) * kTok + lane_row) & (p.P - 1);
+        const int tp = ((tile0 + j + 1) * kTok + tok_row) & (p.P - 1);
         id = page_of(j + 2);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) vnum[g] = num[g];
-        if (!wait(k_free + st, ph ^ 1)) break;
-        const uint32_t kd = base + Ge::kK + st * Ge::kTile + 16 * lane_row;
+        for (int g = 0; g < NG; ++g) cur[g] = num[g];
+        if (!wait(k_free + ks, kph ^ 1)) break;
+        const uint32_t kd = base + Ge::kK + ks * Ge::kTile + 16 * tok_row;
 #pragma unroll
         for (int wi = 0; wi < D / 8; ++wi) {
-          const uint32_t nm = vnum[(wi % KW) / (KW / NG)].x;
-          const __half2 s = scale_of(nm), mn = min_of(nm);
+          const uint32_t nm = cur[(wi % KW) / (KW / NG)].x;
+          const __half2 s = __half2half2(scale_of(nm)), mn = __half2half2(min_of(nm));
           const uint32_t w = kw[wi], w8 = w >> 8;
-          st_shared_v4(kd + wi * 2048, dequant2<false>(w, s, mn), dequant2<true>(w, s, mn), dequant2<false>(w8, s, mn),
-                       dequant2<true>(w8, s, mn));
+          const uint32_t y0 = dequant2<false>(w, s, mn), y1 = dequant2<true>(w, s, mn), y2 = dequant2<false>(w8, s, mn),
+                         y3 = dequant2<true>(w8, s, mn);
+          st_shared_v4(kd + wi * 2048, y0, y1, y2, y3);
+          if constexpr (kExact) {
+            const float sf = __half2float(scale_of(nm)), mf = __half2float(min_of(nm));
+            st_shared_v4(kd + Ge::kTile + wi * 2048, dequant2_low<false>(w, y0, sf, mf), dequant2_low<true>(w, y1, sf, mf),
+                         dequant2_low<false>(w8, y2, sf, mf), dequant2_low<true>(w8, y3, sf, mf));
+          }
         }
         fence_proxy_async_smem();
-        mbar_arrive(k_full + st);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full + ks);
         load_nums(next ? next + p.P * D + tp * 8 * NG : nullptr);
         load_codes(kw, next ? next + tp * (D / 2) : nullptr);
         if (!wait(v_free + st, ph ^ 1)) break;
-        const uint32_t vd = base + Ge::kV + st * Ge::kTile + 16 * lane_row;
+        const uint32_t vd = base + Ge::kV + st * Ge::kTile + 16 * tok_row;
 #pragma unroll
         for (int wi = 0; wi < D / 8; ++wi) {  // pair i: channels 64 (wi % VW) + 16 i + {0, 8} + wi / VW
           uint32_t y[4];
           const uint32_t w = vw[wi], w8 = w >> 8;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t nm = vnum[(64 * (wi % VW) + 16 * i) / (D / NG)].y;
-            const __half2 s = scale_of(nm), mn = min_of(nm);
+            const uint32_t nm = cur[(64 * (wi % VW) + 16 * i) / (D / NG)].y;
+            const __half2 s = __half2half2(scale_of(nm)), mn = __half2half2(min_of(nm));
             const uint32_t src = i < 2 ? w : w8;
             y[i] = (i & 1) ? dequant2<true>(src, s, mn) : dequant2<false>(src, s, mn);
           }
           st_shared_v4(vd + wi * 2048, y[0], y[1], y[2], y[3]);
         }
         fence_proxy_async_smem();
-        mbar_arrive(v_full + st);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_full + st);
         load_codes(vw, next ? next + p.P * (D / 2) + tp * (D / 2) : nullptr);
       }
-    } else if (group == 3) {
-      // ---- products
-      if (lane == 0) {
+    } while (leave_segment(n_tiles, steps));
+  } else if (group == 3) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    int n_tiles, steps;
+    do {
+      n_tiles = sg.tiles, steps = steps_of();
+      if (warp == 13) {
+        // ---- prefetch: the first tiles at once, then one tile for each that is unpacked
+        const int32_t* table = p.page_table + static_cast<size_t>(sg.b) * p.max_pages;
+        const size_t region = static_cast<size_t>(sg.h) * kv4_head_bytes(D, NG, p.P);
+        const int tile0 = sg.tile, t_end = visible(p, sg.T, sg.n, min(sg.n - 1, (sg.rb * R + R - 1) / p.G)).y;
+        auto ask = [&](int j) {
+          if (j >= n_tiles) return;
+          for (int i = lane; i < kTok; i += 32) {
+            const int tok = (tile0 + j) * kTok + i;
+            if (tok >= t_end) break;
+            const int32_t id = __ldg(table + (tok >> p.p_shift));
+            if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(p.n_pages)) continue;
+            const uint8_t* src = p.pool + static_cast<size_t>(static_cast<uint32_t>(id)) * p.page_bytes + region;
+            const int tp = tok & (p.P - 1);
+            prefetch_l2(src + tp * (D / 2));
+            prefetch_l2(src + (p.P + tp) * (D / 2));
+            if ((i & 3) == 0) prefetch_l2(src + p.P * D + tp * 8 * NG);
+          }
+        };
+        for (int j = 1; j < kAhead; ++j) ask(j);
+        __syncthreads();
+        for (int j = 0; j < n_tiles; ++j) {
+          const uint32_t J = tiles_done + j;
+          ask(j + kAhead);
+          if (!wait(v_full + (J & 1), (J >> 1) & 1)) break;
+        }
+      } else {
+        __syncthreads();
+      }
+      if (warp == 12 && lane == 0) {
+        // ---- products
         constexpr uint32_t kDescS = tc5::instr_desc(kTok, false), kDescO = tc5::instr_desc(D, true);
-        auto tile_of = [&](int s) { return two ? s >> 1 : s; };
         auto scores = [&](int s) -> bool {
-          const int u = s & 1, j = tile_of(s);
-          const uint32_t J = tiles_done + j, st = J & 1;
-          if ((!two || u == 0) && !wait(k_full + st, (J >> 1) & 1)) return false;
+          const int u = s & 1, j = two ? s >> 1 : s;
+          const uint32_t J = tiles_done + j, st = kExact ? 0 : J & 1;
+          if ((!two || u == 0) && !wait(k_full + st, kExact ? J & 1 : (J >> 1) & 1)) return false;
           tc5::fence_after();
-          const uint32_t qa = base + Ge::kQ + (two ? u * Ge::kTile : 0), ka = base + Ge::kK + st * Ge::kTile;
+          const uint64_t qa = tc5::smem_desc(base + Ge::kQ + (two ? u * Ge::kTile : 0), 2048, 128);
+          const uint64_t ka = tc5::smem_desc(base + Ge::kK + st * Ge::kTile, 2048, 128);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc5::mma_ss(tmem + Ge::kColS + 128 * u, tc5::smem_desc(qa + 4096 * k, 2048, 128),
-                        tc5::smem_desc(ka + 4096 * k, 2048, 128), kDescS, k > 0);
+          for (int k = 0; k < D / 16; ++k) {  // descriptor addresses count 16 bytes
+            tc5::mma_ss(tmem + Ge::kColS + 128 * u, qa + 256 * k, ka + 256 * k, kDescS, k > 0);
+            if constexpr (kExact)
+              tc5::mma_ss(tmem + Ge::kColS + 128 * u, qa + 256 * k, ka + Ge::kTile / 16 + 256 * k, kDescS, true);
+          }
           tc5::commit(s_full + u);
           if (!two || u == 1) tc5::commit(k_free + st);
           return true;
         };
         bool ok = scores(0) && (steps < 2 || scores(1));
         for (int s = 0; ok && s < steps; ++s) {
-          const int u = s & 1, j = tile_of(s);
+          const int u = s & 1, j = two ? s >> 1 : s;
           const uint32_t J = tiles_done + j, st = J & 1;
           ok = wait(p_ready + u, (steps_done[u] + (s >> 1)) & 1) && ((two && u == 1) || wait(v_full + st, (J >> 1) & 1));
           if (!ok) break;
           tc5::fence_after();
-          const uint32_t va = base + Ge::kV + st * Ge::kTile;
+          const uint64_t va = tc5::smem_desc(base + Ge::kV + st * Ge::kTile, 128, 2048);
 #pragma unroll
           for (int k = 0; k < kTok / 16; ++k)
-            tc5::mma_ts(tmem + Ge::kColO + D * u, tmem + Ge::kColS + 128 * u + 8 * k, tc5::smem_desc(va + 256 * k, 128, 2048),
-                        kDescO, s >= 2 || k > 0);
+            tc5::mma_ts(tmem + Ge::kColO + D * u, tmem + Ge::kColS + 128 * u + 8 * k, va + 16 * k, kDescO, s >= 2 || k > 0);
           if (!two || u == 1) tc5::commit(v_free + st);
           if (s + 2 < steps) ok = scores(s + 2);
         }
@@ -459,70 +510,117 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         }
       }
       __syncwarp();
-    } else {
-      // ---- softmax: thread = row
-      const uint32_t sc = tmem + lane_base + Ge::kColS + 128 * group, oc = tmem + lane_base + Ge::kColO + D * group;
+    } while (leave_segment(n_tiles, steps));
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int lane_row = tid & 127;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t sc = tmem + lane_base + Ge::kColS + 128 * group, oc = tmem + lane_base + Ge::kColO + D * group;
+    int n_tiles, steps;
+    do {
+      n_tiles = sg.tiles, steps = steps_of();
+      const int tile0 = sg.tile;
+      const int rows_left = sg.n * p.G - sg.rb * R;  // live rows of the block
+      const int row = (two ? 128 * group : 0) + lane_row, rr = sg.rb * R + row;
+      const bool live = row < rows_left;
+      float m = kNoMax, l = 0.f, fr;
+      int2 vis = make_int2(0, 0);
+      {
+        // ---- queries: this thread's row, prescaled by a power of two, in the keys' channel order
+        if (live) vis = visible(p, sg.T, sg.n, rr / p.G);
+        const uint16_t* src = p.q.data + static_cast<int64_t>(sg.r0 + rr / p.G) * p.q.row_stride +
+                              static_cast<int64_t>(sg.h * p.G + rr % p.G) * p.q.head_stride;
+        uint4 w[CB];
+        float mx = 0.f;
+#pragma unroll
+        for (int c = 0; c < CB; ++c) w[c] = live ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+          float x[8];
+          unpack8(w[c], p.f16, x);
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) mx = max3(mx, fabsf(x[k]), fabsf(x[k + 1]));
+        }
+        bool range = false;
+        const int E = prescale_exponent(mx, range);
+        const float up = p.scale_log2 < 0.f ? -pow2_int(E) : pow2_int(E);
+        fr = pow2_int(-E) * fabsf(p.scale_log2);
+        if (two || group == 0) {
+          const uint32_t dst = base + Ge::kQ + (two ? group * Ge::kTile : 0) + 16 * lane_row;
+#pragma unroll
+          for (int c = 0; c < CB; ++c) {  // channels 8 c .. 8 c + 7 = 32 j + 8 q ..: chunk (D / 32) q + j
+            float x[8];
+            unpack8(w[c], p.f16, x);
+            st_shared_v4(dst + ((c & 3) * KW + (c >> 2)) * 2048, h2(x[0] * up, x[4] * up), h2(x[1] * up, x[5] * up),
+                         h2(x[2] * up, x[6] * up), h2(x[3] * up, x[7] * up));
+          }
+          fence_proxy_async_smem();
+        }
+      }
       int full_lo, full_hi;  // tiles that every live row of the block sees whole
       {
         const int i0 = sg.rb * R / p.G, i1 = min(sg.n - 1, (sg.rb * R + R - 1) / p.G);
         full_lo = (visible(p, sg.T, sg.n, i1).x + kTok - 1) / kTok;
         full_hi = visible(p, sg.T, sg.n, i0).y / kTok;
       }
+      __syncthreads();
+      // ---- softmax: thread = row
       const int mine = (steps - group + 1) >> 1;
       for (int k = 0; k < mine; ++k) {
         const int t = tile0 + (two ? k : 2 * k + group);
-        const bool edge = t < full_lo || t >= full_hi;
-        const int lo = vis.x - t * kTok, hi = vis.y - t * kTok;  // columns that this row sees: [lo, hi)
         if (!wait(s_full + group, (steps_done[group] + k) & 1)) break;
         tc5::fence_after();
-        float mx = -INFINITY;
+        uint32_t raw[4][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tc5::ld32(sc + 32 * c, v);
-          tc5::wait_ld(v);
-          if (edge) {
+        for (int c = 0; c < 4; ++c) tc5::ld32(sc + 32 * c, raw[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc5::wait_ld(raw[c]);
+        if (t < full_lo || t >= full_hi) {
+          const int lo = vis.x - t * kTok, hi = vis.y - t * kTok;  // columns that this row sees: [lo, hi)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (32 * c + i >= lo && 32 * c + i < hi) mx = fmaxf(mx, __uint_as_float(v[i]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
-          }
+              if (32 * c + i < lo || 32 * c + i >= hi) raw[c][i] = 0xff800000u;  // -inf
         }
-        mx *= fr;
+        float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            mx = max3(mx, __uint_as_float(raw[c][i]), __uint_as_float(raw[c][i + 1]));
+            my = max3(my, __uint_as_float(raw[c][i + 2]), __uint_as_float(raw[c][i + 3]));
+          }
+        mx = fmaxf(mx, my) * fr;
         if (__any_sync(0xffffffffu, mx > m + kSlack)) {
           const float mn = fmaxf(m, mx), a = ex2(m - mn);
           m = mn;
           l *= a;
           if (k > 0) {
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t v[32];
-              tc5::ld32(oc + 32 * c, v);
-              tc5::wait_ld(v);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t v[16];
+              tc5::ld16(oc + 16 * c, v);
+              tc5::wait_ld16(v);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a);
-              tc5::st32(oc + 32 * c, v);
+              for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a);
+              tc5::st16(oc + 16 * c, v);
             }
             tc5::wait_st();
           }
         }
         float l0 = 0.f, l1 = 0.f;
+        const float neg = -m;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t v[32], w[16];
-          tc5::ld32(sc + 32 * c, v);
-          tc5::wait_ld(v);
+          uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            float a = ex2(__fmaf_rn(__uint_as_float(v[i]), fr, -m)), b = ex2(__fmaf_rn(__uint_as_float(v[i + 1]), fr, -m));
-            if (edge) {
-              if (32 * c + i < lo || 32 * c + i >= hi) a = 0.f;
-              if (32 * c + i + 1 < lo || 32 * c + i + 1 >= hi) b = 0.f;
-            }
-            l0 += a;
-            l1 += b;
+            float a = __uint_as_float(raw[c][i]), b = __uint_as_float(raw[c][i + 1]);
+            fma_pair(a, b, fr, neg);
+            a = ex2(a);
+            b = ex2(b);
+            add_pair(l0, l1, a, b);
             w[i >> 1] = h2(a, b);
           }
           tc5::st16(sc + 16 * c, w);
@@ -530,176 +628,167 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         l += l0 + l1;
         tc5::wait_st();
         tc5::fence_before();
-        mbar_arrive(p_ready + group);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready + group);
       }
-    }
-    __syncthreads();
-    tc5::fence_after();
-    if (s_abort) break;
-    tiles_done += n_tiles;
-    steps_done[0] += (steps + 1) >> 1;
-    steps_done[1] += steps >> 1;
-    ++segs;
+      const bool done = wait(o_done, segs & 1) && !s_abort;
+      tc5::fence_after();
 
-    // ---- results: thread = row; with one tile of queries the second group hands its sums over
-    // (tile region of the keys and values, column by column: distinct banks)
-    float* const xo = reinterpret_cast<float*>(smem + Ge::kK);
-    if (!two) {
-      if (group == 1) {
-        s_ml[1][lane_row][0] = m;
-        s_ml[1][lane_row][1] = l;
-        if (steps > 1) {
+      // ---- results: thread = row; with one tile of queries the second group hands its sums over
+      // (tile region of the keys and values, column by column: distinct banks)
+      float* const xo = reinterpret_cast<float*>(smem + Ge::kK);
+      if (!two) {
+        if (group == 1 && done) {
+          s_ml[lane_row][0] = m;
+          s_ml[lane_row][1] = l;
+          if (steps > 1) {
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t v[32];
-            tc5::ld32(tmem + lane_base + Ge::kColO + D + 32 * c, v);
-            tc5::wait_ld(v);
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t v[32];
+              tc5::ld32(oc + 32 * c, v);
+              tc5::wait_ld(v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) xo[(32 * c + i) * 128 + lane_row] = __uint_as_float(v[i]);
-          }
-        }
-      }
-      __syncthreads();
-    }
-    if (group == 0 || (two && group == 1)) {
-      const int row = (two ? 128 * group : 0) + lane_row;
-      const bool live = row < rows_left;
-      const uint32_t oc = tmem + lane_base + Ge::kColO + D * group;
-      float f0 = 1.f, f1 = 0.f;
-      if (!two && steps > 1) {
-        const float m1 = s_ml[1][lane_row][0], l1 = s_ml[1][lane_row][1], M = fmaxf(m, m1);
-        f0 = ex2(m - M);
-        f1 = ex2(m1 - M);
-        m = M;
-        l = l * f0 + l1 * f1;
-      }
-      const int rr = sg.rb * R + row;
-      const size_t orow = static_cast<size_t>(sg.r0 + rr / p.G) * p.Hq + sg.h * p.G + rr % p.G;
-      const float y = l == 0.f ? 0.f : 1.f / l;
-      uint32_t res[D / 2];
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t v[32];
-        tc5::ld32(oc + 32 * c, v);
-        tc5::wait_ld(v);
-        float x[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]) * f0;
-        if (!two && steps > 1) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] += f1 * xo[(32 * c + i) * 128 + lane_row];
-        }
-        if (sg.part >= 0) {
-          if (live) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + (static_cast<size_t>(sg.part) * R + row) * D + 32 * c);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-          }
-        } else {
-          // column 8 wi + 2 i + e is channel 64 (wi % VW) + 16 i + 8 e + wi / VW: neighbouring channels are
-          // columns VW * 8 apart, in the same 32
-#pragma unroll
-          for (int i = 0; i < 8 * VW; ++i) {  // i = 8 w + 2 pair + e
-            constexpr int kPairs = 32 / (16 * VW);  // channel pairs per 32 columns
-#pragma unroll
-            for (int k = 0; k < kPairs; ++k) {
-              const int col = (2 * k) * 8 * VW + i;
-              res[i * (4) + c * kPairs + k] = pack2(x[col] * y, x[col + 8 * VW] * y, p.f16);
+              for (int i = 0; i < 32; ++i) xo[(32 * c + i) * 128 + lane_row] = __uint_as_float(v[i]);
             }
           }
         }
+        softmax_barrier();
+      }
+      if (done && (group == 0 || two)) {
+        float f0 = 1.f, f1 = 0.f;
+        if (!two && steps > 1) {
+          const float m1 = s_ml[lane_row][0], l1 = s_ml[lane_row][1], M = fmaxf(m, m1);
+          f0 = ex2(m - M);
+          f1 = ex2(m1 - M);
+          m = M;
+          l = l * f0 + l1 * f1;
+        }
+        const size_t orow = static_cast<size_t>(sg.r0 + rr / p.G) * p.Hq + sg.h * p.G + rr % p.G;
+        const float y = l == 0.f ? 0.f : 1.f / l;
+        uint32_t res[D / 2];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tc5::ld32(oc + 32 * c, v);
+          tc5::wait_ld(v);
+          float x[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]) * f0;
+          if (!two && steps > 1) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] += f1 * xo[(32 * c + i) * 128 + lane_row];
+          }
+          if (sg.part >= 0) {
+            if (live) {
+              float4* dst = reinterpret_cast<float4*>(p.part_o + (static_cast<size_t>(sg.part) * R + row) * D + 32 * c);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            }
+          } else {
+            // column 8 wi + 2 i + e is channel 64 (wi % VW) + 16 i + 8 e + wi / VW: neighbouring channels are
+            // columns VW * 8 apart, in the same 32
+#pragma unroll
+            for (int i = 0; i < 8 * VW; ++i) {  // i = 8 w + 2 pair + e
+              constexpr int kPairs = 32 / (16 * VW);  // channel pairs per 32 columns
+#pragma unroll
+              for (int k = 0; k < kPairs; ++k) {
+                const int col = (2 * k) * 8 * VW + i;
+                res[i * 4 + c * kPairs + k] = pack2(x[col] * y, x[col + 8 * VW] * y, p.f16);
+              }
+            }
+          }
+        }
+        if (sg.part >= 0) {
+          if (live)
+            reinterpret_cast<float2*>(p.part_ml)[static_cast<size_t>(sg.part) * R + row] = make_float2(m, l);
+        } else if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D);
+#pragma unroll
+          for (int i = 0; i < 8 * VW; ++i)  // channels 64 w + 8 (2 pair + e) .. + 7
+            dst[i] = make_uint4(res[4 * i], res[4 * i + 1], res[4 * i + 2], res[4 * i + 3]);
+          if (p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        }
       }
       if (sg.part >= 0) {
-        if (live)
-          reinterpret_cast<float2*>(p.part_ml)[static_cast<size_t>(sg.part) * R + row] = make_float2(m, l);
-      } else if (live) {
-        uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D);
-#pragma unroll
-        for (int i = 0; i < 8 * VW; ++i)  // channels 64 w + 8 (2 pair + e) .. + 7
-          dst[i] = make_uint4(res[4 * i], res[4 * i + 1], res[4 * i + 2], res[4 * i + 3]);
-        if (p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-      }
-    }
-    if (sg.part >= 0) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const bool last = atomicAdd(p.arrive + sg.c0, 1u) == static_cast<uint32_t>(sg.parts - 1);
-        s_last = last;
-        if (last) {
-          p.arrive[sg.c0] = 0;
-          __threadfence();
+        __threadfence();
+        softmax_barrier();
+        if (tid == 0) {
+          const bool last = !s_abort && atomicAdd(p.arrive + sg.c0, 1u) == static_cast<uint32_t>(sg.parts - 1);
+          s_last = last;
+          if (last) {
+            p.arrive[sg.c0] = 0;
+            __threadfence();
+          }
         }
-      }
-      __syncthreads();
-      if (s_last) {
-        // this CTA came last: the item's parts in CTA order, a warp per row
-        const int rows = min(R, rows_left);
-        for (int row = warp; row < rows; row += kThreads / 32) {
-          const int rr = sg.rb * R + row;
-          const size_t orow = static_cast<size_t>(sg.r0 + rr / p.G) * p.Hq + sg.h * p.G + rr % p.G;
-          const int slot = 2 * (sg.c0 + lane) + (lane == 0 ? 1 : 0);  // part `lane`
-          const float2 ml = lane < sg.parts ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + static_cast<size_t>(slot) * R + row)
-                                            : make_float2(kNoMax, 0.f);
-          float M = ml.x;
+        softmax_barrier();
+        if (s_last) {
+          // this CTA came last: the item's parts in CTA order, a warp per row
+          const int rows = min(R, rows_left);
+          for (int mr = warp; mr < rows; mr += 8) {
+            const int mrr = sg.rb * R + mr;
+            const size_t orow = static_cast<size_t>(sg.r0 + mrr / p.G) * p.Hq + sg.h * p.G + mrr % p.G;
+            const int slot = 2 * (sg.c0 + lane) + (lane == 0 ? 1 : 0);  // part `lane`
+            const float2 ml = lane < sg.parts
+                                  ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + static_cast<size_t>(slot) * R + mr)
+                                  : make_float2(kNoMax, 0.f);
+            float M = ml.x;
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-          const float f = ex2(ml.x - M);
-          float L = f * ml.y;
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            const float f = ex2(ml.x - M);
+            float L = f * ml.y;
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-          const float y = L == 0.f ? 0.f : 1.f / L;
-          constexpr int kPer = D / 32;  // columns per lane
-          float v[kPer];
+            for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+            const float y = L == 0.f ? 0.f : 1.f / L;
+            constexpr int kPer = D / 32;  // columns per lane
+            float v[kPer];
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) v[k] = 0.f;
+            for (int k = 0; k < kPer; ++k) v[k] = 0.f;
 #pragma unroll 8
-          for (int i = 0; i < sg.parts; ++i) {
-            const float fi = __shfl_sync(0xffffffffu, f, i);
-            const float* src = p.part_o + (static_cast<size_t>(2 * (sg.c0 + i) + (i == 0 ? 1 : 0)) * R + row) * D + lane;
+            for (int i = 0; i < sg.parts; ++i) {
+              const float fi = __shfl_sync(0xffffffffu, f, i);
+              const float* src = p.part_o + (static_cast<size_t>(2 * (sg.c0 + i) + (i == 0 ? 1 : 0)) * R + mr) * D + lane;
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) v[k] += fi * __ldcg(src + 32 * k);
-          }
+              for (int k = 0; k < kPer; ++k) v[k] += fi * __ldcg(src + 32 * k);
+            }
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) {
-            const int col = 32 * k + lane, wi = col >> 3;
-            const int ch = 64 * (wi % VW) + 8 * (col & 7) + wi / VW;
-            p.out[orow * D + ch] = static_cast<uint16_t>(pack2(v[k] * y, 0.f, p.f16));
+            for (int k = 0; k < kPer; ++k) {
+              const int col = 32 * k + lane, wi = col >> 3;
+              const int ch = 64 * (wi % VW) + 8 * (col & 7) + wi / VW;
+              p.out[orow * D + ch] = static_cast<uint16_t>(pack2(v[k] * y, 0.f, p.f16));
+            }
+            if (lane == 0 && p.lse) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
           }
-          if (lane == 0 && p.lse) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
         }
       }
-    }
-    tc5::fence_before();
-    __syncthreads();
-    tc5::fence_after();
-    if (!line) break;
-    if (tid == 0) {  // the next segment of the CTA's stretch
-      Seg& s = s_seg;
-      s.at = min(s.end, s.item0 + s.item_tiles);
-      s.valid = 0;
-      if (s.at < s.end) {
-        s.item0 = s.at;
-        bool found = true;
-        if (++s.rb == row_blocks(p, s.n, R)) {
-          s.rb = 0;
-          if (++s.h == p.Hkv) {
-            s.h = 0;
-            int f = 0;
-            do {
-              if (++s.b >= p.B) {  // lengths that changed under the call
-                found = false;
-                break;
+      tc5::fence_before();
+      softmax_barrier();
+      if (tid == 0) {  // the next segment of the CTA's stretch
+        Seg& s = s_seg;
+        s.valid = 0;
+        if (line) {
+          s.at = min(s.end, s.item0 + s.item_tiles);
+          if (s.at < s.end) {
+            s.item0 = s.at;
+            bool found = true;
+            if (++s.rb == row_blocks(p, s.n, R)) {
+              s.rb = 0;
+              if (++s.h == p.Hkv) {
+                s.h = 0;
+                int f = 0;
+                do {
+                  if (++s.b >= p.B) {  // lengths that changed under the call
+                    found = false;
+                    break;
+                  }
+                  load_sequence(p, s.b, s.T, s.n, s.r0, f);
+                } while (s.n == 0);
               }
-              load_sequence(p, s.b, s.T, s.n, s.r0, f);
-            } while (s.n == 0);
+            }
+            if (found) line_segment(p, s, R);
           }
         }
-        if (found) line_segment(p, s, R);
       }
-    }
-    __syncthreads();
-    if (!s_seg.valid) break;
+    } while (leave_segment(n_tiles, steps));
   }
   tc5::fence_before();
   __syncthreads();
@@ -708,20 +797,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   if (lane == 0 && flags) atomicOr(p.err, flags);
 }
 
-template <int D, int NG>
-cudaError_t launch(const Kv4AttnParams& p, int two, int line, int ctas, cudaStream_t stream) {
+template <int D, int NG, bool kExact>
+cudaError_t launch_as(const Kv4AttnParams& p, int two, int line, int ctas, cudaStream_t stream) {
   static bool attr_done[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_done[dev]) {
-    e = cudaFuncSetAttribute(kv4_prompt_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geom<D>::kSmem);
+    e = cudaFuncSetAttribute(kv4_prompt_kernel<D, NG, kExact>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geom<D>::kSmem);
     if (e != cudaSuccess) return e;
     attr_done[dev] = true;
   }
-  kv4_prompt_kernel<D, NG><<<ctas, kThreads, Geom<D>::kSmem, stream>>>(p, two, line);
+  kv4_prompt_kernel<D, NG, kExact><<<ctas, kThreads, Geom<D>::kSmem, stream>>>(p, two, line);
   return cudaGetLastError();
+}
+
+template <int D, int NG>
+cudaError_t launch(const Kv4AttnParams& p, int two, int line, int ctas, cudaStream_t stream) {
+  return p.lse ? launch_as<D, NG, true>(p, two, line, ctas, stream) : launch_as<D, NG, false>(p, two, line, ctas, stream);
 }
 
 }  // namespace
