@@ -16,9 +16,12 @@
 // use and the page id one tile before that; no shared memory and no barrier inside the loop. The warps of a CTA meet
 // once per work item.
 //
-// Work: (sequence, kv head, row block) x its 32-token steps, laid on one line; CTA i takes steps
-// [i S, (i + 1) S). An item cut by CTA borders is joined by the CTA that arrives last (partials in
-// CTA order, so the result does not depend on who that is).
+// Work: items (sequence, kv head, row block), each a row of 32-token steps. Where they can be cut so that
+// every CTA has one part of one item, they are: the share is the smallest of a few multiples of
+// total / CTAs for which the parts fit (a second, short segment costs a CTA ~12 us of latencies: ids,
+// queries, first tokens, meeting, joining). Otherwise the items lie on one line that is cut into equal
+// stretches. An item in several parts is joined by the CTA that arrives last (parts in CTA order, so the
+// result does not depend on who that is).
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -39,8 +42,9 @@ constexpr int kMaxParts = 64;  // CTAs that one item is cut into, at most
 template <int D, int NG, int NT>
 struct Geom {
   static constexpr int kWarps = NT == 1 ? 8 : 6;  // two CTAs per SM: 16 warps of 128 registers, or 12 of 168
+  static constexpr int kPair = NT == 1 ? 2 : 1;  // tiles multiplied side by side
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kMinTiles = kWarps;        // steps per CTA at least
+  static constexpr int kMinSteps = 2 * kWarps;    // an item is not cut below this: joining costs more than it saves
   static constexpr int kR = 8 * NT;
   static constexpr int kCodes = kTok * D / 2;     // bytes of a step's key codes, and of its value codes
   static constexpr int kStage = 2 * kCodes + kTok * 8 * NG;
@@ -147,13 +151,23 @@ __device__ __forceinline__ float max_over_g(float v) {
   return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
 }
 
-// The part of the line that a CTA works on and the item it is in. Kept in shared memory: the loop
-// over tiles needs the registers.
+// The part of an item that a CTA works on. Kept in shared memory: the loop over the tokens needs the
+// registers.
 struct Place {
-  long long at, end, item0, share;  // line position, end of the CTA's stretch, item's first tile, CTA stretch
-  int b, h, rb;                     // the item: sequence, kv head, row block
-  int T, n, r0, tiles, blocks;      // of the sequence: length, query rows, first row, tiles of an item, row blocks
+  int b, h, rb;                 // the item: sequence, kv head, row block
+  int T, n, r0, tiles, blocks;  // of the sequence: length, query rows, first row, steps of an item, row blocks
+  int a0, a1;                   // steps of the item done here
+  int c0, parts;                // first CTA of the item, and how many
+  long long at, end, item0, share;  // on the line: here, end of the CTA's stretch, the item's start, length of a stretch
 };
+
+// The item's steps that lie in the CTA's stretch of the line.
+__device__ __forceinline__ void on_line(Place& s) {
+  s.a0 = static_cast<int>(s.at - s.item0);
+  s.a1 = static_cast<int>(min(s.end - s.item0, static_cast<long long>(s.tiles)));
+  s.c0 = static_cast<int>(s.item0 / s.share);
+  s.parts = static_cast<int>((s.item0 + s.tiles - 1) / s.share) - s.c0 + 1;
+}
 
 // The length, rows and tiles per row block of sequence b.
 template <int R>
@@ -202,12 +216,19 @@ __device__ __forceinline__ void store_out(const Kv4AttnParams& p, const Place& a
 // first the parts' weights, then the outputs, which each thread copies to shared memory (`room`
 // bytes) for as many parts as fit there at once, all in flight and none in registers.
 template <int D, int R, int kThreads>
-__device__ __forceinline__ void merge_parts(const Kv4AttnParams& p, const Place& at, int c0, int parts, uint8_t* smem,
-                                            int room, float (&s_f)[kMaxParts + 1][R], float (&s_ml)[R][2]) {
+__device__ __forceinline__ void merge_parts(const Kv4AttnParams& p, const Place& at, uint8_t* smem, int room,
+                                            float (&s_f)[kMaxParts + 1][R], float (&s_ml)[R][2]) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int c0 = at.c0, parts = at.parts, rows = min(R, at.n * p.G - at.rb * R);
   auto slot_of = [&](int i) { return static_cast<uint32_t>(2 * (c0 + i) + (i == 0 ? 1 : 0)); };
-  constexpr int kPer = (kMaxParts + 31) / 32;
-  for (int row = warp; row < R; row += kThreads / 32) {
+  constexpr int kPer = (kMaxParts + 31) / 32, kPart = R * D * 4;
+  const int batch = room / kPart, n_chunks = rows * (D / 4);  // 16-byte chunks of a part
+  auto ask = [&](int e, int i0, int n) {
+    for (int i = 0; i < n; ++i)
+      cp_async_cg16(smem + i * kPart + e * 16, p.part_o + static_cast<size_t>(slot_of(i0 + i)) * (R * D) + 4 * e);
+  };
+  if (tid < n_chunks) ask(tid, 0, min(batch, parts));  // on their way while the weights are formed
+  for (int row = warp; row < rows; row += kThreads / 32) {
     float M = kNoMax, L = 0.f;
     float2 ml[kPer];
 #pragma unroll
@@ -230,15 +251,12 @@ __device__ __forceinline__ void merge_parts(const Kv4AttnParams& p, const Place&
     if (lane == 0) s_ml[row][0] = M, s_ml[row][1] = L;
   }
   __syncthreads();
-  constexpr int kPart = R * D * 4;
-  for (int e = tid; e < R * D / 4; e += kThreads) {
+  for (int e = tid; e < n_chunks; e += kThreads) {
     const int row = e / (D / 4), c4 = e % (D / 4);
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int batch = room / kPart;
     for (int i0 = 0; i0 < parts; i0 += batch) {
       const int n = min(batch, parts - i0);
-      for (int i = 0; i < n; ++i)
-        cp_async_cg16(smem + i * kPart + e * 16, p.part_o + static_cast<size_t>(slot_of(i0 + i)) * (R * D) + 4 * e);
+      if (e != tid || i0 > 0) ask(e, i0, n);
       cp_async_wait_all();  // a thread reads what it copied itself
 #pragma unroll 4
       for (int i = 0; i < n; ++i) {
@@ -255,101 +273,142 @@ template <int D, int NG, int NT>
 __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kernel(const Kv4AttnParams p) {
   using Ge = Geom<D, NG, NT>;
   constexpr int R = 8 * NT, KW = D / 32, VW = D / 64, MT = D / 16;
+  constexpr int PT = Ge::kPair;
   constexpr int kWarps = Ge::kWarps, kThreads = Ge::kThreads, kRowPad = Ge::kRowPad;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][R], s_l[kWarps][R];
-  __shared__ long long s_sum[kThreads + 1];
   __shared__ float s_f[kMaxParts + 1][R];  // weights of the parts of a cut item; then the rows' (M, L)
   __shared__ float s_ml[R][2];
-  __shared__ int s_last, s_most[kWarps];
+  __shared__ int s_last;
   __shared__ Place s_at;
   __shared__ int s_full[kWarps][3];  // steps that every row sees whole: from, to; tokens seen by any
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
   int flags = 0;
 
-  // ---- this CTA's stretch of the line of tiles: thread i sums sequences [i c, (i + 1) c)
-  const int chunk = (p.B + kThreads - 1) / kThreads;
-  long long mine = 0;
-  int most = 0;
-  for (int b = tid * chunk; b < min(p.B, (tid + 1) * chunk); ++b) {
-    int T, n, r0, tiles, blocks;
-    sequence<R>(p, b, T, n, r0, tiles, blocks, flags);
-    mine += static_cast<long long>(tiles) * blocks * p.Hkv;
-    if (blocks > 0) most = max(most, tiles);
-  }
+  // ---- which part of which item: every warp works it out by itself (no barrier), lane i for
+  // sequences [i c, (i + 1) c)
   {
+    constexpr int kHeld = 8;  // sequences that a lane holds in registers
+    const int chunk = (p.B + 31) / 32, first = lane * chunk, n_ctas = static_cast<int>(gridDim.x);
+    int tb[kHeld], ib[kHeld];  // steps of an item, items
+    long long steps = 0, items = 0;
+    int most = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      tb[i] = 1, ib[i] = 0;
+      if (i < chunk && first + i < p.B) {
+        int T, n, r0, blocks;
+        sequence<R>(p, first + i, T, n, r0, tb[i], blocks, flags);
+        ib[i] = blocks * p.Hkv;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      steps += static_cast<long long>(tb[i]) * ib[i];
+      items += ib[i];
+      if (ib[i] > 0) most = max(most, tb[i]);
+    }
+    for (int b = first + kHeld; b < min(p.B, first + chunk); ++b) {
+      int T, n, r0, tiles, blocks;
+      sequence<R>(p, b, T, n, r0, tiles, blocks, flags);
+      steps += static_cast<long long>(tiles) * blocks * p.Hkv;
+      items += static_cast<long long>(blocks) * p.Hkv;
+      if (blocks > 0) most = max(most, tiles);
+    }
+    if (blockIdx.x == 0 && warp == 0) {
+      const int f = __reduce_or_sync(0xffffffffu, flags);
+      if (lane == 0 && f) atomicOr(p.err, f);
+    }
+    flags = 0;
     most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0) s_most[warp] = most;
-    long long x = mine;
+    long long before = steps;  // of the lanes up to this one
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+      const long long y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
+      items += __shfl_xor_sync(0xffffffffu, items, o);
     }
-    if (lane == 31) s_sum[warp] = x;
-    __syncthreads();
-    long long base = 0;
-    for (int w = 0; w < warp; ++w) base += s_sum[w];
-    for (int w = 0; w < kWarps; ++w) most = max(most, s_most[w]);
-    __syncthreads();
-    s_sum[tid + 1] = base + x;
-    if (tid == 0) s_sum[0] = 0;
-    __syncthreads();
-  }
-  if (blockIdx.x == 0) {
-    const int f = __reduce_or_sync(0xffffffffu, flags);
-    if (lane == 0 && f) atomicOr(p.err, f);
-  }
-  flags = 0;
-  const long long total = s_sum[kThreads];
-  long long share = (total + gridDim.x - 1) / gridDim.x;
-  share = max(share, static_cast<long long>(max(min(Ge::kMinTiles, most), (most + kMaxParts - 2) / (kMaxParts - 1))));
-  const long long at = share * blockIdx.x;
-  const long long end = min(total, at + share);
-  if (at >= end) return;
-
-  // ---- the first item: the thread whose sequences hold tile `at`, then the sequence
-  if (tid == 0) {
-    int lo = 0, hi = kThreads - 1;  // s_sum[lo] <= at < s_sum[lo + 1]
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (s_sum[mid + 1] > at) hi = mid;
-      else lo = mid + 1;
+    const long long total = __shfl_sync(0xffffffffu, before, 31);
+    before -= steps;
+    const int least = max(min(Ge::kMinSteps, most), (most + kMaxParts - 2) / (kMaxParts - 1));
+    const long long base = total < 0x7fffffff ? (static_cast<uint32_t>(total) + n_ctas - 1) / n_ctas : (total + n_ctas - 1) / n_ctas;
+    int share = 0, mine = 0;  // parts of the lane's items
+    if (items <= n_ctas && chunk <= kHeld) {
+      constexpr int kTry = 8;
+      constexpr int kSixteenths[kTry] = {16, 17, 18, 20, 22, 25, 28, 32};
+      for (int k = 0; k < kTry && share == 0; ++k) {
+        const int s = max(least, static_cast<int>((base * kSixteenths[k] + 15) / 16));
+        mine = 0;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+          if (i < chunk) mine += ib[i] * ((tb[i] + s - 1) / s);
+        if (__reduce_add_sync(0xffffffffu, mine) <= n_ctas) share = s;
+      }
     }
-    Place& s = s_at;
-    s.at = at;
-    s.end = end;
-    s.share = share;
-    long long pos = s_sum[lo];
-    int ignore = 0;
-    for (s.b = lo * chunk; s.b < p.B; ++s.b) {
-      sequence<R>(p, s.b, s.T, s.n, s.r0, s.tiles, s.blocks, ignore);
-      const long long w = static_cast<long long>(s.tiles) * s.blocks * p.Hkv;
-      if (at < pos + w) break;
-      pos += w;
-    }
-    if (s.b < p.B) {
-      const long long k = (at - pos) / s.tiles;
-      s.h = static_cast<int>(k / s.blocks);
-      s.rb = static_cast<int>(k % s.blocks);
-      s.item0 = pos + k * s.tiles;
+    if (share > 0) {
+      int upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const int x = static_cast<int>(blockIdx.x);
+      if (x >= __shfl_sync(0xffffffffu, upto, 31)) return;
+      if (x >= upto - mine && x < upto) {  // one lane; every warp stores the same
+        Place s{};
+        int r = x - (upto - mine), ignore = 0;
+        for (s.b = first;; ++s.b) {
+          sequence<R>(p, s.b, s.T, s.n, s.r0, s.tiles, s.blocks, ignore);
+          s.parts = (s.tiles + share - 1) / share;
+          const int w = s.blocks * p.Hkv * s.parts;
+          if (r < w || s.b + 1 >= p.B) break;
+          r -= w;
+        }
+        const int item = s.blocks > 0 ? r / s.parts % (s.blocks * p.Hkv) : 0, part = r % s.parts;
+        s.h = s.blocks > 0 ? item / s.blocks : 0;
+        s.rb = s.blocks > 0 ? item % s.blocks : 0;
+        s.a0 = static_cast<int>(static_cast<long long>(s.tiles) * part / s.parts);
+        s.a1 = static_cast<int>(static_cast<long long>(s.tiles) * (part + 1) / s.parts);
+        s.c0 = x - part;  // at = end: not on the line
+        s_at = s;
+      }
     } else {
-      s.at = s.end;  // lengths that changed under the call
+      const long long stretch = max(base, static_cast<long long>(least));
+      const long long x = stretch * blockIdx.x;
+      if (x >= total) return;
+      if (x >= before && x < before + steps) {  // one lane; every warp stores the same
+        Place s{};
+        s.at = x;
+        s.end = min(total, x + stretch);
+        s.share = stretch;
+        long long pos = before;
+        int ignore = 0;
+        for (s.b = first;; ++s.b) {
+          sequence<R>(p, s.b, s.T, s.n, s.r0, s.tiles, s.blocks, ignore);
+          const long long w = static_cast<long long>(s.tiles) * s.blocks * p.Hkv;
+          if (x < pos + w || s.b + 1 >= p.B) break;
+          pos += w;
+        }
+        const long long k = min((x - pos) / s.tiles, static_cast<long long>(max(1, s.blocks * p.Hkv)) - 1);
+        s.h = s.blocks > 0 ? static_cast<int>(k / s.blocks) : 0;
+        s.rb = s.blocks > 0 ? static_cast<int>(k % s.blocks) : 0;
+        s.item0 = pos + k * s.tiles;
+        on_line(s);
+        s_at = s;
+      }
     }
+    __syncwarp();
   }
-  __syncthreads();
 
-  while (s_at.at < s_at.end) {
+  while (true) {
     // ---- the item's tokens
     int tile, tile_end;
     {
       const int i0 = s_at.rb * R / p.G, i1 = min(s_at.n - 1, (s_at.rb * R + R - 1) / p.G);
       const int2 first = visible(p, s_at.T, s_at.n, i0), last = visible(p, s_at.T, s_at.n, i1);
       const int tile0 = first.x / kTok;
-      const int a0 = static_cast<int>(s_at.at - s_at.item0);  // this CTA's tiles of the item
-      const int a1 = static_cast<int>(min(s_at.end - s_at.item0, static_cast<long long>(s_at.tiles)));
-      tile = tile0 + a0 + warp;
-      tile_end = min(tile0 + a1, (last.y + kTok - 1) / kTok);
+      tile = tile0 + s_at.a0 + warp;
+      tile_end = min(tile0 + s_at.a1, (last.y + kTok - 1) / kTok);
       // steps in [full_lo, full_hi) are seen whole by every row of the block
       if (lane == 0) {
         s_full[warp][0] = (last.x + kTok - 1) / kTok;
@@ -396,25 +455,33 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
       }
       cp_async_commit();
     };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue();
-
-    // ---- queries: B fragments of rows g (+ 8), channels 32 j + 8 q4 + (0 .. 7)
+    // ---- queries: B fragments of rows g (+ 8), channels 32 j + 8 q4 + (0 .. 7); read before the first
+    // copies are asked for (those wait for the page ids), used after
     uint32_t bq[NT][KW][4];
     float fr[NT][2], qs[NT][2][NG];
+    uint4 qraw[NT][KW];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int rr = s_at.rb * R + 8 * nt + g;  // row = (query token rr / G, head rr % G)
       const bool live = rr < s_at.n * p.G;
+#pragma unroll
+      for (int j = 0; j < KW; ++j) {
+        qraw[nt][j] = make_uint4(0, 0, 0, 0);
+        if (live)
+          qraw[nt][j] = __ldg(reinterpret_cast<const uint4*>(p.q.data +
+                                                             static_cast<int64_t>(s_at.r0 + rr / p.G) * p.q.row_stride +
+                                                             (s_at.h * p.G + rr % p.G) * p.q.head_stride + 32 * j) + q4);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
       float x[KW][8];
       float mx = 0.f;
 #pragma unroll
       for (int j = 0; j < KW; ++j) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (live)
-          w = __ldg(reinterpret_cast<const uint4*>(p.q.data + static_cast<int64_t>(s_at.r0 + rr / p.G) * p.q.row_stride +
-                                                   (s_at.h * p.G + rr % p.G) * p.q.head_stride + 32 * j) + q4);
-        unpack8(w, p.f16, x[j]);
+        unpack8(qraw[nt][j], p.f16, x[j]);
 #pragma unroll
         for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(x[j][k]));
       }
@@ -475,50 +542,63 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
       const uint8_t* const st = ring + stage * Ge::kStage;
       const uint32_t here = present >> (2 * stage);
       stage = stage + 1 == kStages ? 0 : stage + 1;
-      const bool edge = tile < full[0] || tile >= full[1];
+      if ((here & 3) == 0) continue;  // the same for all lanes
+      const bool edge = (here & 3) != 3 || tile < full[0] || tile >= full[1];
 #pragma unroll 1
-      for (int r = 0; r < 2; ++r) {
-        if (!((here >> r) & 1)) continue;  // the same for all lanes
-        uint2 num[2][NG];
-        read_numbers<NG>(num, st + 2 * Ge::kCodes + r * (kTile * 8 * NG), g);
-        const int tok = tile * kTok + r * kTile;
-        if (edge) {  // numbers of tokens behind the sequence are not read as such
+      for (int r0 = 0; r0 < 2; r0 += PT) {
+        uint2 num[PT][2][NG];
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (tok + 8 * e + g >= s_at.T)
+        for (int r = 0; r < PT; ++r) read_numbers<NG>(num[r], st + 2 * Ge::kCodes + (r0 + r) * (kTile * 8 * NG), g);
+        if (edge) {  // numbers of tokens behind the sequence, or of no page, are not read as such
 #pragma unroll
-              for (int k = 0; k < NG; ++k) num[e][k] = make_uint2(0, 0);
+          for (int r = 0; r < PT; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (tile * kTok + (r0 + r) * kTile + 8 * e + g >= s_at.T || !((here >> (r0 + r)) & 1))
+#pragma unroll
+                for (int k = 0; k < NG; ++k) num[r][e][k] = make_uint2(0, 0);
         }
         // ---- scores
-        uint32_t kw[2][KW];
-        read_keys<D>(kw, st + r * (Ge::kCodes / 2), g, q4);
-        float x[NT][4];
+        uint32_t kw[PT][2][KW];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
+        for (int r = 0; r < PT; ++r) read_keys<D>(kw[r], st + (r0 + r) * (Ge::kCodes / 2), g, q4);
+        float x[PT][NT][4];
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
-          float s[NT][4];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+          float s[PT][NT][4];
 #pragma unroll
           for (int j = k * (KW / NG); j < (k + 1) * (KW / NG); ++j) {
-            const uint32_t u0 = kw[0][j], u1 = kw[1][j], v0 = u0 >> 8, v1 = u1 >> 8;
-            const uint32_t a01[4] = {u0 & 0x000F000Fu, u1 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x00F000F0u};
-            const uint32_t a23[4] = {v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u};
+            uint32_t a01[PT][4], a23[PT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_f16_16816(s[nt], a01, bq[nt][j][0], bq[nt][j][1]);
-              mma_f16_16816(s[nt], a23, bq[nt][j][2], bq[nt][j][3]);
+            for (int r = 0; r < PT; ++r) {
+              const uint32_t u0 = kw[r][0][j], u1 = kw[r][1][j], v0 = u0 >> 8, v1 = u1 >> 8;
+              a01[r][0] = u0 & 0x000F000Fu, a01[r][1] = u1 & 0x000F000Fu, a01[r][2] = u0 & 0x00F000F0u, a01[r][3] = u1 & 0x00F000F0u;
+              a23[r][0] = v0 & 0x000F000Fu, a23[r][1] = v1 & 0x000F000Fu, a23[r][2] = v0 & 0x00F000F0u, a23[r][3] = v1 & 0x00F000F0u;
             }
+#pragma unroll
+            for (int r = 0; r < PT; ++r)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if (j == k * (KW / NG)) mma_f16_16816_z(s[r][nt], a01[r], bq[nt][j][0], bq[nt][j][1]);
+                else mma_f16_16816(s[r][nt], a01[r], bq[nt][j][0], bq[nt][j][1]);
+              }
+#pragma unroll
+            for (int r = 0; r < PT; ++r)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[r][nt], a23[r], bq[nt][j][2], bq[nt][j][3]);
           }
-          const float2 k0 = half2_to_float2(num[0][k].x), k1 = half2_to_float2(num[1][k].x);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int r = 0; r < PT; ++r) {
+            const float2 k0 = half2_to_float2(num[r][0][k].x), k1 = half2_to_float2(num[r][1][k].x);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              x[nt][c] += k0.x * (fr[nt][c] * s[nt][c]) + k0.y * qs[nt][c][k];
-              x[nt][2 + c] += k1.x * (fr[nt][c] * s[nt][2 + c]) + k1.y * qs[nt][c][k];
-            }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const float m0 = k0.y * qs[nt][c][k], m1 = k1.y * qs[nt][c][k];
+                x[r][nt][c] = (k == 0 ? m0 : x[r][nt][c] + m0) + k0.x * (fr[nt][c] * s[r][nt][c]);
+                x[r][nt][2 + c] = (k == 0 ? m1 : x[r][nt][2 + c] + m1) + k1.x * (fr[nt][c] * s[r][nt][2 + c]);
+              }
+          }
         }
         if (edge) {
 #pragma unroll
@@ -528,27 +608,31 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
               const int rr = s_at.rb * R + 8 * nt + 2 * q4 + c;
               const int2 v = rr < s_at.n * p.G ? visible(p, s_at.T, s_at.n, rr / p.G) : make_int2(0, 0);
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int t = tok + 8 * e + g;
-                if (t < v.x || t >= v.y) x[nt][2 * e + c] = -INFINITY;
-              }
+              for (int r = 0; r < PT; ++r)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int t = tile * kTok + (r0 + r) * kTile + 8 * e + g;
+                  if (t < v.x || t >= v.y || !((here >> (r0 + r)) & 1)) x[r][nt][2 * e + c] = -INFINITY;
+                }
             }
         }
         // ---- running max and weight factor, raised rarely
-        float2 v0[NG], v1[NG];
         float vs = 0.f;
-        bool raise = false;
 #pragma unroll
-        for (int k = 0; k < NG; ++k) {
-          v0[k] = half2_to_float2(num[0][k].y);
-          v1[k] = half2_to_float2(num[1][k].y);
-          vs = fmaxf(vs, fmaxf(v0[k].x, v1[k].x));
-        }
-        raise = vs * wf > kWeightRoom;
+        for (int r = 0; r < PT; ++r)
+#pragma unroll
+          for (int k = 0; k < NG; ++k)
+            vs = fmaxf(vs, fmaxf(half2_to_float2(num[r][0][k].y).x, half2_to_float2(num[r][1][k].y).x));
+        float top[NT][2];
+        bool raise = vs * wf > kWeightRoom;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) raise |= fmaxf(x[nt][c], x[nt][2 + c]) > m[nt][c] + kSlack;
+          for (int c = 0; c < 2; ++c) {
+            top[nt][c] = fmaxf(x[0][nt][c], x[0][nt][2 + c]);
+            if constexpr (PT == 2) top[nt][c] = fmaxf(top[nt][c], fmaxf(x[PT - 1][nt][c], x[PT - 1][nt][2 + c]));
+            raise |= top[nt][c] > m[nt][c] + kSlack;
+          }
         if (__any_sync(0xffffffffu, raise)) {
           float wr = 1.f;
           vs = max_over_g(vs);
@@ -563,7 +647,7 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
             float sc[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const float mn = fmaxf(m[nt][c], max_over_g(fmaxf(x[nt][c], x[nt][2 + c])));
+              const float mn = fmaxf(m[nt][c], max_over_g(top[nt][c]));
               sc[c] = ex2(m[nt][c] - mn);
               m[nt][c] = mn;
               l[nt][c] *= sc[c];
@@ -579,45 +663,51 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
           }
         }
         // ---- weights
-        uint32_t bw[NT][NG][2];
+        uint32_t bw[PT][NT][NG][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float w[4];
+        for (int r = 0; r < PT; ++r)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            w[c] = ex2(x[nt][c] - m[nt][c]);
-            w[2 + c] = ex2(x[nt][2 + c] - m[nt][c]);
-            l[nt][c] += w[c] + w[2 + c];
+          for (int nt = 0; nt < NT; ++nt) {
+            float w[4];
 #pragma unroll
-            for (int k = 0; k < NG; ++k) om[nt][c][k] += w[c] * v0[k].y + w[2 + c] * v1[k].y;
+            for (int c = 0; c < 2; ++c) {
+              w[c] = ex2(x[r][nt][c] - m[nt][c]);
+              w[2 + c] = ex2(x[r][nt][2 + c] - m[nt][c]);
+              l[nt][c] += w[c] + w[2 + c];
+            }
+#pragma unroll
+            for (int k = 0; k < NG; ++k) {
+              const float2 v0 = half2_to_float2(num[r][0][k].y), v1 = half2_to_float2(num[r][1][k].y);
+#pragma unroll
+              for (int c = 0; c < 2; ++c) om[nt][c][k] += w[c] * v0.y + w[2 + c] * v1.y;
+              const float s0 = v0.x * wf, s1 = v1.x * wf;
+              bw[r][nt][k][0] = movmatrix_t(float2_to_half2(w[0] * s0, w[1] * s0));
+              bw[r][nt][k][1] = movmatrix_t(float2_to_half2(w[2] * s1, w[3] * s1));
+            }
           }
-#pragma unroll
-          for (int k = 0; k < NG; ++k) {
-            const float s0 = v0[k].x * wf, s1 = v1[k].x * wf;
-            bw[nt][k][0] = movmatrix_t(float2_to_half2(w[0] * s0, w[1] * s0));
-            bw[nt][k][1] = movmatrix_t(float2_to_half2(w[2] * s1, w[3] * s1));
-          }
-        }
         // ---- readout
-        no_loads_across();
-        uint32_t vw[4][VW];
-        read_values<D>(vw, st + Ge::kCodes + r * (Ge::kCodes / 2), g, q4);
 #pragma unroll
-        for (int u = 0; u < VW; ++u) {
-          const uint32_t p0 = prmt(vw[0][u], vw[1][u], 0x5410), p1 = prmt(vw[0][u], vw[1][u], 0x7632);
-          const uint32_t p2 = prmt(vw[2][u], vw[3][u], 0x5410), p3 = prmt(vw[2][u], vw[3][u], 0x7632);
+        for (int r = 0; r < PT; ++r) {
+          no_loads_across();
+          uint32_t vw[4][VW];
+          read_values<D>(vw, st + Ge::kCodes + (r0 + r) * (Ge::kCodes / 2), g, q4);
 #pragma unroll
-          for (int hi = 0; hi < 2; ++hi) {
-            const int sh = 8 * hi;
-            const uint32_t r0w = p0 >> sh, r1w = p1 >> sh, r2w = p2 >> sh, r3w = p3 >> sh;
-            const uint32_t a0w[4] = {r0w & 0x000F000Fu, r1w & 0x000F000Fu, r2w & 0x000F000Fu, r3w & 0x000F000Fu};
-            const uint32_t a1w[4] = {r0w & 0x00F000F0u, r1w & 0x00F000F0u, r2w & 0x00F000F0u, r3w & 0x00F000F0u};
-            const int j = 4 * u + 2 * hi;
-            constexpr int kPer = MT / NG;  // 16-channel blocks per group
+          for (int u = 0; u < VW; ++u) {
+            const uint32_t p0 = prmt(vw[0][u], vw[1][u], 0x5410), p1 = prmt(vw[0][u], vw[1][u], 0x7632);
+            const uint32_t p2 = prmt(vw[2][u], vw[3][u], 0x5410), p3 = prmt(vw[2][u], vw[3][u], 0x7632);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_f16_16816(o[nt][j], a0w, bw[nt][j / kPer][0], bw[nt][j / kPer][1]);
-              mma_f16_16816(o[nt][j + 1], a1w, bw[nt][(j + 1) / kPer][0], bw[nt][(j + 1) / kPer][1]);
+            for (int hi = 0; hi < 2; ++hi) {
+              const int sh = 8 * hi;
+              const uint32_t w0 = p0 >> sh, w1 = p1 >> sh, w2 = p2 >> sh, w3 = p3 >> sh;
+              const uint32_t a0w[4] = {w0 & 0x000F000Fu, w1 & 0x000F000Fu, w2 & 0x000F000Fu, w3 & 0x000F000Fu};
+              const uint32_t a1w[4] = {w0 & 0x00F000F0u, w1 & 0x00F000F0u, w2 & 0x00F000F0u, w3 & 0x00F000F0u};
+              const int j = 4 * u + 2 * hi;
+              constexpr int kPer = MT / NG;  // 16-channel blocks per group
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma_f16_16816(o[nt][j], a0w, bw[r][nt][j / kPer][0], bw[r][nt][j / kPer][1]);
+                mma_f16_16816(o[nt][j + 1], a1w, bw[r][nt][(j + 1) / kPer][0], bw[r][nt][(j + 1) / kPer][1]);
+              }
             }
           }
         }
@@ -666,11 +756,9 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
       s_ml[tid][0] = M, s_ml[tid][1] = L;
     }
     __syncthreads();
-    const long long item_end = s_at.item0 + s_at.tiles;
-    const bool whole = s_at.at == s_at.item0 && s_at.end >= item_end;
-    const int c0 = static_cast<int>(s_at.item0 / s_at.share);  // first CTA of the item
-    // partial slots: 2 c for the item that CTA c continues, 2 c + 1 for the one that it begins
-    const int slot = 2 * static_cast<int>(blockIdx.x) + (s_at.at == s_at.item0 ? 1 : 0);
+    const bool whole = s_at.parts == 1;
+    // partial slots: 2 c for an item that CTA c goes on with, 2 c + 1 for one that it begins
+    const int slot = 2 * static_cast<int>(blockIdx.x) + (s_at.a0 == 0 ? 1 : 0);
     for (int e = tid; e < R * D / 4; e += kThreads) {
       const int row = e / (D / 4), c4 = e % (D / 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -691,23 +779,21 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
       __threadfence();
       __syncthreads();
       if (tid == 0) {
-        const int parts = static_cast<int>((item_end - 1) / s_at.share) - c0 + 1;  // CTAs of the item
-        const bool last = atomicAdd(p.arrive + c0, 1u) == static_cast<uint32_t>(parts - 1);
-        s_last = last ? parts : 0;
-        if (last) {
-          p.arrive[c0] = 0;
+        s_last = atomicAdd(p.arrive + s_at.c0, 1u) == static_cast<uint32_t>(s_at.parts - 1);
+        if (s_last) {
+          p.arrive[s_at.c0] = 0;
           __threadfence();
         }
       }
       __syncthreads();
-      if (s_last) merge_parts<D, R, kThreads>(p, s_at, c0, s_last, smem, Ge::kSmem, s_f, s_ml);
+      if (s_last) merge_parts<D, R, kThreads>(p, s_at, smem, Ge::kSmem, s_f, s_ml);
     }
     __syncthreads();
 
-    // ---- the next item
+    // ---- the next item on the line
     if (tid == 0) {
       Place& s = s_at;
-      s.at = min(s.end, item_end);
+      if (s.at < s.end) s.at = min(s.end, s.item0 + s.tiles);
       if (s.at < s.end) {
         s.item0 = s.at;
         if (++s.rb == s.blocks) {
@@ -724,9 +810,11 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
             } while (s.blocks == 0);
           }
         }
+        on_line(s);
       }
     }
     __syncthreads();
+    if (s_at.at >= s_at.end) break;
   }
   flags = __reduce_or_sync(0xffffffffu, flags);
   if (lane == 0 && flags) atomicOr(p.err, flags);
