@@ -1,4 +1,5 @@
-"""ctypes binding of the C ABI in include/mla_qcache.h (argument marshalling only).
+"""Binding of the C ABI in include/mla_qcache.h (argument marshalling only): ctypes, and the native
+module _fastcall for the entry points of the grouped-query cache and the BF16 append.
 
 Every step of the hot path runs in the CUDA kernels of libmla_qcache.so; this module only
 checks tensor dtypes/devices and passes raw pointers, sizes and the current CUDA stream.
@@ -433,9 +434,6 @@ def mla_qcache_decode_attn_noalloc(cfg: Config, q_lat, q_rope, page_table, seq_l
 
 
 # ---------------------------------------------------------------- grouped-query cache in 4 bits, BF16 latent append
-_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
-
-
 def kv4_page_bytes(cfg: KV4Config) -> int:
     return int(lib().mla_qcache_kv4_page_bytes(ctypes.byref(cfg)))
 
@@ -444,53 +442,21 @@ def kv4_workspace_bytes(cfg: KV4Config, B: int, n_heads: int, max_q: int, max_pa
     return int(lib().mla_qcache_kv4_workspace_bytes(ctypes.byref(cfg), B, n_heads, max_q, max_pages))
 
 
-def _dev_ptr(t, name, device, dtype, shape):
-    """Pointer of a contiguous tensor of this type, shape (None: any extent) and device."""
-    if t is None:
-        raise QCacheError(f"{name} is required")
-    if t.device != device:
-        raise QCacheError(f"{name} must be on {device}, got {t.device}")
-    if t.dtype != dtype:
-        raise QCacheError(f"{name} must be {dtype}, got {t.dtype}")
-    got = t.shape
-    if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
-        raise ValueError(f"{name} must be {[x if x is not None else 'any' for x in shape]}, got {tuple(got)}")
-    if not t.is_contiguous():
-        raise QCacheError(f"{name} must be contiguous")
-    return t.data_ptr()
+def _native():
+    """The native marshalling module (csrc/fastcall.cpp); like the library, it is built or the calls raise."""
+    global _fast
+    if _fast is None:
+        lib()  # and its own message if nothing is built
+        try:
+            from . import _fastcall
+        except ImportError as e:
+            raise QCacheError(f"the native binding is not built (run __graft_entry__.build()): {e}") from e
+        _fastcall.set_error(QCacheError)
+        _fast = _fastcall
+    return _fast
 
 
-def _call_device(t, name):
-    """Device of a call's tensors: CUDA, and the current one (the launch goes to its stream)."""
-    if t is None or not t.is_cuda:
-        raise QCacheError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise QCacheError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t.device
-
-
-def _head_view(t, name, device, dtype, rows, heads, dim):
-    """View [rows, heads, dim] with contiguous channels; rows and heads may be strided."""
-    if t is None:
-        raise QCacheError(f"{name} is required")
-    if t.device != device or t.dtype != dtype:
-        raise QCacheError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
-    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [{rows}, {heads if heads is not None else 'heads'}, {dim}], got {tuple(t.shape)}")
-    s = t.stride()
-    if s[2] != 1:
-        raise QCacheError(f"{name}: the channels of a head must be contiguous")
-    return _View(t.data_ptr(), s[0] if rows > 1 else 0, s[1] if t.shape[1] > 1 else 0)
-
-
-def _rotation(cos, sin, interleaved, device):
-    if cos is None and sin is None:
-        return None
-    if cos is None or sin is None or cos.dim() != 2:
-        raise ValueError("cos and sin must both be [positions, rot_dim / 2] tables")
-    n, half = cos.shape
-    return ctypes.byref(_Rotation(_dev_ptr(cos, "cos", device, torch.float32, (n, half)),
-                                  _dev_ptr(sin, "sin", device, torch.float32, (n, half)), n, 2 * half, int(interleaved)))
+_fast = None
 
 
 def mla_qcache_kv4_append(cfg: KV4Config, k_new, v_new, cu_new, seq_lens, max_new: int, page_table, pool, err_word,
@@ -499,60 +465,21 @@ def mla_qcache_kv4_append(cfg: KV4Config, k_new, v_new, cu_new, seq_lens, max_ne
     """Append K/V rows to the grouped-query cache in 4 bits, keys and queries rotated on the way (see
     include/mla_qcache.h). k_new, v_new [rows, kv heads, D] and q [rows, heads, D] may be views of one
     projection's output."""
-    dev = _call_device(k_new, "k_new")
-    dtype = k_new.dtype
-    if dtype not in _DTYPES:
-        raise QCacheError(f"k_new must be bfloat16 or float16, got {dtype}")
-    rows, Hkv, D = k_new.shape[0], cfg.n_kv_heads, cfg.head_dim
-    i32 = torch.int32
-    lens = _dev_ptr(seq_lens, "seq_lens", dev, i32, (None,))
-    B = seq_lens.shape[0]
-    if page_table is None or page_table.dim() != 2:
-        raise ValueError("page_table must be [B, max_pages]")
-    heads = q.shape[1] if q is not None and q.dim() == 3 else 0
-    if (q is None) != (q_out is None):
-        raise QCacheError("q and q_out go together")
-    st = lib().mla_qcache_kv4_append(
-        ctypes.byref(cfg), _DTYPES[dtype], B, rows, ctypes.byref(_head_view(k_new, "k_new", dev, dtype, rows, Hkv, D)),
-        ctypes.byref(_head_view(v_new, "v_new", dev, dtype, rows, Hkv, D)), _dev_ptr(cu_new, "cu_new", dev, i32, (B + 1,)),
-        lens, None if seq_lens_next is None else _dev_ptr(seq_lens_next, "seq_lens_next", dev, i32, (B,)), int(max_new),
-        _rotation(cos, sin, interleaved, dev),
-        None if q is None else ctypes.byref(_head_view(q, "q", dev, dtype, rows, None, D)), heads,
-        None if q is None else _dev_ptr(q_out, "q_out", dev, dtype, (rows, heads, D)),
-        None if k_deq is None else _dev_ptr(k_deq, "k_deq", dev, dtype, (rows, Hkv, D)),
-        None if v_deq is None else _dev_ptr(v_deq, "v_deq", dev, dtype, (rows, Hkv, D)),
-        _dev_ptr(page_table, "page_table", dev, i32, (B, None)), page_table.shape[1],
-        _dev_ptr(pool, "pool", dev, torch.uint8, (None, kv4_page_bytes(cfg))), pool.shape[0],
-        _dev_ptr(err_word, "err_word", dev, i32, (1,)), _stream(stream))
-    _raise(st, "mla_qcache_kv4_append")
+    st = (_fast or _native()).kv4_append(cfg, k_new, v_new, cu_new, seq_lens, max_new, page_table, pool, err_word, cos, sin,
+                                         interleaved, q, q_out, k_deq, v_deq, seq_lens_next,
+                                         None if stream is None else stream.cuda_stream)
+    if st:
+        _raise(st, "mla_qcache_kv4_append")
 
 
 def mla_qcache_kv4_attn(cfg: KV4Config, q, page_table, seq_lens, pool, softmax_scale: float, out, workspace, err_word,
                         cu_q=None, max_q: int = 1, lse=None, causal=True, window: int = 0, stream=None) -> None:
     """Attention of query rows q [rows, heads, D] over the cache in 4 bits (see include/mla_qcache.h);
     without cu_q one row per sequence."""
-    dev = _call_device(q, "q")
-    dtype = q.dtype
-    if dtype not in _DTYPES:
-        raise QCacheError(f"q must be bfloat16 or float16, got {dtype}")
-    if q.dim() != 3:
-        raise ValueError(f"q must be [rows, heads, D], got {tuple(q.shape)}")
-    rows, heads, D = q.shape[0], q.shape[1], cfg.head_dim
-    i32 = torch.int32
-    lens = _dev_ptr(seq_lens, "seq_lens", dev, i32, (None,))
-    B = seq_lens.shape[0]
-    if page_table is None or page_table.dim() != 2:
-        raise ValueError("page_table must be [B, max_pages]")
-    st = lib().mla_qcache_kv4_attn(
-        ctypes.byref(cfg), _DTYPES[dtype], B, heads, rows, ctypes.byref(_head_view(q, "q", dev, dtype, rows, heads, D)),
-        None if cu_q is None else _dev_ptr(cu_q, "cu_q", dev, i32, (B + 1,)), int(max_q),
-        _dev_ptr(page_table, "page_table", dev, i32, (B, None)), page_table.shape[1], lens,
-        _dev_ptr(pool, "pool", dev, torch.uint8, (None, kv4_page_bytes(cfg))), pool.shape[0], int(causal), int(window),
-        softmax_scale, _dev_ptr(out, "out", dev, dtype, (rows, heads, D)),
-        None if lse is None else _dev_ptr(lse, "lse", dev, torch.float32, (rows, heads)),
-        _dev_ptr(workspace, "workspace", dev, torch.uint8, (None,)), workspace.shape[0],
-        _dev_ptr(err_word, "err_word", dev, i32, (1,)), _stream(stream))
-    _raise(st, "mla_qcache_kv4_attn")
+    st = (_fast or _native()).kv4_attn(cfg, q, page_table, seq_lens, pool, softmax_scale, out, workspace, err_word, cu_q, max_q,
+                                       lse, causal, window, None if stream is None else stream.cuda_stream)
+    if st:
+        _raise(st, "mla_qcache_kv4_attn")
 
 
 def mla_qcache_append_bf16(kv_new, cu_new, seq_lens, max_new: int, page_table, kv_pool, err_word, norm_weight=None,
@@ -561,28 +488,8 @@ def mla_qcache_append_bf16(kv_new, cu_new, seq_lens, max_new: int, page_table, k
     """Append raw latent rows kv_new [rows, 576] (BF16; rows may be strided) to the paged BF16 cache
     kv_pool [pages, page_size, 576] with RMS norm and rotation on the way (see include/mla_qcache.h).
     kv_pool (and page_table) may be None when only c_out / kr_out, the rows as cached, are wanted."""
-    dev = _call_device(kv_new, "kv_new")
-    bf, i32 = torch.bfloat16, torch.int32
-    if kv_new.dtype != bf or kv_new.dim() != 2 or kv_new.shape[1] != 576 or kv_new.stride(1) != 1:
-        raise ValueError(f"kv_new must be bfloat16 [rows, 576] with contiguous rows, got {kv_new.dtype} {tuple(kv_new.shape)}")
-    rows = kv_new.shape[0]
-    lens = _dev_ptr(seq_lens, "seq_lens", dev, i32, (None,))
-    B = seq_lens.shape[0]
-    P, table, pages, pool, n_pages = 64, None, 1, None, 0
-    if kv_pool is not None:
-        pool = _dev_ptr(kv_pool, "kv_pool", dev, bf, (None, None, 576))
-        n_pages, P = kv_pool.shape[0], kv_pool.shape[1]
-        table = _dev_ptr(page_table, "page_table", dev, i32, (B, None))
-        pages = page_table.shape[1]
-    heads = q_rope.shape[1] if q_rope is not None and q_rope.dim() == 3 else 0
-    if (q_rope is None) != (q_out is None):
-        raise QCacheError("q_rope and q_out go together")
-    opt = lambda t, name, shape: None if t is None else _dev_ptr(t, name, dev, bf, shape)  # noqa: E731
-    st = lib().mla_qcache_append_bf16(
-        B, rows, kv_new.data_ptr(), kv_new.stride(0) if rows > 1 else 0, _dev_ptr(cu_new, "cu_new", dev, i32, (B + 1,)), lens,
-        None if seq_lens_next is None else _dev_ptr(seq_lens_next, "seq_lens_next", dev, i32, (B,)), int(max_new),
-        opt(norm_weight, "norm_weight", (512,)), eps, _rotation(cos, sin, interleaved, dev),
-        None if q_rope is None else ctypes.byref(_head_view(q_rope, "q_rope", dev, bf, rows, None, 64)), heads,
-        opt(q_out, "q_out", (rows, heads, 64)), opt(c_out, "c_out", (rows, 512)), opt(kr_out, "kr_out", (rows, 64)), table,
-        pages, P, pool, n_pages, _dev_ptr(err_word, "err_word", dev, i32, (1,)), _stream(stream))
-    _raise(st, "mla_qcache_append_bf16")
+    st = (_fast or _native()).append_bf16(kv_new, cu_new, seq_lens, max_new, page_table, kv_pool, err_word, norm_weight, eps,
+                                          cos, sin, interleaved, q_rope, q_out, c_out, kr_out, seq_lens_next,
+                                          None if stream is None else stream.cuda_stream)
+    if st:
+        _raise(st, "mla_qcache_append_bf16")
