@@ -7,7 +7,7 @@
 // n 2^-24 (or 16 n 2^-24), so q . n is exact products summed in float32, and a token's scale and
 // minimum enter outside: score = ks (q . n) + km sum(q). The query is prescaled by a power of two
 // to FP16 range. In the readout the weight of a token is w = p vs in FP16 (one rounding, 2^-11),
-// scaled by a power of two that follows the largest vs seen; sum p vm stays in float32.
+// scaled by a power of two that follows the largest vs seen (below 2^-18 of it, by 2^-29 of it); sum p vm stays in float32.
 //
 // A warp owns 16 tokens at a time: S^T[16 tokens x rows] = K q^T with the key codes as the A operand
 // (a lane's fragment is 16 contiguous bytes of the page), softmax on the accumulators, movmatrix
@@ -57,7 +57,8 @@ struct Geom {
 
 constexpr float kSlack = 8.f;      // the running max is raised when a score exceeds it by more than this
 constexpr float kNoMax = -1e30f;  // the running max before the first score
-constexpr float kWeightRoom = 64.f;  // w / p stays at or below this: w <= 2^14 in FP16
+constexpr float kWeightRoom = 64.f;  // w / p stays at or below this: w <= 2^14 in FP16, whose half step below
+                                     // 2^-14 is 2^-25, so a token's weight is off by at most 2^-29 of the largest vs
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -636,9 +637,9 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
         if (__any_sync(0xffffffffu, raise)) {
           float wr = 1.f;
           vs = max_over_g(vs);
-          if (wf == 0.f || vs * wf > kWeightRoom) {  // 2^Ev vs in [1, 2)
+          if (wf == 0.f || vs * wf > kWeightRoom) {  // 2^Ev vs in [16, 32): room upwards, and far down before FP16 ends
             const int e = vs > 0.f ? max(-24, static_cast<int>(__float_as_uint(vs) >> 23) - 127) : -24;
-            const float f = pow2_int(-e);
+            const float f = pow2_int(4 - e);
             wr = wf > 0.f ? f / wf : 1.f;
             wf = f;
           }

@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   __shared__ int s_most[kThreads / 32], s_last;
   __shared__ volatile int s_abort;
   __shared__ float s_ml[128][2];
+  __shared__ __align__(16) uint32_t s_hidden[4][4];  // tokens of a tile (modulo four) whose page id is bad
   uint64_t *const k_full = bars, *const k_free = bars + 2, *const v_full = bars + 4, *const v_free = bars + 6,
            *const s_full = bars + 8, *const p_ready = bars + 10, *const o_done = bars + 12;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -362,6 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         if (id != -2) flags |= kErrBadPage;
         return nullptr;
       };
+      bool bad;  // the token that the registers hold has no page
       auto load_codes = [&](uint32_t (&w)[D / 8], const uint8_t* src) {
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
@@ -378,6 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       int32_t id = page_of(0);
       {
         const uint8_t* src = token_base(id);
+        bad = src == nullptr && id != -2;
         const int tp = (tile0 * kTok + tok_row) & (p.P - 1);
         load_nums(src ? src + p.P * D + tp * 8 * NG : nullptr);
         load_codes(kw, src ? src + tp * (D / 2) : nullptr);
@@ -388,7 +391,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       for (int j = 0; j < n_tiles; ++j) {
         const uint32_t J = tiles_done + j, st = J & 1, ph = (J >> 1) & 1;
         const uint32_t ks = kExact ? 0 : st, kph = kExact ? J & 1 : ph;
+        const uint32_t hidden = __ballot_sync(0xffffffffu, bad);
         const uint8_t* next = token_base(id);
+        bad = next == nullptr && id != -2;
         const int tp = ((tile0 + j + 1) * kTok + tok_row) & (p.P - 1);
         id = page_of(j + 2);
 #pragma unroll
@@ -411,7 +416,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(k_full + ks);
+        if (lane == 0) {  // the tile four back has had its softmax: its values were freed two tiles ago
+          s_hidden[J & 3][warp & 3] = hidden;
+          mbar_arrive(k_full + ks);
+        }
         load_nums(next ? next + p.P * D + tp * 8 * NG : nullptr);
         load_codes(kw, next ? next + tp * (D / 2) : nullptr);
         if (!wait(v_free + st, ph ^ 1)) break;
@@ -544,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         bool range = false;
         const int E = prescale_exponent(mx, range);
         const float up = p.scale_log2 < 0.f ? -pow2_int(E) : pow2_int(E);
-        fr = pow2_int(-E) * fabsf(p.scale_log2);
+        fr = fmaxf(pow2_int(-E) * fabsf(p.scale_log2), 1e-37f);  // a hidden score, -inf, stays one at scale 0
         if (two || group == 0) {
           const uint32_t dst = base + Ge::kQ + (two ? group * Ge::kTile : 0) + 16 * lane_row;
 #pragma unroll
@@ -575,6 +583,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         for (int c = 0; c < 4; ++c) tc5::ld32(sc + 32 * c, raw[c]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc5::wait_ld(raw[c]);
+        const uint4 hid = *reinterpret_cast<const uint4*>(s_hidden[(tiles_done + (two ? k : 2 * k + group)) & 3]);
+        if (hid.x | hid.y | hid.z | hid.w) {
+          const uint32_t bits[4] = {hid.x, hid.y, hid.z, hid.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if ((bits[c] >> i) & 1) raw[c][i] = 0xff800000u;  // -inf
+        }
         if (t < full_lo || t >= full_hi) {
           const int lo = vis.x - t * kTok, hi = vis.y - t * kTok;  // columns that this row sees: [lo, hi)
 #pragma unroll
