@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   __shared__ Seg s_seg;
   __shared__ long long s_sum[kThreads + 1];
   __shared__ int s_most[kThreads / 32], s_last;
-  __shared__ volatile int s_abort;
+  __shared__ volatile int s_abort, s_any_hidden;
   __shared__ float s_ml[128][2];
   __shared__ __align__(16) uint32_t s_hidden[4][4];  // tokens of a tile (modulo four) whose page id is bad
   uint64_t *const k_full = bars, *const k_free = bars + 2, *const v_full = bars + 4, *const v_free = bars + 6,
@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   }
   if (tid == 0) {
     s_abort = 0;
+    s_any_hidden = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + i, 4);  // one arrival per warp
       mbar_init(v_full + i, 4);
@@ -418,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         __syncwarp();
         if (lane == 0) {  // the tile four back has had its softmax: its values were freed two tiles ago
           s_hidden[J & 3][warp & 3] = hidden;
+          if (hidden) s_any_hidden = 1;
           mbar_arrive(k_full + ks);
         }
         load_nums(next ? next + p.P * D + tp * 8 * NG : nullptr);
@@ -477,41 +479,44 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       } else {
         __syncthreads();
       }
-      if (warp == 12 && lane == 0) {
-        // ---- products
+      if (warp == 12) {
+        // ---- products, issued by one lane of the whole warp
         constexpr uint32_t kDescS = tc5::instr_desc(kTok, false), kDescO = tc5::instr_desc(D, true);
+        const uint32_t leader = tc5::elect_one();
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
         auto scores = [&](int s) -> bool {
           const int u = s & 1, j = two ? s >> 1 : s;
           const uint32_t J = tiles_done + j, st = kExact ? 0 : J & 1;
-          if ((!two || u == 0) && !wait(k_full + st, kExact ? J & 1 : (J >> 1) & 1)) return false;
+          if ((!two || u == 0) && !all(wait(k_full + st, kExact ? J & 1 : (J >> 1) & 1))) return false;
           tc5::fence_after();
           const uint64_t qa = tc5::smem_desc(base + Ge::kQ + (two ? u * Ge::kTile : 0), 2048, 128);
           const uint64_t ka = tc5::smem_desc(base + Ge::kK + st * Ge::kTile, 2048, 128);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {  // descriptor addresses count 16 bytes
-            tc5::mma_ss(tmem + Ge::kColS + 128 * u, qa + 256 * k, ka + 256 * k, kDescS, k > 0);
+            tc5::mma_ss(tm + Ge::kColS + 128 * u, qa + 256 * k, ka + 256 * k, kDescS, k > 0, leader);
             if constexpr (kExact)
-              tc5::mma_ss(tmem + Ge::kColS + 128 * u, qa + 256 * k, ka + Ge::kTile / 16 + 256 * k, kDescS, true);
+              tc5::mma_ss(tm + Ge::kColS + 128 * u, qa + 256 * k, ka + Ge::kTile / 16 + 256 * k, kDescS, true, leader);
           }
-          tc5::commit(s_full + u);
-          if (!two || u == 1) tc5::commit(k_free + st);
+          tc5::commit(s_full + u, leader);
+          if (!two || u == 1) tc5::commit(k_free + st, leader);
           return true;
         };
         bool ok = scores(0) && (steps < 2 || scores(1));
         for (int s = 0; ok && s < steps; ++s) {
           const int u = s & 1, j = two ? s >> 1 : s;
           const uint32_t J = tiles_done + j, st = J & 1;
-          ok = wait(p_ready + u, (steps_done[u] + (s >> 1)) & 1) && ((two && u == 1) || wait(v_full + st, (J >> 1) & 1));
+          ok = all(wait(p_ready + u, (steps_done[u] + (s >> 1)) & 1) && ((two && u == 1) || wait(v_full + st, (J >> 1) & 1)));
           if (!ok) break;
           tc5::fence_after();
           const uint64_t va = tc5::smem_desc(base + Ge::kV + st * Ge::kTile, 128, 2048);
 #pragma unroll
           for (int k = 0; k < kTok / 16; ++k)
-            tc5::mma_ts(tmem + Ge::kColO + D * u, tmem + Ge::kColS + 128 * u + 8 * k, va + 16 * k, kDescO, s >= 2 || k > 0);
-          if (!two || u == 1) tc5::commit(v_free + st);
+            tc5::mma_ts(tm + Ge::kColO + D * u, tm + Ge::kColS + 128 * u + 8 * k, va + 16 * k, kDescO, s >= 2 || k > 0, leader);
+          if (!two || u == 1) tc5::commit(v_free + st, leader);
           if (s + 2 < steps) ok = scores(s + 2);
         }
-        tc5::commit(o_done);  // the products in flight end before anyone goes on, whatever happened
+        tc5::commit(o_done, leader);  // the products in flight end before anyone goes on, whatever happened
         if (!mbar_wait_bounded(o_done, segs & 1, ok ? kBudget : kBudget >> 4)) {
           s_abort = 1;
           flags |= kErrTimeout;
@@ -583,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         for (int c = 0; c < 4; ++c) tc5::ld32(sc + 32 * c, raw[c]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc5::wait_ld(raw[c]);
-        const uint4 hid = *reinterpret_cast<const uint4*>(s_hidden[(tiles_done + (two ? k : 2 * k + group)) & 3]);
-        if (hid.x | hid.y | hid.z | hid.w) {
+        if (s_any_hidden) {  // some tile so far
+          const uint4 hid = *reinterpret_cast<const uint4*>(s_hidden[(tiles_done + (two ? k : 2 * k + group)) & 3]);
           const uint32_t bits[4] = {hid.x, hid.y, hid.z, hid.w};
 #pragma unroll
           for (int c = 0; c < 4; ++c)
@@ -739,15 +744,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         }
         softmax_barrier();
         if (s_last) {
-          // this CTA came last: the item's parts in CTA order, a warp per row
-          const int rows = min(R, rows_left);
+          // this CTA came last: the item's parts in CTA order. First each row's weights of the parts
+          // (kept where its queries were), a warp per row; then a thread per row and four columns.
+          const int rows = min(R, rows_left), parts = sg.parts;
+          auto slot_of = [&](int i) { return static_cast<size_t>(2 * (sg.c0 + i) + (i == 0 ? 1 : 0)); };
+          float* const wts = reinterpret_cast<float*>(smem + Ge::kQ);  // [rows][parts], divided by the row's sum
+#pragma unroll 4
           for (int mr = warp; mr < rows; mr += 8) {
-            const int mrr = sg.rb * R + mr;
-            const size_t orow = static_cast<size_t>(sg.r0 + mrr / p.G) * p.Hq + sg.h * p.G + mrr % p.G;
-            const int slot = 2 * (sg.c0 + lane) + (lane == 0 ? 1 : 0);  // part `lane`
-            const float2 ml = lane < sg.parts
-                                  ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + static_cast<size_t>(slot) * R + mr)
-                                  : make_float2(kNoMax, 0.f);
+            const float2 ml = lane < parts ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(lane) * R + mr)
+                                           : make_float2(kNoMax, 0.f);
             float M = ml.x;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -755,25 +760,44 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             float L = f * ml.y;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-            const float y = L == 0.f ? 0.f : 1.f / L;
-            constexpr int kPer = D / 32;  // columns per lane
-            float v[kPer];
+            if (lane < parts) wts[mr * kMaxParts + lane] = L == 0.f ? 0.f : f / L;
+            if (lane == 0 && p.lse) {
+              const int mrr = sg.rb * R + mr;
+              p.lse[static_cast<size_t>(sg.r0 + mrr / p.G) * p.Hq + sg.h * p.G + mrr % p.G] =
+                  L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+            }
+          }
+          softmax_barrier();
+          constexpr int kF = D / 4, kU = 4;  // chunks of a row; chunks of a thread at once
+          for (int e0 = tid; e0 < rows * kF; e0 += 256 * kU) {
+            float4 v[kU];
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) v[k] = 0.f;
-#pragma unroll 8
-            for (int i = 0; i < sg.parts; ++i) {
-              const float fi = __shfl_sync(0xffffffffu, f, i);
-              const float* src = p.part_o + (static_cast<size_t>(2 * (sg.c0 + i) + (i == 0 ? 1 : 0)) * R + mr) * D + lane;
+            for (int u = 0; u < kU; ++u) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int i = 0; i < parts; ++i) {
+              const float4* src = reinterpret_cast<const float4*>(p.part_o + slot_of(i) * R * D);
 #pragma unroll
-              for (int k = 0; k < kPer; ++k) v[k] += fi * __ldcg(src + 32 * k);
+              for (int u = 0; u < kU; ++u) {
+                const int e = e0 + 256 * u;
+                if (e < rows * kF) {
+                  const float f = wts[e / kF * kMaxParts + i];
+                  const float4 x = __ldcg(src + e);
+                  v[u].x += f * x.x, v[u].y += f * x.y, v[u].z += f * x.z, v[u].w += f * x.w;
+                }
+              }
             }
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-              const int col = 32 * k + lane, wi = col >> 3;
-              const int ch = 64 * (wi % VW) + 8 * (col & 7) + wi / VW;
-              p.out[orow * D + ch] = static_cast<uint16_t>(pack2(v[k] * y, 0.f, p.f16));
+            for (int u = 0; u < kU; ++u) {
+              const int e = e0 + 256 * u;
+              if (e < rows * kF) {
+                const int mrr = sg.rb * R + e / kF, col = 4 * (e % kF), wi = col >> 3;
+                uint16_t* dst = p.out + (static_cast<size_t>(sg.r0 + mrr / p.G) * p.Hq + sg.h * p.G + mrr % p.G) * D +
+                                64 * (wi % VW) + 8 * (col & 7) + wi / VW;
+                const uint32_t a = pack2(v[u].x, v[u].y, p.f16), b = pack2(v[u].z, v[u].w, p.f16);
+                dst[0] = static_cast<uint16_t>(a), dst[8] = static_cast<uint16_t>(a >> 16);
+                dst[16] = static_cast<uint16_t>(b), dst[24] = static_cast<uint16_t>(b >> 16);
+              }
             }
-            if (lane == 0 && p.lse) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
           }
         }
       }
