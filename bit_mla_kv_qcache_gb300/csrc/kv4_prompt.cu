@@ -51,12 +51,16 @@ constexpr float kSlack = 8.f;     // the running max is raised when a score exce
 constexpr float kNoMax = -1e30f;  // the running max before the first score
 constexpr long long kBudget = 4ll << 30;  // cycles of a wait before it is given up
 
-template <int D>
+// Shared memory in tiles of 128 x D FP16: queries (one or two tiles), keys, values (two stages). Keys have
+// two stages, in two parts (kExact) two only when one tile of queries leaves the room.
+template <int D, bool kExact>
 struct Geom {
-  static constexpr int kTile = 128 * D * 2;  // bytes of a tile of queries, keys or values
-  static constexpr int kQ = 0, kK = 2 * kTile, kV = 4 * kTile;
-  static constexpr int kSmem = 6 * kTile + 1024;  // slack to align the start
+  static constexpr int kTile = 128 * D * 2;
   static constexpr uint32_t kColS = 0, kColO = 256;
+  __host__ __device__ static constexpr int k_at(bool two) { return (two ? 2 : 1) * kTile; }
+  __host__ __device__ static constexpr int k_stages(bool two) { return kExact && two ? 1 : 2; }
+  __host__ __device__ static constexpr int v_at(bool two) { return k_at(two) + k_stages(two) * (kExact ? 2 : 1) * kTile; }
+  __host__ __device__ static constexpr int smem(bool two) { return v_at(two) + 2 * kTile + 1024; }  // slack to align the start
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -104,13 +108,18 @@ __device__ __forceinline__ uint32_t dequant2(uint32_t w, __half2 s, __half2 m) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// The same pair as a high part and the rest (both FP16).
+// The same pair in float32, as a high part and the rest (both FP16).
 template <bool kHigh>
-__device__ __forceinline__ uint32_t dequant2_low(uint32_t w, uint32_t high, float s, float m) {
-  const uint32_t sh = kHigh ? w >> 4 : w;
-  const float n0 = static_cast<float>(sh & 15u), n1 = static_cast<float>((sh >> 16) & 15u);
+__device__ __forceinline__ void dequant2_parts(uint32_t w, float s, float m, uint32_t& high, uint32_t& low) {
+  const uint32_t b = and_or(w, kHigh ? 0x00F000F0u : 0x000F000Fu, 0x64006400u);
+  const __half2 x = *reinterpret_cast<const __half2*>(&b);
+  const __half2 n = kHigh ? __hfma2(x, __float2half2_rn(0.0625f), __float2half2_rn(-64.f))
+                          : __hadd2(x, __float2half2_rn(-1024.f));
+  float2 v = __half22float2(n);
+  fma_pair(v.x, v.y, s, m);
+  high = h2(v.x, v.y);
   const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&high));
-  return h2(__fmaf_rn(n0, s, m) - h.x, __fmaf_rn(n1, s, m) - h.y);
+  low = h2(v.x - h.x, v.y - h.y);
 }
 
 // The part of an item that the CTA works on.
@@ -120,9 +129,9 @@ struct Seg {
   int tile, tiles;       // first token tile here, and how many
   int part, c0, parts;   // slot of the partial result, or -1 (the item is whole here); CTAs of the item
   int valid;
-  // line mode: position, end of the CTA's stretch, the item's first tile and its tiles, CTA stretch
+  // line mode: position, end of the CTA's stretch, the item's first tile and its tiles, CTA stretch, (b, rb) pair
   long long at, end, item0, share;
-  int item_tiles;
+  int item_tiles, pair;
 };
 
 __device__ __forceinline__ void load_sequence(const Kv4AttnParams& p, int b, int& T, int& n, int& r0, int& flags) {
@@ -174,13 +183,13 @@ __device__ __forceinline__ void line_segment(const Kv4AttnParams& p, Seg& s, int
 
 template <int D, int NG, bool kExact>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnParams p, const int two, const int line) {
-  using Ge = Geom<D>;
+  using Ge = Geom<D, kExact>;
   constexpr int KW = D / 32, VW = D / 64, CB = D / 8;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bars[13];  // k_full[2] k_free[2] v_full[2] v_free[2] s_full[2] p_ready[2] o_done
   __shared__ uint32_t s_tmem;
   __shared__ Seg s_seg;
-  __shared__ long long s_sum[kThreads + 1];
+  __shared__ long long s_part[kThreads / 32];
   __shared__ int s_most[kThreads / 32], s_last;
   __shared__ volatile int s_abort, s_any_hidden;
   __shared__ float s_ml[128][2];
@@ -189,8 +198,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
            *const s_full = bars + 8, *const p_ready = bars + 10, *const o_done = bars + 12;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (base - smem_addr(smem_raw));
+  long long* const s_sum = reinterpret_cast<long long*>(smem);  // tiles before each pair, until the first queries come
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int R = two ? 256 : 128;
+  const uint32_t k_tiles = base + Ge::k_at(two), v_tiles = base + Ge::v_at(two);
   int flags = 0;
 
   // ---- which part of which item
@@ -215,35 +226,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       }
     }
   } else {
-    // thread i sums the tiles of sequences [i c, (i + 1) c)
-    const int chunk = (p.B + kThreads - 1) / kThreads;
+    // the line: pairs (sequence, row block) in order, thread i counts the tiles of pair i; a pair's heads in a row
+    const int blocks_most = line;  // row blocks of the longest sequence
+    const int pairs = p.B * blocks_most;
     long long x = 0;
-    int most = 0;
-    for (int b = tid * chunk; b < min(p.B, (tid + 1) * chunk); ++b) {
+    int t = 0;
+    if (tid < pairs) {
       int T, n, r0, f = 0;
+      const int b = tid / blocks_most, rb = tid - b * blocks_most;
       load_sequence(p, b, T, n, r0, f);
       if (blockIdx.x == 0) flags |= f;
-      const int blocks = row_blocks(p, n, R);
-      for (int rb = 0; rb < blocks; ++rb) {
-        const int t = block_tiles(p, T, n, rb, R).y;
-        x += static_cast<long long>(t) * p.Hkv;
-        most = max(most, t);
-      }
+      if (rb < row_blocks(p, n, R)) t = block_tiles(p, T, n, rb, R).y;
+      x = static_cast<long long>(t) * p.Hkv;
     }
+    const int warp_most = __reduce_max_sync(0xffffffffu, t);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 31) s_sum[warp] = x;
-    if (lane == 0) s_most[warp] = most;
+    if (lane == 31) s_part[warp] = x, s_most[warp] = warp_most;
     __syncthreads();
-    long long before = 0;
-    for (int w = 0; w < warp; ++w) before += s_sum[w];
+    int most = 0;
     for (int w = 0; w < kThreads / 32; ++w) most = max(most, s_most[w]);
-    __syncthreads();
-    s_sum[tid + 1] = before + x;
+    for (int w = 0; w < warp; ++w) x += s_part[w];
+    s_sum[tid + 1] = x;
     if (tid == 0) s_sum[0] = 0;
     __syncthreads();
     if (tid == 0) {
@@ -261,26 +268,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           if (s_sum[mid + 1] > s.at) hi = mid;
           else lo = mid + 1;
         }
-        long long pos = s_sum[lo];
         int f = 0;
-        for (s.b = lo * chunk; s.b < p.B && !s.valid; ++s.b) {
-          load_sequence(p, s.b, s.T, s.n, s.r0, f);
-          const int blocks = row_blocks(p, s.n, R);
-          long long per = 0;  // tiles of one kv head
-          for (int rb = 0; rb < blocks; ++rb) per += block_tiles(p, s.T, s.n, rb, R).y;
-          if (s.at < pos + per * p.Hkv) {
-            s.h = static_cast<int>((s.at - pos) / per);
-            pos += s.h * per;
-            for (s.rb = 0; s.rb < blocks - 1; ++s.rb) {
-              const int t = block_tiles(p, s.T, s.n, s.rb, R).y;
-              if (s.at < pos + t) break;
-              pos += t;
-            }
-            s.item0 = pos;
-            line_segment(p, s, R);
-            break;
-          }
-          pos += per * p.Hkv;
+        s.pair = lo;
+        s.b = lo / blocks_most;
+        s.rb = lo - s.b * blocks_most;
+        load_sequence(p, s.b, s.T, s.n, s.r0, f);
+        if (s.rb < row_blocks(p, s.n, R)) {  // else the lengths changed under the call
+          const int tiles = block_tiles(p, s.T, s.n, s.rb, R).y;
+          s.h = min(static_cast<int>((s.at - s_sum[lo]) / tiles), p.Hkv - 1);
+          s.item0 = s_sum[lo] + static_cast<long long>(s.h) * tiles;
+          line_segment(p, s, R);
         }
       }
     }
@@ -339,7 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     ++segs;
     return !s_abort && sg.valid;
   };
-  constexpr int kKStages = kExact ? 1 : 2;
+  const bool one_k = Ge::k_stages(two) == 1;
+  constexpr int kKeyBytes = Ge::kTile * (kExact ? 2 : 1);  // of a stage
 
   if (group == 2) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
@@ -391,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       __syncthreads();
       for (int j = 0; j < n_tiles; ++j) {
         const uint32_t J = tiles_done + j, st = J & 1, ph = (J >> 1) & 1;
-        const uint32_t ks = kExact ? 0 : st, kph = kExact ? J & 1 : ph;
+        const uint32_t ks = one_k ? 0 : st, kph = one_k ? J & 1 : ph;
         const uint32_t hidden = __ballot_sync(0xffffffffu, bad);
         const uint8_t* next = token_base(id);
         bad = next == nullptr && id != -2;
@@ -400,19 +398,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
 #pragma unroll
         for (int g = 0; g < NG; ++g) cur[g] = num[g];
         if (!wait(k_free + ks, kph ^ 1)) break;
-        const uint32_t kd = base + Ge::kK + ks * Ge::kTile + 16 * tok_row;
+        const uint32_t kd = k_tiles + ks * kKeyBytes + 16 * tok_row;
 #pragma unroll
         for (int wi = 0; wi < D / 8; ++wi) {
           const uint32_t nm = cur[(wi % KW) / (KW / NG)].x;
-          const __half2 s = __half2half2(scale_of(nm)), mn = __half2half2(min_of(nm));
           const uint32_t w = kw[wi], w8 = w >> 8;
-          const uint32_t y0 = dequant2<false>(w, s, mn), y1 = dequant2<true>(w, s, mn), y2 = dequant2<false>(w8, s, mn),
-                         y3 = dequant2<true>(w8, s, mn);
-          st_shared_v4(kd + wi * 2048, y0, y1, y2, y3);
           if constexpr (kExact) {
-            const float sf = __half2float(scale_of(nm)), mf = __half2float(min_of(nm));
-            st_shared_v4(kd + Ge::kTile + wi * 2048, dequant2_low<false>(w, y0, sf, mf), dequant2_low<true>(w, y1, sf, mf),
-                         dequant2_low<false>(w8, y2, sf, mf), dequant2_low<true>(w8, y3, sf, mf));
+            const float s = __half2float(scale_of(nm)), mn = __half2float(min_of(nm));
+            uint32_t y[4], z[4];
+            dequant2_parts<false>(w, s, mn, y[0], z[0]);
+            dequant2_parts<true>(w, s, mn, y[1], z[1]);
+            dequant2_parts<false>(w8, s, mn, y[2], z[2]);
+            dequant2_parts<true>(w8, s, mn, y[3], z[3]);
+            st_shared_v4(kd + wi * 2048, y[0], y[1], y[2], y[3]);
+            st_shared_v4(kd + Ge::kTile + wi * 2048, z[0], z[1], z[2], z[3]);
+          } else {
+            const __half2 s = __half2half2(scale_of(nm)), mn = __half2half2(min_of(nm));
+            st_shared_v4(kd + wi * 2048, dequant2<false>(w, s, mn), dequant2<true>(w, s, mn), dequant2<false>(w8, s, mn),
+                         dequant2<true>(w8, s, mn));
           }
         }
         fence_proxy_async_smem();
@@ -425,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         load_nums(next ? next + p.P * D + tp * 8 * NG : nullptr);
         load_codes(kw, next ? next + tp * (D / 2) : nullptr);
         if (!wait(v_free + st, ph ^ 1)) break;
-        const uint32_t vd = base + Ge::kV + st * Ge::kTile + 16 * tok_row;
+        const uint32_t vd = v_tiles + st * Ge::kTile + 16 * tok_row;
 #pragma unroll
         for (int wi = 0; wi < D / 8; ++wi) {  // pair i: channels 64 (wi % VW) + 16 i + {0, 8} + wi / VW
           uint32_t y[4];
@@ -487,11 +490,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
         auto scores = [&](int s) -> bool {
           const int u = s & 1, j = two ? s >> 1 : s;
-          const uint32_t J = tiles_done + j, st = kExact ? 0 : J & 1;
-          if ((!two || u == 0) && !all(wait(k_full + st, kExact ? J & 1 : (J >> 1) & 1))) return false;
+          const uint32_t J = tiles_done + j, st = one_k ? 0 : J & 1;
+          if ((!two || u == 0) && !all(wait(k_full + st, one_k ? J & 1 : (J >> 1) & 1))) return false;
           tc5::fence_after();
-          const uint64_t qa = tc5::smem_desc(base + Ge::kQ + (two ? u * Ge::kTile : 0), 2048, 128);
-          const uint64_t ka = tc5::smem_desc(base + Ge::kK + st * Ge::kTile, 2048, 128);
+          const uint64_t qa = tc5::smem_desc(base + (two ? u * Ge::kTile : 0), 2048, 128);
+          const uint64_t ka = tc5::smem_desc(k_tiles + st * kKeyBytes, 2048, 128);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {  // descriptor addresses count 16 bytes
             tc5::mma_ss(tm + Ge::kColS + 128 * u, qa + 256 * k, ka + 256 * k, kDescS, k > 0, leader);
@@ -509,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           ok = all(wait(p_ready + u, (steps_done[u] + (s >> 1)) & 1) && ((two && u == 1) || wait(v_full + st, (J >> 1) & 1)));
           if (!ok) break;
           tc5::fence_after();
-          const uint64_t va = tc5::smem_desc(base + Ge::kV + st * Ge::kTile, 128, 2048);
+          const uint64_t va = tc5::smem_desc(v_tiles + st * Ge::kTile, 128, 2048);
 #pragma unroll
           for (int k = 0; k < kTok / 16; ++k)
             tc5::mma_ts(tm + Ge::kColO + D * u, tm + Ge::kColS + 128 * u + 8 * k, va + 16 * k, kDescO, s >= 2 || k > 0, leader);
@@ -539,36 +542,43 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       float m = kNoMax, l = 0.f, fr;
       int2 vis = make_int2(0, 0);
       {
-        // ---- queries: this thread's row, prescaled by a power of two, in the keys' channel order
+        // ---- queries: CB lanes read a row at a time; rows are prescaled by a power of two and stored in the
+        // keys' channel order; this thread keeps its own row's factor
         if (live) vis = visible(p, sg.T, sg.n, rr / p.G);
-        const uint16_t* src = p.q.data + static_cast<int64_t>(sg.r0 + rr / p.G) * p.q.row_stride +
-                              static_cast<int64_t>(sg.h * p.G + rr % p.G) * p.q.head_stride;
+        constexpr int kAtOnce = 32 / CB;  // rows that the warp reads with one load
+        const int c = lane % CB, sub = lane / CB;
         uint4 w[CB];
-        float mx = 0.f;
 #pragma unroll
-        for (int c = 0; c < CB; ++c) w[c] = live ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < CB; ++i) {
+          const int r2 = 32 * warp - (two ? 0 : 128 * group) + kAtOnce * i + sub, q2 = sg.rb * R + r2;  // row of the block
+          w[i] = make_uint4(0, 0, 0, 0);
+          if (r2 < rows_left)
+            w[i] = __ldg(reinterpret_cast<const uint4*>(p.q.data + static_cast<int64_t>(sg.r0 + q2 / p.G) * p.q.row_stride +
+                                                        static_cast<int64_t>(sg.h * p.G + q2 % p.G) * p.q.head_stride) + c);
+        }
+        int mine = 0;
 #pragma unroll
-        for (int c = 0; c < CB; ++c) {
-          float x[8];
-          unpack8(w[c], p.f16, x);
+        for (int i = 0; i < CB; ++i) {
+          float x[8], mx = 0.f;
+          unpack8(w[i], p.f16, x);
 #pragma unroll
           for (int k = 0; k < 8; k += 2) mx = max3(mx, fabsf(x[k]), fabsf(x[k + 1]));
-        }
-        bool range = false;
-        const int E = prescale_exponent(mx, range);
-        const float up = p.scale_log2 < 0.f ? -pow2_int(E) : pow2_int(E);
-        fr = fmaxf(pow2_int(-E) * fabsf(p.scale_log2), 1e-37f);  // a hidden score, -inf, stays one at scale 0
-        if (two || group == 0) {
-          const uint32_t dst = base + Ge::kQ + (two ? group * Ge::kTile : 0) + 16 * lane_row;
 #pragma unroll
-          for (int c = 0; c < CB; ++c) {  // channels 8 c .. 8 c + 7 = 32 j + 8 q ..: chunk (D / 32) q + j
-            float x[8];
-            unpack8(w[c], p.f16, x);
-            st_shared_v4(dst + ((c & 3) * KW + (c >> 2)) * 2048, h2(x[0] * up, x[4] * up), h2(x[1] * up, x[5] * up),
-                         h2(x[2] * up, x[6] * up), h2(x[3] * up, x[7] * up));
+          for (int o = 1; o < CB; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          bool range = false;
+          const int E = prescale_exponent(mx, range);
+          const int of_lane = __shfl_sync(0xffffffffu, E, (lane % kAtOnce) * CB);
+          if (lane / kAtOnce == i) mine = of_lane;
+          if (two || group == 0) {
+            const float up = p.scale_log2 < 0.f ? -pow2_int(E) : pow2_int(E);
+            // channels 8 c .. 8 c + 7 = 32 j + 8 q ..: chunk (D / 32) q + j
+            st_shared_v4(base + (two ? group * Ge::kTile : 0) + 16 * (32 * (warp & 3) + kAtOnce * i + sub) +
+                             ((c & 3) * KW + (c >> 2)) * 2048,
+                         h2(x[0] * up, x[4] * up), h2(x[1] * up, x[5] * up), h2(x[2] * up, x[6] * up), h2(x[3] * up, x[7] * up));
           }
-          fence_proxy_async_smem();
         }
+        fence_proxy_async_smem();
+        fr = fmaxf(pow2_int(-mine) * fabsf(p.scale_log2), 1e-37f);  // a hidden score, -inf, stays one at scale 0
       }
       int full_lo, full_hi;  // tiles that every live row of the block sees whole
       {
@@ -605,47 +615,54 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             for (int i = 0; i < 32; ++i)
               if (32 * c + i < lo || 32 * c + i >= hi) raw[c][i] = 0xff800000u;  // -inf
         }
-        float mx = -INFINITY, my = -INFINITY;
+        // The weights are formed under the running max as it is, and again in the rare case that a score was
+        // more than 2^8 above it (a warp's first tile always finds its max first).
+        bool find = k == 0;
+        float l0, l1;
+        while (true) {
+          if (find) {
+            float mx = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            mx = max3(mx, __uint_as_float(raw[c][i]), __uint_as_float(raw[c][i + 1]));
-            my = max3(my, __uint_as_float(raw[c][i + 2]), __uint_as_float(raw[c][i + 3]));
-          }
-        mx = fmaxf(mx, my) * fr;
-        if (__any_sync(0xffffffffu, mx > m + kSlack)) {
-          const float mn = fmaxf(m, mx), a = ex2(m - mn);
-          m = mn;
-          l *= a;
-          if (k > 0) {
+              for (int i = 0; i < 32; i += 2) mx = max3(mx, __uint_as_float(raw[c][i]), __uint_as_float(raw[c][i + 1]));
+            const float mn = fmaxf(m, mx * fr), a = ex2(m - mn);
+            m = mn;
+            l *= a;
+            if (k > 0) {
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t v[16];
-              tc5::ld16(oc + 16 * c, v);
-              tc5::wait_ld16(v);
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t v[16];
+                tc5::ld16(oc + 16 * c, v);
+                tc5::wait_ld16(v);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a);
-              tc5::st16(oc + 16 * c, v);
+                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a);
+                tc5::st16(oc + 16 * c, v);
+              }
+              tc5::wait_st();
             }
-            tc5::wait_st();
           }
-        }
-        float l0 = 0.f, l1 = 0.f;
-        const float neg = -m;
+          l0 = l1 = 0.f;
+          const float neg = -m;
+          float mx = -INFINITY, my = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float a = __uint_as_float(raw[c][i]), b = __uint_as_float(raw[c][i + 1]);
-            fma_pair(a, b, fr, neg);
-            a = ex2(a);
-            b = ex2(b);
-            add_pair(l0, l1, a, b);
-            w[i >> 1] = h2(a, b);
+            for (int i = 0; i < 32; i += 2) {
+              float a = __uint_as_float(raw[c][i]), b = __uint_as_float(raw[c][i + 1]);
+              if (i & 2) my = max3(my, a, b);
+              else mx = max3(mx, a, b);
+              fma_pair(a, b, fr, neg);
+              a = ex2(a);
+              b = ex2(b);
+              add_pair(l0, l1, a, b);
+              w[i >> 1] = h2(a, b);
+            }
+            tc5::st16(sc + 16 * c, w);
           }
-          tc5::st16(sc + 16 * c, w);
+          if (find || !__any_sync(0xffffffffu, fmaxf(mx, my) * fr > m + kSlack)) break;
+          find = true;
         }
         l += l0 + l1;
         tc5::wait_st();
@@ -658,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
 
       // ---- results: thread = row; with one tile of queries the second group hands its sums over
       // (tile region of the keys and values, column by column: distinct banks)
-      float* const xo = reinterpret_cast<float*>(smem + Ge::kK);
+      float* const xo = reinterpret_cast<float*>(smem + Ge::k_at(two));
       if (!two) {
         if (group == 1 && done) {
           s_ml[lane_row][0] = m;
@@ -685,28 +702,55 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           m = M;
           l = l * f0 + l1 * f1;
         }
-        const size_t orow = static_cast<size_t>(sg.r0 + rr / p.G) * p.Hq + sg.h * p.G + rr % p.G;
         const float y = l == 0.f ? 0.f : 1.f / l;
-        uint32_t res[D / 2];
+        auto out_row = [&](int row_of_block) {
+          const int q2 = sg.rb * R + row_of_block;
+          return static_cast<size_t>(sg.r0 + q2 / p.G) * p.Hq + sg.h * p.G + q2 % p.G;
+        };
+        // rows go out by way of shared memory (each warp its 32 rows), so that lanes store along a row; 16-byte
+        // chunks are exchanged by the row's low bits: distinct banks both ways
+        const int first = (two ? 128 * group : 0) + 32 * (warp & 3);
+        if (sg.part >= 0) {
+          constexpr int kRow = D * 4, kChunks = D / 4;
+          uint8_t* const st = smem + (two ? Ge::k_at(true) : Ge::v_at(false)) + (first >> 5) * 32 * kRow;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t v[32];
-          tc5::ld32(oc + 32 * c, v);
-          tc5::wait_ld(v);
-          float x[32];
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            tc5::ld32(oc + 32 * c, v);
+            tc5::wait_ld(v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]) * f0;
-          if (!two && steps > 1) {
+            for (int i = 0; i < 8; ++i) {
+              float x[4];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] += f1 * xo[(32 * c + i) * 128 + lane_row];
-          }
-          if (sg.part >= 0) {
-            if (live) {
-              float4* dst = reinterpret_cast<float4*>(p.part_o + (static_cast<size_t>(sg.part) * R + row) * D + 32 * c);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+              for (int k = 0; k < 4; ++k) {
+                x[k] = __uint_as_float(v[4 * i + k]) * f0;
+                if (!two && steps > 1) x[k] += f1 * xo[(32 * c + 4 * i + k) * 128 + lane_row];
+              }
+              *reinterpret_cast<float4*>(st + lane * kRow + 16 * ((8 * c + i) ^ (lane & 7))) = make_float4(x[0], x[1], x[2], x[3]);
             }
-          } else {
+          }
+          __syncwarp();
+          const int left = min(32, rows_left - first);
+          float4* const dst = reinterpret_cast<float4*>(p.part_o + (static_cast<size_t>(sg.part) * R + first) * D);
+          for (int e = lane; e < left * kChunks; e += 32) {
+            const int r2 = e / kChunks, ch = e % kChunks;
+            dst[e] = *reinterpret_cast<const float4*>(st + r2 * kRow + 16 * (ch ^ (r2 & 7)));
+          }
+          if (live) reinterpret_cast<float2*>(p.part_ml)[static_cast<size_t>(sg.part) * R + row] = make_float2(m, l);
+        } else {
+          uint32_t res[D / 2];
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            tc5::ld32(oc + 32 * c, v);
+            tc5::wait_ld(v);
+            float x[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]) * f0;
+            if (!two && steps > 1) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] += f1 * xo[(32 * c + i) * 128 + lane_row];
+            }
             // column 8 wi + 2 i + e is channel 64 (wi % VW) + 16 i + 8 e + wi / VW: neighbouring channels are
             // columns VW * 8 apart, in the same 32
 #pragma unroll
@@ -719,16 +763,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
               }
             }
           }
-        }
-        if (sg.part >= 0) {
-          if (live)
-            reinterpret_cast<float2*>(p.part_ml)[static_cast<size_t>(sg.part) * R + row] = make_float2(m, l);
-        } else if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D);
+          constexpr int kRow = D * 2, kChunks = D / 8;  // chunk i holds channels 8 i .. 8 i + 7
+          uint8_t* const st = smem + (first >> 5) * 32 * kRow;  // where the queries were
 #pragma unroll
-          for (int i = 0; i < 8 * VW; ++i)  // channels 64 w + 8 (2 pair + e) .. + 7
-            dst[i] = make_uint4(res[4 * i], res[4 * i + 1], res[4 * i + 2], res[4 * i + 3]);
-          if (p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+          for (int i = 0; i < kChunks; ++i)
+            *reinterpret_cast<uint4*>(st + lane * kRow + 16 * (i ^ (lane & 7))) =
+                make_uint4(res[4 * i], res[4 * i + 1], res[4 * i + 2], res[4 * i + 3]);
+          __syncwarp();
+          const int left = min(32, rows_left - first);
+          for (int e = lane; e < left * kChunks; e += 32) {
+            const int r2 = e / kChunks, ch = e % kChunks;
+            reinterpret_cast<uint4*>(p.out + out_row(first + r2) * D)[ch] =
+                *reinterpret_cast<const uint4*>(st + r2 * kRow + 16 * (ch ^ (r2 & 7)));
+          }
+          if (live && p.lse) p.lse[out_row(row)] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
         }
       }
       if (sg.part >= 0) {
@@ -748,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           // (kept where its queries were), a warp per row; then a thread per row and four columns.
           const int rows = min(R, rows_left), parts = sg.parts;
           auto slot_of = [&](int i) { return static_cast<size_t>(2 * (sg.c0 + i) + (i == 0 ? 1 : 0)); };
-          float* const wts = reinterpret_cast<float*>(smem + Ge::kQ);  // [rows][parts], divided by the row's sum
+          float* const wts = reinterpret_cast<float*>(smem);  // [rows][parts], divided by the row's sum
 #pragma unroll 4
           for (int mr = warp; mr < rows; mr += 8) {
             const float2 ml = lane < parts ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(lane) * R + mr)
@@ -811,19 +859,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           if (s.at < s.end) {
             s.item0 = s.at;
             bool found = true;
-            if (++s.rb == row_blocks(p, s.n, R)) {
-              s.rb = 0;
-              if (++s.h == p.Hkv) {
-                s.h = 0;
-                int f = 0;
-                do {
-                  if (++s.b >= p.B) {  // lengths that changed under the call
-                    found = false;
-                    break;
-                  }
-                  load_sequence(p, s.b, s.T, s.n, s.r0, f);
-                } while (s.n == 0);
-              }
+            if (++s.h == p.Hkv) {  // the next pair with rows
+              s.h = 0;
+              int f = 0;
+              do {
+                if (++s.pair >= p.B * line) {  // lengths that changed under the call
+                  found = false;
+                  break;
+                }
+                s.b = s.pair / line;
+                s.rb = s.pair - s.b * line;
+                load_sequence(p, s.b, s.T, s.n, s.r0, f);
+              } while (s.rb >= row_blocks(p, s.n, R));
             }
             if (found) line_segment(p, s, R);
           }
@@ -846,11 +893,12 @@ cudaError_t launch_as(const Kv4AttnParams& p, int two, int line, int ctas, cudaS
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_done[dev]) {
-    e = cudaFuncSetAttribute(kv4_prompt_kernel<D, NG, kExact>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geom<D>::kSmem);
+    e = cudaFuncSetAttribute(kv4_prompt_kernel<D, NG, kExact>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             std::max(Geom<D, kExact>::smem(false), Geom<D, kExact>::smem(true)));
     if (e != cudaSuccess) return e;
     attr_done[dev] = true;
   }
-  kv4_prompt_kernel<D, NG, kExact><<<ctas, kThreads, Geom<D>::kSmem, stream>>>(p, two, line);
+  kv4_prompt_kernel<D, NG, kExact><<<ctas, kThreads, Geom<D, kExact>::smem(two), stream>>>(p, two, line);
   return cudaGetLastError();
 }
 
@@ -869,7 +917,8 @@ Kv4PromptPlan kv4_prompt_plan(int B, int Hkv, int n_rows, int max_q, int G, int 
   z.two = rows > 128;
   z.rows = z.two ? 256 : 128;
   const int64_t items = static_cast<int64_t>(B) * Hkv * ((rows + z.rows - 1) / z.rows);
-  z.line = items < 2 * static_cast<int64_t>(num_sms);
+  const int64_t blocks = (rows + z.rows - 1) / z.rows;
+  z.line = items < 2 * static_cast<int64_t>(num_sms) && B * blocks <= kThreads ? static_cast<int>(blocks) : 0;
   z.ctas = z.line ? std::min(num_sms, static_cast<int>(kKv4CounterBytes / 4)) : items;
   return z;
 }
