@@ -22,9 +22,10 @@
 // Channels keep the order in which a code word unpacks: eight channels of a word in the order 0 4 1 5
 // 2 6 3 7, for keys matched by the queries, for values undone when a row is stored.
 //
-// kExact (when the log-sum-exp is asked for): keys as a high and a low FP16 part (together 2^-22 of the
-// value), two products per score and one stage, since the rounding of one part, 2^-12 of a key, shows
-// in a log-sum-exp as ~1e-4.
+// kExact (when the log-sum-exp is asked for; the rounding of a key to FP16, 2^-12 of it, shows there as
+// ~1e-4): scores from exact products. With the scale s = s1 + s2 cut after seven bits, n s1 and n s2 fit FP16
+// for every code n: two key operands. The minimum enters as sixteen more channels: its value for each
+// group against the sum of the group's queries, in two FP16 parts. One stage of keys then has the room.
 //
 // Work: with many items (sequence, kv head, row block) one CTA per item, those that see the most
 // tokens first; with few, the items' token tiles are laid on one line and cut evenly over the SMs
@@ -51,16 +52,18 @@ constexpr float kSlack = 8.f;     // the running max is raised when a score exce
 constexpr float kNoMax = -1e30f;  // the running max before the first score
 constexpr long long kBudget = 4ll << 30;  // cycles of a wait before it is given up
 
-// Shared memory in tiles of 128 x D FP16: queries (one or two tiles), keys, values (two stages). Keys have
-// two stages, in two parts (kExact) two only when one tile of queries leaves the room.
+// Shared memory in tiles of 128 x D FP16: queries (one or two tiles), keys (two stages, or two operands),
+// values (two stages); kExact: the sixteen further channels of each tile of queries, and of the keys.
 template <int D, bool kExact>
 struct Geom {
   static constexpr int kTile = 128 * D * 2;
+  static constexpr int kMore = kExact ? 128 * 16 * 2 : 0;
   static constexpr uint32_t kColS = 0, kColO = 256;
   __host__ __device__ static constexpr int k_at(bool two) { return (two ? 2 : 1) * kTile; }
-  __host__ __device__ static constexpr int k_stages(bool two) { return kExact && two ? 1 : 2; }
-  __host__ __device__ static constexpr int v_at(bool two) { return k_at(two) + k_stages(two) * (kExact ? 2 : 1) * kTile; }
-  __host__ __device__ static constexpr int smem(bool two) { return v_at(two) + 2 * kTile + 1024; }  // slack to align the start
+  __host__ __device__ static constexpr int v_at(bool two) { return k_at(two) + 2 * kTile; }
+  __host__ __device__ static constexpr int more_q_at(bool two) { return v_at(two) + 2 * kTile; }
+  __host__ __device__ static constexpr int more_k_at(bool two) { return more_q_at(two) + (two ? 2 : 1) * kMore; }
+  __host__ __device__ static constexpr int smem(bool two) { return more_k_at(two) + kMore + 1024; }  // slack to align the start
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -108,18 +111,16 @@ __device__ __forceinline__ uint32_t dequant2(uint32_t w, __half2 s, __half2 m) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// The same pair in float32, as a high part and the rest (both FP16).
+// The codes of the same pair, times two factors (exact: see kExact).
 template <bool kHigh>
-__device__ __forceinline__ void dequant2_parts(uint32_t w, float s, float m, uint32_t& high, uint32_t& low) {
+__device__ __forceinline__ void codes2_times(uint32_t w, __half2 s1, __half2 s2, uint32_t& y1, uint32_t& y2) {
   const uint32_t b = and_or(w, kHigh ? 0x00F000F0u : 0x000F000Fu, 0x64006400u);
   const __half2 x = *reinterpret_cast<const __half2*>(&b);
   const __half2 n = kHigh ? __hfma2(x, __float2half2_rn(0.0625f), __float2half2_rn(-64.f))
                           : __hadd2(x, __float2half2_rn(-1024.f));
-  float2 v = __half22float2(n);
-  fma_pair(v.x, v.y, s, m);
-  high = h2(v.x, v.y);
-  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&high));
-  low = h2(v.x - h.x, v.y - h.y);
+  const __half2 a = __hmul2(n, s1), c = __hmul2(n, s2);
+  y1 = *reinterpret_cast<const uint32_t*>(&a);
+  y2 = *reinterpret_cast<const uint32_t*>(&c);
 }
 
 // The part of an item that the CTA works on.
@@ -336,8 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     ++segs;
     return !s_abort && sg.valid;
   };
-  const bool one_k = Ge::k_stages(two) == 1;
-  constexpr int kKeyBytes = Ge::kTile * (kExact ? 2 : 1);  // of a stage
+  constexpr bool one_k = kExact;  // one stage of keys
 
   if (group == 2) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
@@ -398,18 +398,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
 #pragma unroll
         for (int g = 0; g < NG; ++g) cur[g] = num[g];
         if (!wait(k_free + ks, kph ^ 1)) break;
-        const uint32_t kd = k_tiles + ks * kKeyBytes + 16 * tok_row;
+        const uint32_t kd = k_tiles + ks * Ge::kTile + 16 * tok_row;
+        __half2 s1[NG], s2[NG];
+        if constexpr (kExact) {  // a quarter of the scale (15 scales fit FP16) in seven bits and the rest; of the minimum
+          uint32_t more[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const __half2 s = __hmul2(__half2half2(scale_of(cur[g].x)), __float2half2_rn(0.25f));
+            const uint32_t top = *reinterpret_cast<const uint32_t*>(&s) & 0xFFF0FFF0u;
+            s1[g] = *reinterpret_cast<const __half2*>(&top);
+            s2[g] = __hsub2(s, s1[g]);
+            const __half2 mn = __hmul2(__half2half2(min_of(cur[g].x)), __float2half2_rn(0.25f));
+            more[g] = *reinterpret_cast<const uint32_t*>(&mn);
+          }
+          st_shared_v4(base + Ge::more_k_at(two) + 16 * tok_row, more[0], more[1], more[2], more[3]);
+        }
 #pragma unroll
         for (int wi = 0; wi < D / 8; ++wi) {
-          const uint32_t nm = cur[(wi % KW) / (KW / NG)].x;
+          const int g = (wi % KW) / (KW / NG);
+          const uint32_t nm = cur[g].x;
           const uint32_t w = kw[wi], w8 = w >> 8;
           if constexpr (kExact) {
-            const float s = __half2float(scale_of(nm)), mn = __half2float(min_of(nm));
             uint32_t y[4], z[4];
-            dequant2_parts<false>(w, s, mn, y[0], z[0]);
-            dequant2_parts<true>(w, s, mn, y[1], z[1]);
-            dequant2_parts<false>(w8, s, mn, y[2], z[2]);
-            dequant2_parts<true>(w8, s, mn, y[3], z[3]);
+            codes2_times<false>(w, s1[g], s2[g], y[0], z[0]);
+            codes2_times<true>(w, s1[g], s2[g], y[1], z[1]);
+            codes2_times<false>(w8, s1[g], s2[g], y[2], z[2]);
+            codes2_times<true>(w8, s1[g], s2[g], y[3], z[3]);
             st_shared_v4(kd + wi * 2048, y[0], y[1], y[2], y[3]);
             st_shared_v4(kd + Ge::kTile + wi * 2048, z[0], z[1], z[2], z[3]);
           } else {
@@ -494,13 +508,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           if ((!two || u == 0) && !all(wait(k_full + st, one_k ? J & 1 : (J >> 1) & 1))) return false;
           tc5::fence_after();
           const uint64_t qa = tc5::smem_desc(base + (two ? u * Ge::kTile : 0), 2048, 128);
-          const uint64_t ka = tc5::smem_desc(k_tiles + st * kKeyBytes, 2048, 128);
+          const uint64_t ka = tc5::smem_desc(k_tiles + st * Ge::kTile, 2048, 128);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {  // descriptor addresses count 16 bytes
             tc5::mma_ss(tm + Ge::kColS + 128 * u, qa + 256 * k, ka + 256 * k, kDescS, k > 0, leader);
             if constexpr (kExact)
               tc5::mma_ss(tm + Ge::kColS + 128 * u, qa + 256 * k, ka + Ge::kTile / 16 + 256 * k, kDescS, true, leader);
           }
+          if constexpr (kExact)
+            tc5::mma_ss(tm + Ge::kColS + 128 * u, tc5::smem_desc(base + Ge::more_q_at(two) + (two ? u * Ge::kMore : 0), 2048, 128),
+                        tc5::smem_desc(base + Ge::more_k_at(two), 2048, 128), kDescS, true, leader);
           tc5::commit(s_full + u, leader);
           if (!two || u == 1) tc5::commit(k_free + st, leader);
           return true;
@@ -539,46 +556,80 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       const int rows_left = sg.n * p.G - sg.rb * R;  // live rows of the block
       const int row = (two ? 128 * group : 0) + lane_row, rr = sg.rb * R + row;
       const bool live = row < rows_left;
-      float m = kNoMax, l = 0.f, fr;
+      float m = kNoMax, l = 0.f, fr = 0.f;
       int2 vis = make_int2(0, 0);
       {
-        // ---- queries: CB lanes read a row at a time; rows are prescaled by a power of two and stored in the
-        // keys' channel order; this thread keeps its own row's factor
+        // ---- queries: the warp's 32 rows, eight rows x 64 bytes with one load (lane: row lane & 7 of the
+        // eight, 16-byte chunk lane >> 3 of the four); prescaled by a power of two and stored in the keys' channel
+        // order, eight rows of a chunk side by side; this thread keeps its own row's factor
         if (live) vis = visible(p, sg.T, sg.n, rr / p.G);
-        constexpr int kAtOnce = 32 / CB;  // rows that the warp reads with one load
-        const int c = lane % CB, sub = lane / CB;
-        uint4 w[CB];
+        uint4 w[4][CB / 4];
 #pragma unroll
-        for (int i = 0; i < CB; ++i) {
-          const int r2 = 32 * warp - (two ? 0 : 128 * group) + kAtOnce * i + sub, q2 = sg.rb * R + r2;  // row of the block
-          w[i] = make_uint4(0, 0, 0, 0);
-          if (r2 < rows_left)
-            w[i] = __ldg(reinterpret_cast<const uint4*>(p.q.data + static_cast<int64_t>(sg.r0 + q2 / p.G) * p.q.row_stride +
-                                                        static_cast<int64_t>(sg.h * p.G + q2 % p.G) * p.q.head_stride) + c);
+        for (int i = 0; i < 4; ++i) {
+          const int r2 = row - lane + 8 * i + (lane & 7), q2 = sg.rb * R + r2;  // row of the block
+          const uint16_t* src = p.q.data + static_cast<int64_t>(sg.r0 + q2 / p.G) * p.q.row_stride +
+                                static_cast<int64_t>(sg.h * p.G + q2 % p.G) * p.q.head_stride;
+#pragma unroll
+          for (int j = 0; j < CB / 4; ++j)
+            w[i][j] = r2 < rows_left ? __ldg(reinterpret_cast<const uint4*>(src) + 4 * j + (lane >> 3)) : make_uint4(0, 0, 0, 0);
         }
-        int mine = 0;
 #pragma unroll
-        for (int i = 0; i < CB; ++i) {
-          float x[8], mx = 0.f;
-          unpack8(w[i], p.f16, x);
+        for (int i = 0; i < 4; ++i) {
+          float mx = 0.f;
 #pragma unroll
-          for (int k = 0; k < 8; k += 2) mx = max3(mx, fabsf(x[k]), fabsf(x[k + 1]));
+          for (int j = 0; j < CB / 4; ++j) {
+            float x[8];
+            unpack8(w[i][j], p.f16, x);
 #pragma unroll
-          for (int o = 1; o < CB; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            for (int k = 0; k < 8; k += 2) mx = max3(mx, fabsf(x[k]), fabsf(x[k + 1]));
+          }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
           bool range = false;
-          const int E = prescale_exponent(mx, range);
-          const int of_lane = __shfl_sync(0xffffffffu, E, (lane % kAtOnce) * CB);
-          if (lane / kAtOnce == i) mine = of_lane;
+          const int E = prescale_exponent(mx, range) - (kExact ? 8 : 0);  // kExact: below 2^7, so that the sums fit
+          if ((lane >> 3) == i)  // a hidden score, -inf, stays one at scale 0
+            fr = fmaxf(pow2_int(-E) * fabsf(p.scale_log2) * (kExact ? 4.f : 1.f), 1e-37f);
           if (two || group == 0) {
             const float up = p.scale_log2 < 0.f ? -pow2_int(E) : pow2_int(E);
-            // channels 8 c .. 8 c + 7 = 32 j + 8 q ..: chunk (D / 32) q + j
-            st_shared_v4(base + (two ? group * Ge::kTile : 0) + 16 * (32 * (warp & 3) + kAtOnce * i + sub) +
-                             ((c & 3) * KW + (c >> 2)) * 2048,
-                         h2(x[0] * up, x[4] * up), h2(x[1] * up, x[5] * up), h2(x[2] * up, x[6] * up), h2(x[3] * up, x[7] * up));
+            const uint32_t dst = base + (two ? group * Ge::kTile : 0) + 16 * (32 * (warp & 3) + 8 * i + (lane & 7));
+            float sum[NG];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) sum[g] = 0.f;
+#pragma unroll
+            for (int j = 0; j < CB / 4; ++j) {  // channels 32 j + 8 (lane >> 3) ..: chunk (D / 32) (lane >> 3) + j
+              float x[8];
+              uint32_t y[4];
+              unpack8(w[i][j], p.f16, x);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) y[k] = h2(x[k] * up, x[k + 4] * up);
+              st_shared_v4(dst + ((lane >> 3) * KW + j) * 2048, y[0], y[1], y[2], y[3]);
+              if constexpr (kExact) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&y[k]));
+                  sum[j / (KW / NG)] += v.x + v.y;
+                }
+              }
+            }
+            if constexpr (kExact) {
+              uint32_t more[4] = {0, 0, 0, 0};
+#pragma unroll
+              for (int g = 0; g < NG; ++g) {
+                sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 8);
+                sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 16);
+                const float high = __half2float(__float2half_rn(sum[g]));
+                more[g] = h2(high, sum[g] - high);
+              }
+              const uint32_t at = base + Ge::more_q_at(two) + (two ? group * Ge::kMore : 0) +
+                                  16 * (32 * (warp & 3) + 8 * i + (lane & 7));
+              if (lane < 8) st_shared_v4(at, more[0], more[1], more[2], more[3]);
+              else if (lane < 16) st_shared_v4(at + 2048, 0, 0, 0, 0);
+              else if (lane < 24 && (!two || group == 0))  // and the keys' last eight channels: nothing
+                st_shared_v4(base + Ge::more_k_at(two) + 2048 + 16 * (32 * (warp & 3) + 8 * i + (lane & 7)), 0, 0, 0, 0);
+            }
           }
         }
         fence_proxy_async_smem();
-        fr = fmaxf(pow2_int(-mine) * fabsf(p.scale_log2), 1e-37f);  // a hidden score, -inf, stays one at scale 0
       }
       int full_lo, full_hi;  // tiles that every live row of the block sees whole
       {
@@ -792,60 +843,47 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         }
         softmax_barrier();
         if (s_last) {
-          // this CTA came last: the item's parts in CTA order. First each row's weights of the parts
-          // (kept where its queries were), a warp per row; then a thread per row and four columns.
+          // this CTA came last: the item's parts in CTA order. First each row's weights of the parts (kept
+          // where the queries were), a thread per row; then a thread per row and eight channels.
           const int rows = min(R, rows_left), parts = sg.parts;
           auto slot_of = [&](int i) { return static_cast<size_t>(2 * (sg.c0 + i) + (i == 0 ? 1 : 0)); };
-          float* const wts = reinterpret_cast<float*>(smem);  // [rows][parts], divided by the row's sum
+          float* const wts = reinterpret_cast<float*>(smem);  // [parts][R], divided by the row's sum
+          if (tid < rows) {
+            const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + tid;
+            float M = kNoMax, L = 0.f;
 #pragma unroll 4
-          for (int mr = warp; mr < rows; mr += 8) {
-            const float2 ml = lane < parts ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(lane) * R + mr)
-                                           : make_float2(kNoMax, 0.f);
-            float M = ml.x;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            const float f = ex2(ml.x - M);
-            float L = f * ml.y;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-            if (lane < parts) wts[mr * kMaxParts + lane] = L == 0.f ? 0.f : f / L;
-            if (lane == 0 && p.lse) {
-              const int mrr = sg.rb * R + mr;
-              p.lse[static_cast<size_t>(sg.r0 + mrr / p.G) * p.Hq + sg.h * p.G + mrr % p.G] =
+            for (int i = 0; i < parts; ++i) {
+              const float2 x = __ldcg(ml + slot_of(i) * R);
+              const float mn = fmaxf(M, x.x);
+              L = L * ex2(M - mn) + x.y * ex2(x.x - mn);
+              M = mn;
+              wts[i * R + tid] = x.x;
+            }
+            const float y = L == 0.f ? 0.f : 1.f / L;
+            for (int i = 0; i < parts; ++i) wts[i * R + tid] = ex2(wts[i * R + tid] - M) * y;
+            if (p.lse) {
+              const int q2 = sg.rb * R + tid;
+              p.lse[static_cast<size_t>(sg.r0 + q2 / p.G) * p.Hq + sg.h * p.G + q2 % p.G] =
                   L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
             }
           }
           softmax_barrier();
-          constexpr int kF = D / 4, kU = 4;  // chunks of a row; chunks of a thread at once
-          for (int e0 = tid; e0 < rows * kF; e0 += 256 * kU) {
-            float4 v[kU];
+          // chunk i of a row, channels 8 i .. 8 i + 7, comes from columns i, i + 8 VW, ..: lanes read along i
+          constexpr int kChunks = D / 8;
+          for (int e = tid; e < rows * kChunks; e += 256) {
+            const int r2 = e / kChunks, i2 = e % kChunks, q2 = sg.rb * R + r2;
+            float x[8];
 #pragma unroll
-            for (int u = 0; u < kU; ++u) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+            for (int k = 0; k < 8; ++k) x[k] = 0.f;
+#pragma unroll 4
             for (int i = 0; i < parts; ++i) {
-              const float4* src = reinterpret_cast<const float4*>(p.part_o + slot_of(i) * R * D);
+              const float* src = p.part_o + (slot_of(i) * R + r2) * D + i2;
+              const float f = wts[i * R + r2];
 #pragma unroll
-              for (int u = 0; u < kU; ++u) {
-                const int e = e0 + 256 * u;
-                if (e < rows * kF) {
-                  const float f = wts[e / kF * kMaxParts + i];
-                  const float4 x = __ldcg(src + e);
-                  v[u].x += f * x.x, v[u].y += f * x.y, v[u].z += f * x.z, v[u].w += f * x.w;
-                }
-              }
+              for (int k = 0; k < 8; ++k) x[k] += f * __ldcg(src + 8 * VW * k);
             }
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-              const int e = e0 + 256 * u;
-              if (e < rows * kF) {
-                const int mrr = sg.rb * R + e / kF, col = 4 * (e % kF), wi = col >> 3;
-                uint16_t* dst = p.out + (static_cast<size_t>(sg.r0 + mrr / p.G) * p.Hq + sg.h * p.G + mrr % p.G) * D +
-                                64 * (wi % VW) + 8 * (col & 7) + wi / VW;
-                const uint32_t a = pack2(v[u].x, v[u].y, p.f16), b = pack2(v[u].z, v[u].w, p.f16);
-                dst[0] = static_cast<uint16_t>(a), dst[8] = static_cast<uint16_t>(a >> 16);
-                dst[16] = static_cast<uint16_t>(b), dst[24] = static_cast<uint16_t>(b >> 16);
-              }
-            }
+            reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(sg.r0 + q2 / p.G) * p.Hq + sg.h * p.G + q2 % p.G) * D)[i2] =
+                pack8(x, p.f16);
           }
         }
       }
