@@ -31,28 +31,41 @@ struct RowPlace {
 };
 
 // Where row r of the call goes. Rows at and behind cu_new[B] belong to no sequence and are skipped
-// without an error (a padded batch). Called by whole warps.
+// without an error (a padded batch). Called by whole warps. Up to 32 sequences are looked at with one
+// load per lane of the offsets and one of the lengths, so that only the page id waits for another load.
 __device__ __forceinline__ RowPlace place_row(const int32_t* cu, const int32_t* lens, const int32_t* table, int B, int r,
                                               int max_new, int max_pages, int p_shift, int64_t n_pages, bool paged,
                                               int n_pos) {
   RowPlace z{-1, 0, 0, 0};
-  int b = -1, r0 = 0, r1 = 0;
-  if (r < B) {  // decode steps: one row per sequence
-    r0 = __ldg(cu + r);
-    r1 = __ldg(cu + r + 1);
-    if (r0 == r && r1 == r + 1) b = r;
-  }
-  if (b < 0) {
-    if (r >= __ldg(cu + B)) return z;
-    b = warp_find_seq(cu, B, r);
-    r0 = __ldg(cu + b);
-    r1 = __ldg(cu + b + 1);
+  int b = 0, r0, r1, s0;
+  if (B <= 32) {
+    const int lane = threadIdx.x & 31, i = min(lane, B - 1);
+    const int end = __ldg(cu + i + 1), len = __ldg(lens + i), begin = __ldg(cu);
+    b = __popc(__ballot_sync(0xffffffffu, lane < B && end <= r));
+    if (b >= B) return z;
+    r1 = __shfl_sync(0xffffffffu, end, b);
+    r0 = __shfl_sync(0xffffffffu, end, b > 0 ? b - 1 : 0);
+    if (b == 0) r0 = begin;
+    s0 = __shfl_sync(0xffffffffu, len, b);
+  } else {
+    b = -1;
+    if (r < B) {  // decode steps: one row per sequence
+      r0 = __ldg(cu + r);
+      r1 = __ldg(cu + r + 1);
+      if (r0 == r && r1 == r + 1) b = r;
+    }
+    if (b < 0) {
+      if (r >= __ldg(cu + B)) return z;
+      b = warp_find_seq(cu, B, r);
+      r0 = __ldg(cu + b);
+      r1 = __ldg(cu + b + 1);
+    }
+    s0 = __ldg(lens + b);
   }
   if (r < r0 || r >= r1 || r1 - r0 > max_new) {
     z.flags = kErrRows;
     return z;
   }
-  const int s0 = __ldg(lens + b);
   const int64_t t = static_cast<int64_t>(s0) + (r - r0);
   const int64_t pg = t >> p_shift;
   if (s0 < 0 || pg >= max_pages || t >= n_pos) {
