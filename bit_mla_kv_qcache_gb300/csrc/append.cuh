@@ -106,9 +106,26 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8], bool f16) {
   return make_uint4(pack2(x[0], x[1], f16), pack2(x[2], x[3], f16), pack2(x[4], x[5], f16), pack2(x[6], x[7], f16));
 }
 
+// Two float32 operations in one instruction. A product and a sum that follow one another may still come
+// out fused (seen with the 13.0 assembler), so these are used where that changes nothing.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{ .reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{ .reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
 // The angles of one thread's eight channels 8 i .. 8 i + 7 at position t: with neighbouring pairs
-// four (c, s), with pairs half a rotation apart eight; rows of the tables are 16-byte aligned
-// (rot_dim / 2 is a multiple of 8).
+// four (c, s), with pairs half a rotation apart eight (s negative for the first of a pair, so that
+// both are x c + partner s); rows of the tables are 16-byte aligned (rot_dim / 2 is a multiple of 8).
 struct Angles {
   float c[8], s[8];
 };
@@ -125,13 +142,15 @@ __device__ __forceinline__ Angles load_angles(const Rotation& rot, int64_t t, in
     a.c[0] = c.x, a.c[1] = c.y, a.c[2] = c.z, a.c[3] = c.w;
     a.s[0] = s.x, a.s[1] = s.y, a.s[2] = s.z, a.s[3] = s.w;
   } else {
-    const int f = 8 * i < half ? 8 * i : 8 * i - half;
+    const bool first = 8 * i < half;
+    const int f = first ? 8 * i : 8 * i - half;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const float4 c = __ldg(reinterpret_cast<const float4*>(rot.cos_tab + row + f) + k);
       const float4 s = __ldg(reinterpret_cast<const float4*>(rot.sin_tab + row + f) + k);
       a.c[4 * k] = c.x, a.c[4 * k + 1] = c.y, a.c[4 * k + 2] = c.z, a.c[4 * k + 3] = c.w;
-      a.s[4 * k] = s.x, a.s[4 * k + 1] = s.y, a.s[4 * k + 2] = s.z, a.s[4 * k + 3] = s.w;
+      a.s[4 * k] = first ? -s.x : s.x, a.s[4 * k + 1] = first ? -s.y : s.y;
+      a.s[4 * k + 2] = first ? -s.z : s.z, a.s[4 * k + 3] = first ? -s.w : s.w;
     }
   }
   return a;
@@ -157,8 +176,8 @@ __device__ __forceinline__ void rotate8(const Rotation& rot, const Angles& a, in
     return;
   }
   const int d = rot.rot_dim >> 4, lane = threadIdx.x & 31;
-  const bool first = i < d, in = i < 2 * d;
-  const int src = !in ? lane : first ? lane + d : lane - d;
+  const bool in = i < 2 * d;
+  const int src = !in ? lane : i < d ? lane + d : lane - d;
   uint4 o;
   o.x = __shfl_sync(0xffffffffu, raw.x, src);
   o.y = __shfl_sync(0xffffffffu, raw.y, src);
@@ -168,10 +187,7 @@ __device__ __forceinline__ void rotate8(const Rotation& rot, const Angles& a, in
   float y[8];
   unpack8(o, f16, y);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float xc = __fmul_rn(x[k], a.c[k]), ys = __fmul_rn(y[k], a.s[k]);
-    x[k] = first ? __fsub_rn(xc, ys) : __fadd_rn(xc, ys);
-  }
+  for (int k = 0; k < 8; ++k) x[k] = __fadd_rn(__fmul_rn(x[k], a.c[k]), __fmul_rn(y[k], a.s[k]));
 }
 
 }  // namespace mlaq

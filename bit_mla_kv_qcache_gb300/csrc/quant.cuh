@@ -73,15 +73,35 @@ __device__ __forceinline__ QParams make_qparams(float lo, float hi, int L) {
   return q;
 }
 
-// quant_code for the common case in a few instructions: t = (x - m) / s from two rounded
-// operations and a rounded reciprocal is off by at most 16 * 3 * 2^-24 < 3e-6, so a t further
-// than 1e-4 from every midpoint has its nearest level already; the others (and NaN) are decided
-// against the exact midpoints. L = 15.
-__device__ __forceinline__ int quant_code4(float x, const QParams& q) {
-  const float t = __fmul_rn(__fsub_rn(x, q.m), q.inv_s);
-  const float k = rintf(t);
-  if (fabsf(__fsub_rn(t, k)) <= 0.4999f) return static_cast<int>(fminf(fmaxf(k, 0.f), 15.f));
-  return quant_code(x, q.m, q.s, q.inv_s, 15);
+// make_qparams for 15 steps without a division: the smallest FP16 scale with min + 15 * scale >= hi. A
+// first candidate from a rounded-up reciprocal is that scale or the next FP16 above it; 15 times the one
+// below is exact in float32, and reaches the exact hi - m where it reaches that difference rounded up.
+__device__ __forceinline__ QParams make_qparams15(float lo, float hi) {
+  QParams q;
+  q.flags = 0;
+  float m = __half2float(__float2half_rd(lo));
+  if (isinf(m)) {
+    q.flags |= kErrRange;
+    m = -65504.f;
+  }
+  const float d = __fsub_ru(hi, m);
+  const __half top = __float2half_ru(__fmul_ru(d, 0.06666667f));  // >= 1 / 15
+  const uint16_t bits = __half_as_ushort(top);
+  const float below = __half2float(__ushort_as_half(static_cast<uint16_t>(bits ? bits - 1 : 0)));
+  float s = bits && __fmul_rn(below, 15.f) >= d ? below : __half2float(top);
+  if (isinf(s) || hi > 65504.f) {
+    q.flags |= kErrRange;
+    s = 65504.f;
+  }
+  q.m = m;
+  q.s = s;
+  q.inv_s = s > 0.f ? __frcp_rn(s) : 0.f;
+  uint32_t mb = __half_as_ushort(__float2half_rn(m));  // m, s are FP16 values: exact
+  uint32_t sb = __half_as_ushort(__float2half_rn(s));
+  if ((mb & 0x7fffu) == 0) mb = 0;  // zero is stored as +0
+  if ((sb & 0x7fffu) == 0) sb = 0;
+  q.meta = sb | (mb << 16);
+  return q;
 }
 
 }  // namespace mlaq
