@@ -97,7 +97,7 @@ __device__ __forceinline__ QParams quantize8(const float (&x)[8], uint32_t& word
 }
 
 template <int D, int NG, bool F16, int kThreads>
-__global__ void __launch_bounds__(kThreads, 768 / kThreads) kv4_append_kernel(const Kv4AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) kv4_append_kernel(const Kv4AppendParams p) {
   constexpr int kLanes = D / 8;                 // threads of one head
   constexpr int kSlots = kThreads / kLanes;     // heads at a time
   constexpr int kGroupLanes = kLanes / NG;

@@ -1,9 +1,10 @@
 // Append of new latent rows to the paged BF16 cache (the one the unquantized decode reads): RMS
 // norm of the latent, rotation of the positional key and of the queries' positional part.
 //
-// CTA r serves row r. Warp 0 normalizes the latent (sixteen channels per lane, sum of squares in
-// float32 over the warp); the other warps rotate the positional key and the queries, eight lanes
-// per head of 64 channels. Bound: the bytes of the rows, read and written once.
+// With few rows a CTA of four warps serves one: warp 0 normalizes the latent (sixteen channels per lane,
+// sum of squares in float32 over the warp), the others rotate the positional key and the queries, eight
+// lanes per head of 64 channels. With many, each warp serves a row of its own, which is placed once and
+// whose angles are read once. Bound: the bytes of the rows, read and written once.
 #include "append.cuh"
 
 namespace mlaq {
@@ -11,29 +12,48 @@ namespace {
 
 constexpr int kLatThreads = 128;
 
-__global__ void __launch_bounds__(kLatThreads) latent_append_kernel(const LatentAppendParams p) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int r = blockIdx.x;
-  if (r >= p.n_rows) {  // the blocks behind the rows: the new lengths
-    const int b = (r - p.n_rows) * kLatThreads + tid;
+// kWarps: warps of one row, 1 or 4.
+template <int kWarps>
+__global__ void __launch_bounds__(kLatThreads, 8) latent_append_kernel(const LatentAppendParams p, const int row_ctas) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (static_cast<int>(blockIdx.x) >= row_ctas) {  // the blocks behind the rows: the new lengths
+    const int b = (blockIdx.x - row_ctas) * kLatThreads + tid;
     if (b < p.B) p.seq_next[b] = __ldg(p.seq_lens + b) + __ldg(p.cu_new + b + 1) - __ldg(p.cu_new + b);
     return;
   }
+  const int r = kWarps == 4 ? blockIdx.x : blockIdx.x * 4 + (tid >> 5), sub = kWarps == 4 ? tid >> 5 : 0;
+  if (r >= p.n_rows) return;
   const uint16_t* row = p.kv.data + r * p.kv.row_stride;
-  const int n_pos = p.rot.rot_dim ? p.rot.n_pos : 0x7fffffff;
-  if (warp == 0) {
-    uint4 w[2], g[2];
+  const bool latent = sub == 0, turns = kWarps == 1 || sub > 0;
+  // the first loads are on their way while the row's place is found
+  uint4 w[2];
+  if (latent) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {  // on their way while the row's place is found
-      w[k] = __ldg(reinterpret_cast<const uint4*>(row) + lane + 32 * k);
-      g[k] = p.weight ? __ldg(reinterpret_cast<const uint4*>(p.weight) + lane + 32 * k) : make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < 2; ++k) w[k] = __ldg(reinterpret_cast<const uint4*>(row) + lane + 32 * k);
+  }
+  constexpr int kSlots = kWarps == 4 ? 12 : 4, kLoads = kWarps == 4 ? 2 : 5;  // heads at a time; of those, asked for at once
+  const int i = lane & 7, slot = (kWarps == 4 ? 4 * (sub - 1) : 0) + (lane >> 3);
+  const int heads = 1 + (p.q.data ? p.H : 0);  // the positional key, then the queries
+  uint4 raw[kLoads];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int h = h0 + u * kSlots + slot;
+      raw[u] = make_uint4(0, 0, 0, 0);
+      if (turns && h < heads)
+        raw[u] = __ldg(reinterpret_cast<const uint4*>(
+                           h == 0 ? row + kLatent : p.q.data + r * p.q.row_stride + (h - 1) * p.q.head_stride) + i);
     }
-    const RowPlace at = place_row(p.cu_new, p.seq_lens, p.page_table, p.B, r, p.max_new, p.max_pages, p.p_shift, p.n_pages,
-                                  p.pool != nullptr, n_pos);
-    if (at.t < 0) {
-      if (lane == 0 && at.flags) atomicOr(p.err, at.flags);
-      return;
-    }
+  };
+  load(0);
+  const RowPlace at = place_row(p.cu_new, p.seq_lens, p.page_table, p.B, r, p.max_new, p.max_pages, p.p_shift, p.n_pages,
+                                p.pool != nullptr, p.rot.rot_dim ? p.rot.n_pos : 0x7fffffff);
+  if (at.t < 0) {
+    if (latent && lane == 0 && at.flags) atomicOr(p.err, at.flags);
+    return;
+  }
+  uint16_t* const dst = p.pool ? p.pool + (static_cast<size_t>(at.pid) * p.P + at.tp) * kRow : nullptr;
+  if (latent) {
     if (p.weight) {
       float x[2][8], ss = 0.f;
 #pragma unroll
@@ -47,39 +67,20 @@ __global__ void __launch_bounds__(kLatThreads) latent_append_kernel(const Latent
       const float inv = 1.f / sqrtf(ss * (1.f / kLatent) + p.eps);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float y[8];
-        unpack8(g[k], false, y);
+        float g[8];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(p.weight) + lane + 32 * k), false, g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[k][j] = x[k][j] * inv * y[j];
+        for (int j = 0; j < 8; ++j) x[k][j] = x[k][j] * inv * g[j];
         w[k] = pack8(x[k], false);
       }
     }
-    uint16_t* dst = p.pool ? p.pool + (static_cast<size_t>(at.pid) * p.P + at.tp) * kRow : nullptr;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (dst) reinterpret_cast<uint4*>(dst)[lane + 32 * k] = w[k];
       if (p.c_out) reinterpret_cast<uint4*>(p.c_out + static_cast<size_t>(r) * kLatent)[lane + 32 * k] = w[k];
     }
-    return;
   }
-  constexpr int kSlots = (kLatThreads - 32) / 8, kLoads = 4;
-  const int i = tid & 7, slot = (tid - 32) / 8;
-  const int heads = 1 + (p.q.data ? p.H : 0);  // the positional key, then the queries
-  uint4 raw[kLoads];
-  auto load = [&](int h0) {
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-      const int h = h0 + u * kSlots + slot;
-      raw[u] = make_uint4(0, 0, 0, 0);
-      if (h < heads)
-        raw[u] = __ldg(reinterpret_cast<const uint4*>(
-                           h == 0 ? row + kLatent : p.q.data + r * p.q.row_stride + (h - 1) * p.q.head_stride) + i);
-    }
-  };
-  load(0);
-  const RowPlace at = place_row(p.cu_new, p.seq_lens, p.page_table, p.B, r, p.max_new, p.max_pages, p.p_shift, p.n_pages,
-                                p.pool != nullptr, n_pos);
-  if (at.t < 0) return;  // warp 0 reports it
+  if (!turns) return;
   const Angles ang = load_angles(p.rot, at.t, i);
   for (int h0 = 0; h0 < heads; h0 += kLoads * kSlots) {
     if (h0 > 0) load(h0);
@@ -91,8 +92,7 @@ __global__ void __launch_bounds__(kLatThreads) latent_append_kernel(const Latent
       rotate8(p.rot, ang, i, raw[u], false, x);
       const uint4 y = pack8(x, false);
       if (h == 0) {
-        if (p.pool)
-          reinterpret_cast<uint4*>(p.pool + (static_cast<size_t>(at.pid) * p.P + at.tp) * kRow + kLatent)[i] = y;
+        if (dst) reinterpret_cast<uint4*>(dst + kLatent)[i] = y;
         if (p.kr_out) reinterpret_cast<uint4*>(p.kr_out + static_cast<size_t>(r) * kRope)[i] = y;
       } else if (h < heads) {
         reinterpret_cast<uint4*>(p.q_out + (static_cast<size_t>(r) * p.H + h - 1) * kRope)[i] = y;
@@ -105,7 +105,12 @@ __global__ void __launch_bounds__(kLatThreads) latent_append_kernel(const Latent
 
 cudaError_t launch_latent_append(const LatentAppendParams& p, cudaStream_t stream) {
   const int tail = p.seq_next ? (p.B + kLatThreads - 1) / kLatThreads : 0;
-  latent_append_kernel<<<p.n_rows + tail, kLatThreads, 0, stream>>>(p);
+  if (p.n_rows < 2048) {  // below, a warp to a row would leave SMs idle
+    latent_append_kernel<4><<<p.n_rows + tail, kLatThreads, 0, stream>>>(p, p.n_rows);
+  } else {
+    const int ctas = (p.n_rows + 3) / 4;
+    latent_append_kernel<1><<<ctas + tail, kLatThreads, 0, stream>>>(p, ctas);
+  }
   return cudaGetLastError();
 }
 
