@@ -5,7 +5,7 @@
 // neighbouring lanes. Rotation partners and group statistics are lane shuffles, a key-code word is
 // one thread's eight channels, and a value-code word is a column of the 8 x 8 matrix of codes that
 // eight lanes hold (transposed by three rounds of exchanges). CTA r serves row r: its threads
-// cover 1024 / D or 2048 / D heads at a time and keep the row's angles in registers over all heads. Bound:
+// cover 512 / D or 2048 / D heads at a time and keep the row's angles in registers over all heads. Bound:
 // the bytes of the rows, read and written once.
 #include "append.cuh"
 #include "quant.cuh"
@@ -186,13 +186,13 @@ cudaError_t launch_as(const Kv4AppendParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// Few rows (decode steps): 256 threads to a row, for its latency. Many: 128, which place the row and
+// Few rows (decode steps): 256 threads to a row, for its latency. Many: 64, which place the row and
 // read its angles half as often.
 template <int D, int NG>
 cudaError_t launch(const Kv4AppendParams& p, cudaStream_t stream) {
   const bool few = p.n_rows <= 512;
-  if (p.f16) return few ? launch_as<D, NG, true, 256>(p, stream) : launch_as<D, NG, true, 128>(p, stream);
-  return few ? launch_as<D, NG, false, 256>(p, stream) : launch_as<D, NG, false, 128>(p, stream);
+  if (p.f16) return few ? launch_as<D, NG, true, 256>(p, stream) : launch_as<D, NG, true, 64>(p, stream);
+  return few ? launch_as<D, NG, false, 256>(p, stream) : launch_as<D, NG, false, 64>(p, stream);
 }
 
 }  // namespace

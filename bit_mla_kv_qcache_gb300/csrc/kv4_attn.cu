@@ -280,70 +280,57 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
   __shared__ float s_m[kWarps][R], s_l[kWarps][R];
   __shared__ float s_f[kMaxParts + 1][R];  // weights of the parts of a cut item; then the rows' (M, L)
   __shared__ float s_ml[R][2];
-  __shared__ int s_last;
+  constexpr int kHeld = 256;  // sequences that the quick way of sharing the work takes
+  __shared__ int s_last, s_steps[kHeld], s_items[kHeld];  // of each sequence: steps of an item, items
   __shared__ Place s_at;
   __shared__ int s_full[kWarps][3];  // steps that every row sees whole: from, to; tokens seen by any
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
   int flags = 0;
 
-  // ---- which part of which item: every warp works it out by itself (no barrier), lane i for
-  // sequences [i c, (i + 1) c)
+  // ---- which part of which item. Thread b looks at sequence b; then every warp works the rest out by
+  // itself, lane i for sequences [i c, (i + 1) c). (Loops stay rolled: this code runs once, from cold
+  // instruction caches.)
   {
-    constexpr int kHeld = 8;  // sequences that a lane holds in registers
     const int chunk = (p.B + 31) / 32, first = lane * chunk, n_ctas = static_cast<int>(gridDim.x);
-    int tb[kHeld], ib[kHeld];  // steps of an item, items
-    long long steps = 0, items = 0;
-    int most = 0;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      tb[i] = 1, ib[i] = 0;
-      if (i < chunk && first + i < p.B) {
-        int T, n, r0, blocks;
-        sequence<R>(p, first + i, T, n, r0, tb[i], blocks, flags);
-        ib[i] = blocks * p.Hkv;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      steps += static_cast<long long>(tb[i]) * ib[i];
-      items += ib[i];
-      if (ib[i] > 0) most = max(most, tb[i]);
-    }
-    for (int b = first + kHeld; b < min(p.B, first + chunk); ++b) {
-      int T, n, r0, tiles, blocks;
-      sequence<R>(p, b, T, n, r0, tiles, blocks, flags);
-      steps += static_cast<long long>(tiles) * blocks * p.Hkv;
-      items += static_cast<long long>(blocks) * p.Hkv;
-      if (blocks > 0) most = max(most, tiles);
-    }
-    if (blockIdx.x == 0 && warp == 0) {
-      const int f = __reduce_or_sync(0xffffffffu, flags);
-      if (lane == 0 && f) atomicOr(p.err, f);
-    }
-    flags = 0;
-    most = __reduce_max_sync(0xffffffffu, most);
-    long long before = steps;  // of the lanes up to this one
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += y;
-      items += __shfl_xor_sync(0xffffffffu, items, o);
-    }
-    const long long total = __shfl_sync(0xffffffffu, before, 31);
-    before -= steps;
-    const int least = max(min(Ge::kMinSteps, most), (most + kMaxParts - 2) / (kMaxParts - 1));
-    const long long base = total < 0x7fffffff ? (static_cast<uint32_t>(total) + n_ctas - 1) / n_ctas : (total + n_ctas - 1) / n_ctas;
+    const int last = min(p.B, first + chunk);
     int share = 0, mine = 0;  // parts of the lane's items
-    if (items <= n_ctas && chunk <= kHeld) {
-      constexpr int kTry = 8;
-      constexpr int kSixteenths[kTry] = {16, 17, 18, 20, 22, 25, 28, 32};
-      for (int k = 0; k < kTry && share == 0; ++k) {
-        const int s = max(least, static_cast<int>((base * kSixteenths[k] + 15) / 16));
-        mine = 0;
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i)
-          if (i < chunk) mine += ib[i] * ((tb[i] + s - 1) / s);
-        if (__reduce_add_sync(0xffffffffu, mine) <= n_ctas) share = s;
+    bool small = p.B <= kHeld;
+    if (small) {
+      for (int b = tid; b < p.B; b += kThreads) {
+        int T, n, r0, tiles, blocks;
+        sequence<R>(p, b, T, n, r0, tiles, blocks, flags);
+        s_steps[b] = tiles;
+        s_items[b] = blocks * p.Hkv;
+      }
+      if (blockIdx.x == 0) {
+        const int f = __reduce_or_sync(0xffffffffu, flags);
+        if (lane == 0 && f) atomicOr(p.err, f);
+      }
+      flags = 0;
+      __syncthreads();
+      float steps = 0.f;
+      int items = 0, most = 0;
+#pragma unroll 1
+      for (int b = first; b < last; ++b) {
+        steps += static_cast<float>(s_steps[b]) * static_cast<float>(s_items[b]);
+        items = min(items + s_items[b], 1 << 20);
+        if (s_items[b] > 0) most = max(most, s_steps[b]);
+      }
+      items = __reduce_add_sync(0xffffffffu, items);
+      small = items <= n_ctas && __all_sync(0xffffffffu, steps < 3e7f);  // 32 lanes: below 2^30
+      if (small) {
+        const int total = __reduce_add_sync(0xffffffffu, static_cast<int>(steps)), top = __reduce_max_sync(0xffffffffu, most);
+        const int least = max(min(Ge::kMinSteps, top), (top + kMaxParts - 2) / (kMaxParts - 1));
+        const float base = static_cast<float>(total) / static_cast<float>(n_ctas);
+        float times = 1.f;
+#pragma unroll 1
+        for (int k = 0; k < 9 && share == 0; ++k, times *= 1.08f) {  // up to about twice
+          const int s = max(least, static_cast<int>(base * times) + 1);
+          mine = 0;
+#pragma unroll 1
+          for (int b = first; b < last; ++b) mine += s_items[b] * ((s_steps[b] + s - 1) / s);
+          if (__reduce_add_sync(0xffffffffu, mine) <= n_ctas) share = s;
+        }
       }
     }
     if (share > 0) {
@@ -358,23 +345,48 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
       if (x >= upto - mine && x < upto) {  // one lane; every warp stores the same
         Place s{};
         int r = x - (upto - mine), ignore = 0;
-        for (s.b = first;; ++s.b) {
-          sequence<R>(p, s.b, s.T, s.n, s.r0, s.tiles, s.blocks, ignore);
-          s.parts = (s.tiles + share - 1) / share;
-          const int w = s.blocks * p.Hkv * s.parts;
-          if (r < w || s.b + 1 >= p.B) break;
+#pragma unroll 1
+        for (s.b = first; s.b + 1 < last; ++s.b) {
+          const int w = s_items[s.b] * ((s_steps[s.b] + share - 1) / share);
+          if (r < w) break;
           r -= w;
         }
-        const int item = s.blocks > 0 ? r / s.parts % (s.blocks * p.Hkv) : 0, part = r % s.parts;
-        s.h = s.blocks > 0 ? item / s.blocks : 0;
-        s.rb = s.blocks > 0 ? item % s.blocks : 0;
-        s.a0 = static_cast<int>(static_cast<long long>(s.tiles) * part / s.parts);
-        s.a1 = static_cast<int>(static_cast<long long>(s.tiles) * (part + 1) / s.parts);
+        sequence<R>(p, s.b, s.T, s.n, s.r0, s.tiles, s.blocks, ignore);
+        s.tiles = s_steps[s.b];
+        s.parts = (s.tiles + share - 1) / share;
+        const uint32_t part = r % s.parts;
+        const int item = min(r / s.parts, max(1, s.blocks * p.Hkv) - 1);  // (lengths may change under the call)
+        s.h = s.blocks > 1 ? item / s.blocks : item;
+        s.rb = s.blocks > 1 ? item - s.h * s.blocks : 0;
+        s.a0 = static_cast<uint32_t>(s.tiles) * part / s.parts;  // steps < 2^25, parts <= 64
+        s.a1 = static_cast<uint32_t>(s.tiles) * (part + 1) / s.parts;
         s.c0 = x - part;  // at = end: not on the line
         s_at = s;
       }
     } else {
-      const long long stretch = max(base, static_cast<long long>(least));
+      long long steps = 0;
+      int most = 0;
+      for (int b = first; b < last; ++b) {
+        int T, n, r0, tiles, blocks;
+        sequence<R>(p, b, T, n, r0, tiles, blocks, flags);
+        steps += static_cast<long long>(tiles) * blocks * p.Hkv;
+        if (blocks > 0) most = max(most, tiles);
+      }
+      if (blockIdx.x == 0 && warp == 0) {
+        const int f = __reduce_or_sync(0xffffffffu, flags);
+        if (lane == 0 && f) atomicOr(p.err, f);
+      }
+      flags = 0;
+      const int top = __reduce_max_sync(0xffffffffu, most);
+      long long before = steps;  // of the lanes up to this one
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+      }
+      const long long total = __shfl_sync(0xffffffffu, before, 31);
+      before -= steps;
+      const long long stretch = max((total + n_ctas - 1) / n_ctas, static_cast<long long>(max(min(Ge::kMinSteps, top), (top + kMaxParts - 2) / (kMaxParts - 1))));
       const long long x = stretch * blockIdx.x;
       if (x >= total) return;
       if (x >= before && x < before + steps) {  // one lane; every warp stores the same
