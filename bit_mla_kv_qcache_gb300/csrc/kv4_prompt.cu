@@ -13,11 +13,12 @@
 //                and O rescaled in place, only when a score exceeds it by more than 2^8.
 // The softmax groups take the registers that the others give up (setmaxnreg), so every role has its own
 // loop over the CTA's work.
-// The groups alternate so that the tensor cores work for one while the other takes its softmax:
-// with more than 128 rows they hold two tiles of queries and see every token tile, with at most 128
-// they hold the same queries, take the even and the odd token tiles and join at the end.
-// Tensor memory: S0, S1 (128 columns each), O0, O1 (D each). A step's S overwrites the P of the same
-// group two steps before; products of one thread run in the order of their issue.
+// The groups alternate so that the tensor cores work for one while the other takes its softmax: with
+// more than 128 rows they hold two tiles of queries and see every token tile. With at most 128 rows one
+// group takes the softmax of every token tile and the other unpacks the values, while warps 8-11 unpack
+// the keys (unpacking is what a tile then waits for).
+// Tensor memory: S0, S1 (128 columns each), O0, O1 (D each). A step's S overwrites the P of two steps
+// before; products of one thread run in the order of their issue.
 //
 // Channels keep the order in which a code word unpacks: eight channels of a word in the order 0 4 1 5
 // 2 6 3 7, for keys matched by the queries, for values undone when a row is stored.
@@ -28,8 +29,8 @@
 // group against the sum of the group's queries, in two FP16 parts. One stage of keys then has the room.
 //
 // Work: with many items (sequence, kv head, row block) one CTA per item, those that see the most
-// tokens first; with few, the items' token tiles are laid on one line and cut evenly over the SMs
-// (as in the kernel for few rows).
+// tokens first; with few, they are cut so that every SM has one part of one item, or, where the parts do
+// not fit, laid on one line and cut evenly (as in the kernel for few rows).
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -97,7 +98,7 @@ __device__ __forceinline__ void add_pair(float& a, float& b, float x, float y) {
       : "f"(x), "f"(y));
 }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-__device__ __forceinline__ void softmax_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void softmax_barrier(int threads) { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); }
 
 // The two codes at bits 0-3 (kHigh: 4-7) of the halves of w as min + code * scale: 1024 + n (1024 + 16 n)
 // is put together by bits, n comes out exactly, then one rounding.
@@ -192,8 +193,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   __shared__ Seg s_seg;
   __shared__ long long s_part[kThreads / 32];
   __shared__ int s_most[kThreads / 32], s_last;
+  constexpr int kTry = 9;
+  __shared__ int s_count[kTry];  // parts that a share would make
   __shared__ volatile int s_abort, s_any_hidden;
-  __shared__ float s_ml[128][2];
   __shared__ __align__(16) uint32_t s_hidden[4][4];  // tokens of a tile (modulo four) whose page id is bad
   uint64_t *const k_full = bars, *const k_free = bars + 2, *const v_full = bars + 4, *const v_free = bars + 6,
            *const s_full = bars + 8, *const p_ready = bars + 10, *const o_done = bars + 12;
@@ -241,29 +243,58 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       x = static_cast<long long>(t) * p.Hkv;
     }
     const int warp_most = __reduce_max_sync(0xffffffffu, t);
+    auto scan = [&](long long v) {  // inclusive, over the block
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) s_part[warp] = x, s_most[warp] = warp_most;
-    __syncthreads();
-    int most = 0;
-    for (int w = 0; w < kThreads / 32; ++w) most = max(most, s_most[w]);
-    for (int w = 0; w < warp; ++w) x += s_part[w];
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      if (lane == 31) s_part[warp] = v;
+      __syncthreads();
+#pragma unroll 1
+      for (int w = 0; w < warp; ++w) v += s_part[w];
+      return v;
+    };
+    if (lane == 0) s_most[warp] = warp_most;
+    if (tid < kTry) s_count[tid] = 0;
+    x = scan(x);
     s_sum[tid + 1] = x;
     if (tid == 0) s_sum[0] = 0;
     __syncthreads();
+    int most = 0;
+#pragma unroll 1
+    for (int w = 0; w < kThreads / 32; ++w) most = max(most, s_most[w]);
+    const long long total = s_sum[kThreads];
+    const int least = max(min(4, most), (most + kMaxParts - 2) / (kMaxParts - 1));
+    // shares for which every part could have a CTA of its own: the smallest of a few multiples of the mean
+    const float mean = static_cast<float>(total) / static_cast<float>(gridDim.x);
+    auto share_of = [&](int k) { return max(least, static_cast<int>(mean * (1.f + 0.12f * k)) + 1); };
+    const bool small = total < (1 << 24);
+#pragma unroll 1
+    for (int k = 0; k < kTry; ++k) {
+      const int sh = share_of(k), parts = __reduce_add_sync(0xffffffffu, small ? p.Hkv * ((t + sh - 1) / sh) : 1 << 20);
+      if (lane == 0) atomicAdd(&s_count[k], parts);
+    }
+    __syncthreads();
+    int share = 0;
+#pragma unroll 1
+    for (int k = 0; k < kTry && share == 0; ++k)
+      if (s_count[k] <= static_cast<int>(gridDim.x)) share = share_of(k);
+    if (share > 0) {  // the parts before each pair
+      x = scan(p.Hkv * ((t + share - 1) / share));
+      __syncthreads();
+      s_sum[tid + 1] = x;
+      __syncthreads();
+    }
     if (tid == 0) {
       Seg& s = s_seg;
-      const long long total = s_sum[kThreads];
-      s.share = max((total + gridDim.x - 1) / gridDim.x,
-                    static_cast<long long>(max(min(4, most), (most + kMaxParts - 2) / (kMaxParts - 1))));
+      s.share = share > 0 ? 1 : max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(least));
       s.at = s.share * blockIdx.x;
-      s.end = min(total, s.at + s.share);
+      s.end = min(s_sum[kThreads], s.at + s.share);
       s.valid = 0;
       if (s.at < s.end) {
         int lo = 0, hi = kThreads - 1;  // s_sum[lo] <= at < s_sum[lo + 1]
+#pragma unroll 1
         while (lo < hi) {
           const int mid = (lo + hi) >> 1;
           if (s_sum[mid + 1] > s.at) hi = mid;
@@ -275,10 +306,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         s.rb = lo - s.b * blocks_most;
         load_sequence(p, s.b, s.T, s.n, s.r0, f);
         if (s.rb < row_blocks(p, s.n, R)) {  // else the lengths changed under the call
-          const int tiles = block_tiles(p, s.T, s.n, s.rb, R).y;
-          s.h = min(static_cast<int>((s.at - s_sum[lo]) / tiles), p.Hkv - 1);
-          s.item0 = s_sum[lo] + static_cast<long long>(s.h) * tiles;
-          line_segment(p, s, R);
+          const int2 tiles = block_tiles(p, s.T, s.n, s.rb, R);
+          const int at = static_cast<int>(s.at - s_sum[lo]);
+          if (share > 0) {
+            const int parts = (tiles.y + share - 1) / share, part = at % parts;
+            s.h = min(at / parts, p.Hkv - 1);
+            s.tile = tiles.x + tiles.y * part / parts;
+            s.tiles = tiles.x + tiles.y * (part + 1) / parts - s.tile;
+            s.parts = parts;
+            s.c0 = static_cast<int>(blockIdx.x) - part;
+            s.part = parts == 1 ? -1 : 2 * static_cast<int>(blockIdx.x) + (part == 0 ? 1 : 0);
+            s.valid = 1;
+            s.item0 = s.end = s.at;  // and nothing after it
+            s.item_tiles = tiles.y;
+          } else {
+            s.h = min(at / tiles.y, p.Hkv - 1);
+            s.item0 = s_sum[lo] + static_cast<long long>(s.h) * tiles.y;
+            line_segment(p, s, R);
+          }
         }
       }
     }
@@ -309,7 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   tc5::fence_after();
   const uint32_t tmem = s_tmem;
 
-  // A wait that runs out raises the abort flag, which ends every other wait too.
+  // A wait that runs out raises the abort flag, which ends every other wait too. Threads go on all the
+  // same (on whatever is there, within their buffers) and leave their loop together, by the flag, which is
+  // looked at where it costs nothing; only the warp that issues products asks whether the wait was done.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
@@ -323,11 +370,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     }
     return true;
   };
+  auto all = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
   // Stages and barrier phases go on from segment to segment: token tiles and steps of the earlier ones.
   uint32_t tiles_done = 0, steps_done[2] = {0, 0}, segs = 0;
   const int group = warp >> 2;  // 0, 1: softmax; 2: unpacking; 3: products, prefetch
   const Seg& sg = s_seg;
-  auto steps_of = [&]() { return two ? 2 * sg.tiles : sg.tiles; };  // step s: group s & 1, token tile two ? s / 2 : s
+  auto steps_of = [&]() { return two ? 2 * sg.tiles : sg.tiles; };  // step s: S buffer s & 1, token tile two ? s / 2 : s
   // Two barriers of all warps frame a segment: queries in place; results stored and the next segment set.
   auto leave_segment = [&](int n_tiles, int steps) -> bool {
     __syncthreads();
@@ -339,10 +387,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   };
   constexpr bool one_k = kExact;  // one stage of keys
 
-  if (group == 2) {
+  if (group == 2 || (group == 1 && !two)) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
     // ---- unpacking: thread = token of the tile
     const int tok_row = tid & 127;
+    const bool keys = group == 2, vals = two || group == 1;
     int n_tiles, steps;
     do {
       n_tiles = sg.tiles, steps = steps_of();
@@ -382,8 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         bad = src == nullptr && id != -2;
         const int tp = (tile0 * kTok + tok_row) & (p.P - 1);
         load_nums(src ? src + p.P * D + tp * 8 * NG : nullptr);
-        load_codes(kw, src ? src + tp * (D / 2) : nullptr);
-        load_codes(vw, src ? src + p.P * (D / 2) + tp * (D / 2) : nullptr);
+        if (keys) load_codes(kw, src ? src + tp * (D / 2) : nullptr);
+        if (vals) load_codes(vw, src ? src + p.P * (D / 2) + tp * (D / 2) : nullptr);
       }
       id = page_of(1);
       __syncthreads();
@@ -397,69 +446,74 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         id = page_of(j + 2);
 #pragma unroll
         for (int g = 0; g < NG; ++g) cur[g] = num[g];
-        if (!wait(k_free + ks, kph ^ 1)) break;
-        const uint32_t kd = k_tiles + ks * Ge::kTile + 16 * tok_row;
-        __half2 s1[NG], s2[NG];
-        if constexpr (kExact) {  // a quarter of the scale (15 scales fit FP16) in seven bits and the rest; of the minimum
-          uint32_t more[4] = {0, 0, 0, 0};
+        if (keys) {
+          wait(k_free + ks, kph ^ 1);
+          const uint32_t kd = k_tiles + ks * Ge::kTile + 16 * tok_row;
+          __half2 s1[NG], s2[NG];
+          if constexpr (kExact) {  // a quarter of the scale (15 scales fit FP16) in seven bits and the rest; of the minimum
+            uint32_t more[4] = {0, 0, 0, 0};
 #pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            const __half2 s = __hmul2(__half2half2(scale_of(cur[g].x)), __float2half2_rn(0.25f));
-            const uint32_t top = *reinterpret_cast<const uint32_t*>(&s) & 0xFFF0FFF0u;
-            s1[g] = *reinterpret_cast<const __half2*>(&top);
-            s2[g] = __hsub2(s, s1[g]);
-            const __half2 mn = __hmul2(__half2half2(min_of(cur[g].x)), __float2half2_rn(0.25f));
-            more[g] = *reinterpret_cast<const uint32_t*>(&mn);
+            for (int g = 0; g < NG; ++g) {
+              const __half2 s = __hmul2(__half2half2(scale_of(cur[g].x)), __float2half2_rn(0.25f));
+              const uint32_t top = *reinterpret_cast<const uint32_t*>(&s) & 0xFFF0FFF0u;
+              s1[g] = *reinterpret_cast<const __half2*>(&top);
+              s2[g] = __hsub2(s, s1[g]);
+              const __half2 mn = __hmul2(__half2half2(min_of(cur[g].x)), __float2half2_rn(0.25f));
+              more[g] = *reinterpret_cast<const uint32_t*>(&mn);
+            }
+            st_shared_v4(base + Ge::more_k_at(two) + 16 * tok_row, more[0], more[1], more[2], more[3]);
           }
-          st_shared_v4(base + Ge::more_k_at(two) + 16 * tok_row, more[0], more[1], more[2], more[3]);
-        }
 #pragma unroll
-        for (int wi = 0; wi < D / 8; ++wi) {
-          const int g = (wi % KW) / (KW / NG);
-          const uint32_t nm = cur[g].x;
-          const uint32_t w = kw[wi], w8 = w >> 8;
-          if constexpr (kExact) {
-            uint32_t y[4], z[4];
-            codes2_times<false>(w, s1[g], s2[g], y[0], z[0]);
-            codes2_times<true>(w, s1[g], s2[g], y[1], z[1]);
-            codes2_times<false>(w8, s1[g], s2[g], y[2], z[2]);
-            codes2_times<true>(w8, s1[g], s2[g], y[3], z[3]);
-            st_shared_v4(kd + wi * 2048, y[0], y[1], y[2], y[3]);
-            st_shared_v4(kd + Ge::kTile + wi * 2048, z[0], z[1], z[2], z[3]);
-          } else {
-            const __half2 s = __half2half2(scale_of(nm)), mn = __half2half2(min_of(nm));
-            st_shared_v4(kd + wi * 2048, dequant2<false>(w, s, mn), dequant2<true>(w, s, mn), dequant2<false>(w8, s, mn),
-                         dequant2<true>(w8, s, mn));
+          for (int wi = 0; wi < D / 8; ++wi) {
+            const int g = (wi % KW) / (KW / NG);
+            const uint32_t nm = cur[g].x;
+            const uint32_t w = kw[wi], w8 = w >> 8;
+            if constexpr (kExact) {
+              uint32_t y[4], z[4];
+              codes2_times<false>(w, s1[g], s2[g], y[0], z[0]);
+              codes2_times<true>(w, s1[g], s2[g], y[1], z[1]);
+              codes2_times<false>(w8, s1[g], s2[g], y[2], z[2]);
+              codes2_times<true>(w8, s1[g], s2[g], y[3], z[3]);
+              st_shared_v4(kd + wi * 2048, y[0], y[1], y[2], y[3]);
+              st_shared_v4(kd + Ge::kTile + wi * 2048, z[0], z[1], z[2], z[3]);
+            } else {
+              const __half2 s = __half2half2(scale_of(nm)), mn = __half2half2(min_of(nm));
+              st_shared_v4(kd + wi * 2048, dequant2<false>(w, s, mn), dequant2<true>(w, s, mn), dequant2<false>(w8, s, mn),
+                           dequant2<true>(w8, s, mn));
+            }
           }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {  // the tile four back has had its softmax: its values were freed two tiles ago
-          s_hidden[J & 3][warp & 3] = hidden;
-          if (hidden) s_any_hidden = 1;
-          mbar_arrive(k_full + ks);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {  // the tile four back has had its softmax: its values were freed two tiles ago
+            s_hidden[J & 3][warp & 3] = hidden;
+            if (hidden) s_any_hidden = 1;
+            mbar_arrive(k_full + ks);
+          }
+          load_codes(kw, next ? next + tp * (D / 2) : nullptr);
         }
         load_nums(next ? next + p.P * D + tp * 8 * NG : nullptr);
-        load_codes(kw, next ? next + tp * (D / 2) : nullptr);
-        if (!wait(v_free + st, ph ^ 1)) break;
-        const uint32_t vd = v_tiles + st * Ge::kTile + 16 * tok_row;
+        if (vals) {
+          wait(v_free + st, ph ^ 1);
+          const uint32_t vd = v_tiles + st * Ge::kTile + 16 * tok_row;
 #pragma unroll
-        for (int wi = 0; wi < D / 8; ++wi) {  // pair i: channels 64 (wi % VW) + 16 i + {0, 8} + wi / VW
-          uint32_t y[4];
-          const uint32_t w = vw[wi], w8 = w >> 8;
+          for (int wi = 0; wi < D / 8; ++wi) {  // pair i: channels 64 (wi % VW) + 16 i + {0, 8} + wi / VW
+            uint32_t y[4];
+            const uint32_t w = vw[wi], w8 = w >> 8;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t nm = cur[(64 * (wi % VW) + 16 * i) / (D / NG)].y;
-            const __half2 s = __half2half2(scale_of(nm)), mn = __half2half2(min_of(nm));
-            const uint32_t src = i < 2 ? w : w8;
-            y[i] = (i & 1) ? dequant2<true>(src, s, mn) : dequant2<false>(src, s, mn);
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t nm = cur[(64 * (wi % VW) + 16 * i) / (D / NG)].y;
+              const __half2 s = __half2half2(scale_of(nm)), mn = __half2half2(min_of(nm));
+              const uint32_t src = i < 2 ? w : w8;
+              y[i] = (i & 1) ? dequant2<true>(src, s, mn) : dequant2<false>(src, s, mn);
+            }
+            st_shared_v4(vd + wi * 2048, y[0], y[1], y[2], y[3]);
           }
-          st_shared_v4(vd + wi * 2048, y[0], y[1], y[2], y[3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_full + st);
+          load_codes(vw, next ? next + p.P * (D / 2) + tp * (D / 2) : nullptr);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v_full + st);
-        load_codes(vw, next ? next + p.P * (D / 2) + tp * (D / 2) : nullptr);
+        if (s_abort) break;
       }
     } while (leave_segment(n_tiles, steps));
   } else if (group == 3) {
@@ -491,7 +545,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         for (int j = 0; j < n_tiles; ++j) {
           const uint32_t J = tiles_done + j;
           ask(j + kAhead);
-          if (!wait(v_full + (J & 1), (J >> 1) & 1)) break;
+          wait(v_full + (J & 1), (J >> 1) & 1);
+          if (s_abort) break;
         }
       } else {
         __syncthreads();
@@ -501,7 +556,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         constexpr uint32_t kDescS = tc5::instr_desc(kTok, false), kDescO = tc5::instr_desc(D, true);
         const uint32_t leader = tc5::elect_one();
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
         auto scores = [&](int s) -> bool {
           const int u = s & 1, j = two ? s >> 1 : s;
           const uint32_t J = tiles_done + j, st = one_k ? 0 : J & 1;
@@ -532,7 +586,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           const uint64_t va = tc5::smem_desc(v_tiles + st * Ge::kTile, 128, 2048);
 #pragma unroll
           for (int k = 0; k < kTok / 16; ++k)
-            tc5::mma_ts(tm + Ge::kColO + D * u, tm + Ge::kColS + 128 * u + 8 * k, va + 16 * k, kDescO, s >= 2 || k > 0, leader);
+            tc5::mma_ts(tm + Ge::kColO + (two ? D * u : 0), tm + Ge::kColS + 128 * u + 8 * k, va + 16 * k, kDescO,
+                        s >= (two ? 2 : 1) || k > 0, leader);
           if (!two || u == 1) tc5::commit(v_free + st, leader);
           if (s + 2 < steps) ok = scores(s + 2);
         }
@@ -548,7 +603,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int lane_row = tid & 127;
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t sc = tmem + lane_base + Ge::kColS + 128 * group, oc = tmem + lane_base + Ge::kColO + D * group;
+    const uint32_t oc = tmem + lane_base + Ge::kColO + D * group;
+    const int n_softmax = two ? 256 : 128;  // threads of the softmax groups
     int n_tiles, steps;
     do {
       n_tiles = sg.tiles, steps = steps_of();
@@ -639,10 +695,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       }
       __syncthreads();
       // ---- softmax: thread = row
-      const int mine = (steps - group + 1) >> 1;
-      for (int k = 0; k < mine; ++k) {
-        const int t = tile0 + (two ? k : 2 * k + group);
-        if (!wait(s_full + group, (steps_done[group] + k) & 1)) break;
+      for (int k = 0; k < n_tiles; ++k) {
+        const int t = tile0 + k, u = two ? group : k & 1;  // S buffer
+        const uint32_t sc = tmem + lane_base + Ge::kColS + 128 * u;
+        const uint32_t ph = two ? steps_done[group] + k : steps_done[u] + (k >> 1);
+        wait(s_full + u, ph & 1);
         tc5::fence_after();
         uint32_t raw[4][32];
 #pragma unroll
@@ -650,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc5::wait_ld(raw[c]);
         if (s_any_hidden) {  // some tile so far
-          const uint4 hid = *reinterpret_cast<const uint4*>(s_hidden[(tiles_done + (two ? k : 2 * k + group)) & 3]);
+          const uint4 hid = *reinterpret_cast<const uint4*>(s_hidden[(tiles_done + k) & 3]);
           const uint32_t bits[4] = {hid.x, hid.y, hid.z, hid.w};
 #pragma unroll
           for (int c = 0; c < 4; ++c)
@@ -681,6 +738,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             m = mn;
             l *= a;
             if (k > 0) {
+              if (!two) {  // the products of the tile before still add to O
+                const uint32_t J = tiles_done + k - 1;
+                wait(v_free + (J & 1), (J >> 1) & 1);
+                tc5::fence_after();
+              }
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
                 uint32_t v[16];
@@ -719,40 +781,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         tc5::wait_st();
         tc5::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_ready + group);
+        if (lane == 0) mbar_arrive(p_ready + u);
+        if (s_abort) break;
       }
-      const bool done = wait(o_done, segs & 1) && !s_abort;
+      const bool done = all(wait(o_done, segs & 1)) && !s_abort;
       tc5::fence_after();
 
-      // ---- results: thread = row; with one tile of queries the second group hands its sums over
-      // (tile region of the keys and values, column by column: distinct banks)
-      float* const xo = reinterpret_cast<float*>(smem + Ge::k_at(two));
-      if (!two) {
-        if (group == 1 && done) {
-          s_ml[lane_row][0] = m;
-          s_ml[lane_row][1] = l;
-          if (steps > 1) {
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t v[32];
-              tc5::ld32(oc + 32 * c, v);
-              tc5::wait_ld(v);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) xo[(32 * c + i) * 128 + lane_row] = __uint_as_float(v[i]);
-            }
-          }
-        }
-        softmax_barrier();
-      }
-      if (done && (group == 0 || two)) {
-        float f0 = 1.f, f1 = 0.f;
-        if (!two && steps > 1) {
-          const float m1 = s_ml[lane_row][0], l1 = s_ml[lane_row][1], M = fmaxf(m, m1);
-          f0 = ex2(m - M);
-          f1 = ex2(m1 - M);
-          m = M;
-          l = l * f0 + l1 * f1;
-        }
+      // ---- results: thread = row
+      if (done) {
         const float y = l == 0.f ? 0.f : 1.f / l;
         auto out_row = [&](int row_of_block) {
           const int q2 = sg.rb * R + row_of_block;
@@ -773,10 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             for (int i = 0; i < 8; ++i) {
               float x[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                x[k] = __uint_as_float(v[4 * i + k]) * f0;
-                if (!two && steps > 1) x[k] += f1 * xo[(32 * c + 4 * i + k) * 128 + lane_row];
-              }
+              for (int k = 0; k < 4; ++k) x[k] = __uint_as_float(v[4 * i + k]);
               *reinterpret_cast<float4*>(st + lane * kRow + 16 * ((8 * c + i) ^ (lane & 7))) = make_float4(x[0], x[1], x[2], x[3]);
             }
           }
@@ -797,11 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             tc5::wait_ld(v);
             float x[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]) * f0;
-            if (!two && steps > 1) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] += f1 * xo[(32 * c + i) * 128 + lane_row];
-            }
+            for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]);
             // column 8 wi + 2 i + e is channel 64 (wi % VW) + 16 i + 8 e + wi / VW: neighbouring channels are
             // columns VW * 8 apart, in the same 32
 #pragma unroll
@@ -832,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       }
       if (sg.part >= 0) {
         __threadfence();
-        softmax_barrier();
+        softmax_barrier(n_softmax);
         if (tid == 0) {
           const bool last = !s_abort && atomicAdd(p.arrive + sg.c0, 1u) == static_cast<uint32_t>(sg.parts - 1);
           s_last = last;
@@ -841,15 +870,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             __threadfence();
           }
         }
-        softmax_barrier();
+        softmax_barrier(n_softmax);
         if (s_last) {
           // this CTA came last: the item's parts in CTA order. First each row's weights of the parts (kept
           // where the queries were), a thread per row; then a thread per row and eight channels.
           const int rows = min(R, rows_left), parts = sg.parts;
           auto slot_of = [&](int i) { return static_cast<size_t>(2 * (sg.c0 + i) + (i == 0 ? 1 : 0)); };
           float* const wts = reinterpret_cast<float*>(smem);  // [parts][R], divided by the row's sum
-          if (tid < rows) {
-            const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + tid;
+          for (int mr = tid; mr < rows; mr += n_softmax) {
+            const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + mr;
             float M = kNoMax, L = 0.f;
 #pragma unroll 4
             for (int i = 0; i < parts; ++i) {
@@ -857,20 +886,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
               const float mn = fmaxf(M, x.x);
               L = L * ex2(M - mn) + x.y * ex2(x.x - mn);
               M = mn;
-              wts[i * R + tid] = x.x;
+              wts[i * R + mr] = x.x;
             }
             const float y = L == 0.f ? 0.f : 1.f / L;
-            for (int i = 0; i < parts; ++i) wts[i * R + tid] = ex2(wts[i * R + tid] - M) * y;
+            for (int i = 0; i < parts; ++i) wts[i * R + mr] = ex2(wts[i * R + mr] - M) * y;
             if (p.lse) {
-              const int q2 = sg.rb * R + tid;
+              const int q2 = sg.rb * R + mr;
               p.lse[static_cast<size_t>(sg.r0 + q2 / p.G) * p.Hq + sg.h * p.G + q2 % p.G] =
                   L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
             }
           }
-          softmax_barrier();
+          softmax_barrier(n_softmax);
           // chunk i of a row, channels 8 i .. 8 i + 7, comes from columns i, i + 8 VW, ..: lanes read along i
           constexpr int kChunks = D / 8;
-          for (int e = tid; e < rows * kChunks; e += 256) {
+          for (int e = tid; e < rows * kChunks; e += n_softmax) {
             const int r2 = e / kChunks, i2 = e % kChunks, q2 = sg.rb * R + r2;
             float x[8];
 #pragma unroll
@@ -888,7 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         }
       }
       tc5::fence_before();
-      softmax_barrier();
+      softmax_barrier(n_softmax);
       if (tid == 0) {  // the next segment of the CTA's stretch
         Seg& s = s_seg;
         s.valid = 0;
