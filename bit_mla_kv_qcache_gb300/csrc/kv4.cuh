@@ -83,7 +83,6 @@ cudaError_t launch_kv4_decode(const Kv4AttnParams& p, int D, int n_groups, int n
 // More rows than the decode kernel holds go to the fifth-generation tensor cores: 128 rows of
 // queries (or two tiles of 128), one CTA per item or, with few items, the items cut over the SMs.
 struct Kv4PromptPlan {
-  bool two;
   int line;      // 0: one CTA per item; else the row blocks of the longest sequence
   int rows;      // rows of one item
   int64_t ctas;

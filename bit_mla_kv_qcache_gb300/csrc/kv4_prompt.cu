@@ -32,6 +32,7 @@
 // tokens first; with few, they are cut so that every SM has one part of one item, or, where the parts do
 // not fit, laid on one line and cut evenly (as in the kernel for few rows).
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -45,7 +46,11 @@ namespace mlaq {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kRegsSoftmax = 184, kRegsUnpack = 96, kRegsIssue = 48;  // x 256, 128, 128 threads: all 64 K
+// registers by role; over the four groups of 128 threads they come to the 512 of the launch
+template <bool two>
+struct Regs {  // two: one group unpacks, else two groups do
+  static constexpr int softmax = 184, unpack = two ? 96 : 120, issue = two ? 48 : 88;
+};
 constexpr int kAhead = 3;         // tiles that warp 13 runs ahead
 constexpr int kTok = 128;         // tokens per tile
 constexpr int kMaxParts = 32;     // CTAs that one item is cut into, at most
@@ -55,7 +60,7 @@ constexpr long long kBudget = 4ll << 30;  // cycles of a wait before it is given
 
 // Shared memory in tiles of 128 x D FP16: queries (one or two tiles), keys (two stages, or two operands),
 // values (two stages); kExact: the sixteen further channels of each tile of queries, and of the keys.
-template <int D, bool kExact>
+template <int D, int NG, bool kExact>
 struct Geom {
   static constexpr int kTile = 128 * D * 2;
   static constexpr int kMore = kExact ? 128 * 16 * 2 : 0;
@@ -64,7 +69,10 @@ struct Geom {
   __host__ __device__ static constexpr int v_at(bool two) { return k_at(two) + 2 * kTile; }
   __host__ __device__ static constexpr int more_q_at(bool two) { return v_at(two) + 2 * kTile; }
   __host__ __device__ static constexpr int more_k_at(bool two) { return more_q_at(two) + (two ? 2 : 1) * kMore; }
-  __host__ __device__ static constexpr int smem(bool two) { return more_k_at(two) + kMore + 1024; }  // slack to align the start
+  __host__ __device__ static constexpr int ring_at(bool two) { return more_k_at(two) + kMore; }
+  // one tile of queries: codes and numbers of two token tiles as they lie in the pages (key codes, value codes, numbers)
+  static constexpr int kCodes = kTok * D / 2, kStage = 2 * kCodes + kTok * 8 * NG;
+  __host__ __device__ static constexpr int smem(bool two) { return ring_at(two) + (two ? 0 : 2 * kStage) + 1024; }  // slack to align the start
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -74,6 +82,12 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ld_shared_v2(uint32_t addr, uint32_t& a, uint32_t& b) {
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ uint32_t h2(float a, float b) {
   const __half2 v = __floats2half2_rn(a, b);
@@ -97,7 +111,9 @@ __device__ __forceinline__ void add_pair(float& a, float& b, float x, float y) {
       : "+f"(a), "+f"(b)
       : "f"(x), "f"(y));
 }
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+__device__ __forceinline__ void bulk_prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void softmax_barrier(int threads) { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); }
 
 // The two codes at bits 0-3 (kHigh: 4-7) of the halves of w as min + code * scale: 1024 + n (1024 + 16 n)
@@ -183,27 +199,30 @@ __device__ __forceinline__ void line_segment(const Kv4AttnParams& p, Seg& s, int
   s.valid = 1;
 }
 
-template <int D, int NG, bool kExact>
-__global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnParams p, const int two, const int line) {
-  using Ge = Geom<D, kExact>;
+template <int D, int NG, bool kExact, bool two>
+__global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnParams p, const int rows, const int line) {
+  using Ge = Geom<D, NG, kExact>;
   constexpr int KW = D / 32, VW = D / 64, CB = D / 8;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t bars[13];  // k_full[2] k_free[2] v_full[2] v_free[2] s_full[2] p_ready[2] o_done
+  __shared__ uint64_t bars[17];  // k_full[2] k_free[2] v_full[2] v_free[2] s_full[2] p_ready[2] o_done c_full[2] c_free[2]
   __shared__ uint32_t s_tmem;
   __shared__ Seg s_seg;
   __shared__ long long s_part[kThreads / 32];
   __shared__ int s_most[kThreads / 32], s_last;
+  __shared__ float2 s_side[kTok];  // max and sum of a row under half of the tokens
   constexpr int kTry = 9;
   __shared__ int s_count[kTry];  // parts that a share would make
   __shared__ volatile int s_abort, s_any_hidden;
+  __shared__ uint32_t s_bad_pages[2];  // of a stage of codes: bit i, its i-th page
   __shared__ __align__(16) uint32_t s_hidden[4][4];  // tokens of a tile (modulo four) whose page id is bad
   uint64_t *const k_full = bars, *const k_free = bars + 2, *const v_full = bars + 4, *const v_free = bars + 6,
-           *const s_full = bars + 8, *const p_ready = bars + 10, *const o_done = bars + 12;
+           *const s_full = bars + 8, *const p_ready = bars + 10, *const o_done = bars + 12, *const c_full = bars + 13, *const c_free = bars + 15;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (base - smem_addr(smem_raw));
   long long* const s_sum = reinterpret_cast<long long*>(smem);  // tiles before each pair, until the first queries come
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int R = two ? 256 : 128;
+  const int R = two ? 256 : rows;
+  const bool half = R == 64;
   const uint32_t k_tiles = base + Ge::k_at(two), v_tiles = base + Ge::v_at(two);
   int flags = 0;
 
@@ -338,6 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       mbar_init(k_free + i, 1);
       mbar_init(v_free + i, 1);
       mbar_init(s_full + i, 1);
+      mbar_init(c_full + i, 1);
+      mbar_init(c_free + i, 8);
     }
     mbar_init(o_done, 1);
     fence_mbar_init();
@@ -388,15 +409,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   constexpr bool one_k = kExact;  // one stage of keys
 
   if (group == 2 || (group == 1 && !two)) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<two>::unpack));
     // ---- unpacking: thread = token of the tile
     const int tok_row = tid & 127;
     const bool keys = group == 2, vals = two || group == 1;
+    const uint32_t page_sh = min(p.p_shift, 7);
+    constexpr int CH = D / 32;  // 16-byte chunks of a token's codes
+    const int rot = two ? 0 : tok_row / (4 / CH * 2);  // lanes take chunks from shared memory in turned orders: distinct banks
     int n_tiles, steps;
     do {
       n_tiles = sg.tiles, steps = steps_of();
       const int tile0 = sg.tile;
       const int t_end = visible(p, sg.T, sg.n, min(sg.n - 1, (sg.rb * R + R - 1) / p.G)).y;
+      auto scale_of = [](uint32_t w) { return __ushort_as_half(static_cast<unsigned short>(w)); };
+      auto min_of = [](uint32_t w) { return __ushort_as_half(static_cast<unsigned short>(w >> 16)); };
+      constexpr int kHalves = one_k ? 2 : 1;  // one stage of keys: its halves (of the channels) fill and empty one by one
+      auto key_chunk = [&](int i) { return i / (CH / kHalves) * (CH / kHalves) + ((i + rot) & (CH / kHalves - 1)); };
+      auto value_chunk = [&](int i) { return (i + rot) & (CH - 1); };
+      // Two tiles of queries leave no room for codes in shared memory: each thread loads its token's into registers, a
+      // tile ahead. With one tile warp 13 copies them.
       const int32_t* table = p.page_table + static_cast<size_t>(sg.b) * p.max_pages;
       const size_t region = static_cast<size_t>(sg.h) * kv4_head_bytes(D, NG, p.P);
       uint32_t kw[D / 8], vw[D / 8];
@@ -411,10 +442,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         if (id != -2) flags |= kErrBadPage;
         return nullptr;
       };
-      bool bad;  // the token that the registers hold has no page
+      bool bad = false;  // the token that the registers hold has no page
       auto load_codes = [&](uint32_t (&w)[D / 8], const uint8_t* src) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
+        for (int i = 0; i < CH; ++i) {
           const uint4 x = src ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
           w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
         }
@@ -423,35 +454,58 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
 #pragma unroll
         for (int g = 0; g < NG; ++g) num[g] = src ? __ldg(reinterpret_cast<const uint2*>(src) + g) : make_uint2(0, 0);
       };
-      auto scale_of = [](uint32_t w) { return __ushort_as_half(static_cast<unsigned short>(w)); };
-      auto min_of = [](uint32_t w) { return __ushort_as_half(static_cast<unsigned short>(w >> 16)); };
-      int32_t id = page_of(0);
-      {
+      int32_t id = -2;
+      if (two) {
+        id = page_of(0);
         const uint8_t* src = token_base(id);
         bad = src == nullptr && id != -2;
         const int tp = (tile0 * kTok + tok_row) & (p.P - 1);
         load_nums(src ? src + p.P * D + tp * 8 * NG : nullptr);
-        if (keys) load_codes(kw, src ? src + tp * (D / 2) : nullptr);
-        if (vals) load_codes(vw, src ? src + p.P * (D / 2) + tp * (D / 2) : nullptr);
+        load_codes(kw, src ? src + tp * (D / 2) : nullptr);
+        load_codes(vw, src ? src + p.P * (D / 2) + tp * (D / 2) : nullptr);
+        id = page_of(1);
       }
-      id = page_of(1);
       __syncthreads();
       for (int j = 0; j < n_tiles; ++j) {
         const uint32_t J = tiles_done + j, st = J & 1, ph = (J >> 1) & 1;
-        const uint32_t ks = one_k ? 0 : st, kph = one_k ? J & 1 : ph;
-        const uint32_t hidden = __ballot_sync(0xffffffffu, bad);
-        const uint8_t* next = token_base(id);
-        bad = next == nullptr && id != -2;
+        const uint8_t* next = nullptr;
         const int tp = ((tile0 + j + 1) * kTok + tok_row) & (p.P - 1);
-        id = page_of(j + 2);
+        uint32_t hidden;
+        if (two) {
+          hidden = __ballot_sync(0xffffffffu, bad);
+          next = token_base(id);
+          bad = next == nullptr && id != -2;
+          id = page_of(j + 2);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) cur[g] = num[g];
+          for (int g = 0; g < NG; ++g) cur[g] = num[g];
+        } else {
+          const uint32_t codes = base + Ge::ring_at(two) + st * Ge::kStage;
+          wait(c_full + st, ph);
+          bad = (s_bad_pages[st] >> (tok_row >> page_sh)) & 1;
+          const bool none = bad || (tile0 + j) * kTok + tok_row >= t_end;
+          hidden = __ballot_sync(0xffffffffu, bad);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            ld_shared_v2(codes + 2 * Ge::kCodes + tok_row * 8 * NG + 8 * g, cur[g].x, cur[g].y);
+            if (none) cur[g] = make_uint2(0, 0);
+          }
+          if (keys) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+              ld_shared_v4(codes + tok_row * (D / 2) + 16 * key_chunk(i), kw[4 * i], kw[4 * i + 1], kw[4 * i + 2], kw[4 * i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+              ld_shared_v4(codes + Ge::kCodes + tok_row * (D / 2) + 16 * value_chunk(i), vw[4 * i], vw[4 * i + 1], vw[4 * i + 2],
+                           vw[4 * i + 3]);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(c_free + st);
+        }
         if (keys) {
-          wait(k_free + ks, kph ^ 1);
-          const uint32_t kd = k_tiles + ks * Ge::kTile + 16 * tok_row;
           __half2 s1[NG], s2[NG];
+          uint32_t more[4] = {0, 0, 0, 0};
           if constexpr (kExact) {  // a quarter of the scale (15 scales fit FP16) in seven bits and the rest; of the minimum
-            uint32_t more[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
               const __half2 s = __hmul2(__half2half2(scale_of(cur[g].x)), __float2half2_rn(0.25f));
@@ -461,92 +515,145 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
               const __half2 mn = __hmul2(__half2half2(min_of(cur[g].x)), __float2half2_rn(0.25f));
               more[g] = *reinterpret_cast<const uint32_t*>(&mn);
             }
-            st_shared_v4(base + Ge::more_k_at(two) + 16 * tok_row, more[0], more[1], more[2], more[3]);
           }
 #pragma unroll
-          for (int wi = 0; wi < D / 8; ++wi) {
-            const int g = (wi % KW) / (KW / NG);
-            const uint32_t nm = cur[g].x;
-            const uint32_t w = kw[wi], w8 = w >> 8;
-            if constexpr (kExact) {
-              uint32_t y[4], z[4];
-              codes2_times<false>(w, s1[g], s2[g], y[0], z[0]);
-              codes2_times<true>(w, s1[g], s2[g], y[1], z[1]);
-              codes2_times<false>(w8, s1[g], s2[g], y[2], z[2]);
-              codes2_times<true>(w8, s1[g], s2[g], y[3], z[3]);
-              st_shared_v4(kd + wi * 2048, y[0], y[1], y[2], y[3]);
-              st_shared_v4(kd + Ge::kTile + wi * 2048, z[0], z[1], z[2], z[3]);
-            } else {
-              const __half2 s = __half2half2(scale_of(nm)), mn = __half2half2(min_of(nm));
-              st_shared_v4(kd + wi * 2048, dequant2<false>(w, s, mn), dequant2<true>(w, s, mn), dequant2<false>(w8, s, mn),
-                           dequant2<true>(w8, s, mn));
+          for (int hf = 0; hf < kHalves; ++hf) {
+            const uint32_t ks = one_k ? hf : st;
+            wait(k_free + ks, (one_k ? J & 1 : ph) ^ 1);
+            if (kExact && hf == 0) st_shared_v4(base + Ge::more_k_at(two) + 16 * tok_row, more[0], more[1], more[2], more[3]);
+#pragma unroll
+            for (int i = hf * (CH / kHalves); i < (hf + 1) * (CH / kHalves); ++i) {
+              const uint32_t kd = k_tiles + (one_k ? 0 : st * Ge::kTile) + 16 * tok_row + 8192 * key_chunk(i);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int g = (k % KW) / (KW / NG);
+                const uint32_t w = kw[4 * i + k], w8 = w >> 8;
+                if constexpr (kExact) {
+                  uint32_t y[4], z[4];
+                  codes2_times<false>(w, s1[g], s2[g], y[0], z[0]);
+                  codes2_times<true>(w, s1[g], s2[g], y[1], z[1]);
+                  codes2_times<false>(w8, s1[g], s2[g], y[2], z[2]);
+                  codes2_times<true>(w8, s1[g], s2[g], y[3], z[3]);
+                  st_shared_v4(kd + k * 2048, y[0], y[1], y[2], y[3]);
+                  st_shared_v4(kd + Ge::kTile + k * 2048, z[0], z[1], z[2], z[3]);
+                } else {
+                  const __half2 s = __half2half2(scale_of(cur[g].x)), mn = __half2half2(min_of(cur[g].x));
+                  st_shared_v4(kd + k * 2048, dequant2<false>(w, s, mn), dequant2<true>(w, s, mn), dequant2<false>(w8, s, mn),
+                               dequant2<true>(w8, s, mn));
+                }
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {  // the tile four back has had its softmax: its values were freed two tiles ago
+              if (hf == 0) {
+                s_hidden[J & 3][warp & 3] = hidden;
+                if (hidden) s_any_hidden = 1;
+              }
+              mbar_arrive(k_full + ks);
             }
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {  // the tile four back has had its softmax: its values were freed two tiles ago
-            s_hidden[J & 3][warp & 3] = hidden;
-            if (hidden) s_any_hidden = 1;
-            mbar_arrive(k_full + ks);
-          }
-          load_codes(kw, next ? next + tp * (D / 2) : nullptr);
+          if (two) load_codes(kw, next ? next + tp * (D / 2) : nullptr);
         }
-        load_nums(next ? next + p.P * D + tp * 8 * NG : nullptr);
+        if (two) load_nums(next ? next + p.P * D + tp * 8 * NG : nullptr);
         if (vals) {
           wait(v_free + st, ph ^ 1);
-          const uint32_t vd = v_tiles + st * Ge::kTile + 16 * tok_row;
 #pragma unroll
-          for (int wi = 0; wi < D / 8; ++wi) {  // pair i: channels 64 (wi % VW) + 16 i + {0, 8} + wi / VW
-            uint32_t y[4];
-            const uint32_t w = vw[wi], w8 = w >> 8;
+          for (int c = 0; c < CH; ++c) {
+            const uint32_t vd = v_tiles + st * Ge::kTile + 16 * tok_row + 8192 * value_chunk(c);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t nm = cur[(64 * (wi % VW) + 16 * i) / (D / NG)].y;
-              const __half2 s = __half2half2(scale_of(nm)), mn = __half2half2(min_of(nm));
-              const uint32_t src = i < 2 ? w : w8;
-              y[i] = (i & 1) ? dequant2<true>(src, s, mn) : dequant2<false>(src, s, mn);
+            for (int k = 0; k < 4; ++k) {  // word 4 chunk + k, pair i: channels 64 (k % VW) + 16 i + {0, 8} + word / VW
+              uint32_t y[4];
+              const uint32_t w = vw[4 * c + k], w8 = w >> 8;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t nm = cur[(64 * (k % VW) + 16 * i) / (D / NG)].y;
+                const __half2 s = __half2half2(scale_of(nm)), mn = __half2half2(min_of(nm));
+                const uint32_t src = i < 2 ? w : w8;
+                y[i] = (i & 1) ? dequant2<true>(src, s, mn) : dequant2<false>(src, s, mn);
+              }
+              st_shared_v4(vd + k * 2048, y[0], y[1], y[2], y[3]);
             }
-            st_shared_v4(vd + wi * 2048, y[0], y[1], y[2], y[3]);
           }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(v_full + st);
-          load_codes(vw, next ? next + p.P * (D / 2) + tp * (D / 2) : nullptr);
+          if (two) load_codes(vw, next ? next + p.P * (D / 2) + tp * (D / 2) : nullptr);
         }
         if (s_abort) break;
       }
     } while (leave_segment(n_tiles, steps));
   } else if (group == 3) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<two>::issue));
     int n_tiles, steps;
     do {
       n_tiles = sg.tiles, steps = steps_of();
       if (warp == 13) {
-        // ---- prefetch: the first tiles at once, then one tile for each that is unpacked
+        // ---- a lane per page of the tile, its key codes, value codes and numbers: copied (one tile of queries), and asked
+        // into L2 some tiles ahead
         const int32_t* table = p.page_table + static_cast<size_t>(sg.b) * p.max_pages;
         const size_t region = static_cast<size_t>(sg.h) * kv4_head_bytes(D, NG, p.P);
         const int tile0 = sg.tile, t_end = visible(p, sg.T, sg.n, min(sg.n - 1, (sg.rb * R + R - 1) / p.G)).y;
-        auto ask = [&](int j) {
-          if (j >= n_tiles) return;
-          for (int i = lane; i < kTok; i += 32) {
-            const int tok = (tile0 + j) * kTok + i;
-            if (tok >= t_end) break;
-            const int32_t id = __ldg(table + (tok >> p.p_shift));
-            if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(p.n_pages)) continue;
-            const uint8_t* src = p.pool + static_cast<size_t>(static_cast<uint32_t>(id)) * p.page_bytes + region;
-            const int tp = tok & (p.P - 1);
-            prefetch_l2(src + tp * (D / 2));
-            prefetch_l2(src + (p.P + tp) * (D / 2));
-            if ((i & 3) == 0) prefetch_l2(src + p.P * D + tp * 8 * NG);
-          }
+        const int part = min(p.P, kTok);  // tokens of a page that are in a tile
+        auto page_of = [&](int j) -> int32_t {
+          const int tok = (tile0 + j) * kTok + lane * part;
+          return j < n_tiles && lane * part < kTok && tok < t_end ? __ldg(table + (tok >> p.p_shift)) : -2;
         };
-        for (int j = 1; j < kAhead; ++j) ask(j);
+        auto good = [&](int32_t id) { return static_cast<uint32_t>(id) < static_cast<uint32_t>(p.n_pages); };
+        auto page_at = [&](int32_t id, int j, int& tp) -> const uint8_t* {
+          tp = ((tile0 + j) * kTok + lane * part) & (p.P - 1);
+          return p.pool + static_cast<size_t>(static_cast<uint32_t>(id)) * p.page_bytes + region;
+        };
+        auto prefetch = [&](int j) {
+          const int32_t id = page_of(j);
+          if (!good(id)) return;
+          int tp;
+          const uint8_t* const src = page_at(id, j, tp);
+          bulk_prefetch_l2(src + tp * (D / 2), part * (D / 2));
+          bulk_prefetch_l2(src + (p.P + tp) * (D / 2), part * (D / 2));
+          bulk_prefetch_l2(src + p.P * D + tp * 8 * NG, part * 8 * NG);
+        };
+        auto copy = [&](int j, int32_t id) -> bool {
+          const uint32_t J = tiles_done + j, cs = J & 1;
+          if (!all(wait(c_free + cs, ((J >> 1) & 1) ^ 1))) return false;
+          const bool have = good(id);
+          if (!have && id != -2) flags |= kErrBadPage;
+          const uint32_t bad = __ballot_sync(0xffffffffu, !have && id != -2), here = __ballot_sync(0xffffffffu, have);
+          if (lane == 0) {
+            s_bad_pages[cs] = bad;
+            mbar_arrive_expect_tx(c_full + cs, __popc(here) * part * (D + 8 * NG));
+          }
+          __syncwarp();
+          if (have) {
+            int tp;
+            const uint8_t* const src = page_at(id, j, tp);
+            uint8_t* const dst = smem + Ge::ring_at(two) + cs * Ge::kStage;
+            bulk_g2s(dst + lane * part * (D / 2), src + tp * (D / 2), part * (D / 2), c_full + cs);
+            bulk_g2s(dst + Ge::kCodes + lane * part * (D / 2), src + (p.P + tp) * (D / 2), part * (D / 2), c_full + cs);
+            bulk_g2s(dst + 2 * Ge::kCodes + lane * part * 8 * NG, src + p.P * D + tp * 8 * NG, part * 8 * NG, c_full + cs);
+          }
+          return true;
+        };
+        int32_t id = two ? -2 : page_of(0);
+        int sent = !two && copy(0, id) ? 1 : 0;
+        if (!two) id = page_of(1);
+        for (int j = 1; j < kAhead; ++j) prefetch(j);
         __syncthreads();
-        for (int j = 0; j < n_tiles; ++j) {
+        if (two) {
+          for (int j = 0; j < n_tiles && !s_abort; ++j) {  // a tile for each that is unpacked
+            prefetch(j + kAhead);
+            wait(v_full + ((tiles_done + j) & 1), ((tiles_done + j) >> 1) & 1);
+          }
+        }
+        for (; sent > 0 && sent < n_tiles; ++sent) {
+          prefetch(sent + kAhead - 1);
+          if (!copy(sent, id)) break;
+          id = page_of(sent + 1);
+        }
+        // copies in flight end before the segment does, whatever happened
+        for (int j = max(0, sent - 2); j < sent; ++j) {
           const uint32_t J = tiles_done + j;
-          ask(j + kAhead);
-          wait(v_full + (J & 1), (J >> 1) & 1);
-          if (s_abort) break;
+          if (!mbar_wait_bounded(c_full + (J & 1), (J >> 1) & 1, kBudget >> 4)) s_abort = 1;
         }
       } else {
         __syncthreads();
@@ -559,21 +666,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         auto scores = [&](int s) -> bool {
           const int u = s & 1, j = two ? s >> 1 : s;
           const uint32_t J = tiles_done + j, st = one_k ? 0 : J & 1;
-          if ((!two || u == 0) && !all(wait(k_full + st, one_k ? J & 1 : (J >> 1) & 1))) return false;
-          tc5::fence_after();
           const uint64_t qa = tc5::smem_desc(base + (two ? u * Ge::kTile : 0), 2048, 128);
           const uint64_t ka = tc5::smem_desc(k_tiles + st * Ge::kTile, 2048, 128);
+          constexpr int kHalves = one_k ? 2 : 1;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {  // descriptor addresses count 16 bytes
-            tc5::mma_ss(tm + Ge::kColS + 128 * u, qa + 256 * k, ka + 256 * k, kDescS, k > 0, leader);
-            if constexpr (kExact)
-              tc5::mma_ss(tm + Ge::kColS + 128 * u, qa + 256 * k, ka + Ge::kTile / 16 + 256 * k, kDescS, true, leader);
+          for (int hf = 0; hf < kHalves; ++hf) {
+            const uint32_t ks = one_k ? hf : st;
+            if ((!two || u == 0) && !all(wait(k_full + ks, one_k ? J & 1 : (J >> 1) & 1))) return false;
+            tc5::fence_after();
+#pragma unroll
+            for (int k = hf * (D / 32); k < (hf + 1) * (D / 16 / kHalves); ++k) {  // descriptor addresses count 16 bytes
+              tc5::mma_ss(tm + Ge::kColS + 128 * u, qa + 256 * k, ka + 256 * k, kDescS, k > 0, leader);
+              if constexpr (kExact)
+                tc5::mma_ss(tm + Ge::kColS + 128 * u, qa + 256 * k, ka + Ge::kTile / 16 + 256 * k, kDescS, true, leader);
+            }
+            if (kExact && hf == 0)
+              tc5::mma_ss(tm + Ge::kColS + 128 * u, tc5::smem_desc(base + Ge::more_q_at(two) + (two ? u * Ge::kMore : 0), 2048, 128),
+                          tc5::smem_desc(base + Ge::more_k_at(two), 2048, 128), kDescS, true, leader);
+            if (hf == kHalves - 1) tc5::commit(s_full + u, leader);
+            if (!two || u == 1) tc5::commit(k_free + ks, leader);
           }
-          if constexpr (kExact)
-            tc5::mma_ss(tm + Ge::kColS + 128 * u, tc5::smem_desc(base + Ge::more_q_at(two) + (two ? u * Ge::kMore : 0), 2048, 128),
-                        tc5::smem_desc(base + Ge::more_k_at(two), 2048, 128), kDescS, true, leader);
-          tc5::commit(s_full + u, leader);
-          if (!two || u == 1) tc5::commit(k_free + st, leader);
           return true;
         };
         bool ok = scores(0) && (steps < 2 || scores(1));
@@ -600,8 +712,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       __syncwarp();
     } while (leave_segment(n_tiles, steps));
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int lane_row = tid & 127;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<two>::softmax));
+    const int lane_row = tid & 127, side = lane_row >> 6;
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t oc = tmem + lane_base + Ge::kColO + D * group;
     const int n_softmax = two ? 256 : 128;  // threads of the softmax groups
@@ -610,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       n_tiles = sg.tiles, steps = steps_of();
       const int tile0 = sg.tile;
       const int rows_left = sg.n * p.G - sg.rb * R;  // live rows of the block
-      const int row = (two ? 128 * group : 0) + lane_row, rr = sg.rb * R + row;
+      const int row = two ? 128 * group + lane_row : half ? lane_row & 63 : lane_row, rr = sg.rb * R + row;
       const bool live = row < rows_left;
       float m = kNoMax, l = 0.f, fr = 0.f;
       int2 vis = make_int2(0, 0);
@@ -695,30 +807,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       }
       __syncthreads();
       // ---- softmax: thread = row
-      for (int k = 0; k < n_tiles; ++k) {
+      auto tile_weights = [&](auto chunks, int k) {
+        constexpr int NC = decltype(chunks)::value;  // chunks of 32 tokens that a thread takes
+        const int first = NC == 4 ? 0 : 2 * side;    // the first of them
         const int t = tile0 + k, u = two ? group : k & 1;  // S buffer
         const uint32_t sc = tmem + lane_base + Ge::kColS + 128 * u;
         const uint32_t ph = two ? steps_done[group] + k : steps_done[u] + (k >> 1);
         wait(s_full + u, ph & 1);
         tc5::fence_after();
-        uint32_t raw[4][32];
+        uint32_t raw[NC][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tc5::ld32(sc + 32 * c, raw[c]);
+        for (int c = 0; c < NC; ++c) tc5::ld32(sc + 32 * (first + c), raw[c]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tc5::wait_ld(raw[c]);
+        for (int c = 0; c < NC; ++c) tc5::wait_ld(raw[c]);
         if (s_any_hidden) {  // some tile so far
-          const uint4 hid = *reinterpret_cast<const uint4*>(s_hidden[(tiles_done + k) & 3]);
-          const uint32_t bits[4] = {hid.x, hid.y, hid.z, hid.w};
+          uint32_t bits[NC];
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < NC; ++c) bits[c] = s_hidden[(tiles_done + k) & 3][first + c];
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if ((bits[c] >> i) & 1) raw[c][i] = 0xff800000u;  // -inf
         }
         if (t < full_lo || t >= full_hi) {
-          const int lo = vis.x - t * kTok, hi = vis.y - t * kTok;  // columns that this row sees: [lo, hi)
+          const int lo = vis.x - t * kTok - 32 * first, hi = vis.y - t * kTok - 32 * first;  // columns that this row sees: [lo, hi)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (32 * c + i < lo || 32 * c + i >= hi) raw[c][i] = 0xff800000u;  // -inf
@@ -731,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           if (find) {
             float mx = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < NC; ++c)
 #pragma unroll
               for (int i = 0; i < 32; i += 2) mx = max3(mx, __uint_as_float(raw[c][i]), __uint_as_float(raw[c][i + 1]));
             const float mn = fmaxf(m, mx * fr), a = ex2(m - mn);
@@ -759,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           const float neg = -m;
           float mx = -INFINITY, my = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < NC; ++c) {
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
@@ -772,23 +887,77 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
               add_pair(l0, l1, a, b);
               w[i >> 1] = h2(a, b);
             }
-            tc5::st16(sc + 16 * c, w);
+            tc5::st16(sc + 16 * (first + c), w);
           }
           if (find || !__any_sync(0xffffffffu, fmaxf(mx, my) * fr > m + kSlack)) break;
           find = true;
         }
         l += l0 + l1;
+        if constexpr (NC == 2) {  // the other half's weights are its twin's
+          uint32_t none[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) none[i] = 0;
+          tc5::st16(sc + 16 * (2 - first), none);
+          tc5::st16(sc + 16 * (3 - first), none);
+        }
         tc5::wait_st();
         tc5::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_ready + u);
-        if (s_abort) break;
+      };
+      for (int k = 0; k < n_tiles && !s_abort; ++k) {
+        if (half) tile_weights(std::integral_constant<int, 2>{}, k);
+        else tile_weights(std::integral_constant<int, 4>{}, k);
       }
       const bool done = all(wait(o_done, segs & 1)) && !s_abort;
       tc5::fence_after();
 
+              constexpr int kPartRow = D * 4;
+              uint8_t* const part_st = smem + (two ? Ge::k_at(true) : Ge::v_at(false));  // 32 rows of floats per warp
+              float f = 1.f;
+              if (half) {  // the row and its twin: a common max, the twin's sums by way of shared memory
+                s_side[lane_row] = make_float2(m, l);
+                softmax_barrier(n_softmax);
+                const float2 a = s_side[row], b = s_side[row + 64];
+                const float M = fmaxf(a.x, b.x);
+                f = ex2(m - M);
+                l = ex2(a.x - M) * a.y + ex2(b.x - M) * b.y;
+                m = M;
+                if (side) {
+                  uint8_t* const st = part_st + (warp & 3) * 32 * kPartRow;
+#pragma unroll
+                  for (int c = 0; c < D / 32; ++c) {
+                    uint32_t v[32];
+                    tc5::ld32(oc + 32 * c, v);
+                    tc5::wait_ld(v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                      *reinterpret_cast<float4*>(st + lane * kPartRow + 16 * ((8 * c + i) ^ (lane & 7))) =
+                          make_float4(__uint_as_float(v[4 * i]) * f, __uint_as_float(v[4 * i + 1]) * f,
+                                      __uint_as_float(v[4 * i + 2]) * f, __uint_as_float(v[4 * i + 3]) * f);
+                  }
+                }
+                softmax_barrier(n_softmax);
+              }
       // ---- results: thread = row
       if (done) {
+        auto load_sums = [&](int c, float (&x)[32]) {  // columns 32 c ..
+          uint32_t v[32];
+          tc5::ld32(oc + 32 * c, v);
+          tc5::wait_ld(v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]);
+          if (half) {
+            const uint8_t* const st = part_st + ((warp & 1) + 2) * 32 * kPartRow;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 o = *reinterpret_cast<const float4*>(st + lane * kPartRow + 16 * ((8 * c + i) ^ (lane & 7)));
+              x[4 * i] = fmaf(x[4 * i], f, o.x), x[4 * i + 1] = fmaf(x[4 * i + 1], f, o.y);
+              x[4 * i + 2] = fmaf(x[4 * i + 2], f, o.z), x[4 * i + 3] = fmaf(x[4 * i + 3], f, o.w);
+            }
+          }
+        };
+        const bool stores = !half || side == 0;
         const float y = l == 0.f ? 0.f : 1.f / l;
         auto out_row = [&](int row_of_block) {
           const int q2 = sg.rb * R + row_of_block;
@@ -797,21 +966,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         // rows go out by way of shared memory (each warp its 32 rows), so that lanes store along a row; 16-byte
         // chunks are exchanged by the row's low bits: distinct banks both ways
         const int first = (two ? 128 * group : 0) + 32 * (warp & 3);
-        if (sg.part >= 0) {
-          constexpr int kRow = D * 4, kChunks = D / 4;
-          uint8_t* const st = smem + (two ? Ge::k_at(true) : Ge::v_at(false)) + (first >> 5) * 32 * kRow;
+        if (!stores) {
+        } else if (sg.part >= 0) {
+          constexpr int kRow = kPartRow, kChunks = D / 4;
+          uint8_t* const st = part_st + (first >> 5) * 32 * kRow;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
-            uint32_t v[32];
-            tc5::ld32(oc + 32 * c, v);
-            tc5::wait_ld(v);
+            float x[32];
+            load_sums(c, x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float x[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) x[k] = __uint_as_float(v[4 * i + k]);
-              *reinterpret_cast<float4*>(st + lane * kRow + 16 * ((8 * c + i) ^ (lane & 7))) = make_float4(x[0], x[1], x[2], x[3]);
-            }
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(st + lane * kRow + 16 * ((8 * c + i) ^ (lane & 7))) =
+                  make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
           }
           __syncwarp();
           const int left = min(32, rows_left - first);
@@ -825,12 +991,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           uint32_t res[D / 2];
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
-            uint32_t v[32];
-            tc5::ld32(oc + 32 * c, v);
-            tc5::wait_ld(v);
             float x[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]);
+            load_sums(c, x);
             // column 8 wi + 2 i + e is channel 64 (wi % VW) + 16 i + 8 e + wi / VW: neighbouring channels are
             // columns VW * 8 apart, in the same 32
 #pragma unroll
@@ -952,26 +1114,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   if (lane == 0 && flags) atomicOr(p.err, flags);
 }
 
-template <int D, int NG, bool kExact>
-cudaError_t launch_as(const Kv4AttnParams& p, int two, int line, int ctas, cudaStream_t stream) {
+template <int D, int NG, bool kExact, bool two>
+cudaError_t launch_as(const Kv4AttnParams& p, int rows, int line, int ctas, cudaStream_t stream) {
   static bool attr_done[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_done[dev]) {
-    e = cudaFuncSetAttribute(kv4_prompt_kernel<D, NG, kExact>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             std::max(Geom<D, kExact>::smem(false), Geom<D, kExact>::smem(true)));
+    e = cudaFuncSetAttribute(kv4_prompt_kernel<D, NG, kExact, two>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Geom<D, NG, kExact>::smem(two));
     if (e != cudaSuccess) return e;
     attr_done[dev] = true;
   }
-  kv4_prompt_kernel<D, NG, kExact><<<ctas, kThreads, Geom<D, kExact>::smem(two), stream>>>(p, two, line);
+  kv4_prompt_kernel<D, NG, kExact, two><<<ctas, kThreads, Geom<D, NG, kExact>::smem(two), stream>>>(p, rows, line);
   return cudaGetLastError();
 }
 
 template <int D, int NG>
-cudaError_t launch(const Kv4AttnParams& p, int two, int line, int ctas, cudaStream_t stream) {
-  return p.lse ? launch_as<D, NG, true>(p, two, line, ctas, stream) : launch_as<D, NG, false>(p, two, line, ctas, stream);
+cudaError_t launch(const Kv4AttnParams& p, int rows, int line, int ctas, cudaStream_t stream) {
+  if (rows == 256)
+    return p.lse ? launch_as<D, NG, true, true>(p, rows, line, ctas, stream) : launch_as<D, NG, false, true>(p, rows, line, ctas, stream);
+  return p.lse ? launch_as<D, NG, true, false>(p, rows, line, ctas, stream) : launch_as<D, NG, false, false>(p, rows, line, ctas, stream);
 }
 
 }  // namespace
@@ -981,8 +1145,7 @@ bool kv4_uses_prompt(int max_q, int G) { return static_cast<int64_t>(max_q) * G 
 Kv4PromptPlan kv4_prompt_plan(int B, int Hkv, int n_rows, int max_q, int G, int num_sms) {
   Kv4PromptPlan z;
   const int64_t rows = static_cast<int64_t>(std::min(max_q, n_rows)) * G;
-  z.two = rows > 128;
-  z.rows = z.two ? 256 : 128;
+  z.rows = rows > 128 ? 256 : rows > 64 ? 128 : 64;
   const int64_t items = static_cast<int64_t>(B) * Hkv * ((rows + z.rows - 1) / z.rows);
   const int64_t blocks = (rows + z.rows - 1) / z.rows;
   z.line = items < 2 * static_cast<int64_t>(num_sms) && B * blocks <= kThreads ? static_cast<int>(blocks) : 0;
@@ -997,11 +1160,11 @@ size_t kv4_prompt_workspace_bytes(const Kv4PromptPlan& z, int D) {
 cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, const Kv4PromptPlan& z, int D, int n_groups, cudaStream_t stream) {
   const int ctas = static_cast<int>(z.ctas);
   if (D == 128) {
-    if (n_groups == 1) return launch<128, 1>(p, z.two, z.line, ctas, stream);
-    if (n_groups == 2) return launch<128, 2>(p, z.two, z.line, ctas, stream);
-    return launch<128, 4>(p, z.two, z.line, ctas, stream);
+    if (n_groups == 1) return launch<128, 1>(p, z.rows, z.line, ctas, stream);
+    if (n_groups == 2) return launch<128, 2>(p, z.rows, z.line, ctas, stream);
+    return launch<128, 4>(p, z.rows, z.line, ctas, stream);
   }
-  return n_groups == 1 ? launch<64, 1>(p, z.two, z.line, ctas, stream) : launch<64, 2>(p, z.two, z.line, ctas, stream);
+  return n_groups == 1 ? launch<64, 1>(p, z.rows, z.line, ctas, stream) : launch<64, 2>(p, z.rows, z.line, ctas, stream);
 }
 
 }  // namespace mlaq
