@@ -1135,12 +1135,15 @@ template <int D, int NG>
 cudaError_t launch(const Kv4AttnParams& p, int rows, int line, int ctas, cudaStream_t stream) {
   if (rows == 256)
     return p.lse ? launch_as<D, NG, true, true>(p, rows, line, ctas, stream) : launch_as<D, NG, false, true>(p, rows, line, ctas, stream);
-  return p.lse ? launch_as<D, NG, true, false>(p, rows, line, ctas, stream) : launch_as<D, NG, false, false>(p, rows, line, ctas, stream);
+  if constexpr (D == 64) {
+    if (!p.lse) return launch_as<D, NG, false, false>(p, rows, line, ctas, stream);
+  }
+  return launch_as<D, NG, true, false>(p, rows, line, ctas, stream);
 }
 
 }  // namespace
 
-bool kv4_uses_prompt(int max_q, int G) { return static_cast<int64_t>(max_q) * G > 16; }
+bool kv4_uses_prompt(int max_q, int G) { return static_cast<int64_t>(max_q) * G > 32; }
 
 Kv4PromptPlan kv4_prompt_plan(int B, int Hkv, int n_rows, int max_q, int G, int num_sms) {
   Kv4PromptPlan z;

@@ -214,6 +214,15 @@ def test_many_rows(D, group, G, dtype, n, lse):
     Case([n, n + 1, 200 + n, 131], [n, n, n, 3], Hkv=2, G=G, D=D, group=group, P=16, dtype=dtype, seed=n + G).check(lse=lse)
 
 
+@pytest.mark.parametrize("n,G,D,group,P", [
+    (17, 1, 128, 128, 16), (5, 5, 128, 64, 256), (8, 4, 64, 32, 64), (32, 1, 128, 32, 128), (33, 1, 128, 128, 256), (12, 5, 64, 64, 16),
+    (16, 4, 128, 32, 32), (13, 5, 128, 64, 64), (32, 4, 64, 32, 128), (43, 3, 128, 32, 256), (37, 7, 64, 64, 256)])
+@pytest.mark.parametrize("window", [0, 130])
+def test_row_counts_at_the_borders_between_kernels(n, G, D, group, P, window):
+    """Up to 32 rows (two blocks of 16), up to 64, up to 128, more; sequences cut over the SMs, ends inside a page and a tile."""
+    Case([n, 700, 1201, 300], [n, n, 1, 2], Hkv=2, G=G, D=D, group=group, P=P, dtype="fp16" if n & 1 else "bf16", seed=n + D).check(window=window)
+
+
 def test_rows_of_several_blocks_and_more_items_than_the_gpu_holds():
     Case([400], [300], Hkv=1, G=4, seed=1).check(lse=False)          # five blocks of 256 rows, cut over the SMs
     Case([40] * 160, [20] * 160, Hkv=2, G=1, seed=2, D=64).check()   # 320 items: one CTA each
