@@ -182,10 +182,11 @@ size_t mla_qcache_kv4_workspace_bytes(const mla_qcache_kv4_config* cfg, int32_t 
   const size_t few = mlaq::kv4_decode_workspace_bytes(mlaq::kv4_decode_rows(max_q, G), D, sms);
   if (!mlaq::kv4_uses_prompt(max_q, G)) return few;
   // the rows of a call, below max_q per sequence, decide how it is cut: the most that any needs
+  const int64_t max_tokens = static_cast<int64_t>(max_pages) * cfg->page_size;
   size_t most = few;
   for (int64_t rows = 1; rows <= max_q; rows = rows < max_q && 2 * rows > max_q ? max_q : 2 * rows) {
     const size_t w = mlaq::kv4_prompt_workspace_bytes(
-        mlaq::kv4_prompt_plan(B, cfg->n_kv_heads, static_cast<int>(rows), max_q, G, sms), D);
+        mlaq::kv4_prompt_plan(B, cfg->n_kv_heads, static_cast<int>(rows), max_q, max_tokens, G, sms), D);
     most = most > w ? most : w;
   }
   return most;
@@ -219,7 +220,8 @@ int mla_qcache_kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t
   int sms = 0;
   if ((st = sm_count(&sms)) != MLA_QCACHE_OK) return st;
   const bool prompt = mlaq::kv4_uses_prompt(max_q, G);
-  const mlaq::Kv4PromptPlan plan = mlaq::kv4_prompt_plan(B, cfg->n_kv_heads, n_rows, max_q, G, sms);
+  const mlaq::Kv4PromptPlan plan =
+      mlaq::kv4_prompt_plan(B, cfg->n_kv_heads, n_rows, max_q, static_cast<int64_t>(max_pages) * cfg->page_size, G, sms);
   const size_t rows = prompt ? plan.rows : mlaq::kv4_decode_rows(max_q, G);
   const size_t need = prompt ? mlaq::kv4_prompt_workspace_bytes(plan, D)
                              : mlaq::kv4_decode_workspace_bytes(static_cast<int>(rows), D, sms);

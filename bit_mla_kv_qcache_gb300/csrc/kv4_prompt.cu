@@ -54,6 +54,7 @@ struct Regs {  // two: one group unpacks, else two groups do
 constexpr int kAhead = 3;         // tiles that warp 13 runs ahead
 constexpr int kTok = 128;         // tokens per tile
 constexpr int kMaxParts = 32;     // CTAs that one item is cut into, at most
+constexpr int kStart = 6;         // tiles' worth of time that an item costs besides its tiles: queries, first tiles, results
 constexpr float kSlack = 8.f;     // the running max is raised when a score exceeds it by more than this
 constexpr float kNoMax = -1e30f;  // the running max before the first score
 constexpr long long kBudget = 4ll << 30;  // cycles of a wait before it is given up
@@ -185,7 +186,8 @@ __device__ __forceinline__ int2 block_tiles(const Kv4AttnParams& p, int T, int n
 }
 __device__ __forceinline__ int row_blocks(const Kv4AttnParams& p, int n, int R) { return (n * p.G + R - 1) / R; }
 
-// Line mode: the segment that starts at s.at (b, h, rb and the sequence are set).
+// Line mode: the segment that starts at s.at (b, h, rb and the sequence are set). An item takes its tiles and kStart more
+// places of the line.
 __device__ __forceinline__ void line_segment(const Kv4AttnParams& p, Seg& s, int R) {
   const int2 t = block_tiles(p, s.T, s.n, s.rb, R);
   s.item_tiles = t.y;
@@ -199,24 +201,42 @@ __device__ __forceinline__ void line_segment(const Kv4AttnParams& p, Seg& s, int
   s.valid = 1;
 }
 
+// Line mode: goes on to the item at s.at, the next head or row block (`line` of them per sequence) or sequence.
+__device__ __forceinline__ void next_item(const Kv4AttnParams& p, Seg& s, int line, int R) {
+  s.valid = 0;
+  if (s.at >= s.end) return;
+  s.item0 = s.at;
+  if (++s.h == p.Hkv) {  // the next pair with rows
+    s.h = 0;
+    int f = 0;
+    do {
+      if (++s.pair >= p.B * line) return;  // lengths that changed under the call
+      s.b = s.pair / line;
+      s.rb = s.pair - s.b * line;
+      load_sequence(p, s.b, s.T, s.n, s.r0, f);
+    } while (s.rb >= row_blocks(p, s.n, R));
+  }
+  line_segment(p, s, R);
+}
+
 template <int D, int NG, bool kExact, bool two>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnParams p, const int rows, const int line) {
   using Ge = Geom<D, NG, kExact>;
   constexpr int KW = D / 32, VW = D / 64, CB = D / 8;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t bars[17];  // k_full[2] k_free[2] v_full[2] v_free[2] s_full[2] p_ready[2] o_done c_full[2] c_free[2]
+  __shared__ uint64_t bars[19];  // k_full[2] k_free[2] v_full[2] v_free[2] s_full[2] p_ready[2] o_done c_full[2] c_free[2]
   __shared__ uint32_t s_tmem;
   __shared__ Seg s_seg;
   __shared__ long long s_part[kThreads / 32];
   __shared__ int s_most[kThreads / 32], s_last;
   __shared__ float2 s_side[kTok];  // max and sum of a row under half of the tokens
   constexpr int kTry = 9;
-  __shared__ int s_count[kTry];  // parts that a share would make
+  __shared__ int s_count[kTry + 1];  // parts that a share would make; tiles in all
   __shared__ volatile int s_abort, s_any_hidden;
   __shared__ uint32_t s_bad_pages[2];  // of a stage of codes: bit i, its i-th page
   __shared__ __align__(16) uint32_t s_hidden[4][4];  // tokens of a tile (modulo four) whose page id is bad
   uint64_t *const k_full = bars, *const k_free = bars + 2, *const v_full = bars + 4, *const v_free = bars + 6,
-           *const s_full = bars + 8, *const p_ready = bars + 10, *const o_done = bars + 12, *const c_full = bars + 13, *const c_free = bars + 15;
+           *const s_full = bars + 8, *const p_ready = bars + 10, *const o_done = bars + 12, *const c_full = bars + 13, *const c_free = bars + 15, *const p_half = bars + 17;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (base - smem_addr(smem_raw));
   long long* const s_sum = reinterpret_cast<long long*>(smem);  // tiles before each pair, until the first queries come
@@ -259,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       load_sequence(p, b, T, n, r0, f);
       if (blockIdx.x == 0) flags |= f;
       if (rb < row_blocks(p, n, R)) t = block_tiles(p, T, n, rb, R).y;
-      x = static_cast<long long>(t) * p.Hkv;
+      if (t > 0) x = static_cast<long long>(t + kStart) * p.Hkv;
     }
     const int warp_most = __reduce_max_sync(0xffffffffu, t);
     auto scan = [&](long long v) {  // inclusive, over the block
@@ -275,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       return v;
     };
     if (lane == 0) s_most[warp] = warp_most;
-    if (tid < kTry) s_count[tid] = 0;
+    if (tid <= kTry) s_count[tid] = 0;
     x = scan(x);
     s_sum[tid + 1] = x;
     if (tid == 0) s_sum[0] = 0;
@@ -284,11 +304,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
 #pragma unroll 1
     for (int w = 0; w < kThreads / 32; ++w) most = max(most, s_most[w]);
     const long long total = s_sum[kThreads];
-    const int least = max(min(4, most), (most + kMaxParts - 2) / (kMaxParts - 1));
-    // shares for which every part could have a CTA of its own: the smallest of a few multiples of the mean
-    const float mean = static_cast<float>(total) / static_cast<float>(gridDim.x);
-    auto share_of = [&](int k) { return max(least, static_cast<int>(mean * (1.f + 0.12f * k)) + 1); };
+    // fewest tiles of a part; items of fewer than 2048 tokens stay whole
+    const int least = most < 2048 / kTok ? max(1, most) : max(4, (most + kMaxParts - 2) / (kMaxParts - 1));
     const bool small = total < (1 << 24);
+    const int tiles_here = __reduce_add_sync(0xffffffffu, small ? p.Hkv * t : 0);
+    if (lane == 0) atomicAdd(&s_count[kTry], tiles_here);
+    __syncthreads();
+    // shares for which every part could have a CTA of its own: the smallest of a few multiples of the mean, or
+    // items uncut where the longest is little more than the line's stretch
+    const float mean = static_cast<float>(s_count[kTry]) / static_cast<float>(gridDim.x);
+    const float stretch = static_cast<float>(total) / static_cast<float>(gridDim.x);
+    const bool uncut = most + kStart <= 1.2f * (stretch + kStart);
+    auto share_of = [&](int k) {
+      return k == kTry - 1 && uncut ? max(1, most) : max(least, static_cast<int>(mean * (1.f + 0.12f * k)) + 1);
+    };
 #pragma unroll 1
     for (int k = 0; k < kTry; ++k) {
       const int sh = share_of(k), parts = __reduce_add_sync(0xffffffffu, small ? p.Hkv * ((t + sh - 1) / sh) : 1 << 20);
@@ -339,9 +368,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             s.item0 = s.end = s.at;  // and nothing after it
             s.item_tiles = tiles.y;
           } else {
-            s.h = min(at / tiles.y, p.Hkv - 1);
-            s.item0 = s_sum[lo] + static_cast<long long>(s.h) * tiles.y;
-            line_segment(p, s, R);
+            s.h = min(at / (tiles.y + kStart), p.Hkv - 1);
+            s.item0 = s_sum[lo] + static_cast<long long>(s.h) * (tiles.y + kStart);
+            if (s.at < s.item0 + tiles.y) {
+              line_segment(p, s, R);
+            } else {
+              s.at = s.item0 + tiles.y + kStart;
+              next_item(p, s, line, R);
+            }
           }
         }
       }
@@ -354,6 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       mbar_init(k_full + i, 4);  // one arrival per warp
       mbar_init(v_full + i, 4);
       mbar_init(p_ready + i, 4);
+      mbar_init(p_half + i, 4);
       mbar_init(k_free + i, 1);
       mbar_init(v_free + i, 1);
       mbar_init(s_full + i, 1);
@@ -692,14 +727,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         for (int s = 0; ok && s < steps; ++s) {
           const int u = s & 1, j = two ? s >> 1 : s;
           const uint32_t J = tiles_done + j, st = J & 1;
-          ok = all(wait(p_ready + u, (steps_done[u] + (s >> 1)) & 1) && ((two && u == 1) || wait(v_full + st, (J >> 1) & 1)));
+          ok = all(wait((two ? p_half : p_ready) + u, (steps_done[u] + (s >> 1)) & 1) && ((two && u == 1) || wait(v_full + st, (J >> 1) & 1)));
           if (!ok) break;
           tc5::fence_after();
           const uint64_t va = tc5::smem_desc(v_tiles + st * Ge::kTile, 128, 2048);
 #pragma unroll
-          for (int k = 0; k < kTok / 16; ++k)
+          for (int k = 0; k < kTok / 16; ++k) {
+            if (two && k == kTok / 32) {
+              ok = all(wait(p_ready + u, (steps_done[u] + (s >> 1)) & 1));
+              tc5::fence_after();
+            }
             tc5::mma_ts(tm + Ge::kColO + (two ? D * u : 0), tm + Ge::kColS + 128 * u + 8 * k, va + 16 * k, kDescO,
                         s >= (two ? 2 : 1) || k > 0, leader);
+          }
           if (!two || u == 1) tc5::commit(v_free + st, leader);
           if (s + 2 < steps) ok = scores(s + 2);
         }
@@ -838,59 +878,60 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             for (int i = 0; i < 32; ++i)
               if (32 * c + i < lo || 32 * c + i >= hi) raw[c][i] = 0xff800000u;  // -inf
         }
-        // The weights are formed under the running max as it is, and again in the rare case that a score was
-        // more than 2^8 above it (a warp's first tile always finds its max first).
-        bool find = k == 0;
-        float l0, l1;
-        while (true) {
-          if (find) {
-            float mx = -INFINITY;
+        // The weights are formed under the running max as it is, unless a score is more than 2^8 above it (a warp's
+        // first tile always finds its max).
+        float mx = -INFINITY, my = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) mx = max3(mx, __uint_as_float(raw[c][i]), __uint_as_float(raw[c][i + 1]));
-            const float mn = fmaxf(m, mx * fr), a = ex2(m - mn);
-            m = mn;
-            l *= a;
-            if (k > 0) {
-              if (!two) {  // the products of the tile before still add to O
-                const uint32_t J = tiles_done + k - 1;
-                wait(v_free + (J & 1), (J >> 1) & 1);
-                tc5::fence_after();
-              }
+          for (int i = 0; i < 32; i += 4) {
+            mx = max3(mx, __uint_as_float(raw[c][i]), __uint_as_float(raw[c][i + 1]));
+            my = max3(my, __uint_as_float(raw[c][i + 2]), __uint_as_float(raw[c][i + 3]));
+          }
+        mx = fmaxf(mx, my);
+        if (k == 0 || __any_sync(0xffffffffu, mx * fr > m + kSlack)) {
+          const float mn = fmaxf(m, mx * fr), a = ex2(m - mn);
+          m = mn;
+          l *= a;
+          if (k > 0) {
+            if (!two) {  // the products of the tile before still add to O
+              const uint32_t J = tiles_done + k - 1;
+              wait(v_free + (J & 1), (J >> 1) & 1);
+              tc5::fence_after();
+            }
 #pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
-                uint32_t v[16];
-                tc5::ld16(oc + 16 * c, v);
-                tc5::wait_ld16(v);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t v[16];
+              tc5::ld16(oc + 16 * c, v);
+              tc5::wait_ld16(v);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a);
-                tc5::st16(oc + 16 * c, v);
-              }
-              tc5::wait_st();
+              for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a);
+              tc5::st16(oc + 16 * c, v);
             }
+            tc5::wait_st();
           }
-          l0 = l1 = 0.f;
-          const float neg = -m;
-          float mx = -INFINITY, my = -INFINITY;
+        }
+        float l0 = 0.f, l1 = 0.f;
+        const float neg = -m;
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            uint32_t w[16];
+        for (int c = 0; c < NC; ++c) {
+          uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float a = __uint_as_float(raw[c][i]), b = __uint_as_float(raw[c][i + 1]);
-              if (i & 2) my = max3(my, a, b);
-              else mx = max3(mx, a, b);
-              fma_pair(a, b, fr, neg);
-              a = ex2(a);
-              b = ex2(b);
-              add_pair(l0, l1, a, b);
-              w[i >> 1] = h2(a, b);
-            }
-            tc5::st16(sc + 16 * (first + c), w);
+          for (int i = 0; i < 32; i += 2) {
+            float a = __uint_as_float(raw[c][i]), b = __uint_as_float(raw[c][i + 1]);
+            fma_pair(a, b, fr, neg);
+            a = ex2(a);
+            b = ex2(b);
+            add_pair(l0, l1, a, b);
+            w[i >> 1] = h2(a, b);
           }
-          if (find || !__any_sync(0xffffffffu, fmaxf(mx, my) * fr > m + kSlack)) break;
-          find = true;
+          tc5::st16(sc + 16 * (first + c), w);
+          if (two && c == 1) {
+            tc5::wait_st();
+            tc5::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_half + u);
+          }
         }
         l += l0 + l1;
         if constexpr (NC == 2) {  // the other half's weights are its twin's
@@ -1084,25 +1125,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         Seg& s = s_seg;
         s.valid = 0;
         if (line) {
-          s.at = min(s.end, s.item0 + s.item_tiles);
-          if (s.at < s.end) {
-            s.item0 = s.at;
-            bool found = true;
-            if (++s.h == p.Hkv) {  // the next pair with rows
-              s.h = 0;
-              int f = 0;
-              do {
-                if (++s.pair >= p.B * line) {  // lengths that changed under the call
-                  found = false;
-                  break;
-                }
-                s.b = s.pair / line;
-                s.rb = s.pair - s.b * line;
-                load_sequence(p, s.b, s.T, s.n, s.r0, f);
-              } while (s.rb >= row_blocks(p, s.n, R));
-            }
-            if (found) line_segment(p, s, R);
-          }
+          s.at = min(s.end, s.item0 + s.item_tiles + kStart);
+          next_item(p, s, line, R);
         }
       }
     } while (leave_segment(n_tiles, steps));
@@ -1145,13 +1169,19 @@ cudaError_t launch(const Kv4AttnParams& p, int rows, int line, int ctas, cudaStr
 
 bool kv4_uses_prompt(int max_q, int G) { return static_cast<int64_t>(max_q) * G > 32; }
 
-Kv4PromptPlan kv4_prompt_plan(int B, int Hkv, int n_rows, int max_q, int G, int num_sms) {
+// An item is worth cutting, which costs a schedule, a second store and a join, when its tokens are many. 48 items
+// of 256 rows, one CTA each against cut: 2K tokens 39 and 43 us, 3K 53 and 47, 8K 122 and 72; four of 40 rows: 1K 20 and 25, 2K 30
+// and 26. Between a half and all of the SMs whole items fill one wave and a cut makes two (96 items, 8K: 123 and 126 us).
+// Up to twice the SMs a cut fills the second wave: 192 items, 4K: 103 and 104, 8K: 215 and 173 us. The lengths are on
+// the device: the room of the page table stands for them here, and there short items stay whole.
+Kv4PromptPlan kv4_prompt_plan(int B, int Hkv, int n_rows, int max_q, int64_t max_tokens, int G, int num_sms) {
   Kv4PromptPlan z;
   const int64_t rows = static_cast<int64_t>(std::min(max_q, n_rows)) * G;
   z.rows = rows > 128 ? 256 : rows > 64 ? 128 : 64;
   const int64_t items = static_cast<int64_t>(B) * Hkv * ((rows + z.rows - 1) / z.rows);
   const int64_t blocks = (rows + z.rows - 1) / z.rows;
-  z.line = items < 2 * static_cast<int64_t>(num_sms) && B * blocks <= kThreads ? static_cast<int>(blocks) : 0;
+  const bool cut = 2 * items <= num_sms ? max_tokens > 2048 : items > num_sms && items < 2 * num_sms && max_tokens > 4096;
+  z.line = cut && B * blocks <= kThreads ? static_cast<int>(blocks) : 0;
   z.ctas = z.line ? std::min(num_sms, static_cast<int>(kKv4CounterBytes / 4)) : items;
   return z;
 }
