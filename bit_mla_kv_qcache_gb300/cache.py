@@ -80,3 +80,56 @@ class QuantizedMLACache:
 
     def error_bits(self) -> int:
         return int(self.err.item())
+
+
+class KV4Cache:
+    """Grouped-query K/V cache in 4 bits of one layer: page pool, page table and lengths for B sequences, and the
+    workspace of its attention. The page table is the caller's, as for QuantizedMLACache."""
+
+    def __init__(self, cfg: binding.KV4Config, batch: int, max_pages: int, n_pages: int | None = None,
+                 page_table: torch.Tensor | None = None, device="cuda"):
+        pb = binding.kv4_page_bytes(cfg)
+        if pb == 0:
+            raise binding.QCacheError("unsupported 4-bit cache configuration")
+        self.cfg, self.B, self.max_pages = cfg, batch, max_pages
+        self.n_pages = n_pages if n_pages is not None else batch * max_pages
+        dev = torch.device(device)
+        self.pool = torch.zeros((self.n_pages, pb), dtype=torch.uint8, device=dev)
+        if page_table is None:
+            page_table = torch.arange(batch * max_pages, dtype=torch.int32, device=dev).view(batch, max_pages)
+        self.page_table = page_table.to(device=dev, dtype=torch.int32).contiguous()
+        self.seq_lens = torch.zeros(batch, dtype=torch.int32, device=dev)
+        self._lens_alt = torch.empty_like(self.seq_lens)
+        self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._ws = None
+        self._ws_need = {}  # workspace bytes per head count and rows
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, cu_new: torch.Tensor, max_new: int, stream=None, **kw) -> None:
+        """Appends rows cu_new[b]..cu_new[b+1]-1 of k, v [N,Hkv,D] to sequence b; the new lengths are stored in a second
+        array, which becomes ``self.seq_lens`` (the two alternate). Further arguments (cos, sin, interleaved, q, q_out,
+        k_deq, v_deq) as for mla_qcache_kv4_append."""
+        binding.mla_qcache_kv4_append(self.cfg, k, v, cu_new, self.seq_lens, max_new, self.page_table, self.pool, self.err,
+                                      seq_lens_next=self._lens_alt, stream=stream, **kw)
+        self.seq_lens, self._lens_alt = self._lens_alt, self.seq_lens
+
+    def workspace(self, heads: int, max_q: int) -> torch.Tensor:
+        need = self._ws_need.get((heads, max_q))
+        if need is None:
+            need = self._ws_need[heads, max_q] = binding.kv4_workspace_bytes(self.cfg, self.B, heads, max_q, self.max_pages)
+        if self._ws is None or self._ws.numel() < need:
+            # zeroed once: the attention keeps the counters at its start zero between calls
+            self._ws = torch.zeros(max(need, 16), dtype=torch.uint8, device=self.pool.device)
+        return self._ws
+
+    def attend(self, q: torch.Tensor, softmax_scale: float, cu_q: torch.Tensor | None = None, max_q: int = 1, out=None,
+               lse=None, causal: bool = True, window: int = 0, stream=None):
+        """Attention of query rows q [N,Hq,D], the last positions of their sequences, over the cache: out in q's type."""
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        binding.mla_qcache_kv4_attn(self.cfg, q, self.page_table, self.seq_lens, self.pool, softmax_scale, out,
+                                    self.workspace(q.shape[1], max_q), self.err, cu_q=cu_q, max_q=max_q, lse=lse, causal=causal,
+                                    window=window, stream=stream)
+        return out
+
+    def error_bits(self) -> int:
+        return int(self.err.item())

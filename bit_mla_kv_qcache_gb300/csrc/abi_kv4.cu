@@ -181,13 +181,17 @@ size_t mla_qcache_kv4_workspace_bytes(const mla_qcache_kv4_config* cfg, int32_t 
   const int G = n_heads / cfg->n_kv_heads, D = cfg->head_dim;
   const size_t few = mlaq::kv4_decode_workspace_bytes(mlaq::kv4_decode_rows(max_q, G), D, sms);
   if (!mlaq::kv4_uses_prompt(max_q, G)) return few;
-  // the rows of a call, below max_q per sequence, decide how it is cut: the most that any needs
+  // the rows of a call, up to max_q per sequence, decide how it is cut: the most that any needs. What a cut
+  // takes goes by the rows of an item (64, 128 or 256) alone; whether it is cut, by the number of row blocks.
   const int64_t max_tokens = static_cast<int64_t>(max_pages) * cfg->page_size;
   size_t most = few;
-  for (int64_t rows = 1; rows <= max_q; rows = rows < max_q && 2 * rows > max_q ? max_q : 2 * rows) {
-    const size_t w = mlaq::kv4_prompt_workspace_bytes(
-        mlaq::kv4_prompt_plan(B, cfg->n_kv_heads, static_cast<int>(rows), max_q, max_tokens, G, sms), D);
+  for (int i = 0; i < 2 * sms + 3; ++i) {
+    const int64_t rows = i == 0 ? 1 : i < 3 ? 64 * i / G + 1 : static_cast<int64_t>(i - 2) * 256 / G + 1;
+    if (rows > max_q) break;
+    const mlaq::Kv4PromptPlan z = mlaq::kv4_prompt_plan(B, cfg->n_kv_heads, static_cast<int>(rows), max_q, max_tokens, G, sms);
+    const size_t w = mlaq::kv4_prompt_workspace_bytes(z, D);
     most = most > w ? most : w;
+    if (z.line && z.rows == 256) break;
   }
   return most;
 }

@@ -5,8 +5,10 @@
 // neighbouring lanes. Rotation partners and group statistics are lane shuffles, a key-code word is
 // one thread's eight channels, and a value-code word is a column of the 8 x 8 matrix of codes that
 // eight lanes hold (transposed by three rounds of exchanges). CTA r serves row r: its threads
-// cover 512 / D or 2048 / D heads at a time and keep the row's angles in registers over all heads. Bound:
-// the bytes of the rows, read and written once.
+// cover 512 / D or 2048 / D heads at a time and keep the row's angles in registers over all heads; rows are
+// loaded two rounds ahead. Bound: instruction issue (65% busy, ALU 43%): 16K rows of 8 + 8 heads of
+// 128 with 32 query heads take 105 us, their bytes, read and written once, 63 at the card's copy rate; a
+// decode step of 32 rows 5.8 us, of which the launch and three dependent loads (offsets, page, row) are most.
 #include "append.cuh"
 #include "quant.cuh"
 
@@ -92,6 +94,7 @@ __device__ __forceinline__ QParams quantize8(const float (&x)[8], uint32_t& word
   }
   QParams qp = make_qparams15(lo, hi);
   if (!(zero == 0.f)) qp.flags |= kErrNonFinite;
+  if (__fmaf_rn(15.f, qp.s, qp.m) >= 65520.f) qp.flags |= kErrRange;  // the top level would not fit FP16
   word = quant_codes8(x, qp, n);
   return qp;
 }
@@ -187,10 +190,11 @@ cudaError_t launch_as(const Kv4AppendParams& p, cudaStream_t stream) {
 }
 
 // Few rows (decode steps): 256 threads to a row, for its latency. Many: 64, which place the row and
-// read its angles half as often.
+// read its angles less often. 256 and 64 threads, 8 + 8 and 32 heads of 128: 64 rows 5.8 and 11.5 us, 512 rows 8.4 and
+// 13.4, 1K 13.0 and 15.8, 2K 23.1 and 22.7; 16K rows 105 with 64.
 template <int D, int NG>
 cudaError_t launch(const Kv4AppendParams& p, cudaStream_t stream) {
-  const bool few = p.n_rows <= 512;
+  const bool few = p.n_rows < 2048;
   if (p.f16) return few ? launch_as<D, NG, true, 256>(p, stream) : launch_as<D, NG, true, 64>(p, stream);
   return few ? launch_as<D, NG, false, 256>(p, stream) : launch_as<D, NG, false, 64>(p, stream);
 }

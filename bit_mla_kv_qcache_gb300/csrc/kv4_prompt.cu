@@ -3,34 +3,45 @@
 // token, head of the group), 128 to a tile of queries.
 //
 // One CTA per SM, 16 warps. Per tile of 128 cached tokens:
-//   warps 8-11   one token per thread: the token's codes become FP16 values min + code * scale (one
+//   unpacking    one token per thread: the token's codes become FP16 values min + code * scale (one
 //                rounding) in shared memory, keys and values, two stages each;
-//   warp 12      one thread issues S = Q K^T (128 rows x 128 tokens, both operands in shared memory)
+//   warp 12      one lane issues S = Q K^T (128 rows x 128 tokens, both operands in shared memory)
 //                and O += P V (P from tensor memory);
-//   warp 13      asks for the codes of later tiles, so that they are in L2 when warps 8-11 read them;
-//   warps 0-3, 4-7  two softmax groups, one row per thread: S is read from tensor memory once (its
-//                maximum, then the weights), P replaces it there as FP16. The running max is raised,
+//   warp 13      asks for the codes of later tiles in L2 or copies them to shared memory, a lane per page;
+//   softmax      one row per thread: S is read from tensor memory once (its maximum, then the weights), P
+//                replaces it there as FP16, handed over in two halves. The running max is raised,
 //                and O rescaled in place, only when a score exceeds it by more than 2^8.
 // The softmax groups take the registers that the others give up (setmaxnreg), so every role has its own
-// loop over the CTA's work.
-// The groups alternate so that the tensor cores work for one while the other takes its softmax: with
-// more than 128 rows they hold two tiles of queries and see every token tile. With at most 128 rows one
-// group takes the softmax of every token tile and the other unpacks the values, while warps 8-11 unpack
-// the keys (unpacking is what a tile then waits for).
+// loop over the CTA's work. The kernel exists in two forms:
+//   two tiles of queries (more than 128 rows): two softmax groups of four warps, which alternate so that the
+//     tensor cores work for one while the other takes its softmax; warps 8-11 unpack keys and values, loaded into
+//     registers a tile ahead. Against one tile of queries per CTA: 654 and 1004 us (two chunks of 4K, the second of each
+//     prompt, 32 heads on 8, D = 128), 133 and 143 us (256 rows of eight sequences up to 32K).
+//   one tile: warps 0-3 take the softmax of every token tile, 4-7 unpack values, 8-11 keys, from copies of the pages
+//     in shared memory, two tiles ahead (loaded into registers: 93 us for 40 rows of eight sequences up to 32K, copied
+//     80-85). With at most 64 rows the tile holds them twice: one twin takes the first 64 tokens of a token tile, the
+//     other the rest, and their sums join at the end (84 us without the twins, 80 with; 64 rows 86 and 83).
 // Tensor memory: S0, S1 (128 columns each), O0, O1 (D each). A step's S overwrites the P of two steps
 // before; products of one thread run in the order of their issue.
 //
 // Channels keep the order in which a code word unpacks: eight channels of a word in the order 0 4 1 5
 // 2 6 3 7, for keys matched by the queries, for values undone when a row is stored.
 //
-// kExact (when the log-sum-exp is asked for; the rounding of a key to FP16, 2^-12 of it, shows there as
+// kExact (the rounding of a key to FP16, up to 2^-11 of it, shows in the log-sum-exp as
 // ~1e-4): scores from exact products. With the scale s = s1 + s2 cut after seven bits, n s1 and n s2 fit FP16
 // for every code n: two key operands. The minimum enters as sixteen more channels: its value for each
-// group against the sum of the group's queries, in two FP16 parts. One stage of keys then has the room.
+// group against the sum of the group's queries, in two FP16 parts. One stage of keys then has the room; its halves
+// (of the channels) fill and empty one by one. Taken when the log-sum-exp is asked for, and always with one tile of queries
+// of 128 channels, where it costs nothing (40 rows: 81 us, rounded keys 79).
 //
-// Work: with many items (sequence, kv head, row block) one CTA per item, those that see the most
-// tokens first; with few, they are cut so that every SM has one part of one item, or, where the parts do
+// Work: one CTA per item (sequence, kv head, row block), those that see the most tokens first; or items cut
+// over the SMs (see kv4_prompt_plan), so that every SM has one part of one item, or, where the parts do
 // not fit, laid on one line and cut evenly (as in the kernel for few rows).
+//
+// Bound: the chain of a group's tile: S, its way to the registers, exponentials, P V. Two chunks of 4K over 8K (824
+// GFLOP) take 654 us where the card's rate for large BF16 products gives 424: the tensor pipe is 46% busy, issue 44%; tensor memory
+// is full, so a group's next S waits for its P V. 40 rows of eight sequences up to 32K: 80-85 us, 16 for their bytes: per
+// token tile of ~3 k cycles the unpacking of two-part keys takes ~1.5 k and waits for the products of the half before.
 #include <algorithm>
 #include <type_traits>
 

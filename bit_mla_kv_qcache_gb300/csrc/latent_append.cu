@@ -4,7 +4,9 @@
 // With few rows a CTA of four warps serves one: warp 0 normalizes the latent (sixteen channels per lane,
 // sum of squares in float32 over the warp), the others rotate the positional key and the queries, eight
 // lanes per head of 64 channels. With many, each warp serves a row of its own, which is placed once and
-// whose angles are read once. Bound: the bytes of the rows, read and written once.
+// whose angles are read once. Bound: for many rows the latency of a row's loads (16K rows with 16 heads 18 us, their
+// bytes, read and written once, 10 at the card's copy rate; issue 52%, long waits on loads); for a decode step the launch and
+// three dependent loads (32 rows 2.8 us).
 #include "append.cuh"
 
 namespace mlaq {
@@ -105,7 +107,9 @@ __global__ void __launch_bounds__(kLatThreads, 8) latent_append_kernel(const Lat
 
 cudaError_t launch_latent_append(const LatentAppendParams& p, cudaStream_t stream) {
   const int tail = p.seq_next ? (p.B + kLatThreads - 1) / kLatThreads : 0;
-  if (p.n_rows < 2048) {  // below, a warp to a row would leave SMs idle
+  // Four warps to a row and one, 16 heads: 256 rows 3.0 and 3.8 us, 1K 3.5 and 4.0, 2K 5.4 and 4.9, 4K 9.1 and 6.2
+  // (below 2K rows a warp to a row leaves SMs idle).
+  if (p.n_rows < 2048) {
     latent_append_kernel<4><<<p.n_rows + tail, kLatThreads, 0, stream>>>(p, p.n_rows);
   } else {
     const int ctas = (p.n_rows + 3) / 4;

@@ -556,8 +556,8 @@ size_t mla_qcache_kv4_page_bytes(const mla_qcache_kv4_config* cfg);
  * Rows from cu_new[B] on (a padded batch) are left alone, in every output. max_new: bound on the rows
  * per sequence; a sequence with more has its rows skipped (MLA_QCACHE_DEV_ROWS).
  * rotation NULL: none. Outputs must not overlap inputs or one another.
- * A group with a NaN or an infinity sets MLA_QCACHE_DEV_NONFINITE, one beyond the FP16 range
- * MLA_QCACHE_DEV_RANGE (what the cache then holds for it is not specified).
+ * A group with a NaN or an infinity sets MLA_QCACHE_DEV_NONFINITE, one whose scale, minimum or largest
+ * level is beyond the FP16 range MLA_QCACHE_DEV_RANGE (what the cache then holds for it is not specified).
  * Errors: bad config or dtype -> MLA_QCACHE_ERR_CONFIG; B < 1 or > 2^20, n_rows < 0, max_new < 1,
  * max_pages < 1, n_pages < 1, n_heads < 1 or > 4096 (with q), bad rotation, negative strides,
  * overlapping buffers -> MLA_QCACHE_ERR_SHAPE; missing pointers, q without q_out -> MLA_QCACHE_ERR_NULL;
@@ -571,9 +571,11 @@ int mla_qcache_kv4_append(const mla_qcache_kv4_config* cfg, int32_t dtype, int32
                           uint8_t* pool, int64_t n_pages, int32_t* err_word, void* stream);
 
 /*
- * Bytes of device workspace for mla_qcache_kv4_attn. The caller zeroes the first 8192 bytes once
- * (counters, left zero by every call); calls that share a workspace must not overlap in time, and a
- * workspace of another operator is not one of these. Returns 0 on invalid arguments.
+ * Bytes of device workspace for mla_qcache_kv4_attn, enough for every call of B sequences with up to
+ * max_q rows each and up to max_pages pages. The caller zeroes the first 8192 bytes once (counters, left
+ * zero by every call but one that reports MLA_QCACHE_DEV_TIMEOUT); calls that share a workspace, replays of
+ * captured ones among them, must not overlap in time, and a workspace of another operator is not one of
+ * these. Returns 0 on invalid arguments.
  */
 size_t mla_qcache_kv4_workspace_bytes(const mla_qcache_kv4_config* cfg, int32_t B, int32_t n_heads, int32_t max_q,
                                       int32_t max_pages);
@@ -590,7 +592,11 @@ size_t mla_qcache_kv4_workspace_bytes(const mla_qcache_kv4_config* cfg, int32_t 
  *   (optional). A row that sees no token gets out = 0, lse = -inf.
  * Scores are products of the exact codes with the queries (prescaled by a power of two to FP16: every
  * value within 2^-14 of the row's largest enters exactly, smaller ones are off by at most 2^-39 of it),
- * summed in float32; weights enter the readout in FP16.
+ * summed in float32, except where max_q * n_heads / n_kv_heads is above 128 (above 32 at D = 64) and no lse is
+ * asked for: keys are then rounded to FP16. Above 32 such rows values are rounded to FP16. Weights enter
+ * the readout in FP16.
+ * Capture: a call may be captured into a graph; grid and path go by the sizes of the call, the lengths are
+ * read on the device at each replay.
  * max_q: bound on the rows per sequence; a sequence with more sets MLA_QCACHE_DEV_ROWS, a length
  * outside [0, max_pages * P] MLA_QCACHE_DEV_SEQ_OVERFLOW (read as 0), a page id outside [0, n_pages)
  * MLA_QCACHE_DEV_BAD_PAGE (its tokens are left out).

@@ -127,6 +127,11 @@ def test_append_reports_what_it_skips():
     assert run([0, 1, 4], [0, 0], [[0], [1]], k=bad)[0] == q.DEV_NONFINITE
     bad[2, 1, 5] = 3e38
     assert run([0, 1, 4], [0, 0], [[0], [1]], k=bad)[0] == q.DEV_RANGE
+    # scale and minimum fit FP16; the top level does (scale 8704: 65280) or not (scale 8733.87 -> 8736: 65536)
+    for top, word in ((65280.0, 0), (65504.0, q.DEV_RANGE)):
+        f16 = torch.zeros(4, 2, 64, device="cuda").half()
+        f16[2, 1, 5], f16[2, 1, 6] = top, -top
+        assert run([0, 1, 4], [0, 0], [[0], [1]], k=f16)[0] == word
 
 
 # ---------------------------------------------------------------- attention
@@ -495,3 +500,65 @@ def test_a_stream_of_ones_own():
     b, _ = c.run(stream=s)
     s.synchronize()
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("G,n", [(4, 6), (4, 11), (8, 12), (4, 60)])
+def test_captured_many_rows_replay_over_other_lengths(G, n):
+    """The calls of the many-row kernels captured once, replayed while the sequences grow, shrink and empty."""
+    c = Case([40, 4500, 9], [n, n, n], Hkv=1, G=G, P=32, seed=n, spare=2)
+    full, lens, table, cu = list(c.lens), ints(c.lens), ints(c.table), offsets(c.new)
+    out, ws = torch.empty_like(c.q), c.workspace()
+    lse = torch.empty(sum(c.new), c.Hq, device="cuda")
+
+    def call():
+        q.mla_qcache_kv4_attn(c.cfg, c.q, table, lens, c.pool, 0.1, out, ws, c.err, cu_q=cu, max_q=n, lse=lse)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for lengths in (full, [min(n, full[0]), 130, 0], [1, 4097, 9], [0, 0, 0], [33, 2047, 1], full):
+        lens.copy_(ints(lengths))
+        g.replay()
+        torch.cuda.synchronize()
+        c.lens = lengths
+        a, l = c.check(scale=0.1)
+        assert torch.equal(a, out) and torch.equal(l, lse)
+
+
+def test_workspace_serves_every_call_up_to_its_sizes():
+    """One workspace of max_q rows and the table's pages for calls of fewer rows, in any order (the counters stay zero)."""
+    for Hkv, G in ((1, 4), (13, 4), (1, 300)):
+        c = Case([5000, 70], [700 if G == 4 else 3, 1], Hkv=Hkv, G=G, D=64, P=256, seed=G)
+        ws, most = c.workspace(700), c.new[0]
+        for n in (most, 1, min(most, 9), min(most, 20), min(most, 33), min(most, 65), 2):
+            c.new = [n, 1]
+            c.run(ws=ws, max_q=700, lse=bool(n & 1), qq=c.q[:n + 1])
+            torch.cuda.synchronize()
+            assert int(c.err) == 0 and not ws[:8192].any()
+
+
+def test_cache_object_prompt_then_steps():
+    """KV4Cache: a prompt with rotation, then decode steps, against dense attention over what the cache holds."""
+    rng, D, Hkv, G = np.random.default_rng(2), 128, 2, 4
+    cfg = q.make_kv4_config(Hkv, D, group=64, page_size=32)
+    cache = q.KV4Cache(cfg, 2, 6)
+    cos, sin = (torch.tensor(x).cuda() for x in tables(200, D))
+    for new in ([100, 37], [1, 1], [1, 1], [4, 2]):
+        rows = sum(new)
+        qkv = torch.tensor(rng.standard_normal((rows, Hkv * (G + 2), D)), dtype=torch.float32).bfloat16().cuda()
+        qr = torch.empty(rows, Hkv * G, D, dtype=torch.bfloat16, device="cuda")
+        cache.append(qkv[:, Hkv * G:-Hkv], qkv[:, -Hkv:], offsets(new), max(new), cos=cos, sin=sin, q=qkv[:, :Hkv * G], q_out=qr)
+        lse = torch.empty(rows, Hkv * G, device="cuda")
+        out = cache.attend(qr, D ** -0.5, cu_q=offsets(new), max_q=max(new), lse=lse)
+        torch.cuda.synchronize()
+        assert cache.error_bits() == 0
+        pool, r = cache.pool.cpu().numpy(), 0
+        for b, n in enumerate(new):
+            T = int(cache.seq_lens[b])
+            k, v, vs, most = ref.read_sequence(pool, cache.page_table[b].cpu().numpy(), T, Hkv, D, 64, 32)
+            qq = qr[r:r + n].double().cpu().numpy()
+            want, wl, bound = ref.attention(qq, k, v, vs, most, D ** -0.5, ref.seen(T, n, True, 0), torch.bfloat16, max(new) * G > 16)
+            assert (np.abs(out[r:r + n].double().cpu().numpy() - want) <= bound).all()
+            r += n
+    assert cache.seq_lens.tolist() == [106, 41]
