@@ -206,7 +206,8 @@ int mla_qcache_kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t
   if (dtype != MLA_QCACHE_BF16 && dtype != MLA_QCACHE_FP16) return MLA_QCACHE_ERR_CONFIG;
   if (B < 1 || B > (1 << 20) || n_heads < 1 || n_heads > 4096 || n_heads % cfg->n_kv_heads || n_rows < 0 ||
       static_cast<int64_t>(n_rows) * n_heads > 0x7fffffff || max_q < 1 || max_pages < 1 || n_pages < 1 || window < 0 ||
-      (window > 0 && !causal) || !std::isfinite(softmax_scale))
+      (window > 0 && !causal) || !std::isfinite(softmax_scale) ||
+      static_cast<int64_t>(max_pages) * cfg->page_size > 0x7ffff000)  // positions and steps are counted in 32 bits
     return MLA_QCACHE_ERR_SHAPE;
   if (!cu_q && (max_q != 1 || n_rows != B)) return MLA_QCACHE_ERR_SHAPE;
   if (n_rows == 0) return MLA_QCACHE_OK;

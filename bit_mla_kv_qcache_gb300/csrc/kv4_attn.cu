@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
   constexpr int kHeld = 256;  // sequences that the quick way of sharing the work takes
   __shared__ int s_last, s_steps[kHeld], s_items[kHeld];  // of each sequence: steps of an item, items
   __shared__ Place s_at;
-  __shared__ int s_full[kWarps][3];  // steps that every row sees whole: from, to; tokens seen by any
+  __shared__ int s_full[kWarps][4];  // steps that every row sees whole: from, to; tokens seen by any: end, begin
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
   int flags = 0;
 
@@ -439,6 +439,7 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
         s_full[warp][0] = (last.x + kTok - 1) / kTok;
         s_full[warp][1] = first.y / kTok;
         s_full[warp][2] = last.y;
+        s_full[warp][3] = first.x;
       }
       __syncwarp();
     }
@@ -453,7 +454,8 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
     uint32_t next_st = 0, present = 0;  // two bits per stage
     auto page_id = [&](int t) {
       const int tok = t * kTok + kTile * (lane & 1);
-      return tok < full[2] ? __ldg(p.page_table + static_cast<size_t>(s_at.b) * p.max_pages + (tok >> p.p_shift)) : -2;
+      // tiles that no row sees are not asked for: their pages may be gone (behind a sliding window)
+      return tok < full[2] && tok + kTile > full[3] ? __ldg(p.page_table + static_cast<size_t>(s_at.b) * p.max_pages + (tok >> p.p_shift)) : -2;
     };
     int32_t pid = page_id(next);
     auto issue = [&]() {

@@ -467,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       n_tiles = sg.tiles, steps = steps_of();
       const int tile0 = sg.tile;
       const int t_end = visible(p, sg.T, sg.n, min(sg.n - 1, (sg.rb * R + R - 1) / p.G)).y;
+      const int t_begin = visible(p, sg.T, sg.n, sg.rb * R / p.G).x;  // pages before it may be gone (behind a sliding window)
       auto scale_of = [](uint32_t w) { return __ushort_as_half(static_cast<unsigned short>(w)); };
       auto min_of = [](uint32_t w) { return __ushort_as_half(static_cast<unsigned short>(w >> 16)); };
       constexpr int kHalves = one_k ? 2 : 1;  // one stage of keys: its halves (of the channels) fill and empty one by one
@@ -480,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       uint2 num[NG], cur[NG];
       auto page_of = [&](int j) -> int32_t {
         const int tok = (tile0 + j) * kTok + tok_row;
-        return j < n_tiles && tok < t_end ? __ldg(table + (tok >> p.p_shift)) : -2;
+        return j < n_tiles && tok >= t_begin && tok < t_end ? __ldg(table + (tok >> p.p_shift)) : -2;
       };
       auto token_base = [&](int32_t id) -> const uint8_t* {
         if (static_cast<uint32_t>(id) < static_cast<uint32_t>(p.n_pages))
@@ -528,7 +529,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           const uint32_t codes = base + Ge::ring_at(two) + st * Ge::kStage;
           wait(c_full + st, ph);
           bad = (s_bad_pages[st] >> (tok_row >> page_sh)) & 1;
-          const bool none = bad || (tile0 + j) * kTok + tok_row >= t_end;
+          const int tok = (tile0 + j) * kTok + tok_row;
+          const bool none = bad || tok < t_begin || tok >= t_end;
           hidden = __ballot_sync(0xffffffffu, bad);
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
@@ -640,10 +642,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         const int32_t* table = p.page_table + static_cast<size_t>(sg.b) * p.max_pages;
         const size_t region = static_cast<size_t>(sg.h) * kv4_head_bytes(D, NG, p.P);
         const int tile0 = sg.tile, t_end = visible(p, sg.T, sg.n, min(sg.n - 1, (sg.rb * R + R - 1) / p.G)).y;
+        const int t_begin = visible(p, sg.T, sg.n, sg.rb * R / p.G).x;
         const int part = min(p.P, kTok);  // tokens of a page that are in a tile
         auto page_of = [&](int j) -> int32_t {
           const int tok = (tile0 + j) * kTok + lane * part;
-          return j < n_tiles && lane * part < kTok && tok < t_end ? __ldg(table + (tok >> p.p_shift)) : -2;
+          return j < n_tiles && lane * part < kTok && tok + part > t_begin && tok < t_end ? __ldg(table + (tok >> p.p_shift)) : -2;
         };
         auto good = [&](int32_t id) { return static_cast<uint32_t>(id) < static_cast<uint32_t>(p.n_pages); };
         auto page_at = [&](int32_t id, int j, int& tp) -> const uint8_t* {

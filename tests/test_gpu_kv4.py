@@ -239,6 +239,22 @@ def test_sliding_window(window, n, G):
     Case([n, 150, 201], [n, n, min(n, 7)], G=G, seed=window).check(window=window)
 
 
+@pytest.mark.parametrize("P", [16, 64, 256])
+@pytest.mark.parametrize("n,G", [(1, 4), (5, 3), (6, 4), (12, 4), (30, 4), (70, 4)])
+def test_pages_behind_the_window_may_be_gone(n, G, P):
+    """A loop that frees the pages behind its window leaves any id there; steps and tiles of a kernel begin before the window."""
+    window = 100
+    c = Case([n, 700, 450], [n, n, min(n, 3)], G=G, P=P, seed=n + P)
+    full = c.table.copy()
+    a, l = c.check(window=window)
+    for b, (T, m) in enumerate(zip(c.lens, c.new)):
+        c.table[b, :max(0, T - m - window + 1) // P] = -1
+    b, k = c.run(window=window)
+    torch.cuda.synchronize()
+    assert (c.table != full).any() and int(c.err) == 0
+    assert torch.equal(a, b) and torch.equal(l, k)
+
+
 @pytest.mark.parametrize("n,G", [(1, 4), (3, 5), (24, 3)])
 def test_rows_that_see_nothing(n, G):
     """More query rows than tokens, and an empty cache: those rows give 0 and -inf, the others are untouched by them."""

@@ -108,6 +108,7 @@ def test_attention_refusals(lib):
     assert _attn(lib, dtype=7) == -2 and _attn(lib, cfg=q.make_kv4_config(4, 128, group=100)) == -2
     for kw in [dict(B=0), dict(heads=0), dict(heads=6), dict(heads=4100), dict(rows=-1), dict(max_q=0, cu=P16), dict(pages=0),
                dict(n_pages=0), dict(window=-1), dict(window=4, causal=0), dict(scale=float("nan")), dict(scale=float("inf")),
+               dict(pages=1 << 27),  # 64 x 2^27 positions
                dict(rows=3), dict(max_q=2), dict(rows=1 << 30, cu=P16), dict(qv=_view(row=-8))]:
         assert _attn(lib, **kw) == -3, kw
     for kw in [dict(qv=None), dict(qv=_view(None)), dict(table=None), dict(lens=None), dict(pool=None), dict(out=None),
