@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bars[19];  // k_full[2] k_free[2] v_full[2] v_free[2] s_full[2] p_ready[2] o_done c_full[2] c_free[2]
   __shared__ uint32_t s_tmem;
-  __shared__ Seg s_seg;
+  __shared__ Seg s_seg, s_next;  // here, and the one after it
   __shared__ long long s_part[kThreads / 32];
   __shared__ int s_most[kThreads / 32], s_last;
   __shared__ float2 s_side[kTok];  // max and sum of a row under half of the tokens
@@ -446,11 +446,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   // Two barriers of all warps frame a segment: queries in place; results stored and the next segment set.
   auto leave_segment = [&](int n_tiles, int steps) -> bool {
     __syncthreads();
+    if (line) {
+      constexpr int kWords = sizeof(Seg) / 4;
+      if (tid < kWords) reinterpret_cast<volatile uint32_t*>(&s_seg)[tid] = reinterpret_cast<volatile uint32_t*>(&s_next)[tid];
+      __syncthreads();
+    }
     tiles_done += n_tiles;
     steps_done[0] += (steps + 1) >> 1;
     steps_done[1] += steps >> 1;
     ++segs;
-    return !s_abort && sg.valid;
+    return !s_abort && line && sg.valid;
   };
   constexpr bool one_k = kExact;  // one stage of keys
 
@@ -706,6 +711,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         }
       } else {
         __syncthreads();
+        if (warp == 15 && lane == 0 && line) {  // the next segment of the CTA's stretch, meanwhile
+          s_next = s_seg;
+          s_next.at = min(s_next.end, s_next.item0 + s_next.item_tiles + kStart);
+          next_item(p, s_next, line, R);
+        }
       }
       if (warp == 12) {
         // ---- products, issued by one lane of the whole warp
@@ -1134,15 +1144,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         }
       }
       tc5::fence_before();
-      softmax_barrier(n_softmax);
-      if (tid == 0) {  // the next segment of the CTA's stretch
-        Seg& s = s_seg;
-        s.valid = 0;
-        if (line) {
-          s.at = min(s.end, s.item0 + s.item_tiles + kStart);
-          next_item(p, s, line, R);
-        }
-      }
     } while (leave_segment(n_tiles, steps));
   }
   tc5::fence_before();
