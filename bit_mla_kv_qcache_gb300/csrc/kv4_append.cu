@@ -77,23 +77,33 @@ __device__ __forceinline__ uint32_t even_fields_first(uint32_t v) {
   return e | (o << 16);
 }
 
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float y;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
 // Quantizes the group that this lane's eight values belong to (LG lanes per group).
 template <int LG>
 __device__ __forceinline__ QParams quantize8(const float (&x)[8], uint32_t& word, float (&n)[8]) {
-  float lo = x[0], hi = x[0], zero = 0.f;
+  float lo = fminf(x[0], x[1]), hi = fmaxf(x[0], x[1]);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    lo = fminf(lo, x[k]);
-    hi = fmaxf(hi, x[k]);
-    zero = __fmaf_rn(x[k], 0.f, zero);  // NaN if a value is NaN or infinite
-  }
+  for (int k = 2; k < 8; k += 2) lo = min3(lo, x[k], x[k + 1]), hi = max3(hi, x[k], x[k + 1]);
+  float2 none = make_float2(0.f, 0.f);  // NaN if a value is NaN or infinite
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) none = add2(none, mul2(make_float2(x[k], x[k + 1]), make_float2(0.f, 0.f)));
 #pragma unroll
   for (int o = 1; o < LG; o <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
   QParams qp = make_qparams15(lo, hi);
-  if (!(zero == 0.f)) qp.flags |= kErrNonFinite;
+  if (!(none.x + none.y == 0.f)) qp.flags |= kErrNonFinite;
   if (__fmaf_rn(15.f, qp.s, qp.m) >= 65520.f) qp.flags |= kErrRange;  // the top level would not fit FP16
   word = quant_codes8(x, qp, n);
   return qp;
@@ -148,7 +158,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) kv4_append_kernel(c
     uint32_t word;
     float n[8];
     const QParams qp = quantize8<kGroupLanes>(x, word, n);
-    const uint32_t col = even_fields_first(transpose_nibbles(word, i & 7));
+    uint32_t col = 0;
+    if (__any_sync(0xffffffffu, !is_k)) col = even_fields_first(transpose_nibbles(word, i & 7));
     if (hh >= Hkv2) continue;
     const int h = is_k ? hh : hh - p.Hkv;
     flags |= qp.flags;
