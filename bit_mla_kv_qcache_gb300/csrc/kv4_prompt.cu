@@ -15,11 +15,11 @@
 // loop over the CTA's work. The kernel exists in two forms:
 //   two tiles of queries (more than 128 rows): two softmax groups of four warps, which alternate so that the
 //     tensor cores work for one while the other takes its softmax; warps 8-11 unpack keys and values, loaded into
-//     registers a tile ahead. Against one tile of queries per CTA: 654 and 1004 us (two chunks of 4K, the second of each
+//     registers a tile ahead. Against one tile of queries per CTA: 649 and 1004 us (two chunks of 4K, the second of each
 //     prompt, 32 heads on 8, D = 128), 133 and 143 us (256 rows of eight sequences up to 32K).
 //   one tile: warps 0-3 take the softmax of every token tile, 4-7 unpack values, 8-11 keys, from copies of the pages
 //     in shared memory, two tiles ahead (loaded into registers: 93 us for 40 rows of eight sequences up to 32K, copied
-//     80-85). With at most 64 rows the tile holds them twice: one twin takes the first 64 tokens of a token tile, the
+//     82). With at most 64 rows the tile holds them twice: one twin takes the first 64 tokens of a token tile, the
 //     other the rest, and their sums join at the end (84 us without the twins, 80 with; 64 rows 86 and 83).
 // Tensor memory: S0, S1 (128 columns each), O0, O1 (D each). A step's S overwrites the P of two steps
 // before; products of one thread run in the order of their issue.
@@ -39,8 +39,8 @@
 // not fit, laid on one line and cut evenly (as in the kernel for few rows).
 //
 // Bound: the chain of a group's tile: S, its way to the registers, exponentials, P V. Two chunks of 4K over 8K (824
-// GFLOP) take 654 us where the card's rate for large BF16 products gives 424: the tensor pipe is 46% busy, issue 44%; tensor memory
-// is full, so a group's next S waits for its P V. 40 rows of eight sequences up to 32K: 80-85 us, 16 for their bytes: per
+// GFLOP) take 649 us where the card's rate for large BF16 products gives 424: the tensor pipe is 46% busy, issue 44%; tensor memory
+// is full, so a group's next S waits for its P V. 40 rows of eight sequences up to 32K: 82 us, 16 for their bytes: per
 // token tile of ~3 k cycles the unpacking of two-part keys takes ~1.5 k and waits for the products of the half before.
 #include <algorithm>
 #include <type_traits>
