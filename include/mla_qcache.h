@@ -556,6 +556,7 @@ size_t mla_qcache_kv4_page_bytes(const mla_qcache_kv4_config* cfg);
  * Rows from cu_new[B] on (a padded batch) are left alone, in every output. max_new: bound on the rows
  * per sequence; a sequence with more has its rows skipped (MLA_QCACHE_DEV_ROWS).
  * rotation NULL: none. Outputs must not overlap inputs or one another.
+ * Sequences may share pages, but not one that a call appends to for two of them.
  * A group with a NaN or an infinity sets MLA_QCACHE_DEV_NONFINITE, one whose scale, minimum or largest
  * level is beyond the FP16 range MLA_QCACHE_DEV_RANGE (what the cache then holds for it is not specified).
  * Errors: bad config or dtype -> MLA_QCACHE_ERR_CONFIG; B < 1 or > 2^20, n_rows < 0, max_new < 1,

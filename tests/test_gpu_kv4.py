@@ -233,6 +233,17 @@ def test_rows_of_several_blocks_and_more_items_than_the_gpu_holds():
     Case([40] * 160, [20] * 160, Hkv=2, G=1, seed=2, D=64).check()   # 320 items: one CTA each
 
 
+@pytest.mark.parametrize("n,G", [(1, 2), (5, 8), (20, 4)])
+def test_many_sequences(n, G):
+    """More sequences than the quick ways of sharing the work hold; a few long ones among many that are short or empty."""
+    rng = np.random.default_rng(n)
+    lens = rng.integers(0, 20, 700)
+    lens[[3, 350, 699]] = [300, 90, 150]
+    new = np.minimum(rng.integers(0, n + 1, 700), lens)
+    c = Case(lens.tolist(), new.tolist(), Hkv=1, G=G, D=64, P=16, seed=n, pad=3)
+    c.check(max_q=n)
+
+
 @pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 40, 100, 1000])
 @pytest.mark.parametrize("n,G", [(1, 3), (5, 2), (30, 4)])
 def test_sliding_window(window, n, G):
