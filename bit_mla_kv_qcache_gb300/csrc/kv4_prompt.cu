@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   constexpr int kTry = 9;
   __shared__ int s_count[kTry + 1];  // parts that a share would make; tiles in all
   __shared__ volatile int s_abort, s_any_hidden;
+  __shared__ volatile uint32_t s_unpacked;  // two tiles of queries: token tiles that warp 8 has unpacked so far
   __shared__ uint32_t s_bad_pages[2];  // of a stage of codes: bit i, its i-th page
   __shared__ __align__(16) uint32_t s_hidden[4][4];  // tokens of a tile (modulo four) whose page id is bad
   uint64_t *const k_full = bars, *const k_free = bars + 2, *const v_full = bars + 4, *const v_free = bars + 6,
@@ -395,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   if (tid == 0) {
     s_abort = 0;
     s_any_hidden = 0;
+    s_unpacked = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + i, 4);  // one arrival per warp
       mbar_init(v_full + i, 4);
@@ -630,7 +632,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(v_full + st);
+          if (lane == 0) {
+            mbar_arrive(v_full + st);
+            if (two && warp == 8) s_unpacked = J + 1;
+          }
           if (two) load_codes(vw, next ? next + p.P * (D / 2) + tp * (D / 2) : nullptr);
         }
         if (s_abort) break;
@@ -694,9 +699,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         for (int j = 1; j < kAhead; ++j) prefetch(j);
         __syncthreads();
         if (two) {
-          for (int j = 0; j < n_tiles && !s_abort; ++j) {  // a tile for each that is unpacked
+          // A tile for each that is unpacked, by a count that only grows: nothing waits for this warp, so a barrier's phase
+          // could come and go while it is late. Where the count does not come the other waits end the call.
+          for (int j = 0; j < n_tiles && !s_abort; ++j) {
             prefetch(j + kAhead);
-            wait(v_full + ((tiles_done + j) & 1), ((tiles_done + j) >> 1) & 1);
+            const long long t0 = clock64();
+            while (static_cast<int32_t>(s_unpacked - (tiles_done + j)) <= 0 && !s_abort && clock64() - t0 <= kBudget) __nanosleep(64);
           }
         }
         for (; sent > 0 && sent < n_tiles; ++sent) {

@@ -1,0 +1,26 @@
+"""4-bit grouped-query cache on the GPU at the edges of its kernels: waits, page ids, windows, sizes of numbers and
+row counts that the first tests leave out."""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_kv4 import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("D,n,lse", [(128, 64, False), (64, 64, True), (128, 130, True)])
+def test_two_tiles_of_queries_over_many_segments_end_without_a_timeout(D, n, lse):
+    """Over 128 rows, items cut over the SMs: a CTA goes through segments of one tile and of many. The warp that asks
+    for later pages runs beside the others without holding them up; every call ends with its results and no error bit."""
+    rng = np.random.default_rng(n)
+    lens = rng.integers(n, 4500, 40)
+    lens[:6] = [n, n + 1, 4499, 127 + n, 128 + n, 129 + n]
+    c = Case([int(x) for x in lens], [n] * 40, Hkv=4 if n == 64 else 1, G=4, D=D, P=32, seed=n)
+    ws = c.workspace()
+    first = c.run(lse=lse, ws=ws)
+    for _ in range(10):
+        again = c.run(lse=lse, ws=ws)
+        assert torch.equal(first[0], again[0]) and (not lse or torch.equal(first[1], again[1]))
+    torch.cuda.synchronize()
+    assert int(c.err) == 0 and not ws[:8192].any() and torch.isfinite(first[0]).all()
