@@ -210,7 +210,7 @@ __device__ __forceinline__ void sequence(const Kv4AttnParams& p, int b, int& T, 
 __device__ __forceinline__ int2 visible(const Kv4AttnParams& p, int T, int n, int i) {
   const int pos = T - n + i;
   const int hi = p.causal ? max(0, min(T, pos + 1)) : T;
-  const int lo = p.window ? max(0, pos - p.window + 1) : 0;
+  const int lo = p.window && pos >= p.window ? pos - p.window + 1 : 0;  // no overflow before the first token
   return make_int2(lo, hi);
 }
 

@@ -24,3 +24,10 @@ def test_two_tiles_of_queries_over_many_segments_end_without_a_timeout(D, n, lse
         assert torch.equal(first[0], again[0]) and (not lse or torch.equal(first[1], again[1]))
     torch.cuda.synchronize()
     assert int(c.err) == 0 and not ws[:8192].any() and torch.isfinite(first[0]).all()
+
+
+@pytest.mark.parametrize("n,G", [(1, 4), (6, 4), (20, 1), (20, 2), (40, 4)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 30])
+def test_windows_of_any_size_with_more_rows_than_tokens(n, G, window):
+    """A window that no sequence fills is none; rows before the first token see nothing."""
+    Case([0, max(1, n - 3), 300], [n, n, n], G=G, seed=n).check(window=window)
