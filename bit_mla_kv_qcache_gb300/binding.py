@@ -47,6 +47,9 @@ def make_config(bits_c=4, page_size=128, n_sink=4, n_recent=128, clip_q=None, bi
     return Config(bits_c, bits_r, page_size, n_sink, n_recent, clip_q)
 
 
+KV4_COUNTER_BYTES = 8192  # the start of mla_qcache_kv4_attn's workspace that is zero before its first call
+
+
 class KV4Config(ctypes.Structure):
     """mla_qcache_kv4_config."""
     _fields_ = [("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("group", ctypes.c_int32),

@@ -101,7 +101,7 @@ class KV4Cache:
         self.seq_lens = torch.zeros(batch, dtype=torch.int32, device=dev)
         self._lens_alt = torch.empty_like(self.seq_lens)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
-        self._ws = None
+        self._ws = {}  # per stream
         self._ws_need = {}  # workspace bytes per head count and rows
 
     def append(self, k: torch.Tensor, v: torch.Tensor, cu_new: torch.Tensor, max_new: int, stream=None, **kw) -> None:
@@ -112,23 +112,39 @@ class KV4Cache:
                                       seq_lens_next=self._lens_alt, stream=stream, **kw)
         self.seq_lens, self._lens_alt = self._lens_alt, self.seq_lens
 
-    def workspace(self, heads: int, max_q: int) -> torch.Tensor:
+    def workspace(self, heads: int, max_q: int, stream=None) -> torch.Tensor:
+        """Workspace of attend() on a stream (None: the current one), allocated and zeroed there. Each stream has one, so
+        that calls on two may overlap. A call that is being captured gets one of its own in the graph's memory, zeroed at
+        each replay: a graph holds nothing that this object replaces later, and shares nothing with other calls."""
         need = self._ws_need.get((heads, max_q))
         if need is None:
             need = self._ws_need[heads, max_q] = binding.kv4_workspace_bytes(self.cfg, self.B, heads, max_q, self.max_pages)
-        if self._ws is None or self._ws.numel() < need:
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.workspace(heads, max_q)
+        device = self.pool.device
+        if torch.cuda.is_current_stream_capturing():
+            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+            ws[:binding.KV4_COUNTER_BYTES].zero_()
+            return ws
+        at = torch.cuda.current_stream(device).cuda_stream
+        ws = self._ws.get(at)
+        if ws is None or ws.numel() < need:
             # zeroed once: the attention keeps the counters at its start zero between calls
-            self._ws = torch.zeros(max(need, 16), dtype=torch.uint8, device=self.pool.device)
-        return self._ws
+            ws = self._ws[at] = torch.zeros(max(need, 16), dtype=torch.uint8, device=device)
+        return ws
 
     def attend(self, q: torch.Tensor, softmax_scale: float, cu_q: torch.Tensor | None = None, max_q: int = 1, out=None,
                lse=None, causal: bool = True, window: int = 0, stream=None):
         """Attention of query rows q [N,Hq,D], the last positions of their sequences, over the cache: out in q's type."""
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            with torch.cuda.stream(stream):  # memory that this stream may write at once (None: the current one)
+                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if stream is not None:
+                out.record_stream(torch.cuda.current_stream(q.device))
         binding.mla_qcache_kv4_attn(self.cfg, q, self.page_table, self.seq_lens, self.pool, softmax_scale, out,
-                                    self.workspace(q.shape[1], max_q), self.err, cu_q=cu_q, max_q=max_q, lse=lse, causal=causal,
-                                    window=window, stream=stream)
+                                    self.workspace(q.shape[1], max_q, stream), self.err, cu_q=cu_q, max_q=max_q, lse=lse,
+                                    causal=causal, window=window, stream=stream)
         return out
 
     def error_bits(self) -> int:
