@@ -467,7 +467,8 @@ def mla_qcache_kv4_append(cfg: KV4Config, k_new, v_new, cu_new, seq_lens, max_ne
                           seq_lens_next=None, stream=None) -> None:
     """Append K/V rows to the grouped-query cache in 4 bits, keys and queries rotated on the way (see
     include/mla_qcache.h). k_new, v_new [rows, kv heads, D] and q [rows, heads, D] may be views of one
-    projection's output."""
+    projection's output. With seq_lens itself as seq_lens_next the lengths advance in place, behind the append
+    (mla_qcache_advance)."""
     st = (_fast or _native()).kv4_append(cfg, k_new, v_new, cu_new, seq_lens, max_new, page_table, pool, err_word, cos, sin,
                                          interleaved, q, q_out, k_deq, v_deq, seq_lens_next,
                                          None if stream is None else stream.cuda_stream)

@@ -99,18 +99,16 @@ class KV4Cache:
             page_table = torch.arange(batch * max_pages, dtype=torch.int32, device=dev).view(batch, max_pages)
         self.page_table = page_table.to(device=dev, dtype=torch.int32).contiguous()
         self.seq_lens = torch.zeros(batch, dtype=torch.int32, device=dev)
-        self._lens_alt = torch.empty_like(self.seq_lens)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
         self._ws = {}  # per stream
         self._ws_need = {}  # workspace bytes per head count and rows
 
     def append(self, k: torch.Tensor, v: torch.Tensor, cu_new: torch.Tensor, max_new: int, stream=None, **kw) -> None:
-        """Appends rows cu_new[b]..cu_new[b+1]-1 of k, v [N,Hkv,D] to sequence b; the new lengths are stored in a second
-        array, which becomes ``self.seq_lens`` (the two alternate). Further arguments (cos, sin, interleaved, q, q_out,
-        k_deq, v_deq) as for mla_qcache_kv4_append."""
+        """Appends rows cu_new[b]..cu_new[b+1]-1 of k, v [N,Hkv,D] to sequence b and advances ``self.seq_lens`` in place,
+        by a launch behind it: a captured append goes on from there at every replay, among calls that are not captured
+        too. Further arguments (cos, sin, interleaved, q, q_out, k_deq, v_deq) as for mla_qcache_kv4_append."""
         binding.mla_qcache_kv4_append(self.cfg, k, v, cu_new, self.seq_lens, max_new, self.page_table, self.pool, self.err,
-                                      seq_lens_next=self._lens_alt, stream=stream, **kw)
-        self.seq_lens, self._lens_alt = self._lens_alt, self.seq_lens
+                                      seq_lens_next=self.seq_lens, stream=stream, **kw)
 
     def workspace(self, heads: int, max_q: int, stream=None) -> torch.Tensor:
         """Workspace of attend() on a stream (None: the current one), allocated and zeroed there. Each stream has one, so

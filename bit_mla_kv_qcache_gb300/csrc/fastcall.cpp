@@ -195,11 +195,16 @@ PyObject* kv4_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     void* k_deq = c.optional(a[14], "k_deq", type, {rows, Hkv, D});
     void* v_deq = c.optional(a[15], "v_deq", type, {rows, Hkv, D});
     void* next = c.optional(a[16], "seq_lens_next", at::kInt, {B});
-    return mla_qcache_kv4_append(cfg.p, dtype, extent(B, "B"), extent(rows, "rows"), &kv, &vv, static_cast<const int32_t*>(cu),
-                                 static_cast<const int32_t*>(lens.data_ptr()), static_cast<int32_t*>(next), max_new,
-                                 rotated ? &rot : nullptr, q_out ? &qv : nullptr, extent(heads, "heads"), q_out, k_deq, v_deq,
-                                 static_cast<const int32_t*>(table.data_ptr()), extent(table.size(1), "page_table"),
-                                 static_cast<uint8_t*>(pool.data_ptr()), pool.size(0), static_cast<int32_t*>(err), c.stream(a[17]));
+    const bool in_place = next && next == lens.data_ptr();
+    void* stream = c.stream(a[17]);
+    const int status = mla_qcache_kv4_append(
+        cfg.p, dtype, extent(B, "B"), extent(rows, "rows"), &kv, &vv, static_cast<const int32_t*>(cu),
+        static_cast<const int32_t*>(lens.data_ptr()), in_place ? nullptr : static_cast<int32_t*>(next), max_new,
+        rotated ? &rot : nullptr, q_out ? &qv : nullptr, extent(heads, "heads"), q_out, k_deq, v_deq,
+        static_cast<const int32_t*>(table.data_ptr()), extent(table.size(1), "page_table"), static_cast<uint8_t*>(pool.data_ptr()),
+        pool.size(0), static_cast<int32_t*>(err), stream);
+    if (status != MLA_QCACHE_OK || !in_place) return status;
+    return mla_qcache_advance(static_cast<const int32_t*>(cu), static_cast<int32_t*>(lens.data_ptr()), extent(B, "B"), stream);
   });
 }
 

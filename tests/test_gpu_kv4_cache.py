@@ -98,3 +98,30 @@ def test_two_captured_calls_replayed_at_once():
                 g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(outs, want)) and cache.error_bits() == 0
+
+
+def test_captured_steps_advance_among_steps_that_are_not():
+    """A step (append, attention) captured once: replays go on from the lengths that the last step left, whoever took it,
+    and leave the same pages and results as steps that are not captured."""
+    twin = [filled([130, 40], seed=6, P=32, spare=3)[0] for _ in range(2)]
+    lens, cu, rng = [130, 40], offsets([1, 1]), np.random.default_rng(8)
+    kv, query = rows(rng, 4, 2), rows(rng, 2, 8)
+    array = twin[0].seq_lens.data_ptr()
+
+    def step(cache):
+        cache.append(kv[:2], kv[2:], cu, 1)
+        return cache.attend(query, SCALE)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step(twin[0])
+    assert twin[0].seq_lens.tolist() == lens  # nothing has run yet
+    for i, captured in enumerate([True, True, False, True, False, False, True, True]):
+        kv.copy_(rows(rng, 4, 2)), query.copy_(rows(rng, 2, 8))
+        if captured:
+            g.replay()
+        got = out if captured else step(twin[0])
+        want = step(twin[1])
+        torch.cuda.synchronize()
+        assert twin[0].seq_lens.tolist() == [n + i + 1 for n in lens] == twin[1].seq_lens.tolist()
+        assert torch.equal(got, want) and torch.equal(twin[0].pool, twin[1].pool)
+    assert twin[0].seq_lens.data_ptr() == array and twin[0].error_bits() == 0 == twin[1].error_bits()
