@@ -447,15 +447,16 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
 
     // ---- this warp's steps tile, tile + kWarps, ...: the first ones are on their way before the
     // queries are read. Lane i holds the page id of tile i & 1 of the next step to be copied; a bad one
-    // drops its tile.
+    // drops its tile. (Any id may stand in the table, so whether a tile was asked for is told by its tokens.)
     constexpr int kStages = Ge::kStages;
     uint8_t* const ring = smem + warp * Ge::kRing;
     int next = tile;
     uint32_t next_st = 0, present = 0;  // two bits per stage
+    // tiles that no row sees are not asked for: their pages may be gone (behind a sliding window)
+    auto asked = [&](int tok) { return tok < full[2] && tok + kTile > full[3]; };
     auto page_id = [&](int t) {
       const int tok = t * kTok + kTile * (lane & 1);
-      // tiles that no row sees are not asked for: their pages may be gone (behind a sliding window)
-      return tok < full[2] && tok + kTile > full[3] ? __ldg(p.page_table + static_cast<size_t>(s_at.b) * p.max_pages + (tok >> p.p_shift)) : -2;
+      return asked(tok) ? __ldg(p.page_table + static_cast<size_t>(s_at.b) * p.max_pages + (tok >> p.p_shift)) : -1;
     };
     int32_t pid = page_id(next);
     auto issue = [&]() {
@@ -472,7 +473,7 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
             copy_tile<D, NG>(st + r * (Ge::kCodes / 2), st + Ge::kCodes + r * (Ge::kCodes / 2),
                              st + 2 * Ge::kCodes + r * (kTile * 8 * NG), base, (next * kTok + r * kTile) & (p.P - 1), p.P, lane);
             present |= 1u << (2 * next_st + r);
-          } else if (id != -2) {
+          } else if (asked(next * kTok + r * kTile)) {
             flags |= kErrBadPage;
           }
         }

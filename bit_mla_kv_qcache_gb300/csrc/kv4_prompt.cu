@@ -486,17 +486,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       const size_t region = static_cast<size_t>(sg.h) * kv4_head_bytes(D, NG, p.P);
       uint32_t kw[D / 8], vw[D / 8];
       uint2 num[NG], cur[NG];
-      auto page_of = [&](int j) -> int32_t {
+      auto asked = [&](int j) {  // by its token, not by the id: any may stand in the table
         const int tok = (tile0 + j) * kTok + tok_row;
-        return j < n_tiles && tok >= t_begin && tok < t_end ? __ldg(table + (tok >> p.p_shift)) : -2;
+        return j < n_tiles && tok >= t_begin && tok < t_end;
       };
-      auto token_base = [&](int32_t id) -> const uint8_t* {
+      auto page_of = [&](int j) -> int32_t { return asked(j) ? __ldg(table + (((tile0 + j) * kTok + tok_row) >> p.p_shift)) : -1; };
+      bool bad = false;  // the token that the registers hold has no page
+      auto token_base = [&](int32_t id, int j) -> const uint8_t* {
+        bad = false;
         if (static_cast<uint32_t>(id) < static_cast<uint32_t>(p.n_pages))
           return p.pool + static_cast<size_t>(static_cast<uint32_t>(id)) * p.page_bytes + region;
-        if (id != -2) flags |= kErrBadPage;
+        bad = asked(j);
+        if (bad) flags |= kErrBadPage;
         return nullptr;
       };
-      bool bad = false;  // the token that the registers hold has no page
       auto load_codes = [&](uint32_t (&w)[D / 8], const uint8_t* src) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
@@ -508,11 +511,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
 #pragma unroll
         for (int g = 0; g < NG; ++g) num[g] = src ? __ldg(reinterpret_cast<const uint2*>(src) + g) : make_uint2(0, 0);
       };
-      int32_t id = -2;
+      int32_t id = -1;
       if (two) {
         id = page_of(0);
-        const uint8_t* src = token_base(id);
-        bad = src == nullptr && id != -2;
+        const uint8_t* src = token_base(id, 0);
         const int tp = (tile0 * kTok + tok_row) & (p.P - 1);
         load_nums(src ? src + p.P * D + tp * 8 * NG : nullptr);
         load_codes(kw, src ? src + tp * (D / 2) : nullptr);
@@ -527,8 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         uint32_t hidden;
         if (two) {
           hidden = __ballot_sync(0xffffffffu, bad);
-          next = token_base(id);
-          bad = next == nullptr && id != -2;
+          next = token_base(id, j + 1);
           id = page_of(j + 2);
 #pragma unroll
           for (int g = 0; g < NG; ++g) cur[g] = num[g];
@@ -654,10 +655,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         const int tile0 = sg.tile, t_end = visible(p, sg.T, sg.n, min(sg.n - 1, (sg.rb * R + R - 1) / p.G)).y;
         const int t_begin = visible(p, sg.T, sg.n, sg.rb * R / p.G).x;
         const int part = min(p.P, kTok);  // tokens of a page that are in a tile
-        auto page_of = [&](int j) -> int32_t {
+        auto asked = [&](int j) {  // by the tokens, not by the id: any may stand in the table
           const int tok = (tile0 + j) * kTok + lane * part;
-          return j < n_tiles && lane * part < kTok && tok + part > t_begin && tok < t_end ? __ldg(table + (tok >> p.p_shift)) : -2;
+          return j < n_tiles && lane * part < kTok && tok + part > t_begin && tok < t_end;
         };
+        auto page_of = [&](int j) -> int32_t { return asked(j) ? __ldg(table + (((tile0 + j) * kTok + lane * part) >> p.p_shift)) : -1; };
         auto good = [&](int32_t id) { return static_cast<uint32_t>(id) < static_cast<uint32_t>(p.n_pages); };
         auto page_at = [&](int32_t id, int j, int& tp) -> const uint8_t* {
           tp = ((tile0 + j) * kTok + lane * part) & (p.P - 1);
@@ -675,9 +677,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         auto copy = [&](int j, int32_t id) -> bool {
           const uint32_t J = tiles_done + j, cs = J & 1;
           if (!all(wait(c_free + cs, ((J >> 1) & 1) ^ 1))) return false;
-          const bool have = good(id);
-          if (!have && id != -2) flags |= kErrBadPage;
-          const uint32_t bad = __ballot_sync(0xffffffffu, !have && id != -2), here = __ballot_sync(0xffffffffu, have);
+          const bool have = good(id), none = !have && asked(j);
+          if (none) flags |= kErrBadPage;
+          const uint32_t bad = __ballot_sync(0xffffffffu, none), here = __ballot_sync(0xffffffffu, have);
           if (lane == 0) {
             s_bad_pages[cs] = bad;
             mbar_arrive_expect_tx(c_full + cs, __popc(here) * part * (D + 8 * NG));
@@ -693,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           }
           return true;
         };
-        int32_t id = two ? -2 : page_of(0);
+        int32_t id = two ? -1 : page_of(0);
         int sent = !two && copy(0, id) ? 1 : 0;
         if (!two) id = page_of(1);
         for (int j = 1; j < kAhead; ++j) prefetch(j);

@@ -4,6 +4,8 @@ import numpy as np
 import pytest
 import torch
 
+import bit_mla_kv_qcache_gb300 as q
+from tests import kv4_paths
 from tests.test_gpu_kv4 import Case
 
 pytestmark = pytest.mark.gpu
@@ -31,3 +33,21 @@ def test_two_tiles_of_queries_over_many_segments_end_without_a_timeout(D, n, lse
 def test_windows_of_any_size_with_more_rows_than_tokens(n, G, window):
     """A window that no sequence fills is none; rows before the first token see nothing."""
     Case([0, max(1, n - 3), 300], [n, n, n], G=G, seed=n).check(window=window)
+
+
+@pytest.mark.parametrize("n,G,D", [(1, 4, 128), (3, 8, 64), (6, 7, 128), (12, 10, 64), (40, 4, 128), (70, 2, 64)])
+@pytest.mark.parametrize("page", [-1, -2, -3, -2 ** 31, "n_pages", 2 ** 31 - 1])
+def test_any_id_outside_the_pool_is_a_bad_page(n, G, D, page):
+    """Whatever the table holds in place of a page: its tokens are left out and the call says so, in each kernel."""
+    c = Case([300, 70], [n, min(n, 2)], Hkv=2, G=G, D=D, P=32, seed=n)
+    table, hide = c.table.copy(), [np.zeros(300, bool), np.zeros(70, bool)]
+    for b, i in ((0, 1), (0, 6), (1, 0)):
+        c.table[b, i] = c.n_pages if page == "n_pages" else page
+        hide[b][32 * i:32 * i + 32] = True
+    for lse in (True, False):
+        c.err.zero_()
+        out, l = c.run(lse=lse, scale=0.09)
+        assert int(c.err) == q.DEV_BAD_PAGE
+        bad, c.table = c.table, table
+        kv4_paths.check(c, out, l, 0.09, hide=hide)
+        c.table = bad
