@@ -68,6 +68,10 @@ constexpr int kMaxParts = 32;     // CTAs that one item is cut into, at most
 constexpr int kStart = 6;         // tiles' worth of time that an item costs besides its tiles: queries, first tiles, results
 constexpr float kSlack = 8.f;     // the running max is raised when a score exceeds it by more than this
 constexpr float kNoMax = -1e30f;  // the running max before the first score
+// Weights carry a factor of 2^kRoom, and so do their sums: at most 2^15 in FP16, and those below its smallest normal
+// number off by at most 2^-32 of the weight at the running max (one token 17.4 nats above 16383 others: their
+// share of the output, 4.5e-4, is off by 3e-6; without the factor it is lost).
+constexpr float kRoom = 7.f;
 constexpr long long kBudget = 4ll << 30;  // cycles of a wait before it is given up
 
 // Shared memory in tiles of 128 x D FP16: queries (one or two tiles), keys (two stages, or two operands),
@@ -946,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           }
         }
         float l0 = 0.f, l1 = 0.f;
-        const float neg = -m;
+        const float neg = kRoom - m;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           uint32_t w[16];
@@ -1093,7 +1097,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             reinterpret_cast<uint4*>(p.out + out_row(first + r2) * D)[ch] =
                 *reinterpret_cast<const uint4*>(st + r2 * kRow + 16 * (ch ^ (r2 & 7)));
           }
-          if (live && p.lse) p.lse[out_row(row)] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+          if (live && p.lse) p.lse[out_row(row)] = l == 0.f ? -INFINITY : (m + (log2f(l) - kRoom)) * 0.69314718055994531f;
         }
       }
       if (sg.part >= 0) {
@@ -1130,7 +1134,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             if (p.lse) {
               const int q2 = sg.rb * R + mr;
               p.lse[static_cast<size_t>(sg.r0 + q2 / p.G) * p.Hq + sg.h * p.G + q2 % p.G] =
-                  L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+                  L == 0.f ? -INFINITY : (M + (log2f(L) - kRoom)) * 0.69314718055994531f;
             }
           }
           softmax_barrier(n_softmax);

@@ -6,7 +6,7 @@ import torch
 
 import bit_mla_kv_qcache_gb300 as q
 from tests import kv4_paths
-from tests.test_gpu_kv4 import Case
+from tests.test_gpu_kv4 import Case, ints, offsets
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,31 @@ def test_any_id_outside_the_pool_is_a_bad_page(n, G, D, page):
         bad, c.table = c.table, table
         kv4_paths.check(c, out, l, 0.09, hide=hide)
         c.table = bad
+
+
+@pytest.mark.parametrize("n,G,D,lse", [(8, 4, 128, True), (9, 4, 128, True), (9, 4, 64, False), (10, 10, 128, False), (35, 4, 128, True),
+                                       (35, 4, 64, False)])
+@pytest.mark.parametrize("nats,at", [(16.3, 5), (17.4, 5), (17.4, 9000), (21.0, 300)])
+def test_a_peak_above_many_small_weights(n, G, D, lse, nats, at):
+    """One token `nats` above 16383 others of one score: what the others add up to is in the output, 1 in their values
+    against 0 in the peak's. Their weights are far below the smallest normal FP16 number. Eighty sequences over the same
+    pages: as many items as leave each whole, with one running max."""
+    T, B = 16384, 80
+    c = Case([1], [n], Hkv=1, G=G, D=D, P=256, seed=1)  # its table, pool and queries are replaced
+    c.lens, c.table = [T], np.random.default_rng(2).permutation(T // 256).astype(np.int32)[None]
+    c.n_pages = T // 256
+    c.pool = torch.zeros((c.n_pages, q.kv4_page_bytes(c.cfg)), dtype=torch.uint8, device="cuda")
+    k, v = torch.zeros((T, 1, D), dtype=c.t, device="cuda"), torch.ones((T, 1, D), dtype=c.t, device="cuda")
+    k[at, 0, 0], v[at] = 15.0, 0.0
+    q.mla_qcache_kv4_append(c.cfg, k, v, offsets([T]), ints([0]), T, ints(c.table), c.pool, c.err)
+    c.lens, c.new, c.table = [T] * B, [n] * B, np.repeat(c.table, B, 0)
+    c.q = torch.zeros((n * B, G, D), dtype=c.t, device="cuda")
+    c.q[..., 0] = 1.0
+    out, l = c.run(scale=nats / 15, lse=lse)
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    if n * G > 32:  # (items of few rows are cut, each at other places)
+        assert torch.equal(out, out[:n].repeat(B, 1, 1)) and (l is None or torch.equal(l, l[:n].repeat(B, 1)))
+    c.lens, c.new = [T], [n]
+    for at in (0, 37 * n, (B - 1) * n)[:1 if n * G > 32 else 3]:
+        kv4_paths.check(c, out[at:at + n], None if l is None else l[at:at + n], nats / 15)
