@@ -29,7 +29,9 @@
 //
 // kExact (the rounding of a key to FP16, up to 2^-11 of it, shows in the log-sum-exp as
 // ~1e-4): scores from exact products. With the scale s = s1 + s2 cut after seven bits, n s1 and n s2 fit FP16
-// for every code n: two key operands. The minimum enters as sixteen more channels: its value for each
+// for every code n: two key operands. (From 4096 on 15 s1 would not: such a token's numbers are quartered and its
+// scores taken four times. Smaller numbers stay as they are, subnormal ones too: quartered, FP16 would drop their last
+// bits.) The minimum enters as sixteen more channels: its value for each
 // group against the sum of the group's queries, in two FP16 parts. One stage of keys then has the room; its halves
 // (of the channels) fill and empty one by one. Taken when the log-sum-exp is asked for, and always with one tile of queries
 // of 128 channels, where it costs nothing (40 rows: 81 us, rounded keys 79).
@@ -247,10 +249,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   __shared__ float2 s_side[kTok];  // max and sum of a row under half of the tokens
   constexpr int kTry = 9;
   __shared__ int s_count[kTry + 1];  // parts that a share would make; tiles in all
-  __shared__ volatile int s_abort, s_any_hidden;
+  __shared__ volatile int s_abort, s_any_odd;  // s_any_odd: a bit of s_hidden or s_large has been set
   __shared__ volatile uint32_t s_unpacked;  // two tiles of queries: token tiles that warp 8 has unpacked so far
   __shared__ uint32_t s_bad_pages[2];  // of a stage of codes: bit i, its i-th page
   __shared__ __align__(16) uint32_t s_hidden[4][4];  // tokens of a tile (modulo four) whose page id is bad
+  __shared__ __align__(16) uint32_t s_large[4][4];   // kExact: tokens of a tile whose scale and minimum are quartered
   uint64_t *const k_full = bars, *const k_free = bars + 2, *const v_full = bars + 4, *const v_free = bars + 6,
            *const s_full = bars + 8, *const p_ready = bars + 10, *const o_done = bars + 12, *const c_full = bars + 13, *const c_free = bars + 15, *const p_half = bars + 17;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -399,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   }
   if (tid == 0) {
     s_abort = 0;
-    s_any_hidden = 0;
+    s_any_odd = 0;
     s_unpacked = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + i, 4);  // one arrival per warp
@@ -564,15 +567,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         }
         if (keys) {
           __half2 s1[NG], s2[NG];
-          uint32_t more[4] = {0, 0, 0, 0};
-          if constexpr (kExact) {  // a quarter of the scale (15 scales fit FP16) in seven bits and the rest; of the minimum
+          uint32_t more[4] = {0, 0, 0, 0}, large = 0;
+          if constexpr (kExact) {  // the scale in seven bits and the rest; the minimum
+            bool over = false;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) over |= (cur[g].x & 0xffffu) >= 0x6C00u;  // FP16 4096; scales are not negative
+            large = __ballot_sync(0xffffffffu, over);
+            const __half2 down = __float2half2_rn(over ? 0.25f : 1.f);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-              const __half2 s = __hmul2(__half2half2(scale_of(cur[g].x)), __float2half2_rn(0.25f));
+              const __half2 s = __hmul2(__half2half2(scale_of(cur[g].x)), down);
               const uint32_t top = *reinterpret_cast<const uint32_t*>(&s) & 0xFFF0FFF0u;
               s1[g] = *reinterpret_cast<const __half2*>(&top);
               s2[g] = __hsub2(s, s1[g]);
-              const __half2 mn = __hmul2(__half2half2(min_of(cur[g].x)), __float2half2_rn(0.25f));
+              const __half2 mn = __hmul2(__half2half2(min_of(cur[g].x)), down);
               more[g] = *reinterpret_cast<const uint32_t*>(&mn);
             }
           }
@@ -608,7 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             if (lane == 0) {  // the tile four back has had its softmax: its values were freed two tiles ago
               if (hf == 0) {
                 s_hidden[J & 3][warp & 3] = hidden;
-                if (hidden) s_any_hidden = 1;
+                if constexpr (kExact) s_large[J & 3][warp & 3] = large;
+                if (hidden | large) s_any_odd = 1;
               }
               mbar_arrive(k_full + ks);
             }
@@ -834,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           bool range = false;
           const int E = prescale_exponent(mx, range) - (kExact ? 8 : 0);  // kExact: below 2^7, so that the sums fit
           if ((lane >> 3) == i)  // a hidden score, -inf, stays one at scale 0
-            fr = fmaxf(pow2_int(-E) * fabsf(p.scale_log2) * (kExact ? 4.f : 1.f), 1e-37f);
+            fr = fmaxf(pow2_int(-E) * fabsf(p.scale_log2), 1e-37f);
           if (two || group == 0) {
             const float up = p.scale_log2 < 0.f ? -pow2_int(E) : pow2_int(E);
             const uint32_t dst = base + (two ? group * Ge::kTile : 0) + 16 * (32 * (warp & 3) + 8 * i + (lane & 7));
@@ -898,7 +907,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         for (int c = 0; c < NC; ++c) tc5::ld32(sc + 32 * (first + c), raw[c]);
 #pragma unroll
         for (int c = 0; c < NC; ++c) tc5::wait_ld(raw[c]);
-        if (s_any_hidden) {  // some tile so far
+        if (s_any_odd) {  // some tile so far
+          if constexpr (kExact) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              const uint32_t four = s_large[(tiles_done + k) & 3][first + c];
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if ((four >> i) & 1) raw[c][i] = __float_as_uint(4.f * __uint_as_float(raw[c][i]));
+            }
+          }
           uint32_t bits[NC];
 #pragma unroll
           for (int c = 0; c < NC; ++c) bits[c] = s_hidden[(tiles_done + k) & 3][first + c];

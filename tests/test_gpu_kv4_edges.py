@@ -1,5 +1,7 @@
 """4-bit grouped-query cache on the GPU at the edges of its kernels: waits, page ids, windows, sizes of numbers and
 row counts that the first tests leave out."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -79,3 +81,34 @@ def test_a_peak_above_many_small_weights(n, G, D, lse, nats, at):
     c.lens, c.new = [T], [n]
     for at in (0, 37 * n, (B - 1) * n)[:1 if n * G > 32 else 3]:
         kv4_paths.check(c, out[at:at + n], None if l is None else l[at:at + n], nats / 15)
+
+
+@pytest.mark.parametrize("n,G,D,group,lse", [(2, 4, 128, 64, True), (8, 4, 64, 32, True), (9, 4, 128, 128, False), (20, 5, 128, 32, True),
+                                             (9, 4, 64, 64, True), (35, 4, 128, 64, True), (35, 4, 64, 32, True)])
+@pytest.mark.parametrize("size", [1e-2, 1e-3, 3e-4, 1e-4, 1e-5, "large", "of every size"])
+def test_keys_of_any_size_are_exact(n, G, D, group, lse, size):
+    """Scales and minima down to the smallest FP16 numbers and up to the largest, one of them beside the other in a
+    sequence, a token and a tile: where keys are promised exactly, scores of ten and more are right to float32."""
+    rng = np.random.default_rng(n + D)
+    c = Case([400, 130], [n, min(n, 3)], Hkv=2, G=G, D=D, group=group, P=32, seed=n)
+    k = rng.standard_normal((530, 2, D))
+    unit = 1.0
+    if size == "large":  # a few groups whose scale is 4096 and more: 15 of it is beyond FP16
+        k = k * 0.5
+        k[::7, :, 3], k[::7, :, 5] = 64000.0, -63000.0
+        k[5::11, 1, group - 1] = -50000.0
+        k[5::11, 1, 0] = 40000.0
+        unit = 2e4
+    elif size == "of every size":
+        k *= 10.0 ** rng.uniform(-5, 0, (530, 2, D // group, 1)).repeat(group, -1).reshape(530, 2, D)
+        unit = 0.3
+    else:
+        k *= size
+        unit = size
+    kv = [torch.tensor(x, dtype=torch.float32).bfloat16().cuda() for x in (k, rng.standard_normal((530, 2, D)))]
+    q.mla_qcache_kv4_append(c.cfg, *kv, offsets([400, 130]), ints([0, 0]), 400, ints(c.table), c.pool, c.err)
+    scale = 1.2 / (unit * math.sqrt(D))  # queries of 2: scores of up to about ten
+    out, l = c.run(scale=scale, lse=lse)
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    kv4_paths.check(c, out, l, scale)
