@@ -592,10 +592,11 @@ size_t mla_qcache_kv4_workspace_bytes(const mla_qcache_kv4_config* cfg, int32_t 
  *   out [n_rows][n_heads][D] in the queries' type, lse [n_rows][n_heads] float32, natural log
  *   (optional). A row that sees no token gets out = 0, lse = -inf.
  * Scores are products of the exact codes with the queries (prescaled by a power of two to FP16: every
- * value within 2^-14 of the row's largest enters exactly, smaller ones are off by at most 2^-39 of it),
+ * value within 2^-20 of the row's largest enters exactly, smaller ones are off by at most 2^-31 of it),
  * summed in float32, except where max_q * n_heads / n_kv_heads is above 128 (above 32 at D = 64) and no lse is
  * asked for: keys are then rounded to FP16. Above 32 such rows values are rounded to FP16. Weights enter
- * the readout in FP16.
+ * the readout in FP16: those of tokens far below the row's top score are off by up to 2^-32 of the top one's weight (up
+ * to 32 such rows: times the value's scale, by 2^-29 of the largest scale).
  * Capture: a call may be captured into a graph; grid and path go by the sizes of the call, the lengths are
  * read on the device at each replay.
  * max_q: bound on the rows per sequence; a sequence with more sets MLA_QCACHE_DEV_ROWS, a length

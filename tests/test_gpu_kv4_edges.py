@@ -112,3 +112,23 @@ def test_keys_of_any_size_are_exact(n, G, D, group, lse, size):
     torch.cuda.synchronize()
     assert int(c.err) == 0
     kv4_paths.check(c, out, l, scale)
+
+
+@pytest.mark.parametrize("n,G,D,lse", [(2, 4, 128, True), (8, 4, 64, True), (9, 4, 128, True), (9, 4, 64, False), (35, 4, 128, True),
+                                       (35, 4, 128, False)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_small_values_next_to_a_large_one_in_a_query(n, G, D, lse, dtype):
+    """The first group of keys is zero and meets a query of 2^10; all that decides is in values of 2^-9 and less."""
+    c = Case([300, 90], [n, min(n, 3)], Hkv=1, G=G, D=D, group=32, P=16, dtype=dtype, seed=n)
+    rng = np.random.default_rng(n)
+    k = rng.standard_normal((390, 1, D)) * 3
+    k[..., :32] = 0
+    kv = [torch.tensor(x, dtype=torch.float32).to(c.t).cuda() for x in (k, rng.standard_normal((390, 1, D)))]
+    q.mla_qcache_kv4_append(c.cfg, *kv, offsets([300, 90]), ints([0, 0]), 300, ints(c.table), c.pool, c.err)
+    c.q = (c.q.float() * 2.0 ** -10).to(c.t)
+    c.q[..., 5] = 1024.0
+    scale = 2.0 ** 9 / math.sqrt(D)
+    out, l = c.run(scale=scale, lse=lse)
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    kv4_paths.check(c, out, l, scale)
