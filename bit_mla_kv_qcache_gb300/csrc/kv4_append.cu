@@ -28,11 +28,11 @@ __device__ __noinline__ uint32_t quant_codes8_exactly(float x0, float x1, float 
 
 // The codes of eight values with few instructions: t = (x - m) / s from two rounded operations and a
 // rounded reciprocal is off by at most 16 * 3 * 2^-24 < 3e-6, so a t further than 1e-4 from every
-// midpoint has its nearest level already; where one of the eight is nearer (or NaN) they are decided
-// against the exact midpoints. Adding 1.5 * 2^23 (bits 0x4B400000) rounds to the nearest whole number and
+// midpoint has its nearest level already; where one of the eight is nearer, or the group is reported (`odd`: NaN,
+// infinities, beyond the range), they are decided against the exact midpoints, within 0 .. 15 (NaN: 0). Adding 1.5 * 2^23 (bits 0x4B400000) rounds to the nearest whole number and
 // leaves it in the low bits (0 <= t <= 15 but for that error; whichever way the packed operations round,
 // the distance from t decides). n: the codes as numbers; returned: as fields.
-__device__ __forceinline__ uint32_t quant_codes8(const float (&x)[8], const QParams& q, float (&n)[8]) {
+__device__ __forceinline__ uint32_t quant_codes8(const float (&x)[8], const QParams& q, bool odd, float (&n)[8]) {
   constexpr float kRound = 12582912.f;
   float far = 0.f;
   uint32_t word = 0;
@@ -46,7 +46,7 @@ __device__ __forceinline__ uint32_t quant_codes8(const float (&x)[8], const QPar
     word += (__float_as_uint(r.x) << (4 * k)) + (__float_as_uint(r.y) << (4 * k + 4));
   }
   word -= 0x3F400000u;  // the sum of 0x4B400000 << 4 k, modulo 2^32
-  if (!(far <= 0.4999f)) {
+  if (!(far <= 0.4999f) || odd) {
     word = quant_codes8_exactly(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], q.m, q.s, q.inv_s);
 #pragma unroll
     for (int k = 0; k < 8; ++k) n[k] = static_cast<float>((word >> (4 * k)) & 15u);
@@ -88,6 +88,20 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return y;
 }
 
+// What the cache holds for a group that is reported: finite numbers, so that rows that do not see the token are not
+// reached by it (a weight of zero times infinity or NaN). With an infinity or without a number: zeros. Beyond
+// FP16: the largest scale whose top level fits.
+__device__ __noinline__ QParams settle_qparams(QParams q, float lo, float hi) {
+  if (!(lo > -INFINITY && hi < INFINITY)) {
+    q.m = q.s = 0.f;
+  } else if (q.flags & kErrRange) {
+    q.s = __half2float(__float2half_rd(__fdiv_rd(65504.f - q.m, 15.f)));
+  }
+  q.inv_s = q.s > 0.f ? 1.f / q.s : 0.f;
+  q.meta = __half_as_ushort(__float2half_rn(q.s)) | static_cast<uint32_t>(__half_as_ushort(__float2half_rn(q.m + 0.f))) << 16;
+  return q;
+}
+
 // Quantizes the group that this lane's eight values belong to (LG lanes per group).
 template <int LG>
 __device__ __forceinline__ QParams quantize8(const float (&x)[8], uint32_t& word, float (&n)[8]) {
@@ -105,7 +119,8 @@ __device__ __forceinline__ QParams quantize8(const float (&x)[8], uint32_t& word
   QParams qp = make_qparams15(lo, hi);
   if (!(none.x + none.y == 0.f)) qp.flags |= kErrNonFinite;
   if (__fmaf_rn(15.f, qp.s, qp.m) >= 65520.f) qp.flags |= kErrRange;  // the top level would not fit FP16
-  word = quant_codes8(x, qp, n);
+  if (qp.flags) qp = settle_qparams(qp, lo, hi);
+  word = quant_codes8(x, qp, qp.flags != 0, n);
   return qp;
 }
 

@@ -558,7 +558,9 @@ size_t mla_qcache_kv4_page_bytes(const mla_qcache_kv4_config* cfg);
  * rotation NULL: none. Outputs must not overlap inputs or one another.
  * Sequences may share pages, but not one that a call appends to for two of them.
  * A group with a NaN or an infinity sets MLA_QCACHE_DEV_NONFINITE, one whose scale, minimum or largest
- * level is beyond the FP16 range MLA_QCACHE_DEV_RANGE (what the cache then holds for it is not specified).
+ * level is beyond the FP16 range MLA_QCACHE_DEV_RANGE. What the cache then holds is finite, so that it stays with the rows
+ * that see the token: zeros for a group with an infinity or without a number, the group's minimum for a NaN
+ * among numbers, levels within the range for one beyond it.
  * Errors: bad config or dtype -> MLA_QCACHE_ERR_CONFIG; B < 1 or > 2^20, n_rows < 0, max_new < 1,
  * max_pages < 1, n_pages < 1, n_heads < 1 or > 4096 (with q), bad rotation, negative strides,
  * overlapping buffers -> MLA_QCACHE_ERR_SHAPE; missing pointers, q without q_out -> MLA_QCACHE_ERR_NULL;

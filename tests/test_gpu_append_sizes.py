@@ -110,3 +110,34 @@ def test_latent_append(rows, B, H, P, interleaved, norm, rot):
     assert torch.equal(pool, want)
     for o in (q_out, c_out, kr_out):
         assert (o[rows:] == 7).all()
+
+
+@pytest.mark.parametrize("D,group", [(128, 128), (64, 32)])
+def test_what_the_cache_holds_for_groups_that_are_reported(D, group):
+    """Finite numbers: zeros for an infinity or for no number at all, the minimum for a NaN among numbers, the end of the
+    range beyond it; the groups beside them as ever."""
+    cfg, rng = q.make_kv4_config(1, D, group=group, page_size=16), np.random.default_rng(D)
+    x = rng.standard_normal((8, 1, D)).astype(np.float32)
+    x = torch.tensor(x).bfloat16().float().numpy()
+    plain = ref.quantize(x.astype(np.float64), group)
+    want = ref.values(*plain, group)
+    x[0, 0, :group], x[1, 0, 3], x[2, 0, :group] = np.nan, np.nan, np.inf
+    x[3, 0, 5], x[4, 0, 6] = -np.inf, 3e38
+    x[5, 0, :group], x[6, 0, 2] = -1e6, 70000.0
+    want[[0, 2], :, :group] = want[3, :, :group] = 0
+    kv = torch.tensor(x).bfloat16().cuda()
+    pool, err = torch.zeros((1, q.kv4_page_bytes(cfg)), dtype=torch.uint8, device="cuda"), error_word()
+    kd, vd = torch.empty_like(kv), torch.empty_like(kv)
+    q.mla_qcache_kv4_append(cfg, kv, kv, ints([0, 8]), ints([0]), 8, ints([[0]]), pool, err, k_deq=kd, v_deq=vd)
+    assert int(err) == q.DEV_NONFINITE | q.DEV_RANGE
+    k, v, _, _ = ref.read_sequence(pool.cpu().numpy(), np.array([0]), 8, 1, D, group, 16)
+    assert np.array_equal(k, v) and np.isfinite(k).all() and np.abs(k).max() <= 65504
+    assert torch.equal(kd.cpu(), torch.tensor(k[0, :, None]).float().bfloat16()) and torch.equal(kd, vd)
+    k = k[0, :, None]
+    for r in (0, 2, 3, 7):
+        assert np.array_equal(k[r], want[r]), r
+    assert np.array_equal(k[:, :, group:], want[:, :, group:])
+    rest = np.arange(group) != 3
+    assert np.abs(k[1, 0, :group][rest] - x[1, 0, :group][rest]).max() <= (x[1, 0, :group][rest].max() - x[1, 0, :group][rest].min()) / 29
+    assert k[1, 0, 3] == k[1, 0, :group].min()  # (the minimum level itself may be held by no other)
+    assert (k[5, 0, :group] == -65504).all() and k[4, 0, 6] > 60000 and k[6, 0, 2] > 60000

@@ -132,3 +132,41 @@ def test_small_values_next_to_a_large_one_in_a_query(n, G, D, lse, dtype):
     torch.cuda.synchronize()
     assert int(c.err) == 0
     kv4_paths.check(c, out, l, scale)
+
+
+@pytest.mark.parametrize("n,G,D,group,lse", [(3, 2, 128, 128, True), (5, 6, 64, 32, True), (9, 4, 128, 64, False), (40, 4, 128, 128, False),
+                                             (40, 4, 64, 64, True)])
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf"), 3e38, "nan among others", "both infinities"])
+def test_values_that_are_no_numbers_stay_with_the_rows_that_see_them(n, G, D, group, lse, what):
+    """The last of the new tokens has keys and values that are no numbers, or none of FP16's. The append says so; the rows
+    in front of it, and those of the other sequence, get what they get without it."""
+    lens, scale = [200, 77], 1 / math.sqrt(D)
+    c = Case(lens, [n, min(n, 2)], Hkv=2, G=G, D=D, group=group, P=32, seed=n)
+    rng = np.random.default_rng(n)
+    good = torch.tensor(rng.standard_normal((2, 277, 2, D)), dtype=torch.float32).bfloat16().cuda()
+    bad = good.clone()
+    if what == "nan among others":
+        bad[:, 199, :, 3::7] = float("nan")
+    elif what == "both infinities":
+        bad[:, 199, :, 0::2], bad[:, 199, :, 1::2] = float("inf"), -float("inf")
+    else:
+        bad[:, 199] = what
+    results = []
+    for kv in (good, bad):
+        c.err.zero_()
+        q.mla_qcache_kv4_append(c.cfg, kv[0], kv[1], offsets(lens), ints([0, 0]), 200, ints(c.table), c.pool, c.err)
+        word = int(c.err)
+        assert (word != 0) == (kv is bad) and word & ~(q.DEV_NONFINITE | q.DEV_RANGE) == 0
+        c.err.zero_()
+        out, l = c.run(lse=lse, scale=scale)
+        assert int(c.err) == 0
+        results.append((out, l))
+    keep = torch.ones(sum(c.new), dtype=torch.bool)
+    keep[n - 1] = False
+    if what == 3e38:
+        # held as 65504: a score that raises the running max of the rows beside it early, so that they round at other places;
+        # every row is within its bound over what the cache holds
+        kv4_paths.check(c, *results[1], scale)
+        return
+    assert torch.equal(results[0][0][keep], results[1][0][keep])
+    assert not lse or torch.equal(results[0][1][keep], results[1][1][keep])
