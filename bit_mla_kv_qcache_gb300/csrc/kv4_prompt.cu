@@ -447,6 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     return true;
   };
   auto all = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
+  auto any = [](bool x) { return __any_sync(0xffffffffu, x) != 0; };
   // Stages and barrier phases go on from segment to segment: token tiles and steps of the earlier ones.
   uint32_t tiles_done = 0, steps_done[2] = {0, 0}, segs = 0;
   const int group = warp >> 2;  // 0, 1: softmax; 2: unpacking; 3: products, prefetch
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           }
           if (two) load_codes(vw, next ? next + p.P * (D / 2) + tp * (D / 2) : nullptr);
         }
-        if (s_abort) break;
+        if (any(s_abort)) break;  // the warp together: it votes again at the next tile
       }
     } while (leave_segment(n_tiles, steps));
   } else if (group == 3) {
@@ -1002,11 +1003,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         __syncwarp();
         if (lane == 0) mbar_arrive(p_ready + u);
       };
-      for (int k = 0; k < n_tiles && !s_abort; ++k) {
+      for (int k = 0; k < n_tiles && !any(s_abort); ++k) {
         if (half) tile_weights(std::integral_constant<int, 2>{}, k);
         else tile_weights(std::integral_constant<int, 4>{}, k);
       }
-      const bool done = all(wait(o_done, segs & 1)) && !s_abort;
+      const bool done = all(wait(o_done, segs & 1) && !s_abort);
       tc5::fence_after();
 
               constexpr int kPartRow = D * 4;
