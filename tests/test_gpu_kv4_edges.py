@@ -170,3 +170,17 @@ def test_values_that_are_no_numbers_stay_with_the_rows_that_see_them(n, G, D, gr
         return
     assert torch.equal(results[0][0][keep], results[1][0][keep])
     assert not lse or torch.equal(results[0][1][keep], results[1][1][keep])
+
+
+@pytest.mark.parametrize("n,G,D,lse", [(2, 4, 128, True), (8, 4, 64, True), (9, 4, 128, False), (9, 4, 64, True), (35, 4, 128, True),
+                                       (35, 4, 128, False)])
+@pytest.mark.parametrize("size", [2.0 ** 126, 2.0 ** 116, 2.0 ** -90, 2.0 ** -104])
+def test_queries_of_any_size(n, G, D, lse, size):
+    """BF16 queries near both ends of their type, under a scale that makes scores of them."""
+    c = Case([150, 40], [n, min(n, 3)], Hkv=2, G=G, D=D, P=16, seed=n)
+    c.q = (c.q.float().clamp(-3.9, 3.9) * (size / 2)).to(c.t)
+    scale = 2 / (size * math.sqrt(D))
+    out, l = c.run(scale=scale, lse=lse)
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    kv4_paths.check(c, out, l, scale)
