@@ -35,6 +35,12 @@ std::string shape_of(const at::Tensor& t) {
   return s + ")";
 }
 
+int32_t as_bool(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};  // a tensor of several values, for one
+  return v;
+}
+
 // The tensors of one call: on one device, which is the current one.
 struct Call {
   c10::Device device{c10::kCPU};
@@ -98,7 +104,7 @@ struct Call {
     const void* s = ptr(sin, "sin", at::kFloat, {c.size(0), c.size(1)});
     if (c.size(0) > INT32_MAX || c.size(1) > INT32_MAX / 2) raise(PyExc_ValueError, "cos: too large a table");
     *out = {static_cast<const float*>(c.data_ptr()), static_cast<const float*>(s), static_cast<int32_t>(c.size(0)),
-            static_cast<int32_t>(2 * c.size(1)), PyObject_IsTrue(interleaved) ? 1 : 0};
+            static_cast<int32_t>(2 * c.size(1)), as_bool(interleaved)};
     return true;
   }
   void* stream(PyObject* o) const {
@@ -232,7 +238,7 @@ PyObject* kv4_attn(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return mla_qcache_kv4_attn(cfg.p, dtype, extent(B, "B"), extent(heads, "heads"), extent(rows, "rows"), &qv,
                                static_cast<const int32_t*>(cu), as_int(a[10], "max_q"), static_cast<const int32_t*>(table.data_ptr()),
                                extent(table.size(1), "page_table"), static_cast<const int32_t*>(lens.data_ptr()),
-                               static_cast<const uint8_t*>(pool.data_ptr()), pool.size(0), PyObject_IsTrue(a[12]) ? 1 : 0,
+                               static_cast<const uint8_t*>(pool.data_ptr()), pool.size(0), as_bool(a[12]),
                                as_int(a[13], "window"), scale, out, static_cast<float*>(lse), ws.data_ptr(),
                                static_cast<size_t>(ws.size(0)), static_cast<int32_t*>(err), c.stream(a[14]));
   });

@@ -184,3 +184,16 @@ def test_queries_of_any_size(n, G, D, lse, size):
     torch.cuda.synchronize()
     assert int(c.err) == 0
     kv4_paths.check(c, out, l, scale)
+
+
+def test_a_flag_that_is_no_truth_value_is_refused():
+    c = Case([40], [2], G=2)
+    both = torch.tensor([True, False])
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        c.run(causal=both)
+    angle = torch.ones(50, 64, device="cuda")
+    kv = torch.zeros(2, 1, 2, 128, dtype=c.t, device="cuda")
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        q.mla_qcache_kv4_append(c.cfg, kv[0], kv[1], offsets([1]), ints([40]), 1, ints(c.table), c.pool, c.err, cos=angle, sin=angle,
+                                interleaved=both)
+    c.check()
