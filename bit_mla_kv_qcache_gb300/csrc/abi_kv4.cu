@@ -204,9 +204,10 @@ int mla_qcache_kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t
   int st = check_kv4(cfg);
   if (st != MLA_QCACHE_OK) return st;
   if (dtype != MLA_QCACHE_BF16 && dtype != MLA_QCACHE_FP16) return MLA_QCACHE_ERR_CONFIG;
+  const float scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634074);
   if (B < 1 || B > (1 << 20) || n_heads < 1 || n_heads > 4096 || n_heads % cfg->n_kv_heads || n_rows < 0 ||
       static_cast<int64_t>(n_rows) * n_heads > 0x7fffffff || max_q < 1 || max_pages < 1 || n_pages < 1 || window < 0 ||
-      (window > 0 && !causal) || !std::isfinite(softmax_scale) ||
+      (window > 0 && !causal) || !std::isfinite(scale_log2) ||
       static_cast<int64_t>(max_pages) * cfg->page_size > 0x7ffff000)  // positions and steps are counted in 32 bits
     return MLA_QCACHE_ERR_SHAPE;
   if (!cu_q && (max_q != 1 || n_rows != B)) return MLA_QCACHE_ERR_SHAPE;
@@ -245,7 +246,7 @@ int mla_qcache_kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t
   p.part_ml = p.part_o + 2 * ctas * rows * D;
   p.n_pages = n_pages;
   p.page_bytes = kv4_page_bytes(cfg);
-  p.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634074);
+  p.scale_log2 = scale_log2;
   p.B = B;
   p.n_rows = n_rows;
   p.max_q = max_q;

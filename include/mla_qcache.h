@@ -606,7 +606,7 @@ size_t mla_qcache_kv4_workspace_bytes(const mla_qcache_kv4_config* cfg, int32_t 
  * MLA_QCACHE_DEV_BAD_PAGE (its tokens are left out). Pages that no row of a sequence sees any token of (behind a
  * sliding window) are not read: their ids may be anything.
  * Errors: as for mla_qcache_kv4_append; n_heads no multiple of n_kv_heads, n_rows * n_heads > 2^31 - 1,
- * a window without causal, a scale that is not finite, max_pages * P > 2^31 - 4096 -> MLA_QCACHE_ERR_SHAPE; too small a workspace ->
+ * a window without causal, a scale that is not finite (nor 1.45 times it), max_pages * P > 2^31 - 4096 -> MLA_QCACHE_ERR_SHAPE; too small a workspace ->
  * MLA_QCACHE_ERR_WORKSPACE.
  */
 int mla_qcache_kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t n_heads, int32_t n_rows,
