@@ -197,3 +197,18 @@ def test_a_flag_that_is_no_truth_value_is_refused():
         q.mla_qcache_kv4_append(c.cfg, kv[0], kv[1], offsets([1]), ints([40]), 1, ints(c.table), c.pool, c.err, cos=angle, sin=angle,
                                 interleaved=both)
     c.check()
+
+
+@pytest.mark.parametrize("n,G,D,group,P", [
+    (17, 1, 128, 128, 16), (8, 4, 64, 32, 64), (4, 8, 128, 64, 128), (32, 1, 128, 32, 128), (33, 1, 128, 128, 256), (12, 5, 64, 64, 16),
+    (16, 4, 128, 32, 32), (13, 5, 128, 64, 64), (32, 4, 64, 32, 128), (32, 4, 128, 128, 64), (43, 3, 128, 32, 256), (37, 7, 64, 64, 256)])
+@pytest.mark.parametrize("lse", [True, False])
+def test_every_kernel_is_within_its_own_bound(n, G, D, group, P, lse):
+    """Exact keys and values up to 32 rows, exact keys wherever they are promised: bounds without what does not apply."""
+    for dtype in ("bf16", "fp16"):
+        c = Case([n, 700, 1201, 3300], [n, n, 1, 2], Hkv=1, G=G, D=D, group=group, P=P, dtype=dtype, seed=n + D)
+        for scale in (0.09, 0.5):
+            out, l = c.run(lse=lse, scale=scale)
+            torch.cuda.synchronize()
+            assert int(c.err) == 0
+            kv4_paths.check(c, out, l, scale)
