@@ -1,4 +1,5 @@
-// What the appending kernels share: where a new row goes, and the rotation of channel pairs.
+// What the appending kernels share: where a new row goes, and the rotation of channel pairs; small arithmetic that the
+// attention over their pages takes too.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -104,6 +105,22 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, bool f16) {
 }
 __device__ __forceinline__ uint4 pack8(const float (&x)[8], bool f16) {
   return make_uint4(pack2(x[0], x[1], f16), pack2(x[2], x[3], f16), pack2(x[4], x[5], f16), pack2(x[6], x[7], f16));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float y;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
 }
 
 // Two float32 operations in one instruction. A product and a sum that follow one another may still come

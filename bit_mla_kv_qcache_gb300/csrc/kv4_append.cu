@@ -15,7 +15,6 @@
 namespace mlaq {
 namespace {
 
-
 // Eight codes against the exact midpoints, 4 bits each. Rarely called, and not inlined.
 __device__ __noinline__ uint32_t quant_codes8_exactly(float x0, float x1, float x2, float x3, float x4, float x5, float x6,
                                                       float x7, float m, float s, float inv_s) {
@@ -75,17 +74,6 @@ __device__ __forceinline__ uint32_t even_fields_first(uint32_t v) {
   e = (e | (e >> 8)) & 0x0000FFFFu;
   o = (o | (o >> 8)) & 0x0000FFFFu;
   return e | (o << 16);
-}
-
-__device__ __forceinline__ float min3(float a, float b, float c) {
-  float y;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float y;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
 }
 
 // What the cache holds for a group that is reported: finite numbers, so that rows that do not see the token are not

@@ -72,11 +72,6 @@ constexpr float kNoMax = -1e30f;  // the running max before the first score
 constexpr float kWeightRoom = 64.f;  // w / p stays at or below this: w <= 2^14 in FP16, whose half step below
                                      // 2^-14 is 2^-25, so a token's weight is off by at most 2^-29 of the largest vs
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t r;
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));

@@ -93,11 +93,6 @@ struct Geom {
   __host__ __device__ static constexpr int smem(bool two) { return ring_at(two) + (two ? 0 : 2 * kStage) + 1024; }  // slack to align the start
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -112,11 +107,6 @@ __device__ __forceinline__ uint32_t h2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float y;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
 // (a, b) * (f, f) + (c, c) in one instruction
 __device__ __forceinline__ void fma_pair(float& a, float& b, float f, float c) {
   asm("{ .reg .b64 x, f, c; mov.b64 x, {%0, %1}; mov.b64 f, {%2, %2}; mov.b64 c, {%3, %3}; fma.rn.f32x2 x, x, f, c;"
