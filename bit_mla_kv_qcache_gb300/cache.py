@@ -84,7 +84,8 @@ class QuantizedMLACache:
 
 class KV4Cache:
     """Grouped-query K/V cache in 4 bits of one layer: page pool, page table and lengths for B sequences, and the
-    workspace of its attention. The page table is the caller's, as for QuantizedMLACache."""
+    workspaces of its attention. The page table is the caller's, as for QuantizedMLACache. The lengths must not change under
+    a call that reads them: appends and attend() are ordered by their stream or, on several, by the caller."""
 
     def __init__(self, cfg: binding.KV4Config, batch: int, max_pages: int, n_pages: int | None = None,
                  page_table: torch.Tensor | None = None, device="cuda"):

@@ -6,9 +6,11 @@
 // one thread's eight channels, and a value-code word is a column of the 8 x 8 matrix of codes that
 // eight lanes hold (transposed by three rounds of exchanges). CTA r serves row r: its threads
 // cover 512 / D or 2048 / D heads at a time and keep the row's angles in registers over all heads; rows are
-// loaded two rounds ahead. Bound: instruction issue (65% busy, ALU 43%): 16K rows of 8 + 8 heads of
-// 128 with 32 query heads take 105 us, their bytes, read and written once, 63 at the card's copy rate; a
-// decode step of 32 rows 5.8 us, of which the launch and three dependent loads (offsets, page, row) are most.
+// loaded two rounds ahead. Bound: with many rows the wait for a warp's own loads with 44% of the warps resident (of eleven issue slots
+// between two instructions five are that, two fixed latencies); issue is 64% busy, DRAM 46%, the ALU pipe 42%: 16K rows of 8 + 8 heads of
+// 128 with 32 query heads take 107 us, their bytes, read and written once, 63 at the card's copy rate. A
+// decode step of 32 rows takes 5.8 us: 32 SMs, each behind the launch and three dependent loads (offsets, page, row; with these
+// alone the latent append takes 2.8) in three rounds of 16 heads.
 #include "append.cuh"
 #include "quant.cuh"
 

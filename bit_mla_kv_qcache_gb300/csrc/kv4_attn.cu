@@ -31,9 +31,10 @@
 // side (eight ragged sequences up to 32K, 8 heads on each of 4, D = 128): 24 rows 79 us here and 79 there, 40 rows 117 and 81;
 // one sequence of 4K: 24 rows 17 and 26 us, 40 rows 19 and 27; D = 64, 24 rows 49 and 52 us.
 //
-// Bound: instruction issue. 32 sequences of 8K take 64 us where their bytes take 42 at the card's copy rate: the
-// ALU pipe (masks, shifts and byte permutes of codes) is 53% busy, issue 55%, the tensor pipe 25%; ~9 us of it are launch, the
-// first tokens, and the joining (one sequence of 1K: 9.8 us).
+// Bound: the chain of a step within a warp. 32 sequences of 8K take 65 us where their bytes take 42 at the card's copy rate, and no
+// unit is full: issue 55%, the ALU pipe (masks, shifts and byte permutes of codes) 53%, DRAM 54%, the tensor pipe 25%. Four warps
+// share a scheduler; between two instructions a warp waits 1.5 issue slots for fixed latencies, 1.0 for its turn, 0.8 for
+// the ALU pipe and 0.5 for shared memory. ~9 us are launch, the first tokens, and the joining (one sequence of 1K: 10.1 us).
 #include <algorithm>
 
 #include <cuda_bf16.h>

@@ -34,15 +34,15 @@
 // bits.) The minimum enters as sixteen more channels: its value for each
 // group against the sum of the group's queries, in two FP16 parts. One stage of keys then has the room; its halves
 // (of the channels) fill and empty one by one. Taken when the log-sum-exp is asked for, and always with one tile of queries
-// of 128 channels, where it costs nothing (40 rows: 81 us, rounded keys 79).
+// of 128 channels, where it costs little (40 rows: 81 us, rounded keys 79).
 //
 // Work: one CTA per item (sequence, kv head, row block), those that see the most tokens first; or items cut
 // over the SMs (see kv4_prompt_plan), so that every SM has one part of one item, or, where the parts do
 // not fit, laid on one line and cut evenly (as in the kernel for few rows).
 //
 // Bound: the chain of a group's tile: S, its way to the registers, exponentials, P V. Two chunks of 4K over 8K (824
-// GFLOP) take 649 us where the card's rate for large BF16 products gives 424: the tensor pipe is 46% busy, issue 44%; tensor memory
-// is full, so a group's next S waits for its P V. 40 rows of eight sequences up to 32K: 82 us, 16 for their bytes: per
+// GFLOP) take 648 us where the card's rate for large BF16 products gives 424: the tensor pipe is 47% busy, issue 45%; tensor memory
+// is full at D = 128, so a group's next S waits for its P V. 40 rows of eight sequences up to 32K: 81 us, 16 for their bytes: per
 // token tile of ~3 k cycles the unpacking of two-part keys takes ~1.5 k and waits for the products of the half before.
 #include <algorithm>
 #include <type_traits>

@@ -600,7 +600,7 @@ size_t mla_qcache_kv4_workspace_bytes(const mla_qcache_kv4_config* cfg, int32_t 
  * the readout in FP16: those of tokens far below the row's top score are off by up to 2^-32 of the top one's weight (up
  * to 32 such rows: times the value's scale, by 2^-29 of the largest scale).
  * Capture: a call may be captured into a graph; grid and path go by the sizes of the call, the lengths are
- * read on the device at each replay.
+ * read on the device at each replay. They must not change while a call runs.
  * max_q: bound on the rows per sequence; a sequence with more sets MLA_QCACHE_DEV_ROWS, a length
  * outside [0, max_pages * P] MLA_QCACHE_DEV_SEQ_OVERFLOW (read as 0), a page id outside [0, n_pages)
  * MLA_QCACHE_DEV_BAD_PAGE (its tokens are left out). Pages that no row of a sequence sees any token of (behind a
