@@ -107,6 +107,10 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8], bool f16) {
   return make_uint4(pack2(x[0], x[1], f16), pack2(x[2], x[3], f16), pack2(x[4], x[5], f16), pack2(x[6], x[7], f16));
 }
 
+// The largest exponent E with max_abs * 2^E < 2^15 for every finite max_abs, at most 120: brings a row of queries into FP16.
+__device__ __forceinline__ int fp16_exponent(float max_abs) {
+  return max_abs > 0.f ? min(14 + 127 - static_cast<int>(__float_as_uint(max_abs) >> 23), 120) : 0;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -511,8 +511,7 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
       }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      bool range = false;
-      const int E = prescale_exponent<-114, 120>(mx, range);
+      const int E = fp16_exponent(mx);
       const float up = pow2_int(E);
       float sum[NG];
 #pragma unroll

@@ -831,8 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           }
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          bool range = false;
-          const int E = prescale_exponent<-114, 120>(mx, range) - (kExact ? 8 : 0);  // kExact: below 2^7, so that the sums fit
+          const int E = fp16_exponent(mx) - (kExact ? 8 : 0);  // kExact: below 2^7, so that the sums fit
           if ((lane >> 3) == i)  // a hidden score, -inf, stays one at scale 0
             fr = fmaxf(pow2_int(-E) * fabsf(p.scale_log2), 1e-37f);
           if (two || group == 0) {

@@ -125,3 +125,22 @@ def test_captured_steps_advance_among_steps_that_are_not():
         assert twin[0].seq_lens.tolist() == [n + i + 1 for n in lens] == twin[1].seq_lens.tolist()
         assert torch.equal(got, want) and torch.equal(twin[0].pool, twin[1].pool)
     assert twin[0].seq_lens.data_ptr() == array and twin[0].error_bits() == 0 == twin[1].error_bits()
+
+
+def test_captured_on_a_forked_stream():
+    """Inside a capture a second stream branches off, attends, and joins; the replayed graph gives what a plain call gives."""
+    cache, rng = filled([5000, 700], seed=9)
+    a, b = rows(rng, 2, 8), rows(rng, 2, 8)
+    want = [cache.attend(x, SCALE).clone() for x in (a, b)]
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        got = [cache.attend(a, SCALE, stream=side), cache.attend(b, SCALE)]
+        main.wait_stream(side)
+        total = got[0] + got[1]
+    for _ in range(5):
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(total, want[0] + want[1])
+    assert cache.error_bits() == 0
