@@ -1,5 +1,5 @@
 """Binding of the C ABI in include/mla_qcache.h (argument marshalling only): ctypes, and the native
-module _fastcall for the entry points of the grouped-query cache and the BF16 append.
+module _fastcall for the entry points of the grouped-query cache, of drafted trees and the BF16 append.
 
 Every step of the hot path runs in the CUDA kernels of libmla_qcache.so; this module only
 checks tensor dtypes/devices and passes raw pointers, sizes and the current CUDA stream.
@@ -27,7 +27,9 @@ EXPORTS = ("mla_qcache_page_bytes", "mla_qcache_config_check", "mla_qcache_works
            "mla_qcache_up_project", "mla_qcache_decode_attn_multi", "mla_qcache_decode_plan",
            "mla_qcache_selftest_wait_timeout", "mla_qcache_decode_attn_pending", "mla_qcache_decode_launches",
            "mla_qcache_kv4_config_check", "mla_qcache_kv4_page_bytes", "mla_qcache_kv4_append",
-           "mla_qcache_kv4_workspace_bytes", "mla_qcache_kv4_attn", "mla_qcache_append_bf16")
+           "mla_qcache_kv4_workspace_bytes", "mla_qcache_kv4_attn", "mla_qcache_append_bf16",
+           "mla_qcache_tree_mask", "mla_qcache_kv4_append_tree", "mla_qcache_kv4_attn_tree", "mla_qcache_verify_sampled",
+           "mla_qcache_verify_greedy", "mla_qcache_kv4_keep")
 
 
 class Config(ctypes.Structure):
@@ -72,6 +74,11 @@ class _View(ctypes.Structure):
 class _Rotation(ctypes.Structure):
     _fields_ = [("cos_tab", ctypes.c_void_p), ("sin_tab", ctypes.c_void_p), ("n_pos", ctypes.c_int32),
                 ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class _Tree(ctypes.Structure):
+    """mla_qcache_tree."""
+    _fields_ = [("mask", ctypes.c_void_p), ("mask_words", ctypes.c_int32), ("base", ctypes.c_void_p)]
 
 
 class QCacheError(RuntimeError):
@@ -152,6 +159,21 @@ def lib() -> ctypes.CDLL:
         L.mla_qcache_append_bf16.restype = ctypes.c_int
         L.mla_qcache_append_bf16.argtypes = [i32, i32, vp, i64, vp, vp, vp, i32, vp, ctypes.c_float, R, V, i32, vp, vp, vp,
                                              vp, i32, i32, vp, i64, vp, vp]
+        T, f32 = P(_Tree), ctypes.c_float
+        L.mla_qcache_tree_mask.restype = ctypes.c_int
+        L.mla_qcache_tree_mask.argtypes = [i32, i32, vp, vp, i32, i32, vp, vp, vp]
+        L.mla_qcache_kv4_append_tree.restype = ctypes.c_int
+        L.mla_qcache_kv4_append_tree.argtypes = [KC, i32, i32, i32, V, V, vp, vp, vp, i32, R, V, i32, vp, vp, vp, vp, i32, vp, i64, T,
+                                                 vp, vp]
+        L.mla_qcache_kv4_attn_tree.restype = ctypes.c_int
+        L.mla_qcache_kv4_attn_tree.argtypes = [KC, i32, i32, i32, i32, V, vp, i32, T, vp, i32, vp, vp, i64, i32, f32, vp, vp, vp, sz,
+                                               vp, vp]
+        L.mla_qcache_verify_sampled.restype = ctypes.c_int
+        L.mla_qcache_verify_sampled.argtypes = [i32, i32, i32, vp, i64, vp, i64, vp, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp]
+        L.mla_qcache_verify_greedy.restype = ctypes.c_int
+        L.mla_qcache_verify_greedy.argtypes = [i32, i32, i32, i32, vp, i64, vp, vp, i32, vp, i32, vp, vp, vp, vp, vp]
+        L.mla_qcache_kv4_keep.restype = ctypes.c_int
+        L.mla_qcache_kv4_keep.argtypes = [KC, i32, vp, i32, vp, vp, vp, i32, vp, i64, vp, vp, vp]
         L.mla_qcache_strerror.restype = ctypes.c_char_p
         L.mla_qcache_strerror.argtypes = [i32]
         _lib = L
@@ -464,16 +486,17 @@ _fast = None
 
 def mla_qcache_kv4_append(cfg: KV4Config, k_new, v_new, cu_new, seq_lens, max_new: int, page_table, pool, err_word,
                           cos=None, sin=None, interleaved=False, q=None, q_out=None, k_deq=None, v_deq=None,
-                          seq_lens_next=None, stream=None) -> None:
+                          seq_lens_next=None, stream=None, tree_mask=None, tree_base=None) -> None:
     """Append K/V rows to the grouped-query cache in 4 bits, keys and queries rotated on the way (see
     include/mla_qcache.h). k_new, v_new [rows, kv heads, D] and q [rows, heads, D] may be views of one
     projection's output. With seq_lens itself as seq_lens_next the lengths advance in place, behind the append
-    (mla_qcache_advance)."""
+    (mla_qcache_advance). With tree_mask ([rows] or [rows, words] int64) the rows are nodes of trees of drafted tokens, rotated to
+    tree_base [B] (by default the lengths) + the mask's bits - 1 (mla_qcache_kv4_append_tree)."""
     st = (_fast or _native()).kv4_append(cfg, k_new, v_new, cu_new, seq_lens, max_new, page_table, pool, err_word, cos, sin,
                                          interleaved, q, q_out, k_deq, v_deq, seq_lens_next,
-                                         None if stream is None else stream.cuda_stream)
+                                         None if stream is None else stream.cuda_stream, tree_mask, tree_base)
     if st:
-        _raise(st, "mla_qcache_kv4_append")
+        _raise(st, "mla_qcache_kv4_append" if tree_mask is None else "mla_qcache_kv4_append_tree")
 
 
 def mla_qcache_kv4_attn(cfg: KV4Config, q, page_table, seq_lens, pool, softmax_scale: float, out, workspace, err_word,
@@ -497,3 +520,52 @@ def mla_qcache_append_bf16(kv_new, cu_new, seq_lens, max_new: int, page_table, k
                                           None if stream is None else stream.cuda_stream)
     if st:
         _raise(st, "mla_qcache_append_bf16")
+
+
+# ---------------------------------------------------------------- trees of drafted tokens
+def mla_qcache_tree_mask(parents, cu_rows, max_rows: int, mask, err_word, stream=None) -> None:
+    """Masks [rows] or [rows, words] (int64) of nodes whose parents [rows] are given as numbers in their sequence (see
+    include/mla_qcache.h)."""
+    st = (_fast or _native()).tree_mask(parents, cu_rows, max_rows, mask, err_word, None if stream is None else stream.cuda_stream)
+    if st:
+        _raise(st, "mla_qcache_tree_mask")
+
+
+def mla_qcache_kv4_attn_tree(cfg: KV4Config, q, tree_mask, cu_q, max_q: int, page_table, seq_lens, pool, softmax_scale: float, out,
+                             workspace, err_word, tree_base=None, lse=None, window: int = 0, stream=None) -> None:
+    """Attention of nodes q [rows, heads, D] of trees of drafted tokens over the cache in 4 bits: each sees the tokens before its
+    tree (tree_base [B]; by default all but the sequence's rows) and the nodes that its mask names (see include/mla_qcache.h).
+    Workspace of kv4_workspace_bytes. Without cu_q one row per sequence."""
+    st = (_fast or _native()).kv4_attn_tree(cfg, q, page_table, seq_lens, pool, softmax_scale, out, workspace, err_word, cu_q, max_q,
+                                            lse, tree_mask, tree_base, window, None if stream is None else stream.cuda_stream)
+    if st:
+        _raise(st, "mla_qcache_kv4_attn_tree")
+
+
+def mla_qcache_verify_sampled(target_probs, tokens, cu_rows, max_rows: int, u_accept, u_sample, kept, new_tokens, n_kept, err_word,
+                              draft_probs=None, tree_mask=None, stream=None) -> None:
+    """Which drafted tokens the target accepts, and the token behind them, from the target's and the draft's probabilities [rows,
+    vocab] (float32, rows may be strided) and given random numbers (see include/mla_qcache.h). Without draft_probs the drafts were picked
+    without chance; without tree_mask each sequence's rows are a chain."""
+    st = (_fast or _native()).verify_sampled(target_probs, draft_probs, tokens, cu_rows, max_rows, tree_mask, u_accept, u_sample, kept,
+                                             new_tokens, n_kept, err_word, None if stream is None else stream.cuda_stream)
+    if st:
+        _raise(st, "mla_qcache_verify_sampled")
+
+
+def mla_qcache_verify_greedy(logits, tokens, cu_rows, max_rows: int, kept, new_tokens, n_kept, err_word, tree_mask=None,
+                             stream=None) -> None:
+    """The same for greedy decoding, from the target's logits [rows, vocab] (bfloat16, float16 or float32; rows may be strided)."""
+    st = (_fast or _native()).verify_greedy(logits, tokens, cu_rows, max_rows, tree_mask, kept, new_tokens, n_kept, err_word,
+                                            None if stream is None else stream.cuda_stream)
+    if st:
+        _raise(st, "mla_qcache_verify_greedy")
+
+
+def mla_qcache_kv4_keep(cfg: KV4Config, kept, n_kept, tree_base, page_table, pool, seq_lens, err_word, stream=None) -> None:
+    """Moves the accepted nodes kept [B, max_kept] (n_kept [B] of them) of each tree to the places behind tree_base [B] tokens and sets
+    seq_lens [B] to tree_base + n_kept (see include/mla_qcache.h)."""
+    st = (_fast or _native()).kv4_keep(cfg, kept, n_kept, tree_base, page_table, pool, seq_lens, err_word,
+                                       None if stream is None else stream.cuda_stream)
+    if st:
+        _raise(st, "mla_qcache_kv4_keep")

@@ -101,13 +101,17 @@ class KV4Cache:
         self.page_table = page_table.to(device=dev, dtype=torch.int32).contiguous()
         self.seq_lens = torch.zeros(batch, dtype=torch.int32, device=dev)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.tree_base = torch.zeros(batch, dtype=torch.int32, device=dev)  # tokens before the tree of drafted ones
         self._ws = {}  # per stream
         self._ws_need = {}  # workspace bytes per head count and rows
 
     def append(self, k: torch.Tensor, v: torch.Tensor, cu_new: torch.Tensor, max_new: int, stream=None, **kw) -> None:
         """Appends rows cu_new[b]..cu_new[b+1]-1 of k, v [N,Hkv,D] to sequence b and advances ``self.seq_lens`` in place,
         by a launch behind it: a captured append goes on from there at every replay, among calls that are not captured
-        too. Further arguments (cos, sin, interleaved, q, q_out, k_deq, v_deq) as for mla_qcache_kv4_append."""
+        too. Further arguments (cos, sin, interleaved, q, q_out, k_deq, v_deq) as for mla_qcache_kv4_append. With tree_mask the rows
+        are nodes of the trees that start_tree() began."""
+        if kw.get("tree_mask") is not None:
+            kw.setdefault("tree_base", self.tree_base)
         binding.mla_qcache_kv4_append(self.cfg, k, v, cu_new, self.seq_lens, max_new, self.page_table, self.pool, self.err,
                                       seq_lens_next=self.seq_lens, stream=stream, **kw)
 
@@ -134,17 +138,37 @@ class KV4Cache:
         return ws
 
     def attend(self, q: torch.Tensor, softmax_scale: float, cu_q: torch.Tensor | None = None, max_q: int = 1, out=None,
-               lse=None, causal: bool = True, window: int = 0, stream=None):
-        """Attention of query rows q [N,Hq,D], the last positions of their sequences, over the cache: out in q's type."""
+               lse=None, causal: bool = True, window: int = 0, stream=None, tree_mask: torch.Tensor | None = None):
+        """Attention of query rows q [N,Hq,D], the last positions of their sequences, over the cache: out in q's type. With
+        tree_mask ([N] or [N, words] int64) the rows are nodes of the trees that start_tree() began: each sees the tokens before its
+        tree and the nodes that its mask names."""
+        if tree_mask is not None and not causal:
+            raise ValueError("nodes of a tree see what their masks name: causal=False has no meaning for them")
         if out is None:
             with torch.cuda.stream(stream):  # memory that this stream may write at once (None: the current one)
                 out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
             if stream is not None:
                 out.record_stream(torch.cuda.current_stream(q.device))
+        if tree_mask is not None:
+            binding.mla_qcache_kv4_attn_tree(self.cfg, q, tree_mask, cu_q, max_q, self.page_table, self.seq_lens, self.pool, softmax_scale,
+                                             out, self.workspace(q.shape[1], max_q, stream), self.err, tree_base=self.tree_base, lse=lse,
+                                             window=window, stream=stream)
+            return out
         binding.mla_qcache_kv4_attn(self.cfg, q, self.page_table, self.seq_lens, self.pool, softmax_scale, out,
                                     self.workspace(q.shape[1], max_q, stream), self.err, cu_q=cu_q, max_q=max_q, lse=lse,
                                     causal=causal, window=window, stream=stream)
         return out
+
+    def start_tree(self, stream=None) -> None:
+        """Trees of drafted tokens begin behind the tokens that the sequences hold now: rows with a tree_mask, in append() and
+        attend(), are nodes of these trees until keep()."""
+        with torch.cuda.stream(stream):
+            self.tree_base.copy_(self.seq_lens)
+
+    def keep(self, kept: torch.Tensor, n_kept: torch.Tensor, stream=None) -> None:
+        """Of each tree the nodes kept [B, most] (n_kept [B] of them, as mla_qcache_verify_sampled and _greedy give them) stay, moved to the
+        places behind the tokens before the tree; ``self.seq_lens`` becomes their end."""
+        binding.mla_qcache_kv4_keep(self.cfg, kept, n_kept, self.tree_base, self.page_table, self.pool, self.seq_lens, self.err, stream)
 
     def error_bits(self) -> int:
         return int(self.err.item())

@@ -9,6 +9,7 @@
 #include "kernels.cuh"
 #include "kv4.cuh"
 #include "mla_qcache.h"
+#include "verify.cuh"
 
 namespace {
 
@@ -74,6 +75,17 @@ int check_rotation(const mla_qcache_rotation* r, int max_dim, mlaq::Rotation* ou
   return MLA_QCACHE_OK;
 }
 
+// Masks of up to 256 nodes. (Read as words of 32 bits, the low half of each first.)
+int check_tree(const mla_qcache_tree* t, const uint32_t** mask, const int32_t** base, int* words32) {
+  if (!t || !t->mask) return MLA_QCACHE_ERR_NULL;
+  if (t->mask_words < 1 || t->mask_words > mlaq::kMaxTreeRows / 64) return MLA_QCACHE_ERR_SHAPE;
+  if (!aligned(t->mask, 8) || !aligned(t->base, 4)) return MLA_QCACHE_ERR_ALIGN;
+  *mask = reinterpret_cast<const uint32_t*>(t->mask);
+  *base = t->base;
+  *words32 = 2 * t->mask_words;
+  return MLA_QCACHE_OK;
+}
+
 // The arrays that both appends take; n_rows == 0 leaves only the lengths to copy (*done).
 int check_append(int32_t B, int32_t n_rows, const int32_t* cu_new, const int32_t* seq_lens, int32_t* seq_next,
                  int32_t max_new, const int32_t* page_table, int32_t max_pages, bool paged, const int32_t* err_word,
@@ -99,22 +111,11 @@ int check_append(int32_t B, int32_t n_rows, const int32_t* cu_new, const int32_t
   return MLA_QCACHE_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-int mla_qcache_kv4_config_check(const mla_qcache_kv4_config* cfg) { return check_kv4(cfg); }
-
-size_t mla_qcache_kv4_page_bytes(const mla_qcache_kv4_config* cfg) {
-  return check_kv4(cfg) == MLA_QCACHE_OK ? static_cast<size_t>(kv4_page_bytes(cfg)) : 0;
-}
-
-int mla_qcache_kv4_append(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t n_rows,
-                          const mla_qcache_view* k_new, const mla_qcache_view* v_new, const int32_t* cu_new,
-                          const int32_t* seq_lens, int32_t* seq_lens_next, int32_t max_new,
-                          const mla_qcache_rotation* rotation, const mla_qcache_view* q, int32_t n_heads, void* q_out,
-                          void* k_deq, void* v_deq, const int32_t* page_table, int32_t max_pages, uint8_t* pool,
-                          int64_t n_pages, int32_t* err_word, void* stream) {
+int kv4_append(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t n_rows, const mla_qcache_view* k_new,
+               const mla_qcache_view* v_new, const int32_t* cu_new, const int32_t* seq_lens, int32_t* seq_lens_next,
+               int32_t max_new, const mla_qcache_rotation* rotation, const mla_qcache_view* q, int32_t n_heads, void* q_out,
+               void* k_deq, void* v_deq, const int32_t* page_table, int32_t max_pages, uint8_t* pool, int64_t n_pages,
+               int32_t* err_word, bool of_tree, const mla_qcache_tree* tree, void* stream) {
   int st = check_kv4(cfg);
   if (st != MLA_QCACHE_OK) return st;
   if (dtype != MLA_QCACHE_BF16 && dtype != MLA_QCACHE_FP16) return MLA_QCACHE_ERR_CONFIG;
@@ -123,6 +124,7 @@ int mla_qcache_kv4_append(const mla_qcache_kv4_config* cfg, int32_t dtype, int32
                     &done);
   if (st != MLA_QCACHE_OK || done) return st;
   mlaq::Kv4AppendParams p{};
+  if (of_tree && (st = check_tree(tree, &p.tree_mask, &p.tree_base, &p.mask_words)) != MLA_QCACHE_OK) return st;
   const int D = cfg->head_dim;
   if ((st = check_view(k_new, &p.k)) != MLA_QCACHE_OK || (st = check_view(v_new, &p.v)) != MLA_QCACHE_OK ||
       (st = check_rotation(rotation, D, &p.rot)) != MLA_QCACHE_OK)
@@ -171,36 +173,11 @@ int mla_qcache_kv4_append(const mla_qcache_kv4_config* cfg, int32_t dtype, int32
   return e == cudaSuccess ? MLA_QCACHE_OK : MLA_QCACHE_ERR_CUDA;
 }
 
-size_t mla_qcache_kv4_workspace_bytes(const mla_qcache_kv4_config* cfg, int32_t B, int32_t n_heads, int32_t max_q,
-                                      int32_t max_pages) {
-  if (check_kv4(cfg) != MLA_QCACHE_OK || max_pages < 1 || B < 1 || B > (1 << 20) || n_heads < 1 || n_heads > 4096 ||
-      n_heads % cfg->n_kv_heads || max_q < 1)
-    return 0;
-  int sms = 0;
-  if (sm_count(&sms) != MLA_QCACHE_OK) return 0;
-  const int G = n_heads / cfg->n_kv_heads, D = cfg->head_dim;
-  const size_t few = mlaq::kv4_decode_workspace_bytes(mlaq::kv4_decode_rows(max_q, G), D, sms);
-  if (!mlaq::kv4_uses_prompt(max_q, G)) return few;
-  // the rows of a call, up to max_q per sequence, decide how it is cut: the most that any needs. What a cut
-  // takes goes by the rows of an item (64, 128 or 256) alone; whether it is cut, by the number of row blocks.
-  const int64_t max_tokens = static_cast<int64_t>(max_pages) * cfg->page_size;
-  size_t most = few;
-  for (int i = 0; i < 2 * sms + 3; ++i) {
-    const int64_t rows = i == 0 ? 1 : i < 3 ? 64 * i / G + 1 : static_cast<int64_t>(i - 2) * 256 / G + 1;
-    if (rows > max_q) break;
-    const mlaq::Kv4PromptPlan z = mlaq::kv4_prompt_plan(B, cfg->n_kv_heads, static_cast<int>(rows), max_q, max_tokens, G, sms);
-    const size_t w = mlaq::kv4_prompt_workspace_bytes(z, D);
-    most = most > w ? most : w;
-    if (z.line && z.rows == 256) break;
-  }
-  return most;
-}
-
-int mla_qcache_kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t n_heads, int32_t n_rows,
-                        const mla_qcache_view* q, const int32_t* cu_q, int32_t max_q, const int32_t* page_table,
-                        int32_t max_pages, const int32_t* seq_lens, const uint8_t* pool, int64_t n_pages,
-                        int32_t causal, int32_t window, float softmax_scale, void* out, float* lse, void* workspace,
-                        size_t workspace_bytes, int32_t* err_word, void* stream) {
+int kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t n_heads, int32_t n_rows,
+             const mla_qcache_view* q, const int32_t* cu_q, int32_t max_q, const int32_t* page_table, int32_t max_pages,
+             const int32_t* seq_lens, const uint8_t* pool, int64_t n_pages, int32_t causal, int32_t window,
+             float softmax_scale, void* out, float* lse, void* workspace, size_t workspace_bytes, int32_t* err_word,
+             bool of_tree, const mla_qcache_tree* tree, void* stream) {
   int st = check_kv4(cfg);
   if (st != MLA_QCACHE_OK) return st;
   if (dtype != MLA_QCACHE_BF16 && dtype != MLA_QCACHE_FP16) return MLA_QCACHE_ERR_CONFIG;
@@ -211,8 +188,10 @@ int mla_qcache_kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t
       static_cast<int64_t>(max_pages) * cfg->page_size > 0x7ffff000)  // positions and steps are counted in 32 bits
     return MLA_QCACHE_ERR_SHAPE;
   if (!cu_q && (max_q != 1 || n_rows != B)) return MLA_QCACHE_ERR_SHAPE;
+  if (of_tree && tree && (max_q > mlaq::kMaxTreeRows || max_q > 64 * static_cast<int64_t>(tree->mask_words))) return MLA_QCACHE_ERR_SHAPE;
   if (n_rows == 0) return MLA_QCACHE_OK;
   mlaq::Kv4AttnParams p{};
+  if (of_tree && (st = check_tree(tree, &p.tree_mask, &p.tree_base, &p.mask_words)) != MLA_QCACHE_OK) return st;
   if ((st = check_view(q, &p.q)) != MLA_QCACHE_OK) return st;
   if (!page_table || !seq_lens || !pool || !out || !workspace || !err_word) return MLA_QCACHE_ERR_NULL;
   if (!aligned(cu_q, 4) || !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(pool, 16) || !aligned(out, 16) ||
@@ -260,8 +239,122 @@ int mla_qcache_kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t
   p.causal = causal != 0;
   p.f16 = dtype == MLA_QCACHE_FP16;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = prompt ? mlaq::launch_kv4_prompt(p, plan, D, D / cfg->group, cs)
-                               : mlaq::launch_kv4_decode(p, D, D / cfg->group, sms, cs);
+  const int groups = D / cfg->group;
+  const cudaError_t e = !of_tree ? (prompt ? mlaq::launch_kv4_prompt(p, plan, D, groups, cs) : mlaq::launch_kv4_decode(p, D, groups, sms, cs))
+                        : prompt ? mlaq::launch_kv4_prompt_tree(p, plan, D, groups, cs)
+                                 : mlaq::launch_kv4_decode_tree(p, D, groups, sms, cs);
+  return e == cudaSuccess ? MLA_QCACHE_OK : MLA_QCACHE_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mla_qcache_kv4_config_check(const mla_qcache_kv4_config* cfg) { return check_kv4(cfg); }
+
+size_t mla_qcache_kv4_page_bytes(const mla_qcache_kv4_config* cfg) {
+  return check_kv4(cfg) == MLA_QCACHE_OK ? static_cast<size_t>(kv4_page_bytes(cfg)) : 0;
+}
+
+int mla_qcache_kv4_append(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t n_rows,
+                          const mla_qcache_view* k_new, const mla_qcache_view* v_new, const int32_t* cu_new,
+                          const int32_t* seq_lens, int32_t* seq_lens_next, int32_t max_new,
+                          const mla_qcache_rotation* rotation, const mla_qcache_view* q, int32_t n_heads, void* q_out,
+                          void* k_deq, void* v_deq, const int32_t* page_table, int32_t max_pages, uint8_t* pool,
+                          int64_t n_pages, int32_t* err_word, void* stream) {
+  return kv4_append(cfg, dtype, B, n_rows, k_new, v_new, cu_new, seq_lens, seq_lens_next, max_new, rotation, q, n_heads, q_out,
+                    k_deq, v_deq, page_table, max_pages, pool, n_pages, err_word, false, nullptr, stream);
+}
+
+int mla_qcache_kv4_append_tree(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t n_rows,
+                          const mla_qcache_view* k_new, const mla_qcache_view* v_new, const int32_t* cu_new,
+                          const int32_t* seq_lens, int32_t* seq_lens_next, int32_t max_new,
+                          const mla_qcache_rotation* rotation, const mla_qcache_view* q, int32_t n_heads, void* q_out,
+                          void* k_deq, void* v_deq, const int32_t* page_table, int32_t max_pages, uint8_t* pool,
+                          int64_t n_pages, const mla_qcache_tree* tree, int32_t* err_word,
+                          void* stream) {
+  return kv4_append(cfg, dtype, B, n_rows, k_new, v_new, cu_new, seq_lens, seq_lens_next, max_new, rotation, q, n_heads, q_out,
+                    k_deq, v_deq, page_table, max_pages, pool, n_pages, err_word, true, tree, stream);
+}
+
+size_t mla_qcache_kv4_workspace_bytes(const mla_qcache_kv4_config* cfg, int32_t B, int32_t n_heads, int32_t max_q,
+                                      int32_t max_pages) {
+  if (check_kv4(cfg) != MLA_QCACHE_OK || max_pages < 1 || B < 1 || B > (1 << 20) || n_heads < 1 || n_heads > 4096 ||
+      n_heads % cfg->n_kv_heads || max_q < 1)
+    return 0;
+  int sms = 0;
+  if (sm_count(&sms) != MLA_QCACHE_OK) return 0;
+  const int G = n_heads / cfg->n_kv_heads, D = cfg->head_dim;
+  const size_t few = mlaq::kv4_decode_workspace_bytes(mlaq::kv4_decode_rows(max_q, G), D, sms);
+  if (!mlaq::kv4_uses_prompt(max_q, G)) return few;
+  // the rows of a call, up to max_q per sequence, decide how it is cut: the most that any needs. What a cut
+  // takes goes by the rows of an item (64, 128 or 256) alone; whether it is cut, by the number of row blocks.
+  const int64_t max_tokens = static_cast<int64_t>(max_pages) * cfg->page_size;
+  size_t most = few;
+  for (int i = 0; i < 2 * sms + 3; ++i) {
+    const int64_t rows = i == 0 ? 1 : i < 3 ? 64 * i / G + 1 : static_cast<int64_t>(i - 2) * 256 / G + 1;
+    if (rows > max_q) break;
+    const mlaq::Kv4PromptPlan z = mlaq::kv4_prompt_plan(B, cfg->n_kv_heads, static_cast<int>(rows), max_q, max_tokens, G, sms);
+    const size_t w = mlaq::kv4_prompt_workspace_bytes(z, D);
+    most = most > w ? most : w;
+    if (z.line && z.rows == 256) break;
+  }
+  return most;
+}
+
+int mla_qcache_kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t n_heads, int32_t n_rows,
+                        const mla_qcache_view* q, const int32_t* cu_q, int32_t max_q, const int32_t* page_table,
+                        int32_t max_pages, const int32_t* seq_lens, const uint8_t* pool, int64_t n_pages,
+                        int32_t causal, int32_t window, float softmax_scale, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, int32_t* err_word, void* stream) {
+  return kv4_attn(cfg, dtype, B, n_heads, n_rows, q, cu_q, max_q, page_table, max_pages, seq_lens, pool, n_pages, causal, window,
+                  softmax_scale, out, lse, workspace, workspace_bytes, err_word, false, nullptr, stream);
+}
+
+int mla_qcache_kv4_attn_tree(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t n_heads, int32_t n_rows,
+                             const mla_qcache_view* q, const int32_t* cu_q, int32_t max_q, const mla_qcache_tree* tree,
+                             const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens, const uint8_t* pool,
+                             int64_t n_pages, int32_t window, float softmax_scale, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, int32_t* err_word, void* stream) {
+  return kv4_attn(cfg, dtype, B, n_heads, n_rows, q, cu_q, max_q, page_table, max_pages, seq_lens, pool, n_pages, 1, window,
+                  softmax_scale, out, lse, workspace, workspace_bytes, err_word, true, tree, stream);
+}
+
+int mla_qcache_kv4_keep(const mla_qcache_kv4_config* cfg, int32_t B, const int32_t* kept, int32_t max_kept,
+                        const int32_t* n_kept, const int32_t* tree_base, const int32_t* page_table, int32_t max_pages,
+                        uint8_t* pool, int64_t n_pages, int32_t* seq_lens, int32_t* err_word, void* stream) {
+  const int st = check_kv4(cfg);
+  if (st != MLA_QCACHE_OK) return st;
+  if (B < 1 || B > (1 << 20) || max_kept < 1 || max_kept > mlaq::kMaxTreeRows || max_pages < 1 || n_pages < 1 ||
+      static_cast<int64_t>(max_pages) * cfg->page_size > 0x7ffff000)
+    return MLA_QCACHE_ERR_SHAPE;
+  if (!kept || !n_kept || !tree_base || !page_table || !pool || !seq_lens || !err_word) return MLA_QCACHE_ERR_NULL;
+  if (!aligned(kept, 4) || !aligned(n_kept, 4) || !aligned(tree_base, 4) || !aligned(page_table, 4) || !aligned(pool, 16) ||
+      !aligned(seq_lens, 4) || !aligned(err_word, 4))
+    return MLA_QCACHE_ERR_ALIGN;
+  const int64_t bytes = 4 * static_cast<int64_t>(B);  // heads of a sequence read the lists while the first stores its length
+  const Span lens = span_of(seq_lens, bytes), pages = span_of(pool, n_pages * kv4_page_bytes(cfg));
+  const Span in[4] = {span_of(kept, bytes * max_kept), span_of(n_kept, bytes), span_of(tree_base, bytes), span_of(page_table, bytes * max_pages)};
+  for (const Span& x : in)
+    if (overlap(lens, x) || overlap(pages, x)) return MLA_QCACHE_ERR_SHAPE;
+  if (overlap(lens, pages)) return MLA_QCACHE_ERR_SHAPE;
+  mlaq::Kv4KeepParams p{};
+  p.kept = kept;
+  p.n_kept = n_kept;
+  p.tree_base = tree_base;
+  p.page_table = page_table;
+  p.pool = pool;
+  p.seq_lens = seq_lens;
+  p.err = err_word;
+  p.n_pages = n_pages;
+  p.page_bytes = kv4_page_bytes(cfg);
+  p.B = B;
+  p.max_kept = max_kept;
+  p.max_pages = max_pages;
+  p.P = cfg->page_size;
+  p.p_shift = log2_of(p.P);
+  p.Hkv = cfg->n_kv_heads;
+  const cudaError_t e = mlaq::launch_kv4_keep(p, cfg->head_dim, cfg->head_dim / cfg->group, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MLA_QCACHE_OK : MLA_QCACHE_ERR_CUDA;
 }
 

@@ -29,6 +29,7 @@ struct RowPlace {
   int32_t pid;  // page
   int tp;       // token within the page
   int flags;    // device error bits
+  int b, len;   // its sequence, and the tokens that this held before
 };
 
 // Where row r of the call goes. Rows at and behind cu_new[B] belong to no sequence and are skipped
@@ -37,7 +38,7 @@ struct RowPlace {
 __device__ __forceinline__ RowPlace place_row(const int32_t* cu, const int32_t* lens, const int32_t* table, int B, int r,
                                               int max_new, int max_pages, int p_shift, int64_t n_pages, bool paged,
                                               int n_pos) {
-  RowPlace z{-1, 0, 0, 0};
+  RowPlace z{-1, 0, 0, 0, 0, 0};
   int b = 0, r0, r1, s0;
   if (B <= 32) {
     const int lane = threadIdx.x & 31, i = min(lane, B - 1);
@@ -82,6 +83,8 @@ __device__ __forceinline__ RowPlace place_row(const int32_t* cu, const int32_t* 
   }
   z.tp = static_cast<int>(t & ((1 << p_shift) - 1));
   z.t = t;
+  z.b = b;
+  z.len = s0;
   return z;
 }
 

@@ -93,7 +93,7 @@ struct Call {
     if (t.dim() != 3 || t.size(0) != rows || t.size(2) != dim || (heads >= 0 && t.size(1) != heads))
       raise(PyExc_ValueError, std::string(name) + " must be [" + std::to_string(rows) + ", " +
                                   (heads >= 0 ? std::to_string(heads) : "heads") + ", " + std::to_string(dim) + "], got " + shape_of(t));
-    if (t.stride(2) != 1) raise(error_type(), std::string(name) + ": the channels of a head must be contiguous");
+    if (t.numel() > 0 && t.stride(2) != 1) raise(error_type(), std::string(name) + ": the channels of a head must be contiguous");
     return {t.data_ptr(), rows > 1 ? t.stride(0) : 0, t.size(1) > 1 ? t.stride(1) : 0};
   }
   // cos and sin tables [positions, rot_dim / 2]; false: no rotation.
@@ -106,6 +106,32 @@ struct Call {
     *out = {static_cast<const float*>(c.data_ptr()), static_cast<const float*>(s), static_cast<int32_t>(c.size(0)),
             static_cast<int32_t>(2 * c.size(1)), as_bool(interleaved)};
     return true;
+  }
+  // Masks [rows] or [rows, words] of trees of drafted tokens; false: none.
+  bool tree(PyObject* mask, PyObject* base, int64_t rows, int64_t B, mla_qcache_tree* out) const {
+    if (mask == Py_None) {
+      if (base != Py_None) raise(PyExc_ValueError, "tree_base needs a tree_mask");
+      return false;
+    }
+    const at::Tensor& m = tensor(mask, "tree_mask");
+    if (m.dim() == 1) plain(mask, "tree_mask", at::kLong, {rows});
+    else plain(mask, "tree_mask", at::kLong, {rows, -1});
+    const int64_t words = m.dim() == 1 ? 1 : m.size(1);
+    if (words > INT32_MAX) raise(PyExc_ValueError, "tree_mask: too many words");
+    *out = {static_cast<const uint64_t*>(m.data_ptr()), static_cast<int32_t>(words),
+            static_cast<const int32_t*>(optional(base, "tree_base", at::kInt, {B}))};
+    return true;
+  }
+  // Rows [rows, any] with contiguous entries, strided from row to row.
+  const at::Tensor& strided(PyObject* o, const char* name, at::ScalarType type, int64_t rows, int64_t width) const {
+    const at::Tensor& t = tensor(o, name);
+    if (t.device() != device || t.scalar_type() != type)
+      raise(error_type(), std::string(name) + " must be " + c10::toString(type) + " on " + device.str() + ", got " +
+                              c10::toString(t.scalar_type()) + " on " + t.device().str());
+    if (t.dim() != 2 || (rows >= 0 && t.size(0) != rows) || (width >= 0 && t.size(1) != width))
+      raise(PyExc_ValueError, std::string(name) + " must be [rows, vocab], got " + shape_of(t));
+    if (t.numel() > 0 && t.size(1) > 1 && t.stride(1) != 1) raise(error_type(), std::string(name) + ": the entries of a row must be contiguous");
+    return t;
   }
   void* stream(PyObject* o) const {
     if (o != Py_None) {
@@ -170,7 +196,7 @@ PyObject* guarded(PyObject* const* a, Py_ssize_t got, Py_ssize_t want, F f) {
 }
 
 PyObject* kv4_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return guarded(args, n, 18, [](PyObject* const* a) {
+  return guarded(args, n, 20, [](PyObject* const* a) {
     const Config cfg(a[0]);
     const int64_t Hkv = cfg.p->n_kv_heads, D = cfg.p->head_dim;
     Call c;
@@ -202,45 +228,153 @@ PyObject* kv4_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     void* v_deq = c.optional(a[15], "v_deq", type, {rows, Hkv, D});
     void* next = c.optional(a[16], "seq_lens_next", at::kInt, {B});
     const bool in_place = next && next == lens.data_ptr();
+    mla_qcache_tree tree{};
+    const bool of_tree = c.tree(a[18], a[19], rows, B, &tree);
     void* stream = c.stream(a[17]);
-    const int status = mla_qcache_kv4_append(
-        cfg.p, dtype, extent(B, "B"), extent(rows, "rows"), &kv, &vv, static_cast<const int32_t*>(cu),
-        static_cast<const int32_t*>(lens.data_ptr()), in_place ? nullptr : static_cast<int32_t*>(next), max_new,
-        rotated ? &rot : nullptr, q_out ? &qv : nullptr, extent(heads, "heads"), q_out, k_deq, v_deq,
-        static_cast<const int32_t*>(table.data_ptr()), extent(table.size(1), "page_table"), static_cast<uint8_t*>(pool.data_ptr()),
-        pool.size(0), static_cast<int32_t*>(err), stream);
+    const int32_t* const cu32 = static_cast<const int32_t*>(cu);
+    const int32_t* const lens32 = static_cast<const int32_t*>(lens.data_ptr());
+    int32_t* const next32 = in_place ? nullptr : static_cast<int32_t*>(next);
+    const int32_t* const table32 = static_cast<const int32_t*>(table.data_ptr());
+    const int32_t pages = extent(table.size(1), "page_table");
+    uint8_t* const bytes = static_cast<uint8_t*>(pool.data_ptr());
+    const int status =
+        of_tree ? mla_qcache_kv4_append_tree(cfg.p, dtype, extent(B, "B"), extent(rows, "rows"), &kv, &vv, cu32, lens32, next32, max_new,
+                                             rotated ? &rot : nullptr, q_out ? &qv : nullptr, extent(heads, "heads"), q_out, k_deq,
+                                             v_deq, table32, pages, bytes, pool.size(0), &tree, static_cast<int32_t*>(err), stream)
+                : mla_qcache_kv4_append(cfg.p, dtype, extent(B, "B"), extent(rows, "rows"), &kv, &vv, cu32, lens32, next32, max_new,
+                                        rotated ? &rot : nullptr, q_out ? &qv : nullptr, extent(heads, "heads"), q_out, k_deq, v_deq,
+                                        table32, pages, bytes, pool.size(0), static_cast<int32_t*>(err), stream);
     if (status != MLA_QCACHE_OK || !in_place) return status;
     return mla_qcache_advance(static_cast<const int32_t*>(cu), static_cast<int32_t*>(lens.data_ptr()), extent(B, "B"), stream);
   });
 }
 
-PyObject* kv4_attn(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return guarded(args, n, 15, [](PyObject* const* a) {
+// With a tree (kv4_attn_tree) the arguments 12 .. 14 are its mask and base and the window, else causal and the window.
+template <bool kTree>
+int attn(PyObject* const* a) {
+  const Config cfg(a[0]);
+  const int64_t D = cfg.p->head_dim;
+  Call c;
+  const at::Tensor& q = c.lead(a[1], "q");
+  const at::ScalarType type = q.scalar_type();
+  const int32_t dtype = row_type(q, "q");
+  if (q.dim() != 3) raise(PyExc_ValueError, "q must be [rows, heads, D], got " + shape_of(q));
+  const int64_t rows = q.size(0), heads = q.size(1);
+  const mla_qcache_view qv = c.view(a[1], "q", type, rows, heads, D);
+  const at::Tensor& lens = c.plain(a[3], "seq_lens", at::kInt, {-1});
+  const int64_t B = lens.size(0);
+  const at::Tensor& table = c.plain(a[2], "page_table", at::kInt, {B, -1});
+  const at::Tensor& pool = c.plain(a[4], "pool", at::kByte, {-1, static_cast<int64_t>(mla_qcache_kv4_page_bytes(cfg.p))});
+  const float scale = as_float(a[5]);
+  void* out = c.ptr(a[6], "out", type, {rows, heads, D});
+  const at::Tensor& ws = c.plain(a[7], "workspace", at::kByte, {-1});
+  int32_t* const err = static_cast<int32_t*>(c.ptr(a[8], "err_word", at::kInt, {1}));
+  const int32_t* const cu = static_cast<const int32_t*>(c.optional(a[9], "cu_q", at::kInt, {B + 1}));
+  float* const lse = static_cast<float*>(c.optional(a[11], "lse", at::kFloat, {rows, heads}));
+  const int32_t* const table32 = static_cast<const int32_t*>(table.data_ptr());
+  const int32_t* const lens32 = static_cast<const int32_t*>(lens.data_ptr());
+  const uint8_t* const bytes = static_cast<const uint8_t*>(pool.data_ptr());
+  const int32_t pages = extent(table.size(1), "page_table"), max_q = as_int(a[10], "max_q");
+  if constexpr (kTree) {
+    mla_qcache_tree tree{};
+    if (!c.tree(a[12], a[13], rows, B, &tree)) raise(error_type(), "tree_mask is required");
+    return mla_qcache_kv4_attn_tree(cfg.p, dtype, extent(B, "B"), extent(heads, "heads"), extent(rows, "rows"), &qv, cu, max_q, &tree,
+                                    table32, pages, lens32, bytes, pool.size(0), as_int(a[14], "window"), scale, out, lse,
+                                    ws.data_ptr(), static_cast<size_t>(ws.size(0)), err, c.stream(a[15]));
+  }
+  return mla_qcache_kv4_attn(cfg.p, dtype, extent(B, "B"), extent(heads, "heads"), extent(rows, "rows"), &qv, cu, max_q, table32,
+                             pages, lens32, bytes, pool.size(0), as_bool(a[12]), as_int(a[13], "window"), scale, out, lse,
+                             ws.data_ptr(), static_cast<size_t>(ws.size(0)), err, c.stream(a[14]));
+}
+PyObject* kv4_attn(PyObject*, PyObject* const* args, Py_ssize_t n) { return guarded(args, n, 15, attn<false>); }
+PyObject* kv4_attn_tree(PyObject*, PyObject* const* args, Py_ssize_t n) { return guarded(args, n, 16, attn<true>); }
+
+PyObject* kv4_keep(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded(args, n, 9, [](PyObject* const* a) {
     const Config cfg(a[0]);
-    const int64_t D = cfg.p->head_dim;
     Call c;
-    const at::Tensor& q = c.lead(a[1], "q");
-    const at::ScalarType type = q.scalar_type();
-    const int32_t dtype = row_type(q, "q");
-    if (q.dim() != 3) raise(PyExc_ValueError, "q must be [rows, heads, D], got " + shape_of(q));
-    const int64_t rows = q.size(0), heads = q.size(1);
-    const mla_qcache_view qv = c.view(a[1], "q", type, rows, heads, D);
-    const at::Tensor& lens = c.plain(a[3], "seq_lens", at::kInt, {-1});
-    const int64_t B = lens.size(0);
-    const at::Tensor& table = c.plain(a[2], "page_table", at::kInt, {B, -1});
-    const at::Tensor& pool = c.plain(a[4], "pool", at::kByte, {-1, static_cast<int64_t>(mla_qcache_kv4_page_bytes(cfg.p))});
-    const float scale = as_float(a[5]);
-    void* out = c.ptr(a[6], "out", type, {rows, heads, D});
-    const at::Tensor& ws = c.plain(a[7], "workspace", at::kByte, {-1});
-    void* err = c.ptr(a[8], "err_word", at::kInt, {1});
-    const void* cu = c.optional(a[9], "cu_q", at::kInt, {B + 1});
-    void* lse = c.optional(a[11], "lse", at::kFloat, {rows, heads});
-    return mla_qcache_kv4_attn(cfg.p, dtype, extent(B, "B"), extent(heads, "heads"), extent(rows, "rows"), &qv,
-                               static_cast<const int32_t*>(cu), as_int(a[10], "max_q"), static_cast<const int32_t*>(table.data_ptr()),
-                               extent(table.size(1), "page_table"), static_cast<const int32_t*>(lens.data_ptr()),
-                               static_cast<const uint8_t*>(pool.data_ptr()), pool.size(0), as_bool(a[12]),
-                               as_int(a[13], "window"), scale, out, static_cast<float*>(lse), ws.data_ptr(),
-                               static_cast<size_t>(ws.size(0)), static_cast<int32_t*>(err), c.stream(a[14]));
+    const at::Tensor& kept = c.lead(a[1], "kept");
+    c.plain(a[1], "kept", at::kInt, {-1, -1});
+    const int64_t B = kept.size(0);
+    const void* count = c.ptr(a[2], "n_kept", at::kInt, {B});
+    const void* base = c.ptr(a[3], "tree_base", at::kInt, {B});
+    const at::Tensor& table = c.plain(a[4], "page_table", at::kInt, {B, -1});
+    const at::Tensor& pool = c.plain(a[5], "pool", at::kByte, {-1, static_cast<int64_t>(mla_qcache_kv4_page_bytes(cfg.p))});
+    void* lens = c.ptr(a[6], "seq_lens", at::kInt, {B});
+    void* err = c.ptr(a[7], "err_word", at::kInt, {1});
+    return mla_qcache_kv4_keep(cfg.p, extent(B, "B"), static_cast<const int32_t*>(kept.data_ptr()), extent(kept.size(1), "kept"),
+                               static_cast<const int32_t*>(count), static_cast<const int32_t*>(base),
+                               static_cast<const int32_t*>(table.data_ptr()), extent(table.size(1), "page_table"),
+                               static_cast<uint8_t*>(pool.data_ptr()), pool.size(0), static_cast<int32_t*>(lens),
+                               static_cast<int32_t*>(err), c.stream(a[8]));
+  });
+}
+
+// What both ways of verifying take beside the rows: tokens, offsets, masks, results.
+struct Drafts {
+  const int32_t *tokens, *cu;
+  mla_qcache_tree tree{};
+  int32_t B, rows, max_rows, *kept, *news, *count, *err;
+  Drafts(const Call& c, int64_t n, PyObject* tokens_, PyObject* cu_, PyObject* max_rows_, PyObject* mask, PyObject* kept_,
+         PyObject* new_, PyObject* count_, PyObject* err_) {
+    const at::Tensor& k = c.plain(kept_, "kept", at::kInt, {-1, -1});
+    B = extent(k.size(0), "B"), rows = extent(n, "rows"), max_rows = as_int(max_rows_, "max_rows");
+    if (k.size(1) != max_rows) raise(PyExc_ValueError, "kept must be [B, max_rows], got " + shape_of(k));
+    tokens = static_cast<const int32_t*>(c.ptr(tokens_, "tokens", at::kInt, {n}));
+    cu = static_cast<const int32_t*>(c.ptr(cu_, "cu_rows", at::kInt, {B + 1ll}));
+    c.tree(mask, Py_None, n, B, &tree);
+    kept = static_cast<int32_t*>(k.data_ptr());
+    news = static_cast<int32_t*>(c.ptr(new_, "new_tokens", at::kInt, {B, max_rows}));
+    count = static_cast<int32_t*>(c.ptr(count_, "n_kept", at::kInt, {B}));
+    err = static_cast<int32_t*>(c.ptr(err_, "err_word", at::kInt, {1}));
+  }
+};
+
+PyObject* verify_sampled(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded(args, n, 13, [](PyObject* const* a) {
+    Call c;
+    const at::Tensor& p = c.lead(a[0], "target_probs");
+    c.strided(a[0], "target_probs", at::kFloat, -1, -1);
+    const int64_t rows = p.size(0), vocab = p.size(1);
+    const at::Tensor* const q = a[1] == Py_None ? nullptr : &c.strided(a[1], "draft_probs", at::kFloat, rows, vocab);
+    const Drafts d(c, rows, a[2], a[3], a[4], a[5], a[8], a[9], a[10], a[11]);
+    const void* ua = c.ptr(a[6], "u_accept", at::kFloat, {rows});
+    const void* us = c.ptr(a[7], "u_sample", at::kFloat, {d.B});
+    return mla_qcache_verify_sampled(d.B, d.rows, extent(vocab, "vocab"), static_cast<const float*>(p.data_ptr()),
+                                     rows > 1 ? p.stride(0) : 0, q ? static_cast<const float*>(q->data_ptr()) : nullptr,
+                                     q && rows > 1 ? q->stride(0) : 0, d.tokens, d.cu, d.max_rows, d.tree.mask, d.tree.mask_words,
+                                     static_cast<const float*>(ua), static_cast<const float*>(us), d.kept, d.news, d.count, d.err,
+                                     c.stream(a[12]));
+  });
+}
+
+PyObject* verify_greedy(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded(args, n, 10, [](PyObject* const* a) {
+    Call c;
+    const at::Tensor& x = c.lead(a[0], "logits");
+    const int32_t dtype = x.scalar_type() == at::kFloat ? MLA_QCACHE_FP32 : row_type(x, "logits");
+    c.strided(a[0], "logits", x.scalar_type(), -1, -1);
+    const int64_t rows = x.size(0);
+    const Drafts d(c, rows, a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8]);
+    return mla_qcache_verify_greedy(d.B, d.rows, extent(x.size(1), "vocab"), dtype, x.data_ptr(), rows > 1 ? x.stride(0) : 0, d.tokens,
+                                    d.cu, d.max_rows, d.tree.mask, d.tree.mask_words, d.kept, d.news, d.count, d.err, c.stream(a[9]));
+  });
+}
+
+PyObject* tree_mask(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded(args, n, 6, [](PyObject* const* a) {
+    Call c;
+    const at::Tensor& parents = c.lead(a[0], "parents");
+    c.plain(a[0], "parents", at::kInt, {-1});
+    const int64_t rows = parents.size(0);
+    const at::Tensor& cu = c.plain(a[1], "cu_rows", at::kInt, {-1});
+    if (cu.size(0) < 2) raise(PyExc_ValueError, "cu_rows must be [B + 1], got " + shape_of(cu));
+    mla_qcache_tree tree{};
+    if (!c.tree(a[3], Py_None, rows, 0, &tree)) raise(error_type(), "mask is required");
+    void* err = c.ptr(a[4], "err_word", at::kInt, {1});
+    return mla_qcache_tree_mask(extent(cu.size(0) - 1, "B"), extent(rows, "rows"), static_cast<const int32_t*>(parents.data_ptr()),
+                                static_cast<const int32_t*>(cu.data_ptr()), as_int(a[2], "max_rows"), tree.mask_words,
+                                const_cast<uint64_t*>(tree.mask), static_cast<int32_t*>(err), c.stream(a[5]));
   });
 }
 
@@ -304,6 +438,11 @@ PyObject* set_error(PyObject*, PyObject* type) {
 #define FASTCALL(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr
 PyMethodDef kMethods[] = {{"kv4_append", FASTCALL(kv4_append)},
                           {"kv4_attn", FASTCALL(kv4_attn)},
+                          {"kv4_attn_tree", FASTCALL(kv4_attn_tree)},
+                          {"kv4_keep", FASTCALL(kv4_keep)},
+                          {"verify_sampled", FASTCALL(verify_sampled)},
+                          {"verify_greedy", FASTCALL(verify_greedy)},
+                          {"tree_mask", FASTCALL(tree_mask)},
                           {"append_bf16", FASTCALL(append_bf16)},
                           {"set_error", set_error, METH_O, nullptr},
                           {nullptr, nullptr, 0, nullptr}};

@@ -36,6 +36,10 @@ struct Kv4AppendParams {
   int64_t n_pages, page_bytes;
   int B, n_rows, max_new, max_pages, P, p_shift, Hq, Hkv;
   bool f16;  // FP16 rows (else BF16)
+  // Nodes of trees of drafted tokens: rotated to tree_base[b] (nullptr: seq_lens[b]) + bits of the row's mask - 1.
+  const uint32_t* tree_mask;  // [rows][mask_words], else nullptr
+  const int32_t* tree_base;
+  int mask_words;  // of 32 bits
 };
 cudaError_t launch_kv4_append(const Kv4AppendParams& p, int D, int n_groups, cudaStream_t stream);
 
@@ -70,6 +74,9 @@ struct Kv4AttnParams {
   float scale_log2;
   int B, n_rows, max_q, Hq, Hkv, G, max_pages, P, p_shift, window;
   bool causal, f16;
+  const uint32_t* tree_mask;  // trees of drafted tokens: [rows][mask_words], else nullptr
+  const int32_t* tree_base;   // [B] tokens before the tree, or nullptr: all but the sequence's rows
+  int mask_words;             // of 32 bits
 };
 // The workspace begins with one counter per CTA, at the same place for every problem size (a
 // workspace may serve calls of different sizes one after the other).
@@ -79,6 +86,17 @@ int kv4_decode_rows(int max_q, int G);
 int kv4_decode_ctas(int num_sms);
 size_t kv4_decode_workspace_bytes(int rows, int D, int num_sms);
 cudaError_t launch_kv4_decode(const Kv4AttnParams& p, int D, int n_groups, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv4_decode_tree(const Kv4AttnParams& p, int D, int n_groups, int num_sms, cudaStream_t stream);
+
+// Tokens base + kept[i] of a sequence move to base + i, i < n_kept, and its length becomes base + n_kept.
+struct Kv4KeepParams {
+  const int32_t *kept, *n_kept, *tree_base, *page_table;  // kept: [B][max_kept]
+  uint8_t* pool;
+  int32_t *seq_lens, *err;
+  int64_t n_pages, page_bytes;
+  int B, max_kept, max_pages, P, p_shift, Hkv;
+};
+cudaError_t launch_kv4_keep(const Kv4KeepParams& p, int D, int n_groups, cudaStream_t stream);
 
 // More rows than the decode kernel holds go to the fifth-generation tensor cores: 128 rows of
 // queries (or two tiles of 128), one CTA per item or, with few items, the items cut over the SMs.
@@ -91,5 +109,6 @@ bool kv4_uses_prompt(int max_q, int G);
 Kv4PromptPlan kv4_prompt_plan(int B, int Hkv, int n_rows, int max_q, int64_t max_tokens, int G, int num_sms);
 size_t kv4_prompt_workspace_bytes(const Kv4PromptPlan& z, int D);
 cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, const Kv4PromptPlan& z, int D, int n_groups, cudaStream_t stream);
+cudaError_t launch_kv4_prompt_tree(const Kv4AttnParams& p, const Kv4PromptPlan& z, int D, int n_groups, cudaStream_t stream);
 
 }  // namespace mlaq

@@ -140,12 +140,21 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) kv4_append_kernel(c
   // two heads of each kind ahead of their use; the first ones while the row's place is found
   uint4 kv0 = load_kv(slot), kv1 = load_kv(slot + kSlots), q0 = load_q(slot), q1 = load_q(slot + kSlots);
   const RowPlace at = place_row(p.cu_new, p.seq_lens, p.page_table, p.B, r, p.max_new, p.max_pages, p.p_shift, p.n_pages,
-                                true, p.rot.rot_dim ? p.rot.n_pos : 0x7fffffff);
+                                true, p.rot.rot_dim && !p.tree_mask ? p.rot.n_pos : 0x7fffffff);
   if (at.t < 0) {
     if (tid == 0 && at.flags) atomicOr(p.err, at.flags);
     return;
   }
-  const Angles ang = load_angles(p.rot, at.t, i);
+  int64_t pos = at.t;  // that the rotation turns to
+  if (p.tree_mask) {  // a node of a tree: as many behind the tree's base as it has ancestors
+    pos = (p.tree_base ? __ldg(p.tree_base + at.b) : at.len) - 1;
+    for (int w = 0; w < p.mask_words; ++w) pos += __popc(__ldg(p.tree_mask + static_cast<size_t>(r) * p.mask_words + w));
+    if (p.rot.rot_dim && (pos < 0 || pos >= p.rot.n_pos)) {
+      if (tid == 0) atomicOr(p.err, kErrSeqOverflow);
+      return;
+    }
+  }
+  const Angles ang = load_angles(p.rot, pos, i);
   uint8_t* page = p.pool + static_cast<size_t>(at.pid) * p.page_bytes;
   const int head_bytes = kv4_head_bytes(D, NG, p.P);
   int flags = 0;

@@ -1,0 +1,10 @@
+// Attention over the 4-bit grouped-query cache for few query rows per kv head: nodes of trees of drafted tokens.
+#include "kv4_attn.cuh"
+
+namespace mlaq {
+
+cudaError_t launch_kv4_decode_tree(const Kv4AttnParams& p, int D, int n_groups, int num_sms, cudaStream_t stream) {
+  return launch_decode_kernel<true>(p, D, n_groups, num_sms, stream);
+}
+
+}  // namespace mlaq

@@ -513,6 +513,7 @@ typedef struct {
 /* Element type of the rows (keys, values, queries, outputs). */
 #define MLA_QCACHE_BF16 0
 #define MLA_QCACHE_FP16 1
+#define MLA_QCACHE_FP32 2 /* logits alone */
 
 /* Rows of heads in device memory: element (r, h, c) at data[r*row_stride + h*head_stride + c].
  * Strides are in elements, >= 0 and multiples of 8; data is 16-byte aligned. (The struct itself is
@@ -614,6 +615,129 @@ int mla_qcache_kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t
                         int32_t max_pages, const int32_t* seq_lens, const uint8_t* pool, int64_t n_pages,
                         int32_t causal, int32_t window, float softmax_scale, void* out, float* lse, void* workspace,
                         size_t workspace_bytes, int32_t* err_word, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------------------------
+ * Trees of drafted tokens
+ *
+ * A drafting model offers several continuations at once, a tree; the target model reads all of them in one call, accepts one path
+ * from the root, and the cache keeps that path alone. A step:
+ *   1. the nodes' keys and values enter the cache behind its tokens       mla_qcache_kv4_append_tree
+ *   2. every node attends to the tokens before the tree and its ancestors mla_qcache_kv4_attn_tree     (1, 2: per layer)
+ *   3. the accepted path and the token behind it                          mla_qcache_verify_sampled / _greedy
+ *   4. the path's tokens move to the front, the others go                 mla_qcache_kv4_keep          (per layer)
+ * Node 0, the root, is the last token that is certain (the one that step 3 of the step before chose): its key is not in the cache
+ * yet and its row of the target's output is the distribution of the first drafted token. Nodes are numbered so that a parent
+ * comes before its children; node j of sequence b is the cached token tree_base[b] + j. A drafting model that grows its tree level
+ * by level appends and attends with the newest nodes alone; its tree begins at the same base.
+ */
+typedef struct {
+  const uint64_t* mask; /* device [n_rows][mask_words], 8-byte aligned: for each row of the call, bit j % 64 of word j / 64 says
+                           that node j is an ancestor of the row's node or that node itself */
+  int32_t mask_words;   /* 1..4: trees of up to 256 nodes */
+  const int32_t* base;  /* device [B], 4-byte aligned: tokens of each sequence before its tree; NULL: see the entry points */
+} mla_qcache_tree;
+
+/*
+ * Masks of trees whose parents are known: rows cu_rows[b] .. cu_rows[b+1]-1 are sequence b's nodes in order, parents[r] the number of
+ * row r's parent in its sequence (-1: none). mask [n_rows][mask_words]; at most max_rows (up to 64 * mask_words) nodes per
+ * sequence. A parent that does not come before its child is taken as none, a sequence with more rows is skipped: both set
+ * MLA_QCACHE_DEV_ROWS. Rows from cu_rows[B] on are left alone.
+ * Errors: B < 1 or > 2^20, n_rows < 0, mask_words not 1..4, max_rows < 1 or > 64 * mask_words, overlapping buffers ->
+ * MLA_QCACHE_ERR_SHAPE; NULL -> MLA_QCACHE_ERR_NULL; misaligned -> MLA_QCACHE_ERR_ALIGN.
+ */
+int mla_qcache_tree_mask(int32_t B, int32_t n_rows, const int32_t* parents, const int32_t* cu_rows, int32_t max_rows,
+                         int32_t mask_words, uint64_t* mask, int32_t* err_word, void* stream);
+
+/*
+ * mla_qcache_kv4_append of a tree's nodes: rows go behind the sequence's tokens as there, but are rotated to the positions that
+ * they would have as text, base + (bits of the row's mask) - 1: siblings share a position. tree->base NULL: seq_lens (the whole tree
+ * enters in this call). A position outside the rotation's table sets MLA_QCACHE_DEV_SEQ_OVERFLOW and the row is skipped.
+ * Errors: as mla_qcache_kv4_append; tree or its mask NULL -> MLA_QCACHE_ERR_NULL; mask_words not 1..4 -> MLA_QCACHE_ERR_SHAPE.
+ */
+int mla_qcache_kv4_append_tree(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t n_rows,
+                               const mla_qcache_view* k_new, const mla_qcache_view* v_new, const int32_t* cu_new,
+                               const int32_t* seq_lens, int32_t* seq_lens_next, int32_t max_new,
+                               const mla_qcache_rotation* rotation, const mla_qcache_view* q, int32_t n_heads,
+                               void* q_out, void* k_deq, void* v_deq, const int32_t* page_table, int32_t max_pages,
+                               uint8_t* pool, int64_t n_pages, const mla_qcache_tree* tree, int32_t* err_word,
+                               void* stream);
+
+/*
+ * mla_qcache_kv4_attn for rows that are nodes of trees. seq_lens[b] counts the tree's tokens in; a row sees
+ *   the tokens t < base, with window > 0 only those with t > base + (bits of its mask) - 1 - window, and
+ *   the tokens base + j < seq_lens[b] whose bit j its mask has (whatever the window).
+ * tree->base NULL: seq_lens[b] minus the sequence's rows. A base outside [0, seq_lens[b]] sets MLA_QCACHE_DEV_SEQ_OVERFLOW (the
+ * sequence is read as empty). A mask need not name the row's own node, and a row that sees nothing gets out = 0, lse = -inf.
+ * Pages without a token in [base - window, base + 64 * mask_words) are not read with a window: their ids may be anything.
+ * Numerics, workspace (mla_qcache_kv4_workspace_bytes for the same sizes) and capture as for mla_qcache_kv4_attn.
+ * Errors: as mla_qcache_kv4_attn; max_q > 64 * mask_words, mask_words not 1..4 -> MLA_QCACHE_ERR_SHAPE; tree or its mask NULL ->
+ * MLA_QCACHE_ERR_NULL.
+ */
+int mla_qcache_kv4_attn_tree(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t n_heads, int32_t n_rows,
+                             const mla_qcache_view* q, const int32_t* cu_q, int32_t max_q, const mla_qcache_tree* tree,
+                             const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens, const uint8_t* pool,
+                             int64_t n_pages, int32_t window, float softmax_scale, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, int32_t* err_word, void* stream);
+
+/*
+ * Verification of drafted tokens by the target model's probabilities, from given random numbers: what comes out is distributed as
+ * if the target alone had been sampled. Rows cu_rows[b] .. cu_rows[b+1]-1 are sequence b's nodes 0, 1, ..; p = target[r] is the
+ * target's distribution behind node r, q = draft[r] the one from which the children of node r were drawn, independently of one
+ * another. From node 0 on, the children x of the node reached are tried in order, beginning with c = 0, Z = 1:
+ *   accepted  if u_accept[x] q(x) Z < max(p(x) - c q(x), 0): its children are next, with c = 0, Z = 1;
+ *   else      c <- c + Z, Z <- sum over the vocabulary of max(p - c q, 0).
+ * Where no child is accepted, the new token is the first one at which the running sum of max(p - c q, 0) over the vocabulary
+ * exceeds u_sample[b] times its whole sum (p itself, if nothing is left).
+ * draft NULL: the children were picked without chance (the draft's most likely tokens, say), q(x) = 1 at a child's own token:
+ * accepted if u_accept[x] Z < p(x), else p(x) leaves Z and the row.
+ *   target     [n_rows] rows of vocab float32, target_stride elements apart (any, >= 0); draft the same.
+ *              Probabilities that are negative, infinite or NaN count as 0; the rows are not summed: each is taken to sum to 1.
+ *   tokens     [n_rows] int32, node 0's is not looked at; a token outside [0, vocab) is never accepted (-1 pads a tree).
+ *   tree_mask  as mla_qcache_tree.mask, a node's parent being the last node before it in its mask; NULL: chains, a row's parent is the
+ *              row before it.
+ *   max_rows   bound on the rows per sequence, 1..256 (and 64 * mask_words).
+ *   u_accept   [n_rows] float32 in [0, 1), node 0's is not looked at; u_sample [B] float32 in [0, 1).
+ *   kept       [B][max_rows] int32: node 0 and the accepted nodes, in order; then -1.
+ *   new_tokens [B][max_rows] int32: the accepted tokens, then the new one, n_kept in all; then -1.
+ *   n_kept     [B] int32: nodes kept (accepted ones + 1). 0 for a sequence without rows.
+ * Sums and comparisons carry 45 bits or more. A sequence with more than max_rows rows sets MLA_QCACHE_DEV_ROWS (n_kept = 0); a
+ * node without any probability to draw from sets MLA_QCACHE_DEV_RANGE (its token is -1).
+ * Errors: B < 1 or > 2^20, n_rows < 0, vocab < 1, max_rows or mask_words out of range, negative strides, outputs that overlap
+ * inputs or one another -> MLA_QCACHE_ERR_SHAPE; missing pointers -> MLA_QCACHE_ERR_NULL; misaligned -> MLA_QCACHE_ERR_ALIGN.
+ */
+int mla_qcache_verify_sampled(int32_t B, int32_t n_rows, int32_t vocab, const float* target, int64_t target_stride,
+                              const float* draft, int64_t draft_stride, const int32_t* tokens, const int32_t* cu_rows,
+                              int32_t max_rows, const uint64_t* tree_mask, int32_t mask_words, const float* u_accept,
+                              const float* u_sample, int32_t* kept, int32_t* new_tokens, int32_t* n_kept, int32_t* err_word,
+                              void* stream);
+
+/*
+ * Verification for greedy decoding: the token behind node r is the largest of logits[r] (BF16, FP16 or float32; the lowest index
+ * among equal ones, never a NaN); the first child of the node that carries it is accepted, and where there is none, it is the new
+ * token. A row of NaN alone sets MLA_QCACHE_DEV_NONFINITE (its token is -1).
+ * Other arguments, results and errors as for mla_qcache_verify_sampled; bad dtype -> MLA_QCACHE_ERR_CONFIG.
+ */
+int mla_qcache_verify_greedy(int32_t B, int32_t n_rows, int32_t vocab, int32_t dtype, const void* logits, int64_t logits_stride,
+                             const int32_t* tokens, const int32_t* cu_rows, int32_t max_rows, const uint64_t* tree_mask,
+                             int32_t mask_words, int32_t* kept, int32_t* new_tokens, int32_t* n_kept, int32_t* err_word,
+                             void* stream);
+
+/*
+ * Keeps the accepted nodes of trees in the 4-bit cache: for i < n_kept[b], token tree_base[b] + kept[b][i] moves to tree_base[b] + i,
+ * and seq_lens[b] becomes tree_base[b] + n_kept[b] (n_kept 0: the tree goes as a whole). kept [B][max_kept] int32, as
+ * mla_qcache_verify_sampled gives it: the first n_kept[b] ascend, from 0 at the least; max_kept 1..256. The order within a sequence
+ * does not matter to the caller: a token is read before its place is taken.
+ * A list that does not ascend or n_kept outside [0, max_kept] sets MLA_QCACHE_DEV_ROWS, a negative base or a token beyond the page
+ * table MLA_QCACHE_DEV_SEQ_OVERFLOW: the sequence and its length stay as they are. A bad page id sets MLA_QCACHE_DEV_BAD_PAGE (tokens from
+ * or to that page are not moved). Sequences may share pages, but not those in which tokens move.
+ * Errors: bad config -> MLA_QCACHE_ERR_CONFIG; B < 1 or > 2^20, max_kept not 1..256, max_pages < 1, n_pages < 1, max_pages * P >
+ * 2^31 - 4096, seq_lens or pool overlapping other arguments -> MLA_QCACHE_ERR_SHAPE; NULL -> MLA_QCACHE_ERR_NULL; misaligned ->
+ * MLA_QCACHE_ERR_ALIGN.
+ */
+int mla_qcache_kv4_keep(const mla_qcache_kv4_config* cfg, int32_t B, const int32_t* kept, int32_t max_kept,
+                        const int32_t* n_kept, const int32_t* tree_base, const int32_t* page_table, int32_t max_pages,
+                        uint8_t* pool, int64_t n_pages, int32_t* seq_lens, int32_t* err_word, void* stream);
 
 /*
  * Append to the paged BF16 latent cache that mla_qcache_decode_attn_bf16 reads, from the raw output
