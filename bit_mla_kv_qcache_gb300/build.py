@@ -29,6 +29,7 @@ SOURCES = {  # file -> extra flags
     "kv4_attn_tree.cu": [],
     "kv4_prompt.cu": [],
     "kv4_prompt_tree.cu": [],
+    "kv4_prompt_tree_f16.cu": [],
     "kv4_keep.cu": [],
     "verify.cu": [],
     "abi_tree.cu": [],

@@ -223,6 +223,7 @@ int kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t
   p.arrive = static_cast<uint32_t*>(workspace);
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + mlaq::kKv4CounterBytes);
   p.part_ml = p.part_o + 2 * ctas * rows * D;
+  p.joined = reinterpret_cast<mlaq::Kv4Joined*>(p.part_ml + 2 * ctas * rows * 2);
   p.n_pages = n_pages;
   p.page_bytes = kv4_page_bytes(cfg);
   p.scale_log2 = scale_log2;

@@ -59,6 +59,11 @@ struct LatentAppendParams {
 };
 cudaError_t launch_latent_append(const LatentAppendParams& p, cudaStream_t stream);
 
+// An item that several CTAs took: what the kernel that joins its parts has to know. One place for each CTA, that of the item which
+// it begins; parts 0: none.
+struct Kv4Joined {
+  int h, rb, parts, r0, rows;  // kv head, row block, its parts, the sequence's first row, rows (of all heads of the group)
+};
 struct Kv4AttnParams {
   HeadView q;
   const int32_t* cu_q;  // [B+1], or nullptr: one row per sequence
@@ -70,6 +75,7 @@ struct Kv4AttnParams {
   uint32_t* arrive;  // one counter per CTA, zero between calls
   float* part_o;     // [2 * CTAs][rows of a block][D] unnormalized partial outputs
   float* part_ml;    // [2 * CTAs][rows of a block][2] partial (max in log2 units, sum)
+  Kv4Joined* joined;  // [CTAs], for many rows
   int64_t n_pages, page_bytes;
   float scale_log2;
   int B, n_rows, max_q, Hq, Hkv, G, max_pages, P, p_shift, window;
@@ -109,6 +115,8 @@ bool kv4_uses_prompt(int max_q, int G);
 Kv4PromptPlan kv4_prompt_plan(int B, int Hkv, int n_rows, int max_q, int64_t max_tokens, int G, int num_sms);
 size_t kv4_prompt_workspace_bytes(const Kv4PromptPlan& z, int D);
 cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, const Kv4PromptPlan& z, int D, int n_groups, cudaStream_t stream);
+cudaError_t launch_kv4_join(const Kv4AttnParams& p, const Kv4PromptPlan& z, int D, cudaStream_t stream);  // behind it, where items are cut
+cudaError_t launch_kv4_prompt_tree_f16(const Kv4AttnParams& p, const Kv4PromptPlan& z, int D, int n_groups, cudaStream_t stream);
 cudaError_t launch_kv4_prompt_tree(const Kv4AttnParams& p, const Kv4PromptPlan& z, int D, int n_groups, cudaStream_t stream);
 
 }  // namespace mlaq

@@ -46,6 +46,9 @@
 // token tile of ~3 k cycles the unpacking of two-part keys takes ~1.5 k and waits for the products of the half before.
 //
 // kTree: as in the kernel for few rows; a row's bits of 32 tokens are read at the tiles of the tree alone.
+// kSplit, for trees with FP16 outputs: weights enter in two FP16 parts, the second in the columns of S that the first leaves free: what is
+// rounded off them counts as much as the output's own rounding (error of the output 3.4e-4 -> 2.8e-4 of it, of which that is
+// 2.1e-4; 16 nodes of 64 sequences up to 8K 239 -> 254 us).
 #pragma once
 #include <algorithm>
 #include <type_traits>
@@ -243,7 +246,7 @@ __device__ __forceinline__ void next_item(const Kv4AttnParams& p, Seg& s, int li
   line_segment<kTree>(p, s, R);
 }
 
-template <int D, int NG, bool kExact, bool two, bool kTree>
+template <int D, int NG, bool kExact, bool two, bool kTree, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnParams p, const int rows, const int line) {
   using Ge = Geom<D, NG, kExact>;
   constexpr int KW = D / 32, VW = D / 64, CB = D / 8;
@@ -252,7 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   __shared__ uint32_t s_tmem;
   __shared__ Seg s_seg, s_next;  // here, and the one after it
   __shared__ long long s_part[kThreads / 32];
-  __shared__ int s_most[kThreads / 32], s_last;
+  __shared__ int s_most[kThreads / 32];
+  __shared__ Kv4Joined s_joined;  // the item that the CTA begins and others go on with
   __shared__ float2 s_side[kTok];  // max and sum of a row under half of the tokens
   constexpr int kTry = 9;
   __shared__ int s_count[kTry + 1];  // parts that a share would make; tiles in all
@@ -272,15 +276,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   const uint32_t k_tiles = base + Ge::k_at(two), v_tiles = base + Ge::v_at(two);
   int flags = 0;
 
+  if (warp == 12) tc5::alloc512(&s_tmem);
+  if (tid == 0) s_joined = Kv4Joined{0, 0, 0, 0, 0};
   // ---- which part of which item
   if (!line) {
+    const int per = p.B * p.Hkv, blocks = static_cast<int>(gridDim.x) / per;
+    if constexpr (kTree) {  // the longest sequences first: a node sees as much of its sequence as any other
+      const int bh = static_cast<int>(blockIdx.x) / p.Hkv;
+      if (tid == 0) {
+        s_seg.h = static_cast<int>(blockIdx.x) % p.Hkv;
+        s_seg.rb = bh % blocks;
+        s_seg.b = bh / blocks;
+      }
+      if (p.B > 1 && p.B <= kThreads) {
+        int* const lens = reinterpret_cast<int*>(smem);
+        const int mine = tid < p.B ? __ldg(p.seq_lens + tid) : 0;
+        lens[tid] = mine;
+        __syncthreads();
+        int before = 0;
+#pragma unroll 4
+        for (int b = 0; b < p.B; ++b) before += lens[b] > mine || (lens[b] == mine && b < tid);
+        if (tid < p.B && before == bh / blocks) s_seg.b = tid;
+        __syncthreads();
+      }
+    }
     if (tid == 0) {
       Seg& s = s_seg;
-      const int per = p.B * p.Hkv, blocks = static_cast<int>(gridDim.x) / per;
       const int bh = static_cast<int>(blockIdx.x) % per;
-      s.rb = blocks - 1 - static_cast<int>(blockIdx.x) / per;
-      s.b = bh / p.Hkv;
-      s.h = bh % p.Hkv;
+      if constexpr (!kTree) {
+        s.rb = blocks - 1 - static_cast<int>(blockIdx.x) / per;
+        s.b = bh / p.Hkv;
+        s.h = bh % p.Hkv;
+      }
       int f = 0;
       load_sequence<kTree>(p, s.b, s.T, s.n, s.r0, s.base, f);
       flags |= f;
@@ -294,115 +321,166 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       }
     }
   } else {
-    // the line: pairs (sequence, row block) in order, thread i counts the tiles of pair i; a pair's heads in a row
     const int blocks_most = line;  // row blocks of the longest sequence
-    const int pairs = p.B * blocks_most;
-    long long x = 0;
-    int t = 0;
-    if (tid < pairs) {
+    const int pairs = p.B * blocks_most;  // (sequence, row block), in order; a pair's heads in a row
+    // Thread or lane i looks at pair i: its tiles, and its places on the line.
+    auto look = [&](int i, int& t) -> long long {
+      t = 0;
+      if (i >= pairs) return 0;
       int T, n, r0, base_ = 0, f = 0;
-      const int b = tid / blocks_most, rb = tid - b * blocks_most;
+      const int b = i / blocks_most, rb = i - b * blocks_most;
       load_sequence<kTree>(p, b, T, n, r0, base_, f);
       if (blockIdx.x == 0) flags |= f;
       if (rb < row_blocks(p, n, R)) t = block_tiles<kTree>(p, T, n, base_, rb, R).y;
-      if (t > 0) x = static_cast<long long>(t + kStart) * p.Hkv;
-    }
-    const int warp_most = __reduce_max_sync(0xffffffffu, t);
-    auto scan = [&](long long v) {  // inclusive, over the block
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
-      }
-      if (lane == 31) s_part[warp] = v;
-      __syncthreads();
-#pragma unroll 1
-      for (int w = 0; w < warp; ++w) v += s_part[w];
-      return v;
+      return t > 0 ? static_cast<long long>(t + kStart) * p.Hkv : 0;
     };
-    if (lane == 0) s_most[warp] = warp_most;
-    if (tid <= kTry) s_count[tid] = 0;
-    x = scan(x);
-    s_sum[tid + 1] = x;
-    if (tid == 0) s_sum[0] = 0;
-    __syncthreads();
-    int most = 0;
-#pragma unroll 1
-    for (int w = 0; w < kThreads / 32; ++w) most = max(most, s_most[w]);
-    const long long total = s_sum[kThreads];
     // fewest tiles of a part; items of fewer than 2048 tokens stay whole
-    const int least = most < 2048 / kTok ? max(1, most) : max(4, (most + kMaxParts - 2) / (kMaxParts - 1));
-    const bool small = total < (1 << 24);
-    const int tiles_here = __reduce_add_sync(0xffffffffu, small ? p.Hkv * t : 0);
-    if (lane == 0) atomicAdd(&s_count[kTry], tiles_here);
-    __syncthreads();
+    auto least_of = [](int most) { return most < 2048 / kTok ? max(1, most) : max(4, (most + kMaxParts - 2) / (kMaxParts - 1)); };
     // shares for which every part could have a CTA of its own: the smallest of a few multiples of the mean, or
     // items uncut where the longest is little more than the line's stretch
-    const float mean = static_cast<float>(s_count[kTry]) / static_cast<float>(gridDim.x);
-    const float stretch = static_cast<float>(total) / static_cast<float>(gridDim.x);
-    const bool uncut = most + kStart <= 1.2f * (stretch + kStart);
-    auto share_of = [&](int k) {
+    auto share_of = [&](int k, int most, int least, int tiles, long long total) {
+      const float mean = static_cast<float>(tiles) / static_cast<float>(gridDim.x);
+      const float stretch = static_cast<float>(total) / static_cast<float>(gridDim.x);
+      const bool uncut = most + kStart <= 1.2f * (stretch + kStart);
       return k == kTry - 1 && uncut ? max(1, most) : max(least, static_cast<int>(mean * (1.f + 0.12f * k)) + 1);
     };
-#pragma unroll 1
-    for (int k = 0; k < kTry; ++k) {
-      const int sh = share_of(k), parts = __reduce_add_sync(0xffffffffu, small ? p.Hkv * ((t + sh - 1) / sh) : 1 << 20);
-      if (lane == 0) atomicAdd(&s_count[k], parts);
-    }
-    __syncthreads();
-    int share = 0;
-#pragma unroll 1
-    for (int k = 0; k < kTry && share == 0; ++k)
-      if (s_count[k] <= static_cast<int>(gridDim.x)) share = share_of(k);
-    if (share > 0) {  // the parts before each pair
-      x = scan(p.Hkv * ((t + share - 1) / share));
-      __syncthreads();
-      s_sum[tid + 1] = x;
-      __syncthreads();
-    }
-    if (tid == 0) {
-      Seg& s = s_seg;
-      s.share = share > 0 ? 1 : max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(least));
-      s.at = s.share * blockIdx.x;
-      s.end = min(s_sum[kThreads], s.at + s.share);
-      s.valid = 0;
-      if (s.at < s.end) {
-        int lo = 0, hi = kThreads - 1;  // s_sum[lo] <= at < s_sum[lo + 1]
-#pragma unroll 1
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (s_sum[mid + 1] > s.at) hi = mid;
-          else lo = mid + 1;
+    // What lies at the CTA's place: pair `lo`, whose places begin at `before`. share > 0: parts of one CTA each; else stretches of the line.
+    auto locate = [&](Seg& s, int share, int lo, long long before) {
+      int f = 0;
+      s.pair = lo;
+      s.b = lo / blocks_most;
+      s.rb = lo - s.b * blocks_most;
+      load_sequence<kTree>(p, s.b, s.T, s.n, s.r0, s.base, f);
+      if (s.rb >= row_blocks(p, s.n, R)) return;  // the lengths changed under the call
+      const int2 tiles = block_tiles<kTree>(p, s.T, s.n, s.base, s.rb, R);
+      const int at = static_cast<int>(s.at - before);
+      if (share > 0) {
+        const int parts = (tiles.y + share - 1) / share, part = at % parts;
+        s.h = min(at / parts, p.Hkv - 1);
+        s.tile = tiles.x + tiles.y * part / parts;
+        s.tiles = tiles.x + tiles.y * (part + 1) / parts - s.tile;
+        s.parts = parts;
+        s.c0 = static_cast<int>(blockIdx.x) - part;
+        s.part = parts == 1 ? -1 : 2 * static_cast<int>(blockIdx.x) + (part == 0 ? 1 : 0);
+        s.valid = 1;
+        s.item0 = s.end = s.at;  // and nothing after it
+        s.item_tiles = tiles.y;
+      } else {
+        s.h = min(at / (tiles.y + kStart), p.Hkv - 1);
+        s.item0 = before + static_cast<long long>(s.h) * (tiles.y + kStart);
+        if (s.at < s.item0 + tiles.y) {
+          line_segment<kTree>(p, s, R);
+        } else {
+          s.at = s.item0 + tiles.y + kStart;
+          next_item<kTree>(p, s, line, R);
         }
-        int f = 0;
-        s.pair = lo;
-        s.b = lo / blocks_most;
-        s.rb = lo - s.b * blocks_most;
-        load_sequence<kTree>(p, s.b, s.T, s.n, s.r0, s.base, f);
-        if (s.rb < row_blocks(p, s.n, R)) {  // else the lengths changed under the call
-          const int2 tiles = block_tiles<kTree>(p, s.T, s.n, s.base, s.rb, R);
-          const int at = static_cast<int>(s.at - s_sum[lo]);
-          if (share > 0) {
-            const int parts = (tiles.y + share - 1) / share, part = at % parts;
-            s.h = min(at / parts, p.Hkv - 1);
-            s.tile = tiles.x + tiles.y * part / parts;
-            s.tiles = tiles.x + tiles.y * (part + 1) / parts - s.tile;
-            s.parts = parts;
-            s.c0 = static_cast<int>(blockIdx.x) - part;
-            s.part = parts == 1 ? -1 : 2 * static_cast<int>(blockIdx.x) + (part == 0 ? 1 : 0);
-            s.valid = 1;
-            s.item0 = s.end = s.at;  // and nothing after it
-            s.item_tiles = tiles.y;
-          } else {
-            s.h = min(at / (tiles.y + kStart), p.Hkv - 1);
-            s.item0 = s_sum[lo] + static_cast<long long>(s.h) * (tiles.y + kStart);
-            if (s.at < s.item0 + tiles.y) {
-              line_segment<kTree>(p, s, R);
-            } else {
-              s.at = s.item0 + tiles.y + kStart;
-              next_item<kTree>(p, s, line, R);
-            }
+      }
+    };
+    if (pairs <= 32) {  // one warp, without the block's barriers (2.5 us less)
+      if (warp == 0) {
+        int t;
+        const long long x = look(lane, t);
+        auto scan = [&](long long v) {
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
           }
+          return v;
+        };
+        const int most = __reduce_max_sync(0xffffffffu, t), least = least_of(most);
+        long long upto = scan(x);
+        const long long total = __shfl_sync(0xffffffffu, upto, 31);
+        const bool small = total < (1 << 24);
+        const int tiles = __reduce_add_sync(0xffffffffu, small ? p.Hkv * t : 0);
+        int share = 0;
+#pragma unroll 1
+        for (int k = 0; k < kTry && share == 0 && small; ++k) {
+          const int sh = share_of(k, most, least, tiles, total);
+          if (__reduce_add_sync(0xffffffffu, p.Hkv * ((t + sh - 1) / sh)) <= static_cast<int>(gridDim.x)) share = sh;
+        }
+        long long mine = x, places = total;
+        if (share > 0) {
+          mine = p.Hkv * ((t + share - 1) / share);
+          upto = scan(mine);
+          places = __shfl_sync(0xffffffffu, upto, 31);
+        }
+        Seg& s = s_seg;
+        if (lane == 0) {
+          s.share = share > 0 ? 1 : max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(least));
+          s.at = s.share * blockIdx.x;
+          s.end = min(places, s.at + s.share);
+          s.valid = 0;
+        }
+        __syncwarp();
+        const long long at = s.at;
+        if (at < s.end && at >= upto - mine && at < upto) locate(s, share, lane, upto - mine);  // one lane
+        __syncwarp();
+      }
+    } else {
+      int t;
+      long long x = look(tid, t);
+      const int warp_most = __reduce_max_sync(0xffffffffu, t);
+      auto scan = [&](long long v) {  // inclusive, over the block
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += y;
+        }
+        if (lane == 31) s_part[warp] = v;
+        __syncthreads();
+#pragma unroll 1
+        for (int w = 0; w < warp; ++w) v += s_part[w];
+        return v;
+      };
+      if (lane == 0) s_most[warp] = warp_most;
+      if (tid <= kTry) s_count[tid] = 0;
+      x = scan(x);
+      s_sum[tid + 1] = x;
+      if (tid == 0) s_sum[0] = 0;
+      __syncthreads();
+      int most = 0;
+#pragma unroll 1
+      for (int w = 0; w < kThreads / 32; ++w) most = max(most, s_most[w]);
+      const long long total = s_sum[kThreads];
+      const int least = least_of(most);
+      const bool small = total < (1 << 24);
+      const int tiles_here = __reduce_add_sync(0xffffffffu, small ? p.Hkv * t : 0);
+      if (lane == 0) atomicAdd(&s_count[kTry], tiles_here);
+      __syncthreads();
+      const int tiles = s_count[kTry];
+#pragma unroll 1
+      for (int k = 0; k < kTry; ++k) {
+        const int sh = share_of(k, most, least, tiles, total);
+        const int parts = __reduce_add_sync(0xffffffffu, small ? p.Hkv * ((t + sh - 1) / sh) : 1 << 20);
+        if (lane == 0) atomicAdd(&s_count[k], parts);
+      }
+      __syncthreads();
+      int share = 0;
+#pragma unroll 1
+      for (int k = 0; k < kTry && share == 0; ++k)
+        if (s_count[k] <= static_cast<int>(gridDim.x)) share = share_of(k, most, least, tiles, total);
+      if (share > 0) {  // the parts before each pair
+        x = scan(p.Hkv * ((t + share - 1) / share));
+        __syncthreads();
+        s_sum[tid + 1] = x;
+        __syncthreads();
+      }
+      if (tid == 0) {
+        Seg& s = s_seg;
+        s.share = share > 0 ? 1 : max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(least));
+        s.at = s.share * blockIdx.x;
+        s.end = min(s_sum[kThreads], s.at + s.share);
+        s.valid = 0;
+        if (s.at < s.end) {
+          int lo = 0, hi = kThreads - 1;  // s_sum[lo] <= at < s_sum[lo + 1]
+#pragma unroll 1
+          while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (s_sum[mid + 1] > s.at) hi = mid;
+            else lo = mid + 1;
+          }
+          locate(s, share, lo, s_sum[lo]);
         }
       }
     }
@@ -425,16 +503,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     mbar_init(o_done, 1);
     fence_mbar_init();
   }
-  __syncthreads();
-  if (!s_seg.valid) {
-    flags = __reduce_or_sync(0xffffffffu, flags);
-    if (lane == 0 && flags) atomicOr(p.err, flags);
-    return;
-  }
-  if (warp == 12) tc5::alloc512(&s_tmem);
   tc5::fence_before();
   __syncthreads();
   tc5::fence_after();
+  if (!s_seg.valid) {
+    if (line && tid == 0) p.joined[blockIdx.x] = Kv4Joined{0, 0, 0, 0, 0};
+    flags = __reduce_or_sync(0xffffffffu, flags);
+    if (lane == 0 && flags) atomicOr(p.err, flags);
+    tc5::fence_before();
+    __syncthreads();
+    if (warp == 12) tc5::dealloc512(s_tmem);
+    return;
+  }
   const uint32_t tmem = s_tmem;
 
   // A wait that runs out raises the abort flag, which ends every other wait too. Threads go on all the
@@ -794,6 +874,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             }
             tc5::mma_ts(tm + Ge::kColO + (two ? D * u : 0), tm + Ge::kColS + 128 * u + 8 * k, va + 16 * k, kDescO,
                         s >= (two ? 2 : 1) || k > 0, leader);
+            if (kSplit)
+              tc5::mma_ts(tm + Ge::kColO + (two ? D * u : 0), tm + Ge::kColS + 128 * u + 64 + 8 * k, va + 16 * k, kDescO, true, leader);
           }
           if (!two || u == 1) tc5::commit(v_free + st, leader);
           if (s + 2 < steps) ok = scores(s + 2);
@@ -990,24 +1072,49 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         }
         float l0 = 0.f, l1 = 0.f;
         const float neg = kRoom - m;
+        auto half_ready = [&]() {
+          tc5::wait_st();
+          tc5::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_half + u);
+        };
+        if constexpr (kSplit) {  // sixteen at a time: both parts of 32 would not fit the registers
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          uint32_t w[16];
+          for (int c = 0; c < NC; ++c) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float a = __uint_as_float(raw[c][i]), b = __uint_as_float(raw[c][i + 1]);
-            fma_pair(a, b, fr, neg);
-            a = ex2(a);
-            b = ex2(b);
-            add_pair(l0, l1, a, b);
-            w[i >> 1] = h2(a, b);
+            for (int i0 = 0; i0 < 32; i0 += 16) {
+              uint32_t w[8], rest[8];
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                float a = __uint_as_float(raw[c][i0 + i]), b = __uint_as_float(raw[c][i0 + i + 1]);
+                fma_pair(a, b, fr, neg);
+                a = ex2(a);
+                b = ex2(b);
+                add_pair(l0, l1, a, b);
+                w[i >> 1] = h2(a, b);
+                const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&w[i >> 1]));
+                rest[i >> 1] = h2(a - r.x, b - r.y);
+              }
+              tc5::st8(sc + 16 * (first + c) + i0 / 2, w);
+              tc5::st8(sc + 64 + 16 * (first + c) + i0 / 2, rest);
+            }
+            if (two && c == 1) half_ready();
           }
-          tc5::st16(sc + 16 * (first + c), w);
-          if (two && c == 1) {
-            tc5::wait_st();
-            tc5::fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_half + u);
+        } else {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float a = __uint_as_float(raw[c][i]), b = __uint_as_float(raw[c][i + 1]);
+              fma_pair(a, b, fr, neg);
+              a = ex2(a);
+              b = ex2(b);
+              add_pair(l0, l1, a, b);
+              w[i >> 1] = h2(a, b);
+            }
+            tc5::st16(sc + 16 * (first + c), w);
+            if (two && c == 1) half_ready();
           }
         }
         l += l0 + l1;
@@ -1017,6 +1124,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           for (int i = 0; i < 16; ++i) none[i] = 0;
           tc5::st16(sc + 16 * (2 - first), none);
           tc5::st16(sc + 16 * (3 - first), none);
+          if (kSplit) {
+            tc5::st16(sc + 64 + 16 * (2 - first), none);
+            tc5::st16(sc + 64 + 16 * (3 - first), none);
+          }
         }
         tc5::wait_st();
         tc5::fence_before();
@@ -1105,6 +1216,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             dst[e] = *reinterpret_cast<const float4*>(st + r2 * kRow + 16 * (ch ^ (r2 & 7)));
           }
           if (live) reinterpret_cast<float2*>(p.part_ml)[static_cast<size_t>(sg.part) * R + row] = make_float2(m, l);
+          if (tid == 0 && sg.c0 == static_cast<int>(blockIdx.x)) s_joined = Kv4Joined{sg.h, sg.rb, sg.parts, sg.r0, sg.n * p.G};
         } else {
           uint32_t res[D / 2];
 #pragma unroll
@@ -1139,74 +1251,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           if (live && p.lse) p.lse[out_row(row)] = l == 0.f ? -INFINITY : (m + (log2f(l) - kRoom)) * 0.69314718055994531f;
         }
       }
-      if (sg.part >= 0) {
-        __threadfence();
-        softmax_barrier(n_softmax);
-        if (tid == 0) {
-          const bool last = !s_abort && atomicAdd(p.arrive + sg.c0, 1u) == static_cast<uint32_t>(sg.parts - 1);
-          s_last = last;
-          if (last) {
-            p.arrive[sg.c0] = 0;
-            __threadfence();
-          }
-        }
-        softmax_barrier(n_softmax);
-        if (s_last) {
-          // this CTA came last: the item's parts in CTA order. First each row's weights of the parts (kept
-          // where the queries were), a thread per row; then a thread per row and eight channels.
-          const int rows = min(R, rows_left), parts = sg.parts;
-          auto slot_of = [&](int i) { return static_cast<size_t>(2 * (sg.c0 + i) + (i == 0 ? 1 : 0)); };
-          float* const wts = reinterpret_cast<float*>(smem);  // [parts][R], divided by the row's sum
-          for (int mr = tid; mr < rows; mr += n_softmax) {
-            const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + mr;
-            float M = kNoMax, L = 0.f;
-#pragma unroll 4
-            for (int i = 0; i < parts; ++i) {
-              const float2 x = __ldcg(ml + slot_of(i) * R);
-              const float mn = fmaxf(M, x.x);
-              L = L * ex2(M - mn) + x.y * ex2(x.x - mn);
-              M = mn;
-              wts[i * R + mr] = x.x;
-            }
-            const float y = L == 0.f ? 0.f : 1.f / L;
-            for (int i = 0; i < parts; ++i) wts[i * R + mr] = ex2(wts[i * R + mr] - M) * y;
-            if (p.lse) {
-              const int q2 = sg.rb * R + mr;
-              p.lse[static_cast<size_t>(sg.r0 + q2 / p.G) * p.Hq + sg.h * p.G + q2 % p.G] =
-                  L == 0.f ? -INFINITY : (M + (log2f(L) - kRoom)) * 0.69314718055994531f;
-            }
-          }
-          softmax_barrier(n_softmax);
-          // chunk i of a row, channels 8 i .. 8 i + 7, comes from columns i, i + 8 VW, ..: lanes read along i
-          constexpr int kChunks = D / 8;
-          for (int e = tid; e < rows * kChunks; e += n_softmax) {
-            const int r2 = e / kChunks, i2 = e % kChunks, q2 = sg.rb * R + r2;
-            float x[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = 0.f;
-#pragma unroll 4
-            for (int i = 0; i < parts; ++i) {
-              const float* src = p.part_o + (slot_of(i) * R + r2) * D + i2;
-              const float f = wts[i * R + r2];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) x[k] += f * __ldcg(src + 8 * VW * k);
-            }
-            reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(sg.r0 + q2 / p.G) * p.Hq + sg.h * p.G + q2 % p.G) * D)[i2] =
-                pack8(x, p.f16);
-          }
-        }
-      }
       tc5::fence_before();
     } while (leave_segment(n_tiles, steps));
   }
   tc5::fence_before();
   __syncthreads();
   if (warp == 12) tc5::dealloc512(tmem);
+  if (line && tid == 0) p.joined[blockIdx.x] = s_joined;
   flags = __reduce_or_sync(0xffffffffu, flags);
   if (lane == 0 && flags) atomicOr(p.err, flags);
 }
 
-template <int D, int NG, bool kExact, bool two, bool kTree>
+template <int D, int NG, bool kExact, bool two, bool kTree, bool kSplit>
 cudaError_t launch_as(const Kv4AttnParams& p, int rows, int line, int ctas, cudaStream_t stream) {
   static bool attr_done[64] = {};
   int dev = 0;
@@ -1214,34 +1270,40 @@ cudaError_t launch_as(const Kv4AttnParams& p, int rows, int line, int ctas, cuda
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_done[dev]) {
-    e = cudaFuncSetAttribute(kv4_prompt_kernel<D, NG, kExact, two, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(kv4_prompt_kernel<D, NG, kExact, two, kTree, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Geom<D, NG, kExact>::smem(two));
     if (e != cudaSuccess) return e;
     attr_done[dev] = true;
   }
-  kv4_prompt_kernel<D, NG, kExact, two, kTree><<<ctas, kThreads, Geom<D, NG, kExact>::smem(two), stream>>>(p, rows, line);
+  kv4_prompt_kernel<D, NG, kExact, two, kTree, kSplit><<<ctas, kThreads, Geom<D, NG, kExact>::smem(two), stream>>>(p, rows, line);
   return cudaGetLastError();
 }
 
-template <int D, int NG, bool kTree>
+template <int D, int NG, bool kTree, bool kSplit>
 cudaError_t launch_many(const Kv4AttnParams& p, int rows, int line, int ctas, cudaStream_t stream) {
   if (rows == 256)
-    return p.lse ? launch_as<D, NG, true, true, kTree>(p, rows, line, ctas, stream) : launch_as<D, NG, false, true, kTree>(p, rows, line, ctas, stream);
+    return p.lse ? launch_as<D, NG, true, true, kTree, kSplit>(p, rows, line, ctas, stream) : launch_as<D, NG, false, true, kTree, kSplit>(p, rows, line, ctas, stream);
   if constexpr (D == 64) {
-    if (!p.lse) return launch_as<D, NG, false, false, kTree>(p, rows, line, ctas, stream);
+    if (!p.lse) return launch_as<D, NG, false, false, kTree, kSplit>(p, rows, line, ctas, stream);
   }
-  return launch_as<D, NG, true, false, kTree>(p, rows, line, ctas, stream);
+  return launch_as<D, NG, true, false, kTree, kSplit>(p, rows, line, ctas, stream);
 }
 
-template <bool kTree>
-cudaError_t launch_prompt_kernel(const Kv4AttnParams& p, const Kv4PromptPlan& z, int D, int n_groups, cudaStream_t stream) {
+template <bool kTree, bool kSplit>
+cudaError_t launch_prompt_part(const Kv4AttnParams& p, const Kv4PromptPlan& z, int D, int n_groups, cudaStream_t stream) {
   const int ctas = static_cast<int>(z.ctas);
   if (D == 128) {
-    if (n_groups == 1) return launch_many<128, 1, kTree>(p, z.rows, z.line, ctas, stream);
-    if (n_groups == 2) return launch_many<128, 2, kTree>(p, z.rows, z.line, ctas, stream);
-    return launch_many<128, 4, kTree>(p, z.rows, z.line, ctas, stream);
+    if (n_groups == 1) return launch_many<128, 1, kTree, kSplit>(p, z.rows, z.line, ctas, stream);
+    if (n_groups == 2) return launch_many<128, 2, kTree, kSplit>(p, z.rows, z.line, ctas, stream);
+    return launch_many<128, 4, kTree, kSplit>(p, z.rows, z.line, ctas, stream);
   }
-  return n_groups == 1 ? launch_many<64, 1, kTree>(p, z.rows, z.line, ctas, stream) : launch_many<64, 2, kTree>(p, z.rows, z.line, ctas, stream);
+  return n_groups == 1 ? launch_many<64, 1, kTree, kSplit>(p, z.rows, z.line, ctas, stream) : launch_many<64, 2, kTree, kSplit>(p, z.rows, z.line, ctas, stream);
+}
+
+template <bool kTree, bool kSplit>
+cudaError_t launch_prompt_kernel(const Kv4AttnParams& p, const Kv4PromptPlan& z, int D, int n_groups, cudaStream_t stream) {
+  const cudaError_t e = launch_prompt_part<kTree, kSplit>(p, z, D, n_groups, stream);
+  return e != cudaSuccess || !z.line ? e : launch_kv4_join(p, z, D, stream);
 }
 
 }  // namespace

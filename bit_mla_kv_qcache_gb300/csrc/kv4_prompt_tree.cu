@@ -4,7 +4,7 @@
 namespace mlaq {
 
 cudaError_t launch_kv4_prompt_tree(const Kv4AttnParams& p, const Kv4PromptPlan& z, int D, int n_groups, cudaStream_t stream) {
-  return launch_prompt_kernel<true>(p, z, D, n_groups, stream);
+  return p.f16 ? launch_kv4_prompt_tree_f16(p, z, D, n_groups, stream) : launch_prompt_kernel<true, false>(p, z, D, n_groups, stream);
 }
 
 }  // namespace mlaq
