@@ -151,6 +151,20 @@ def test_long_sequences_in_parts():
         Tree(lens, sizes, Hkv=2, G=G, P=64, seed=len(lens)).check()
 
 
+@pytest.mark.parametrize("D,group,G,size,dtype", [(64, 32, 7, 9, "fp16"), (64, 64, 8, 16, "bf16"), (64, 64, 16, 20, "fp16"), (128, 64, 8, 14, "fp16")])
+@pytest.mark.parametrize("lse", [True, False])
+def test_parts_of_every_form_are_joined(D, group, G, size, dtype, lse):
+    """64, 128 and 256 rows to an item, cut over the CTAs."""
+    Tree([6000, 2500, size, 4001], [size, size, size, 3], Hkv=1, G=G, D=D, group=group, P=64, dtype=dtype, seed=size).check(lse=lse)
+
+
+def test_more_sequences_than_a_warp_or_a_block_looks_at():
+    """40 pairs on the line are shared out by the block; 600 sequences are not ordered by length; 70 are."""
+    Tree([2600] + [int(x) for x in np.random.default_rng(0).integers(12, 400, 39)], [12] * 40, Hkv=1, G=4, P=64, seed=1).check()
+    for B in (70, 600):
+        Tree([int(x) for x in np.random.default_rng(B).integers(9, 200, B)], [9] * B, Hkv=1, G=4, D=64, P=16, seed=B).check()
+
+
 def test_strided_queries_masks_of_one_dimension_and_other_streams():
     c = Tree([77, 150], [6, 7], Hkv=2, G=4, P=16)
     out, l = c.check()
