@@ -32,7 +32,7 @@ namespace cg = cooperative_groups;
 constexpr int kCtas = 8;  // of a cluster
 
 // A sequence's nodes. parent -2: never accepted.
-struct Node {
+struct __align__(8) Node {
   int parent, token;
   int first;  // whether it is accepted as the first child that is tried
   float u, p, q;  // its random number; p and q of its token at its parent
@@ -311,16 +311,19 @@ __device__ __forceinline__ Sum sum_of(const Rest& w, const int* gone, const Slic
 }
 
 // Of a list of sums, one to a lane, the part in which the running sum passes pos: the last with something in it whose predecessors
-// together do not; -1: nothing anywhere. start: what comes before the list; before it the part's predecessors' sum.
+// together do not; -1: nothing anywhere. start: what comes before the list, and what comes before the part.
+struct Found {
+  int part;
+  Sum start;
+};
 template <int kLanes>
-__device__ __forceinline__ int find_part(const Sum& x, const Sum& pos, Sum& start) {
+__device__ __forceinline__ Found find_part(Sum x, Sum pos, Sum start) {
   const Sum up = upto<kLanes>((threadIdx.x & 31) == 0 ? start + x : x);
   Sum prior = {__shfl_up_sync(0xffffffffu, up.s, 1), __shfl_up_sync(0xffffffffu, up.e, 1)};
   if ((threadIdx.x & 31) == 0) prior = start;
   const unsigned some = __ballot_sync(0xffffffffu, x.s > 0.f), open = __ballot_sync(0xffffffffu, x.s > 0.f && !above(prior, pos));
   const int part = open ? 31 - __clz(open) : some ? __ffs(some) - 1 : -1;
-  if (part >= 0) start = of_lane(prior, part);
-  return part;
+  return {part, of_lane(prior, max(part, 0))};
 }
 
 // The first entry in a warp's vectors at which the running sum, `run` before them, passes pos; the last entry with something in it,
@@ -370,6 +373,7 @@ struct __align__(16) Ask {
   int last, count;  // count: nodes kept
   float u;
 };
+constexpr int kAlone = 64;  // vectors in which one warp finds the new token by itself
 struct Find {  // a CTA's warp 0 to its others: the slice in which the new token is, the sum before it, the sum that it passes
   Rest rest;
   int here;
@@ -412,11 +416,17 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1024 /
   __shared__ int s_n, s_r0, s_at, s_after, s_count, s_n_gone, s_fresh;
   __shared__ Sum s_c, s_Z;
   if (rank == 0) {
-    int r0, flags = 0;
+    // Where every sequence has max_rows rows, what stands at b max_rows is this one's: asked for while the offsets come.
+    const bool even = static_cast<int64_t>(p.B) * p.max_rows == p.n_rows && tid < p.max_rows;
+    const int guess = b * p.max_rows;
+    int token = 0, r0, flags = 0;
+    float u = 0.f;
+    if (even) token = __ldg(p.tokens + guess + tid), u = __ldg(p.u_accept + guess + tid);
     const int n = rows_of(p, b, r0, flags), i = tid;
     if (i < n) {
       const int r = r0 + i;
-      Node x = {-2, __ldg(p.tokens + r), 0, __ldg(p.u_accept + r), 0.f, 0.f};
+      if (!even || r0 != guess) token = __ldg(p.tokens + r), u = __ldg(p.u_accept + r);
+      Node x = {-2, token, 0, u, 0.f, 0.f};
       const int parent = i == 0 ? -1 : parent_of(p, r, i);
       if (x.token >= 0 && x.token < p.vocab && parent >= 0) {
         x.parent = parent;
@@ -441,18 +451,31 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1024 /
     int at = s_at, after = s_after, count = s_count, n_gone = s_n_gone;
     bool fresh = s_fresh, last = false;  // fresh: no child of the node refused yet
     Sum c = s_c, Z = s_Z;
-    if (n <= 32) {  // while every node is accepted as its parent's first child
+    bool done = false;
+    if (n <= 32 && fresh) {  // while every node is accepted as its parent's first child
       const int parent = lane < n ? nodes[lane].parent : -2;
       const unsigned ok = __ballot_sync(0xffffffffu, lane < n && nodes[lane].first);
-      while (fresh) {
-        const unsigned m = __ballot_sync(0xffffffffu, parent == at && lane > after);
-        if (!m || !(m & -m & ok)) break;
-        at = after = __ffs(m) - 1;
-        if (lane == 0) s_kept[count] = at;
-        ++count;
+      while (true) {
+        const unsigned m = __ballot_sync(0xffffffffu, parent == at && lane > after), first = m & -m;
+        if (first & ok) {
+          at = after = __ffs(first) - 1;
+          if (lane == 0) s_kept[count] = at;
+          ++count;
+          continue;
+        }
+        if (!m) {
+          last = done = true;
+        } else if (p.draft) {  // the first child is refused: the row has to be summed
+          after = __ffs(first) - 1;
+          fresh = false;
+          c = Sum{1.f, 0.f};
+          last = m == first;
+          done = true;
+        }
+        break;
       }
     }
-    while (true) {
+    while (!done) {
       const int x = next_child(nodes, n, at, after, false, 0);
       if (x >= n) {
         last = true;
@@ -535,28 +558,28 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1024 /
     }
     if (warp == 0) {
       const Sum pos = Sum{s_ask.u, 0.f} * total();
-      Sum start{0.f, 0.f};
-      const int cta = find_part<kCtas>(lane < kCtas ? s_cta[turn][lane] : Sum{0.f, 0.f}, pos, start);
-      if (cta == rank) {
-        const int part = find_part<kWarps>(lane < kWarps ? s_warp[lane] : Sum{0.f, 0.f}, pos, start);
-        if (lane == 0) s_find = Find{w, 1, slice_of<4>(w.p, p.vocab, rank * kWarps + part, kCtas * kWarps), start, pos};
-      } else {
-        if (lane == 0) s_find.here = 0;
-        if (cta < 0 && rank == 0) {
-          if (lane == 0) atomicOr(p.err, kErrRange);
-          store_new(count, -1);
-        }
+      const Found cta = find_part<kCtas>(lane < kCtas ? s_cta[turn][lane] : Sum{0.f, 0.f}, pos, Sum{0.f, 0.f});
+      int here = 0;
+      if (cta.part == rank) {
+        const Found at = find_part<kWarps>(lane < kWarps ? s_warp[lane] : Sum{0.f, 0.f}, pos, cta.start);
+        const Slice slice = slice_of<4>(w.p, p.vocab, rank * kWarps + at.part, kCtas * kWarps);
+        here = slice.last - slice.first > kAlone;
+        if (!here) store_new(count, find_entry(w, s_gone, slice, p.vocab, at.start, pos));
+        else if (lane == 0) s_find = Find{w, 1, slice, at.start, pos};
+      } else if (cta.part < 0 && rank == 0) {
+        if (lane == 0) atomicOr(p.err, kErrRange);
+        store_new(count, -1);
       }
+      if (lane == 0 && !here) s_find.here = 0;
     }
     __syncthreads();
-    if (s_find.here) {  // the warp's part in which it is, cut over the CTA's warps once more
+    if (s_find.here) {  // a long part of a warp is cut over the CTA's warps once more
       const Slice mine = part_of(s_find.at, warp, kWarps);
       const Sum x = sum_of(s_find.rest, s_gone, mine, p.vocab);
       if (lane == 0) s_warp[warp] = x;
       __syncthreads();
-      Sum start = s_find.start;
-      const int part = find_part<kWarps>(lane < kWarps ? s_warp[lane] : Sum{0.f, 0.f}, s_find.pos, start);
-      if (part == warp) store_new(count, find_entry(s_find.rest, s_gone, mine, p.vocab, start, s_find.pos));
+      const Found at = find_part<kWarps>(lane < kWarps ? s_warp[lane] : Sum{0.f, 0.f}, s_find.pos, s_find.start);
+      if (at.part == warp) store_new(count, find_entry(s_find.rest, s_gone, mine, p.vocab, at.start, s_find.pos));
     }
   }
   if (rank == 0) {
@@ -685,16 +708,27 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1024 /
   const int b = static_cast<int>(blockIdx.x) / kCtas;
   const T* const target = static_cast<const T*>(p.target);
   auto started = cl.barrier_arrive();
-  // The first CTA reads the nodes. What the CTAs do goes by what it tells them: they take the same way whatever happens to the inputs.
+  const bool all_walk = !whole;
+  // The first CTA reads the nodes and, where all walk, gives them to the others: the CTAs take the same way whatever happens to
+  // the inputs meanwhile.
   if (rank == 0) {
     int r0, flags = 0;
     const int n = rows_of(p, b, r0, flags);
+    Node x = {-2, 0, 0, 0.f, 0.f, 0.f};
     if (tid < n) {
-      nodes[tid].token = __ldg(p.tokens + r0 + tid);
-      nodes[tid].parent = tid == 0 ? -2 : parent_of(p, r0 + tid, tid);
+      x.token = __ldg(p.tokens + r0 + tid);
+      x.parent = tid == 0 ? -2 : parent_of(p, r0 + tid, tid);
+      nodes[tid] = x;
     }
     if (tid == 0 && flags) atomicOr(p.err, flags);
     cl.barrier_wait(std::move(started));
+    if (tid < n && all_walk) {
+#pragma unroll
+      for (int c = 1; c < kCtas; ++c) {
+        Node* const to = cl.map_shared_rank(nodes, c) + tid;
+        *reinterpret_cast<int2*>(&to->parent) = make_int2(x.parent, x.token);
+      }
+    }
     if (tid < kCtas) *cl.map_shared_rank(&s_n, tid) = n, *cl.map_shared_rank(&s_r0, tid) = r0;
   } else {
     cl.barrier_wait(std::move(started));
@@ -703,7 +737,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1024 /
   const int n = s_n, r0 = s_r0;
   constexpr int kPer = 16 / sizeof(T);
   int turn = 0;
-  // The CTA's part of row `row`, one of `parts`; its key to the first CTA.
+  // The CTA's part of row `row`, one of `parts`; its key to every CTA.
   auto meet = [&](int row, int part, int parts) {
     unsigned long long key = 0;
     if (part < parts) {
@@ -715,50 +749,41 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1024 /
     turn ^= 1;
     if (warp == 0) {
       key = warp_max(lane < kWarps ? s_warp[lane] : 0ull);
-      if (lane == 0) cl.map_shared_rank(&s_best[turn][0], 0)[rank] = key;
+      if (lane < kCtas) cl.map_shared_rank(&s_best[turn][0], lane)[rank] = key;
     }
     cl.sync();
   };
-  int count = 0, at = 0, last = -1;
-  __shared__ int s_next;
-  // One step of the walk (warp 0 of the first CTA): the token behind node `at`, and the child that carries it.
+  int count = 0, at = n > 0 ? 0 : -1, last = -1;
+  // One step of the walk, by any warp: the token behind node `at`, and the child that carries it.
   auto step = [&](unsigned long long key) {
-    if (lane == 0) s_kept[count] = at;
+    if (warp == 0 && lane == 0) s_kept[count] = at;
     ++count;
     last = key ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(key)) : -1;
-    if (!key && lane == 0) atomicOr(p.err, kErrNonFinite);
+    if (!key && rank == 0 && tid == 0) atomicOr(p.err, kErrNonFinite);
     const int x = last < 0 ? n : next_child(nodes, n, at, at, true, last);
     at = x < n ? x : -1;
   };
-  if (whole && n > 0 && n <= kCtas) {
-    const int parts = kCtas / n, row = rank % n;
-    meet(row, rank / n, parts);
-    if (rank == 0 && warp == 0) {
-      while (at >= 0) {
-        const bool mine = lane < kCtas && lane % n == at && lane / n < parts;
-        step(warp_max(mine ? s_best[turn][lane] : 0ull));
-      }
+  if (!all_walk) {  // at most eight rows
+    const int parts = n > 0 ? kCtas / n : 0, row = n > 0 ? rank % n : 0;
+    if (n > 0) meet(row, rank / n, parts);
+    if (rank > 0 || warp > 0) return;
+    while (at >= 0) {
+      const bool mine = lane < kCtas && lane % n == at && lane / n < parts;
+      step(warp_max(mine ? s_best[turn][lane] : 0ull));
     }
   } else {
-    while (n > 0) {
+    while (at >= 0) {
       meet(at, rank, kCtas);
-      if (rank == 0 && warp == 0) {
-        step(warp_max(lane < kCtas ? s_best[turn][lane] : 0ull));
-        if (lane < kCtas) *cl.map_shared_rank(&s_next, lane) = at;
-      }
-      cl.sync();
-      at = s_next;
-      if (at < 0) break;
+      step(warp_max(lane < kCtas ? s_best[turn][lane] : 0ull));
     }
+    if (rank > 0 || warp > 0) return;
   }
-  if (rank == 0 && warp == 0) {
-    __syncwarp();
-    for (int i = lane; i < p.max_rows; i += 32) {
-      p.kept[static_cast<size_t>(b) * p.max_rows + i] = i < count ? s_kept[i] : -1;
-      p.new_tokens[static_cast<size_t>(b) * p.max_rows + i] = i < count - 1 ? nodes[s_kept[i + 1]].token : i == count - 1 ? last : -1;
-    }
-    if (lane == 0) p.n_kept[b] = count;
+  __syncwarp();
+  for (int i = lane; i < p.max_rows; i += 32) {
+    p.kept[static_cast<size_t>(b) * p.max_rows + i] = i < count ? s_kept[i] : -1;
+    p.new_tokens[static_cast<size_t>(b) * p.max_rows + i] = i < count - 1 ? nodes[s_kept[i + 1]].token : i == count - 1 ? last : -1;
   }
+  if (lane == 0) p.n_kept[b] = count;
 }
 
 // ---------------------------------------------------------------- masks
