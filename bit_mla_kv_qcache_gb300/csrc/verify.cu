@@ -488,8 +488,13 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1024 /
         ok = y.first;
       } else {
         for (int i0 = 0; i0 < n_gone; i0 += 32) gone |= __any_sync(0xffffffffu, i0 + lane < n_gone && s_gone[i0 + lane] == y.token);
-        const Pair left = gone ? Pair{0.f, 0.f} : residual(y.p, p.draft ? y.q : 0.f, c.s, c.e);
-        ok = above(Sum{left.d, left.e}, Sum{y.u, 0.f} * Sum{y.q, 0.f} * Z);
+        if (p.draft) {
+          const Pair left = residual(y.p, y.q, c.s, c.e);
+          ok = above(Sum{left.d, left.e}, Sum{y.u, 0.f} * Sum{y.q, 0.f} * Z);
+        } else {  // u Z < p
+          const float h = __fmul_rn(y.u, Z.s), l = __fmaf_rn(y.u, Z.e, __fmaf_rn(y.u, Z.s, -h));
+          ok = __fsub_rn(__fsub_rn(gone ? 0.f : y.p, h), l) > 0.f;
+        }
       }
       if (ok) {
         at = x;
@@ -708,33 +713,35 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1024 /
   const int b = static_cast<int>(blockIdx.x) / kCtas;
   const T* const target = static_cast<const T*>(p.target);
   auto started = cl.barrier_arrive();
-  const bool all_walk = !whole;
-  // The first CTA reads the nodes and, where all walk, gives them to the others: the CTAs take the same way whatever happens to
-  // the inputs meanwhile.
-  if (rank == 0) {
-    int r0, flags = 0;
-    const int n = rows_of(p, b, r0, flags);
-    Node x = {-2, 0, 0, 0.f, 0.f, 0.f};
-    if (tid < n) {
-      x.token = __ldg(p.tokens + r0 + tid);
-      x.parent = tid == 0 ? -2 : parent_of(p, r0 + tid, tid);
-      nodes[tid] = x;
-    }
-    if (tid == 0 && flags) atomicOr(p.err, flags);
+  // At most eight rows, taken at once: every CTA meets the others once, whatever the offsets are by then. Else the first CTA reads the
+  // nodes and gives them to the others: the CTAs take the same way whatever happens to the inputs meanwhile.
+  int n, r0, token = 0, flags = 0;
+  if (whole) {
+    n = rows_of(p, b, r0, flags);
+    if (rank == 0 && tid < n) token = __ldg(p.tokens + r0 + tid);
+    if (rank == 0 && tid == 0 && flags) atomicOr(p.err, flags);
     cl.barrier_wait(std::move(started));
-    if (tid < n && all_walk) {
-#pragma unroll
-      for (int c = 1; c < kCtas; ++c) {
-        Node* const to = cl.map_shared_rank(nodes, c) + tid;
-        *reinterpret_cast<int2*>(&to->parent) = make_int2(x.parent, x.token);
-      }
-    }
-    if (tid < kCtas) *cl.map_shared_rank(&s_n, tid) = n, *cl.map_shared_rank(&s_r0, tid) = r0;
   } else {
-    cl.barrier_wait(std::move(started));
+    if (rank == 0) {
+      n = rows_of(p, b, r0, flags);
+      int parent = -2;
+      if (tid < n) {
+        token = __ldg(p.tokens + r0 + tid);
+        parent = tid == 0 ? -2 : parent_of(p, r0 + tid, tid);
+      }
+      if (tid == 0 && flags) atomicOr(p.err, flags);
+      cl.barrier_wait(std::move(started));
+      if (tid < n) {
+#pragma unroll
+        for (int c = 0; c < kCtas; ++c) *reinterpret_cast<int2*>(&(cl.map_shared_rank(nodes, c) + tid)->parent) = make_int2(parent, token);
+      }
+      if (tid < kCtas) *cl.map_shared_rank(&s_n, tid) = n, *cl.map_shared_rank(&s_r0, tid) = r0;
+    } else {
+      cl.barrier_wait(std::move(started));
+    }
+    cl.sync();
+    n = s_n, r0 = s_r0;
   }
-  cl.sync();
-  const int n = s_n, r0 = s_r0;
   constexpr int kPer = 16 / sizeof(T);
   int turn = 0;
   // The CTA's part of row `row`, one of `parts`; its key to every CTA.
@@ -763,10 +770,12 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1024 /
     const int x = last < 0 ? n : next_child(nodes, n, at, at, true, last);
     at = x < n ? x : -1;
   };
-  if (!all_walk) {  // at most eight rows
+  if (whole) {
     const int parts = n > 0 ? kCtas / n : 0, row = n > 0 ? rank % n : 0;
-    if (n > 0) meet(row, rank / n, parts);
+    meet(row, n > 0 ? rank / n : 0, parts);
     if (rank > 0 || warp > 0) return;
+    if (lane < n) nodes[lane].token = token, nodes[lane].parent = lane == 0 ? -2 : parent_of(p, r0 + lane, lane);
+    __syncwarp();
     while (at >= 0) {
       const bool mine = lane < kCtas && lane % n == at && lane / n < parts;
       step(warp_max(mine ? s_best[turn][lane] : 0ull));
