@@ -3,7 +3,8 @@
 The compute path is the CUDA library libmla_qcache.so (C ABI in include/mla_qcache.h);
 ``binding`` marshals torch tensors into it and ``cache.QuantizedMLACache`` owns the device
 buffers (pool, BF16 sink/recent buffers, workspace) of one layer, ``cache.KV4Cache`` those of a
-grouped-query layer in 4 bits.
+grouped-query layer in 4 bits, also for decoding with trees of drafted tokens (start_tree, append and
+attend with masks, mla_qcache_verify_sampled or _greedy, keep).
 """
 from .binding import (DEV_BAD_PAGE, mla_qcache_absorb_query, mla_qcache_decode_attn_pending, mla_qcache_decode_attn_multi, mla_qcache_up_project, DEV_NONFINITE, DEV_RANGE, DEV_ROWS, DEV_SEQ_OVERFLOW, DEV_TIMEOUT, EXPORTS,
                       Config, QCacheError, bf16_workspace_bytes, decode_plan, decode_launches, lib, selftest_wait_timeout, make_config, mla_qcache_advance,

@@ -670,7 +670,8 @@ int mla_qcache_kv4_append_tree(const mla_qcache_kv4_config* cfg, int32_t dtype, 
  * tree->base NULL: seq_lens[b] minus the sequence's rows. A base outside [0, seq_lens[b]] sets MLA_QCACHE_DEV_SEQ_OVERFLOW (the
  * sequence is read as empty). A mask need not name the row's own node, and a row that sees nothing gets out = 0, lse = -inf.
  * Pages without a token in [base - window, base + 64 * mask_words) are not read with a window: their ids may be anything.
- * Numerics, workspace (mla_qcache_kv4_workspace_bytes for the same sizes) and capture as for mla_qcache_kv4_attn.
+ * Numerics, workspace (mla_qcache_kv4_workspace_bytes for the same sizes) and capture as for mla_qcache_kv4_attn; above 32 rows the
+ * weights of FP16 outputs enter in two FP16 parts.
  * Errors: as mla_qcache_kv4_attn; max_q > 64 * mask_words, mask_words not 1..4 -> MLA_QCACHE_ERR_SHAPE; tree or its mask NULL ->
  * MLA_QCACHE_ERR_NULL.
  */
@@ -702,7 +703,8 @@ int mla_qcache_kv4_attn_tree(const mla_qcache_kv4_config* cfg, int32_t dtype, in
  *   new_tokens [B][max_rows] int32: the accepted tokens, then the new one, n_kept in all; then -1.
  *   n_kept     [B] int32: nodes kept (accepted ones + 1). 0 for a sequence without rows.
  * Sums and comparisons carry 45 bits or more. A sequence with more than max_rows rows sets MLA_QCACHE_DEV_ROWS (n_kept = 0); a
- * node without any probability to draw from sets MLA_QCACHE_DEV_RANGE (its token is -1).
+ * node without any probability to draw from, or whose probabilities' sum overflows, sets MLA_QCACHE_DEV_RANGE (its token is -1). Inputs
+ * must not change while a call runs (its results are then not defined).
  * Errors: B < 1 or > 2^20, n_rows < 0, vocab < 1, max_rows or mask_words out of range, negative strides, outputs that overlap
  * inputs or one another -> MLA_QCACHE_ERR_SHAPE; missing pointers -> MLA_QCACHE_ERR_NULL; misaligned -> MLA_QCACHE_ERR_ALIGN.
  */
