@@ -562,8 +562,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1024 /
       round(w);
     }
     if (warp == 0) {
-      const Sum pos = Sum{s_ask.u, 0.f} * total();
-      const Found cta = find_part<kCtas>(lane < kCtas ? s_cta[turn][lane] : Sum{0.f, 0.f}, pos, Sum{0.f, 0.f});
+      const Sum all = total(), pos = Sum{s_ask.u, 0.f} * all;
+      Found cta = find_part<kCtas>(lane < kCtas ? s_cta[turn][lane] : Sum{0.f, 0.f}, pos, Sum{0.f, 0.f});
+      if (!(all.s <= FLT_MAX)) cta.part = -1;  // a part that overflowed: the others' sums are not the row's
       int here = 0;
       if (cta.part == rank) {
         const Found at = find_part<kWarps>(lane < kWarps ? s_warp[lane] : Sum{0.f, 0.f}, pos, cta.start);

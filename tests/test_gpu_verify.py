@@ -144,6 +144,19 @@ def test_numbers_that_do_not_count():
 
 
 @pytest.mark.parametrize("drawn", [True, False])
+@pytest.mark.parametrize("V,at", [(50, 0), (100000, 0), (100000, 60000), (100000, 99990)])
+def test_a_sum_that_overflows_gives_no_token(V, at, drawn):
+    """Wherever in the row it overflows, and whatever else the row holds; the sequences beside it are answered."""
+    big = float(np.finfo(np.float32).max)
+    p = torch.full((4, V), 1 / V, device="cuda")
+    p[1, at:at + 3] = big
+    d = torch.full((4, V), 1 / V, device="cuda") if drawn else None
+    got = call_sampled(p, d, [0, -1, -1, -1], [1, 2, 1], [0.5] * 4, [0.5] * 3)
+    assert got[3] == q.DEV_RANGE and got[2] == [1, 1, 1]
+    assert got[1][1, 0] == -1 and abs(got[1][0, 0] - V // 2) <= 1 and abs(got[1][2, 0] - V // 2) <= 1
+
+
+@pytest.mark.parametrize("drawn", [True, False])
 def test_equal_distributions_accept_and_leave_nothing(drawn):
     """p = q: a draft is accepted whatever the number; one with p(x) = q(x) = 0 is refused, nothing is left, and p is drawn from."""
     V = 50
