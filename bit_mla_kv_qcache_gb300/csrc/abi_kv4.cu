@@ -86,6 +86,11 @@ int check_tree(const mla_qcache_tree* t, const uint32_t** mask, const int32_t** 
   return MLA_QCACHE_OK;
 }
 
+// An output over the masks or the bases, which other CTAs still read.
+bool over_tree(const Span& x, const uint32_t* mask, const int32_t* base, int words32, int64_t rows, int64_t B) {
+  return overlap(x, span_of(mask, 4 * rows * words32)) || (base && overlap(x, span_of(base, 4 * B)));
+}
+
 // The arrays that both appends take; n_rows == 0 leaves only the lengths to copy (*done).
 int check_append(int32_t B, int32_t n_rows, const int32_t* cu_new, const int32_t* seq_lens, int32_t* seq_next,
                  int32_t max_new, const int32_t* page_table, int32_t max_pages, bool paged, const int32_t* err_word,
@@ -148,7 +153,10 @@ int kv4_append(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32
       if (overlap(out[i], in[j])) return MLA_QCACHE_ERR_SHAPE;
     for (int j = 0; j < i; ++j)
       if (overlap(out[i], out[j])) return MLA_QCACHE_ERR_SHAPE;
+    if (of_tree && over_tree(out[i], p.tree_mask, p.tree_base, p.mask_words, n_rows, B)) return MLA_QCACHE_ERR_SHAPE;
   }
+  if (of_tree && seq_lens_next && over_tree(span_of(seq_lens_next, 4 * static_cast<int64_t>(B)), p.tree_mask, p.tree_base, p.mask_words, n_rows, B))
+    return MLA_QCACHE_ERR_SHAPE;
   p.q_out = static_cast<uint16_t*>(q_out);
   p.k_deq = static_cast<uint16_t*>(k_deq);
   p.v_deq = static_cast<uint16_t*>(v_deq);
@@ -201,6 +209,9 @@ int kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t
   const int64_t out_rows = static_cast<int64_t>(n_rows) * n_heads;
   const Span os = span_of(out, out_rows * D * 2);
   if (overlap(os, span_of(p.q, n_rows, n_heads, D)) || (lse && overlap(os, span_of(lse, out_rows * 4))))
+    return MLA_QCACHE_ERR_SHAPE;
+  if (of_tree && (over_tree(os, p.tree_mask, p.tree_base, p.mask_words, n_rows, B) ||
+                  (lse && over_tree(span_of(lse, out_rows * 4), p.tree_mask, p.tree_base, p.mask_words, n_rows, B))))
     return MLA_QCACHE_ERR_SHAPE;
   int sms = 0;
   if ((st = sm_count(&sms)) != MLA_QCACHE_OK) return st;

@@ -653,7 +653,8 @@ int mla_qcache_tree_mask(int32_t B, int32_t n_rows, const int32_t* parents, cons
  * mla_qcache_kv4_append of a tree's nodes: rows go behind the sequence's tokens as there, but are rotated to the positions that
  * they would have as text, base + (bits of the row's mask) - 1: siblings share a position. tree->base NULL: seq_lens (the whole tree
  * enters in this call). A position outside the rotation's table sets MLA_QCACHE_DEV_SEQ_OVERFLOW and the row is skipped.
- * Errors: as mla_qcache_kv4_append; tree or its mask NULL -> MLA_QCACHE_ERR_NULL; mask_words not 1..4 -> MLA_QCACHE_ERR_SHAPE.
+ * Errors: as mla_qcache_kv4_append; tree or its mask NULL -> MLA_QCACHE_ERR_NULL; mask_words not 1..4, outputs (seq_lens_next too) that
+ * overlap the masks or tree->base -> MLA_QCACHE_ERR_SHAPE.
  */
 int mla_qcache_kv4_append_tree(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t n_rows,
                                const mla_qcache_view* k_new, const mla_qcache_view* v_new, const int32_t* cu_new,
@@ -672,8 +673,8 @@ int mla_qcache_kv4_append_tree(const mla_qcache_kv4_config* cfg, int32_t dtype, 
  * Pages without a token in [base - window, base + 64 * mask_words) are not read with a window: their ids may be anything.
  * Numerics, workspace (mla_qcache_kv4_workspace_bytes for the same sizes) and capture as for mla_qcache_kv4_attn; above 32 rows the
  * weights of FP16 outputs enter in two FP16 parts.
- * Errors: as mla_qcache_kv4_attn; max_q > 64 * mask_words, mask_words not 1..4 -> MLA_QCACHE_ERR_SHAPE; tree or its mask NULL ->
- * MLA_QCACHE_ERR_NULL.
+ * Errors: as mla_qcache_kv4_attn; max_q > 64 * mask_words, mask_words not 1..4, outputs that overlap the masks or tree->base ->
+ * MLA_QCACHE_ERR_SHAPE; tree or its mask NULL -> MLA_QCACHE_ERR_NULL.
  */
 int mla_qcache_kv4_attn_tree(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t n_heads, int32_t n_rows,
                              const mla_qcache_view* q, const int32_t* cu_q, int32_t max_q, const mla_qcache_tree* tree,
@@ -702,7 +703,7 @@ int mla_qcache_kv4_attn_tree(const mla_qcache_kv4_config* cfg, int32_t dtype, in
  *   kept       [B][max_rows] int32: node 0 and the accepted nodes, in order; then -1.
  *   new_tokens [B][max_rows] int32: the accepted tokens, then the new one, n_kept in all; then -1.
  *   n_kept     [B] int32: nodes kept (accepted ones + 1). 0 for a sequence without rows.
- * Sums and comparisons carry 45 bits or more. A sequence with more than max_rows rows sets MLA_QCACHE_DEV_ROWS (n_kept = 0); a
+ * Sums and comparisons carry 42 bits or more. A sequence with more than max_rows rows sets MLA_QCACHE_DEV_ROWS (n_kept = 0); a
  * node without any probability to draw from, or whose probabilities' sum overflows, sets MLA_QCACHE_DEV_RANGE (its token is -1). Inputs
  * must not change while a call runs (its results are then not defined).
  * Errors: B < 1 or > 2^20, n_rows < 0, vocab < 1, max_rows or mask_words out of range, negative strides, outputs that overlap
@@ -729,7 +730,8 @@ int mla_qcache_verify_greedy(int32_t B, int32_t n_rows, int32_t vocab, int32_t d
  * Keeps the accepted nodes of trees in the 4-bit cache: for i < n_kept[b], token tree_base[b] + kept[b][i] moves to tree_base[b] + i,
  * and seq_lens[b] becomes tree_base[b] + n_kept[b] (n_kept 0: the tree goes as a whole). kept [B][max_kept] int32, as
  * mla_qcache_verify_sampled gives it: the first n_kept[b] ascend, from 0 at the least; max_kept 1..256. The order within a sequence
- * does not matter to the caller: a token is read before its place is taken.
+ * does not matter to the caller: a token is read before its place is taken. The lists are not compared with seq_lens: that the nodes
+ * are in the cache is the caller's to see to.
  * A list that does not ascend or n_kept outside [0, max_kept] sets MLA_QCACHE_DEV_ROWS, a negative base or a token beyond the page
  * table MLA_QCACHE_DEV_SEQ_OVERFLOW: the sequence and its length stay as they are. A bad page id sets MLA_QCACHE_DEV_BAD_PAGE (tokens from
  * or to that page are not moved). Sequences may share pages, but not those in which tokens move.

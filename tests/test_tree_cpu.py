@@ -87,9 +87,9 @@ def test_attention_refusals(lib):  # noqa: F811
         assert _attn_tree(lib, **kw) == -4, kw
 
 
-def _append_tree(lib, cfg=None, rows=2, tree=..., pool=PFAR, rot=None, kd=None):  # noqa: F811
+def _append_tree(lib, cfg=None, rows=2, tree=..., pool=PFAR, rot=None, kd=None, next=None):  # noqa: F811
     cfg = cfg or q.make_kv4_config(4)
-    return lib.mla_qcache_kv4_append_tree(ctypes.byref(cfg), 0, 2, rows, _view(), _view(), P16, P16, None, 1, rot, None, 0, None, kd, None,
+    return lib.mla_qcache_kv4_append_tree(ctypes.byref(cfg), 0, 2, rows, _view(), _view(), P16, P16, next, 1, rot, None, 0, None, kd, None,
                                           P16, 4, pool, 4, _tree() if tree is ... else tree, P16, None)
 
 
@@ -100,6 +100,16 @@ def test_append_refusals(lib):  # noqa: F811
         assert _append_tree(lib, tree=_tree(words=words)) == -3
     assert _append_tree(lib, tree=_tree(ODD)) == -4 and _append_tree(lib, tree=_tree(base=ODD)) == -4
     assert _append_tree(lib, rot=_rot(dim=24)) == -3 and _append_tree(lib, kd=P16) == -3  # as the plain append
+
+
+def test_outputs_over_masks_and_bases_are_refused(lib):  # noqa: F811
+    near = ctypes.c_void_p(PFAR.value + 16)  # the second row's mask; base of the later sequences
+    for tree in (_tree(PB, base=PFAR), _tree(PFAR, words=2), _tree(ctypes.c_void_p(PFAR.value - 24), words=2), _tree(PB, base=near)):
+        assert _attn_tree(lib, tree=tree) == -3 and _append_tree(lib, tree=tree) == -3
+    for tree in (_tree(PB), _tree(PC, base=PB)):
+        assert _attn_tree(lib, tree=tree, lse=PB) == -3
+        assert _append_tree(lib, tree=tree, next=PB) == -3
+        assert _append_tree(lib, tree=tree, kd=PB) == -3
 
 
 def _sampled(lib, B=2, rows=6, V=100, target=PFAR, ts=100, draft=PB, ds=100, tokens=P16, cu=P16, max_rows=3, mask=None, words=0,  # noqa: F811
