@@ -20,8 +20,12 @@
 //   one tile: warps 0-3 take the softmax of every token tile, 4-7 unpack values, 8-11 keys, from copies of the pages
 //     in shared memory, two tiles ahead (loaded into registers: 93 us for 40 rows of eight sequences up to 32K, copied
 //     82). With at most 64 rows the tile holds them twice: one twin takes the first 64 tokens of a token tile, the
-//     other the rest, and their sums join at the end (84 us without the twins, 80 with; 64 rows 86 and 83).
-// Tensor memory: S0, S1 (128 columns each), O0, O1 (D each). A step's S overwrites the P of two steps
+//     other the rest, and their sums join at the end (84 us without the twins, 80 with; 64 rows 86 and 83). Queries lie in
+//     tensor memory, so that a score product reads keys alone from shared memory, which is busy with the unpacked tiles, and the
+//     values' group unpacks the last quarter of the keys (16 nodes of 64 sequences of 8K, 32 heads on 8, D = 128: 399 us,
+//     with the first 360, the second 371, both 343; 16 sequences of 32K 355, 310, 321 and 289; 40 rows 80.5 and 78.5). The
+//     products then set the pace: 25 of ~70 cycles to a token tile.
+// Tensor memory: S0, S1 (128 columns each), O0, O1 (D each; one tile: the queries in place of O1). A step's S overwrites the P of two steps
 // before; products of one thread run in the order of their issue.
 //
 // Channels keep the order in which a code word unpacks: eight channels of a word in the order 0 4 1 5
@@ -43,8 +47,8 @@
 //
 // Bound: the chain of a group's tile: S, its way to the registers, exponentials, P V. Two chunks of 4K over 8K (824
 // GFLOP) take 648 us where the card's rate for large BF16 products gives 424: the tensor pipe is 47% busy, issue 45%; tensor memory
-// is full at D = 128, so a group's next S waits for its P V. 40 rows of eight sequences up to 32K: 81 us, 16 for their bytes: per
-// token tile of ~3 k cycles the unpacking of two-part keys takes ~1.5 k and waits for the products of the half before.
+// is full at D = 128, so a group's next S waits for its P V. 40 rows of eight sequences up to 32K: 78.5 us, 16 for their bytes: per
+// token tile of ~2.5 k cycles 25 products take 1.7 k.
 //
 // kTree: as in the kernel for few rows; a row's bits of 32 tokens are read at the tiles of the tree alone.
 // kSplit, for trees with FP16 outputs: weights enter in two FP16 parts, the second in the columns of S that the first leaves free: what is
@@ -90,7 +94,7 @@ template <int D, int NG, bool kExact>
 struct Geom {
   static constexpr int kTile = 128 * D * 2;
   static constexpr int kMore = kExact ? 128 * 16 * 2 : 0;
-  static constexpr uint32_t kColS = 0, kColO = 256;
+  static constexpr uint32_t kColS = 0, kColO = 256, kColQ = kColO + D;
   __host__ __device__ static constexpr int k_at(bool two) { return (two ? 2 : 1) * kTile; }
   __host__ __device__ static constexpr int v_at(bool two) { return k_at(two) + 2 * kTile; }
   __host__ __device__ static constexpr int more_q_at(bool two) { return v_at(two) + 2 * kTile; }
@@ -491,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     s_any_odd = 0;
     s_unpacked = 0;
     for (int i = 0; i < 2; ++i) {
-      mbar_init(k_full + i, 4);  // one arrival per warp
+      mbar_init(k_full + i, !two && kExact && D == 128 && i == 1 ? 8 : 4);  // one arrival per warp
       mbar_init(v_full + i, 4);
       mbar_init(p_ready + i, 4);
       mbar_init(p_half + i, 4);
@@ -556,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     return !s_abort && line && sg.valid;
   };
   constexpr bool one_k = kExact;  // one stage of keys
+  constexpr bool kTmemQ = !two && !kSplit;  // queries in tensor memory; with weights in two parts it is the busier side (229 us, so 241)
 
   if (group == 2 || (group == 1 && !two)) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<two>::unpack));
@@ -575,6 +580,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       auto min_of = [](uint32_t w) { return __ushort_as_half(static_cast<unsigned short>(w >> 16)); };
       constexpr int kHalves = one_k ? 2 : 1;  // one stage of keys: its halves (of the channels) fill and empty one by one
       auto key_chunk = [&](int i) { return i / (CH / kHalves) * (CH / kHalves) + ((i + rot) & (CH / kHalves - 1)); };
+      constexpr bool kShared = !two && kExact && CH == 4;  // the values' group takes the last chunk of the keys
+      auto takes = [&](int i) { return keys ? !kShared || i < CH - 1 : kShared && i == CH - 1; };
       auto value_chunk = [&](int i) { return (i + rot) & (CH - 1); };
       // Two tiles of queries leave no room for codes in shared memory: each thread loads its token's into registers, a
       // tile ahead. With one tile warp 13 copies them.
@@ -641,11 +648,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             ld_shared_v2(codes + 2 * Ge::kCodes + tok_row * 8 * NG + 8 * g, cur[g].x, cur[g].y);
             if (none) cur[g] = make_uint2(0, 0);
           }
-          if (keys) {
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
-              ld_shared_v4(codes + tok_row * (D / 2) + 16 * key_chunk(i), kw[4 * i], kw[4 * i + 1], kw[4 * i + 2], kw[4 * i + 3]);
-          } else {
+          for (int i = 0; i < CH; ++i)
+            if (takes(i)) ld_shared_v4(codes + tok_row * (D / 2) + 16 * key_chunk(i), kw[4 * i], kw[4 * i + 1], kw[4 * i + 2], kw[4 * i + 3]);
+          if (!keys) {
 #pragma unroll
             for (int i = 0; i < CH; ++i)
               ld_shared_v4(codes + Ge::kCodes + tok_row * (D / 2) + 16 * value_chunk(i), vw[4 * i], vw[4 * i + 1], vw[4 * i + 2],
@@ -654,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           __syncwarp();
           if (lane == 0) mbar_arrive(c_free + st);
         }
-        if (keys) {
+        if (keys || kShared) {
           __half2 s1[NG], s2[NG];
           uint32_t more[4] = {0, 0, 0, 0}, large = 0;
           if constexpr (kExact) {  // the scale in seven bits and the rest; the minimum
@@ -675,11 +681,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           }
 #pragma unroll
           for (int hf = 0; hf < kHalves; ++hf) {
+            if (!keys && hf < kHalves - 1) continue;
             const uint32_t ks = one_k ? hf : st;
             wait(k_free + ks, (one_k ? J & 1 : ph) ^ 1);
             if (kExact && hf == 0) st_shared_v4(base + Ge::more_k_at(two) + 16 * tok_row, more[0], more[1], more[2], more[3]);
 #pragma unroll
             for (int i = hf * (CH / kHalves); i < (hf + 1) * (CH / kHalves); ++i) {
+              if (!takes(i)) continue;
               const uint32_t kd = k_tiles + (one_k ? 0 : st * Ge::kTile) + 16 * tok_row + 8192 * key_chunk(i);
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -847,13 +855,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             tc5::fence_after();
 #pragma unroll
             for (int k = hf * (D / 32); k < (hf + 1) * (D / 16 / kHalves); ++k) {  // descriptor addresses count 16 bytes
-              tc5::mma_ss(tm + Ge::kColS + 128 * u, qa + 256 * k, ka + 256 * k, kDescS, k > 0, leader);
-              if constexpr (kExact)
+              if constexpr (!kTmemQ) tc5::mma_ss(tm + Ge::kColS + 128 * u, qa + 256 * k, ka + 256 * k, kDescS, k > 0, leader);
+              else tc5::mma_ts(tm + Ge::kColS + 128 * u, tm + Ge::kColQ + 8 * k, ka + 256 * k, kDescS, k > 0, leader);
+              if constexpr (kExact && !kTmemQ)
                 tc5::mma_ss(tm + Ge::kColS + 128 * u, qa + 256 * k, ka + Ge::kTile / 16 + 256 * k, kDescS, true, leader);
+              else if constexpr (kExact)
+                tc5::mma_ts(tm + Ge::kColS + 128 * u, tm + Ge::kColQ + 8 * k, ka + Ge::kTile / 16 + 256 * k, kDescS, true, leader);
             }
-            if (kExact && hf == 0)
-              tc5::mma_ss(tm + Ge::kColS + 128 * u, tc5::smem_desc(base + Ge::more_q_at(two) + (two ? u * Ge::kMore : 0), 2048, 128),
-                          tc5::smem_desc(base + Ge::more_k_at(two), 2048, 128), kDescS, true, leader);
+            if constexpr (kExact) {
+              const uint64_t more_k = tc5::smem_desc(base + Ge::more_k_at(two), 2048, 128);
+              if (hf > 0) {
+              } else if constexpr (!kTmemQ) {
+                tc5::mma_ss(tm + Ge::kColS + 128 * u, tc5::smem_desc(base + Ge::more_q_at(two) + (two ? u * Ge::kMore : 0), 2048, 128), more_k,
+                            kDescS, true, leader);
+              } else {
+                tc5::mma_ts(tm + Ge::kColS + 128 * u, tm + Ge::kColQ + D / 2, more_k, kDescS, true, leader);
+              }
+            }
             if (hf == kHalves - 1) tc5::commit(s_full + u, leader);
             if (!two || u == 1) tc5::commit(k_free + ks, leader);
           }
@@ -974,7 +992,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             }
           }
         }
-        fence_proxy_async_smem();
+        if constexpr (!kTmemQ) {
+          fence_proxy_async_smem();
+        } else {  // on to tensor memory, a thread its row
+          __syncwarp();
+          const uint32_t at = base + 16 * lane_row, to = tmem + lane_base + Ge::kColQ;
+#pragma unroll
+          for (int c = 0; c < CB; c += 4) {
+            uint32_t y[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ld_shared_v4(at + 2048 * (c + i), y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            tc5::st16(to + 4 * c, y);
+          }
+          if constexpr (kExact) {
+            uint32_t y[8];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              ld_shared_v4(at + Ge::more_q_at(two) + 2048 * i, y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            tc5::st8(to + D / 2, y);
+            fence_proxy_async_smem();  // the keys' last channels
+          }
+          tc5::wait_st();
+          tc5::fence_before();
+        }
       }
       int full_lo, full_hi;  // tiles that every live row of the block sees whole
       if constexpr (kTree) {
