@@ -218,7 +218,7 @@ int kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t
   const bool prompt = mlaq::kv4_uses_prompt(max_q, G);
   const mlaq::Kv4PromptPlan plan =
       mlaq::kv4_prompt_plan(B, cfg->n_kv_heads, n_rows, max_q, static_cast<int64_t>(max_pages) * cfg->page_size, G, sms);
-  const size_t rows = prompt ? plan.rows : mlaq::kv4_decode_rows(max_q, G);
+  const size_t rows = prompt ? plan.rows : mlaq::kv4_decode_rows(B, cfg->n_kv_heads, max_q, G, static_cast<int64_t>(max_pages) * cfg->page_size, sms);
   const size_t need = prompt ? mlaq::kv4_prompt_workspace_bytes(plan, D)
                              : mlaq::kv4_decode_workspace_bytes(static_cast<int>(rows), D, sms);
   if (workspace_bytes < need) return MLA_QCACHE_ERR_WORKSPACE;
@@ -297,7 +297,7 @@ size_t mla_qcache_kv4_workspace_bytes(const mla_qcache_kv4_config* cfg, int32_t 
   int sms = 0;
   if (sm_count(&sms) != MLA_QCACHE_OK) return 0;
   const int G = n_heads / cfg->n_kv_heads, D = cfg->head_dim;
-  const size_t few = mlaq::kv4_decode_workspace_bytes(mlaq::kv4_decode_rows(max_q, G), D, sms);
+  const size_t few = mlaq::kv4_decode_workspace_bytes(static_cast<int64_t>(max_q) * G <= 8 ? 8 : 16, D, sms);
   if (!mlaq::kv4_uses_prompt(max_q, G)) return few;
   // the rows of a call, up to max_q per sequence, decide how it is cut: the most that any needs. What a cut
   // takes goes by the rows of an item (64, 128 or 256) alone; whether it is cut, by the number of row blocks.

@@ -88,7 +88,7 @@ struct Kv4AttnParams {
 // workspace may serve calls of different sizes one after the other).
 constexpr size_t kKv4CounterBytes = 8192;
 // Rows of one work item of the decode kernel (8 or 16) and the CTAs that it launches.
-int kv4_decode_rows(int max_q, int G);
+int kv4_decode_rows(int B, int Hkv, int max_q, int G, int64_t max_tokens, int num_sms);  // of a block
 int kv4_decode_ctas(int num_sms);
 size_t kv4_decode_workspace_bytes(int rows, int D, int num_sms);
 cudaError_t launch_kv4_decode(const Kv4AttnParams& p, int D, int n_groups, int num_sms, cudaStream_t stream);

@@ -3,7 +3,15 @@
 
 namespace mlaq {
 
-int kv4_decode_rows(int max_q, int G) { return static_cast<int64_t>(max_q) * G <= 8 ? 8 : 16; }
+// 9 to 32 rows in blocks of eight, as long as these are few and short: the blocks of a head read its tokens each for itself, but
+// eight warps go through a block of eight at twice the pace, there are more parts to share out, and less to join. Blocks of eight and
+// of 16, 8 kv heads, D = 128: 32 rows of one sequence, 1K tokens 10.5 and 16.7 us, 4K 13.8 and 20.2, 16K 25.0 and 31.3; of four, 4K 26.2
+// and 28.6, 8K 42.4 and 42.3, 16K 73.6 and 67.9; of eight, 2K 24.0 and 28.4, 8K 71.5 and 68.0. 16 rows of eight, 2K 18.1 and 21.8, 16K
+// 73.3 and 68.2; of 32, 1K 36.2 and 25.7 (more blocks than CTAs). The lengths are on the device: the room of the page table stands for them.
+int kv4_decode_rows(int B, int Hkv, int max_q, int G, int64_t max_tokens, int num_sms) {
+  const int64_t rows = static_cast<int64_t>(max_q) * G, items = (rows + 7) / 8 * B * Hkv;
+  return rows <= 8 || (items <= kv4_decode_ctas(num_sms) && items * max_tokens <= (1 << 20)) ? 8 : 16;
+}
 int kv4_decode_ctas(int num_sms) { return std::min(2 * num_sms, static_cast<int>(kKv4CounterBytes / 4)); }
 size_t kv4_decode_workspace_bytes(int rows, int D, int num_sms) {
   const size_t ctas = kv4_decode_ctas(num_sms);

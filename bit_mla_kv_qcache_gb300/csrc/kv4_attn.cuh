@@ -27,7 +27,7 @@
 // stretches (one sequence of 128K, 64 heads on 8: 47.3 us on the line, 39.6 with one part each). An item in several
 // parts is joined by the CTA that arrives last (parts in CTA order, so the result does not depend on who that is).
 //
-// Rows: 8 or 16 to an item; two blocks of 16 up to 32 rows, above that the kernel for many rows. Measured on either
+// Rows: blocks of 8 or 16 to an item (kv4_decode_rows) up to 32 rows, above that the kernel for many rows. Measured on either
 // side (eight ragged sequences up to 32K, 8 heads on each of 4, D = 128): 24 rows 79 us here and 79 there, 40 rows 117 and 81;
 // one sequence of 4K: 24 rows 17 and 26 us, 40 rows 19 and 27; D = 64, 24 rows 49 and 52 us.
 //
@@ -901,7 +901,7 @@ cudaError_t launch_few(const Kv4AttnParams& p, int rows, int ctas, cudaStream_t 
 }
 template <bool kTree>
 cudaError_t launch_decode_kernel(const Kv4AttnParams& p, int D, int n_groups, int num_sms, cudaStream_t stream) {
-  const int rows = kv4_decode_rows(p.max_q, p.G), ctas = kv4_decode_ctas(num_sms);
+  const int rows = kv4_decode_rows(p.B, p.Hkv, p.max_q, p.G, static_cast<int64_t>(p.max_pages) * p.P, num_sms), ctas = kv4_decode_ctas(num_sms);
   if (D == 128) {
     if (n_groups == 1) return launch_few<128, 1, kTree>(p, rows, ctas, stream);
     if (n_groups == 2) return launch_few<128, 2, kTree>(p, rows, ctas, stream);

@@ -84,6 +84,20 @@ def test_layouts_and_kernels(D, group, P, Hkv, G, dtype, size, lse):
          seed=D + size, pad=2).check(lse=lse)
 
 
+@pytest.mark.parametrize("G,n", [(1, 9), (4, 3), (4, 4), (7, 2), (7, 3), (8, 3), (5, 5), (8, 4), (32, 1)])
+@pytest.mark.parametrize("D,group,P,dtype", [(128, 64, 64, "fp16"), (64, 64, 16, "bf16"), (128, 128, 128, "bf16"), (128, 32, 32, "bf16")])
+@pytest.mark.parametrize("wide", [False, True])
+def test_up_to_32_rows_under_short_and_wide_tables(G, n, D, group, P, dtype, wide):
+    """Blocks of 8 or 16 rows, by the table's room: both hold their bounds, for nodes and for last positions."""
+    args = dict(Hkv=2, G=G, D=D, group=group, P=P, dtype=dtype, seed=G + n)
+    for c in (Tree([700, 40 + n, n, 0], [n, n, n, 0], **args), Case([700, 40 + n, n, 0], [n, n, n, 0], **args)):
+        if wide:  # room for 2^20 tokens: of all row blocks together above the border
+            more = np.full((4, 2 ** 20 // P), 10 ** 6, np.int32)
+            c.table = np.ascontiguousarray(np.concatenate([c.table, more], 1))
+        c.check()
+        c.check(window=33)
+
+
 @pytest.mark.parametrize("size", [1, 2, 31, 32, 33, 63, 64, 65, 100, 127, 128, 129, 200, 256])
 def test_sizes_of_trees(size):
     Tree([size + 37, size], [size, size], Hkv=1, G=2, D=64, P=16, seed=size).check()
