@@ -215,10 +215,11 @@ int kv4_attn(const mla_qcache_kv4_config* cfg, int32_t dtype, int32_t B, int32_t
     return MLA_QCACHE_ERR_SHAPE;
   int sms = 0;
   if ((st = sm_count(&sms)) != MLA_QCACHE_OK) return st;
-  const bool prompt = mlaq::kv4_uses_prompt(max_q, G);
+  const int64_t room = static_cast<int64_t>(max_pages) * cfg->page_size;
+  const bool prompt = mlaq::kv4_uses_prompt(max_q, G) && !(of_tree && mlaq::kv4_tree_stays(B, cfg->n_kv_heads, max_q, G, room, D, sms));
   const mlaq::Kv4PromptPlan plan =
-      mlaq::kv4_prompt_plan(B, cfg->n_kv_heads, n_rows, max_q, static_cast<int64_t>(max_pages) * cfg->page_size, G, sms);
-  const size_t rows = prompt ? plan.rows : mlaq::kv4_decode_rows(B, cfg->n_kv_heads, max_q, G, static_cast<int64_t>(max_pages) * cfg->page_size, sms);
+      mlaq::kv4_prompt_plan(B, cfg->n_kv_heads, n_rows, max_q, room, G, sms);
+  const size_t rows = prompt ? plan.rows : mlaq::kv4_decode_rows(B, cfg->n_kv_heads, max_q, G, room, sms);
   const size_t need = prompt ? mlaq::kv4_prompt_workspace_bytes(plan, D)
                              : mlaq::kv4_decode_workspace_bytes(static_cast<int>(rows), D, sms);
   if (workspace_bytes < need) return MLA_QCACHE_ERR_WORKSPACE;

@@ -112,6 +112,7 @@ struct Kv4PromptPlan {
   int64_t ctas;
 };
 bool kv4_uses_prompt(int max_q, int G);
+bool kv4_tree_stays(int B, int Hkv, int max_q, int G, int64_t max_tokens, int D, int num_sms);  // a tree stays with the kernel for few rows
 Kv4PromptPlan kv4_prompt_plan(int B, int Hkv, int n_rows, int max_q, int64_t max_tokens, int G, int num_sms);
 size_t kv4_prompt_workspace_bytes(const Kv4PromptPlan& z, int D);
 cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, const Kv4PromptPlan& z, int D, int n_groups, cudaStream_t stream);

@@ -671,8 +671,9 @@ int mla_qcache_kv4_append_tree(const mla_qcache_kv4_config* cfg, int32_t dtype, 
  * tree->base NULL: seq_lens[b] minus the sequence's rows. A base outside [0, seq_lens[b]] sets MLA_QCACHE_DEV_SEQ_OVERFLOW (the
  * sequence is read as empty). A mask need not name the row's own node, and a row that sees nothing gets out = 0, lse = -inf.
  * Pages without a token in [base - window, base + 64 * mask_words) are not read with a window: their ids may be anything.
- * Numerics, workspace (mla_qcache_kv4_workspace_bytes for the same sizes) and capture as for mla_qcache_kv4_attn; above 32 rows the
- * weights of FP16 outputs enter in two FP16 parts.
+ * Numerics, workspace (mla_qcache_kv4_workspace_bytes for the same sizes) and capture as for mla_qcache_kv4_attn; its arithmetic of
+ * few rows holds up to 128 rows where sequences, kv heads and the table's room are few, and above that the weights of FP16 outputs
+ * enter in two FP16 parts.
  * Errors: as mla_qcache_kv4_attn; max_q > 64 * mask_words, mask_words not 1..4, outputs that overlap the masks or tree->base ->
  * MLA_QCACHE_ERR_SHAPE; tree or its mask NULL -> MLA_QCACHE_ERR_NULL.
  */

@@ -13,6 +13,23 @@ from tests.test_gpu_kv4 import Case, TYPES, error_word, ints, offsets, tables
 pytestmark = pytest.mark.gpu
 
 
+WIDE = False
+
+
+@pytest.fixture(params=["short", "wide"], autouse=True)
+def room(request):
+    """Tables as long as the sequences, or with room for 2^20 tokens: which kernel takes a call goes by it."""
+    global WIDE
+    WIDE = request.param == "wide"
+
+
+def stays_few(c, rows):
+    """33 to 128 rows whose blocks of eight are few and short stay with the kernel for few rows."""
+    items = -(-rows // 8) * len(c.lens) * c.Hkv
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    return rows <= 128 and items <= 2 * sms and items * c.table.shape[1] * c.P * c.D <= 9 << 22
+
+
 class Tree(Case):
     """lens: tokens with the tree, sizes: nodes of each tree, new: rows of queries, the tree's newest nodes."""
 
@@ -20,6 +37,8 @@ class Tree(Case):
         super().__init__(lens, sizes if new is None else new, **kw)
         rng = np.random.default_rng(kw.get("seed", 0) + 1000)
         self.base = [T - n for T, n in zip(lens, sizes)]
+        if WIDE:
+            self.table = np.ascontiguousarray(np.concatenate([self.table, np.full((len(lens), 2 ** 20 // self.P), 10 ** 6, np.int32)], 1))
         self.words = words or max(1, -(-max(sizes) // 64))
         self.masks = []
         for n, rows in zip(sizes, self.new):
@@ -42,7 +61,8 @@ class Tree(Case):
     def compare(self, out, l, scale=None, window=0, hide=None, masks=None, max_q=None):
         scale = 1 / math.sqrt(self.D) if scale is None else scale
         pool, r = self.pool.cpu().numpy(), 0
-        way = kv4_paths.path((max_q or max(1, max(self.new))) * (self.Hq // self.Hkv), self.D, l is not None)
+        rows = (max_q or max(1, max(self.new))) * (self.Hq // self.Hkv)
+        way = "few" if stays_few(self, rows) else kv4_paths.path(rows, self.D, l is not None)
         for b, (T, n, base) in enumerate(zip(self.lens, self.new, self.base)):
             k, v, vs, most = ref.read_sequence(pool, self.table[b], T, self.Hkv, self.D, self.group, self.P)
             ok = tr.seen(T, base, (masks or self.masks)[b], self.words, window)
@@ -86,16 +106,15 @@ def test_layouts_and_kernels(D, group, P, Hkv, G, dtype, size, lse):
 
 @pytest.mark.parametrize("G,n", [(1, 9), (4, 3), (4, 4), (7, 2), (7, 3), (8, 3), (5, 5), (8, 4), (32, 1)])
 @pytest.mark.parametrize("D,group,P,dtype", [(128, 64, 64, "fp16"), (64, 64, 16, "bf16"), (128, 128, 128, "bf16"), (128, 32, 32, "bf16")])
-@pytest.mark.parametrize("wide", [False, True])
-def test_up_to_32_rows_under_short_and_wide_tables(G, n, D, group, P, dtype, wide):
+def test_up_to_32_rows(G, n, D, group, P, dtype):
     """Blocks of 8 or 16 rows, by the table's room: both hold their bounds, for nodes and for last positions."""
     args = dict(Hkv=2, G=G, D=D, group=group, P=P, dtype=dtype, seed=G + n)
-    for c in (Tree([700, 40 + n, n, 0], [n, n, n, 0], **args), Case([700, 40 + n, n, 0], [n, n, n, 0], **args)):
-        if wide:  # room for 2^20 tokens: of all row blocks together above the border
-            more = np.full((4, 2 ** 20 // P), 10 ** 6, np.int32)
-            c.table = np.ascontiguousarray(np.concatenate([c.table, more], 1))
-        c.check()
-        c.check(window=33)
+    c = Tree([700, 40 + n, n, 0], [n, n, n, 0], **args)
+    plain = Case([700, 40 + n, n, 0], [n, n, n, 0], **args)
+    plain.table = np.ascontiguousarray(np.concatenate([plain.table, c.table[:, plain.table.shape[1]:]], 1))
+    for x in (c, plain):
+        x.check()
+        x.check(window=33)
 
 
 @pytest.mark.parametrize("size", [1, 2, 31, 32, 33, 63, 64, 65, 100, 127, 128, 129, 200, 256])
@@ -213,7 +232,7 @@ def test_what_is_reported(G, size):
         e, out, l = word(base=ints([base, c.base[1]]))
         assert e == q.DEV_SEQ_OVERFLOW and (out[:n] == 0).all() and torch.isneginf(l[:n]).all()
         assert torch.equal(out[n:], want[n:])
-    e, out, _ = word(lens=[10 ** 6, c.lens[1]])
+    e, out, _ = word(lens=[c.table.shape[1] * c.P + 1, c.lens[1]])
     assert e & q.DEV_SEQ_OVERFLOW and (out[:n] == 0).all() and torch.equal(out[n:], want[n:])
     e, out, l = word(max_q=size, base=None, lens=[size - 1, c.lens[1]])  # more rows than tokens
     assert e == q.DEV_SEQ_OVERFLOW and (out[:n] == 0).all()
