@@ -27,9 +27,9 @@
 // stretches (one sequence of 128K, 64 heads on 8: 47.3 us on the line, 39.6 with one part each). An item in several
 // parts is joined by the CTA that arrives last (parts in CTA order, so the result does not depend on who that is).
 //
-// Rows: blocks of 8 or 16 to an item (kv4_decode_rows) up to 32 rows, above that the kernel for many rows (not for short trees, kv4_tree_stays). Measured on either
-// side (eight ragged sequences up to 32K, 8 heads on each of 4, D = 128): 24 rows 79 us here and 79 there, 40 rows 117 and 81;
-// one sequence of 4K: 24 rows 17 and 26 us, 40 rows 19 and 27; D = 64, 24 rows 49 and 52 us.
+// Rows: blocks of 8 or 16 to an item (kv4_decode_rows) up to 32 rows, above that the kernel for many rows (not for short trees:
+// kv4_tree_stays). In blocks of 16 on either side (eight ragged sequences up to 32K, 8 heads on each of 4, D = 128): 24 rows 79 us here
+// and 79 there, 40 rows 117 and 81; one sequence of 4K: 24 rows 17 and 26 us, 40 rows 19 and 27; D = 64, 24 rows 49 and 52 us.
 //
 // Bound: the chain of a step within a warp. 32 sequences of 8K take 65 us where their bytes take 42 at the card's copy rate, and no
 // unit is full: issue 55%, the ALU pipe (masks, shifts and byte permutes of codes) 53%, DRAM 54%, the tensor pipe 25%. Four warps
