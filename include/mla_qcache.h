@@ -606,6 +606,7 @@ size_t mla_qcache_kv4_workspace_bytes(const mla_qcache_kv4_config* cfg, int32_t 
  * outside [0, max_pages * P] MLA_QCACHE_DEV_SEQ_OVERFLOW (read as 0), a page id outside [0, n_pages)
  * MLA_QCACHE_DEV_BAD_PAGE (its tokens are left out). Pages that no row of a sequence sees any token of (behind a
  * sliding window) are not read: their ids may be anything.
+ * MLA_QCACHE_DEV_TIMEOUT (a wait within a kernel ran out): rows whose work was not done to its end keep what out and lse held.
  * Errors: as for mla_qcache_kv4_append; n_heads no multiple of n_kv_heads, n_rows * n_heads > 2^31 - 1,
  * a window without causal, a scale that is not finite (nor 1.45 times it), max_pages * P > 2^31 - 4096 -> MLA_QCACHE_ERR_SHAPE; too small a workspace ->
  * MLA_QCACHE_ERR_WORKSPACE.
