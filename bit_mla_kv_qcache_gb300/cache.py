@@ -102,6 +102,7 @@ class KV4Cache:
         self.seq_lens = torch.zeros(batch, dtype=torch.int32, device=dev)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
         self.tree_base = torch.zeros(batch, dtype=torch.int32, device=dev)  # tokens before the tree of drafted ones
+        self._trees = False  # start_tree() has been called: tree_base says something
         self._ws = {}  # per stream
         self._ws_need = {}  # workspace bytes per head count and rows
 
@@ -109,9 +110,9 @@ class KV4Cache:
         """Appends rows cu_new[b]..cu_new[b+1]-1 of k, v [N,Hkv,D] to sequence b and advances ``self.seq_lens`` in place,
         by a launch behind it: a captured append goes on from there at every replay, among calls that are not captured
         too. Further arguments (cos, sin, interleaved, q, q_out, k_deq, v_deq) as for mla_qcache_kv4_append. With tree_mask the rows
-        are nodes of the trees that start_tree() began."""
-        if kw.get("tree_mask") is not None:
-            kw.setdefault("tree_base", self.tree_base)
+        are nodes of the trees that start_tree() began (or, where a tree_base is given, of trees that begin there)."""
+        if kw.get("tree_mask") is not None and "tree_base" not in kw:
+            kw["tree_base"] = self._base("append() of nodes")
         binding.mla_qcache_kv4_append(self.cfg, k, v, cu_new, self.seq_lens, max_new, self.page_table, self.pool, self.err,
                                       seq_lens_next=self.seq_lens, stream=stream, **kw)
 
@@ -144,6 +145,7 @@ class KV4Cache:
         tree and the nodes that its mask names."""
         if tree_mask is not None and not causal:
             raise ValueError("nodes of a tree see what their masks name: causal=False has no meaning for them")
+        base = None if tree_mask is None else self._base("attend() of nodes")
         if out is None:
             with torch.cuda.stream(stream):  # memory that this stream may write at once (None: the current one)
                 out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
@@ -151,7 +153,7 @@ class KV4Cache:
                 out.record_stream(torch.cuda.current_stream(q.device))
         if tree_mask is not None:
             binding.mla_qcache_kv4_attn_tree(self.cfg, q, tree_mask, cu_q, max_q, self.page_table, self.seq_lens, self.pool, softmax_scale,
-                                             out, self.workspace(q.shape[1], max_q, stream), self.err, tree_base=self.tree_base, lse=lse,
+                                             out, self.workspace(q.shape[1], max_q, stream), self.err, tree_base=base, lse=lse,
                                              window=window, stream=stream)
             return out
         binding.mla_qcache_kv4_attn(self.cfg, q, self.page_table, self.seq_lens, self.pool, softmax_scale, out,
@@ -164,11 +166,17 @@ class KV4Cache:
         attend(), are nodes of these trees until keep()."""
         with torch.cuda.stream(stream):
             self.tree_base.copy_(self.seq_lens)
+        self._trees = True
+
+    def _base(self, what: str) -> torch.Tensor:
+        if not self._trees:
+            raise binding.QCacheError(f"{what} needs start_tree() before it: nothing says where the trees begin")
+        return self.tree_base
 
     def keep(self, kept: torch.Tensor, n_kept: torch.Tensor, stream=None) -> None:
         """Of each tree the nodes kept [B, most] (n_kept [B] of them, as mla_qcache_verify_sampled and _greedy give them) stay, moved to the
         places behind the tokens before the tree; ``self.seq_lens`` becomes their end."""
-        binding.mla_qcache_kv4_keep(self.cfg, kept, n_kept, self.tree_base, self.page_table, self.pool, self.seq_lens, self.err, stream)
+        binding.mla_qcache_kv4_keep(self.cfg, kept, n_kept, self._base("keep()"), self.page_table, self.pool, self.seq_lens, self.err, stream)
 
     def error_bits(self) -> int:
         return int(self.err.item())
