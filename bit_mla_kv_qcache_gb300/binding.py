@@ -534,8 +534,9 @@ def mla_qcache_tree_mask(parents, cu_rows, max_rows: int, mask, err_word, stream
 def mla_qcache_kv4_attn_tree(cfg: KV4Config, q, tree_mask, cu_q, max_q: int, page_table, seq_lens, pool, softmax_scale: float, out,
                              workspace, err_word, tree_base=None, lse=None, window: int = 0, stream=None) -> None:
     """Attention of nodes q [rows, heads, D] of trees of drafted tokens over the cache in 4 bits: each sees the tokens before its
-    tree (tree_base [B]; by default all but the sequence's rows) and the nodes that its mask names (see include/mla_qcache.h).
-    Workspace of kv4_workspace_bytes. Without cu_q one row per sequence."""
+    tree (tree_base [B]; by default all but the sequence's rows) and the nodes that its mask names (see include/mla_qcache.h). A window
+    cuts the tokens before the tree, by the node's depth, not the nodes: a row deeper than the window sees what the causal call's window
+    would leave of its path where its mask names the last `window` nodes of that alone. Workspace of kv4_workspace_bytes. Without cu_q one row per sequence."""
     st = (_fast or _native()).kv4_attn_tree(cfg, q, page_table, seq_lens, pool, softmax_scale, out, workspace, err_word, cu_q, max_q,
                                             lse, tree_mask, tree_base, window, None if stream is None else stream.cuda_stream)
     if st:

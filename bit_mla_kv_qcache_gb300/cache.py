@@ -142,7 +142,8 @@ class KV4Cache:
                lse=None, causal: bool = True, window: int = 0, stream=None, tree_mask: torch.Tensor | None = None):
         """Attention of query rows q [N,Hq,D], the last positions of their sequences, over the cache: out in q's type. With
         tree_mask ([N] or [N, words] int64) the rows are nodes of the trees that start_tree() began: each sees the tokens before its
-        tree and the nodes that its mask names."""
+        tree and the nodes that its mask names. A window cuts the tokens before the tree alone, by the node's depth: for rows deeper
+        than the window, give masks of the last `window` nodes of their paths here (append() takes the whole paths)."""
         if tree_mask is not None and not causal:
             raise ValueError("nodes of a tree see what their masks name: causal=False has no meaning for them")
         base = None if tree_mask is None else self._base("attend() of nodes")

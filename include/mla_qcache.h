@@ -669,6 +669,9 @@ int mla_qcache_kv4_append_tree(const mla_qcache_kv4_config* cfg, int32_t dtype, 
  * mla_qcache_kv4_attn for rows that are nodes of trees. seq_lens[b] counts the tree's tokens in; a row sees
  *   the tokens t < base, with window > 0 only those with t > base + (bits of its mask) - 1 - window, and
  *   the tokens base + j < seq_lens[b] whose bit j its mask has (whatever the window).
+ * So a node with `window` ancestors or more sees ancestors that the windowed rows of mla_qcache_kv4_attn would not: where the model
+ * attends within its window in the tree too, such a row's mask here names the last `window` nodes of its path alone (it then sees no
+ * token before the tree); mla_qcache_kv4_append_tree takes the whole path, which its positions go by.
  * tree->base NULL: seq_lens[b] minus the sequence's rows. A base outside [0, seq_lens[b]] sets MLA_QCACHE_DEV_SEQ_OVERFLOW (the
  * sequence is read as empty). A mask need not name the row's own node, and a row that sees nothing gets out = 0, lse = -inf.
  * Pages without a token in [base - window, base + 64 * mask_words) are not read with a window: their ids may be anything.
