@@ -9,7 +9,8 @@
 // token is drawn from the last res by its running sum. Without q (drafts picked without chance) a child is accepted where
 // u Z < p(x), and a rejected child's probability goes from the row and from Z.
 //
-// Sums decide whole numbers here, so they are pairs of float32 (a sum and the exact error of its additions, ~2^-42 of it): in 64 bits,
+// Sums decide whole numbers here, so they are pairs of float32 (a sum and the exact error of its additions, after Knuth's and Dekker's
+// two-sums, products by a fused multiply-add; ~2^-42 of it): in 64 bits,
 // which a B300 adds at a sixty-fourth of the float32 rate, five drafts of 64 sequences took 102 us, with pairs 19.
 //
 // A cluster of eight CTAs takes a sequence: the row that is summed is cut over them, their sums meet in distributed shared memory. The first CTA
@@ -824,33 +825,56 @@ __global__ void __launch_bounds__(kMaxTreeRows) tree_mask_kernel(const TreeMaskP
     if (k < p.mask_words) p.mask[static_cast<size_t>(r0 + i) * p.mask_words + k] = w[k];
 }
 
-}  // namespace
+// Clusters of a kernel that the GPU holds at once: asked for once on each device.
+template <auto kKernel, int kThreads>
+cudaError_t clusters_held(int* out) {
+  static int known[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (known[dev] == 0) {
+    cudaLaunchConfig_t at{};
+    at.gridDim = dim3(kCtas);
+    at.blockDim = dim3(kThreads);
+    int n = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&n, kKernel, &at)) != cudaSuccess) return e;
+    known[dev] = n;
+  }
+  *out = known[dev];
+  return cudaSuccess;
+}
 
-// Few sequences: 512 threads to a CTA, for the latency of a row; many: 256, so that the clusters of more sequences are there at
-// once. 512 and 256: 16 trees of picked drafts 12.5 and 13.5 us, greedy chains of 32 16.9 and 20.2, drafts of 64 25.8 and 18.7.
-bool wide(int B) { return B <= 36; }
-
-cudaError_t launch_verify_sampled(const VerifyParams& p, cudaStream_t stream) {
+// 512 threads to a CTA, for the latency of a row, as long as the GPU holds every sequence's cluster at once (36 of them); with more, 256,
+// of which it holds twice as many. 512 and 256, sampled chains of five drafts, 102400 entries: 32 sequences 13.0 and 13.5 us, 36 13.1 and
+// 14.0, 37 19.1 and 14.3, 48 22.1 and 15.5; greedy in float32 32 20.8 and 30.6, 36 21.9 and 31.5, 37 36.3 and 31.5, 48 37.5 and 33.0.
+template <auto kWide, auto kNarrow, typename... Args>
+cudaError_t launch_clusters(const VerifyParams& p, cudaStream_t stream, Args... more) {
+  int held = 0;
+  const cudaError_t e = clusters_held<kWide, 512>(&held);
+  if (e != cudaSuccess) return e;
   const unsigned ctas = static_cast<unsigned>(p.B) * kCtas;
-  if (wide(p.B)) verify_sampled_kernel<512><<<ctas, 512, 0, stream>>>(p);
-  else verify_sampled_kernel<256><<<ctas, 256, 0, stream>>>(p);
+  if (p.B <= held) kWide<<<ctas, 512, 0, stream>>>(p, more...);
+  else kNarrow<<<ctas, 256, 0, stream>>>(p, more...);
   return cudaGetLastError();
 }
 
 template <typename T>
-static void greedy(const VerifyParams& p, cudaStream_t stream) {
-  const unsigned ctas = static_cast<unsigned>(p.B) * kCtas;
+cudaError_t launch_greedy(const VerifyParams& p, cudaStream_t stream) {
   // all rows at once, and one after the other (150001 BF16 logits, chains of five drafts): one sequence 7.8 and 10.3 us, 8 9.1 and
   // 18.9, 32 16.7 and 27.8; 64 with 102400 20.1 and 27.3; 230 MB of rows 43.0 and 43.6
   const bool whole = p.max_rows <= kCtas && static_cast<int64_t>(p.n_rows) * p.vocab * sizeof(T) <= (256 << 20);
-  if (wide(p.B)) verify_greedy_kernel<T, 512><<<ctas, 512, 0, stream>>>(p, whole);
-  else verify_greedy_kernel<T, 256><<<ctas, 256, 0, stream>>>(p, whole);
+  return launch_clusters<verify_greedy_kernel<T, 512>, verify_greedy_kernel<T, 256>>(p, stream, whole);
 }
+
+}  // namespace
+
+cudaError_t launch_verify_sampled(const VerifyParams& p, cudaStream_t stream) {
+  return launch_clusters<verify_sampled_kernel<512>, verify_sampled_kernel<256>>(p, stream);
+}
+
 cudaError_t launch_verify_greedy(const VerifyParams& p, cudaStream_t stream) {
-  if (p.type == 0) greedy<__nv_bfloat16>(p, stream);
-  else if (p.type == 1) greedy<__half>(p, stream);
-  else greedy<float>(p, stream);
-  return cudaGetLastError();
+  return p.type == 0 ? launch_greedy<__nv_bfloat16>(p, stream) : p.type == 1 ? launch_greedy<__half>(p, stream) : launch_greedy<float>(p, stream);
 }
 
 cudaError_t launch_tree_mask(const TreeMaskParams& p, cudaStream_t stream) {
