@@ -861,9 +861,12 @@ cudaError_t launch_clusters(const VerifyParams& p, cudaStream_t stream, Args... 
 
 template <typename T>
 cudaError_t launch_greedy(const VerifyParams& p, cudaStream_t stream) {
-  // all rows at once, and one after the other (150001 BF16 logits, chains of five drafts): one sequence 7.8 and 10.3 us, 8 9.1 and
-  // 18.9, 32 16.7 and 27.8; 64 with 102400 20.1 and 27.3; 230 MB of rows 43.0 and 43.6
-  const bool whole = p.max_rows <= kCtas && static_cast<int64_t>(p.n_rows) * p.vocab * sizeof(T) <= (256 << 20);
+  // All rows at once save a meeting of ~2 us for each row on the path, and read rows that the path never reaches: the more bytes these
+  // are, the dearer. At once and one after the other (geometric means over 30, 60 and 80% of the drafts accepted, all but the smallest from
+  // DRAM): six BF16 rows of 150001 of one sequence 9.0 and 12.3 us, of 8 12.7 and 19.2, 32 (55 MB) 16.6 and 21.7, 48 (82 MB) 24.1 and 24.4, 128
+  // (220 MB) 51.3 and 37.9; float32 rows of 102400, four of 32 (50 MB) 15.4 and 15.2, six (75 MB) 22.2 and 18.3, six of 64 (150 MB) 36.6 and 21.3.
+  // Over 330 sizes up to 256 MB the time is 0.742 of one after the other with this bound, 0.750 with half of it, 0.764 with three times as much.
+  const bool whole = p.max_rows <= kCtas && static_cast<int64_t>(p.n_rows) * p.vocab * sizeof(T) <= (80 << 20);
   return launch_clusters<verify_greedy_kernel<T, 512>, verify_greedy_kernel<T, 256>>(p, stream, whole);
 }
 
