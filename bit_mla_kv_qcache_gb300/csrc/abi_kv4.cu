@@ -347,7 +347,8 @@ int mla_qcache_kv4_keep(const mla_qcache_kv4_config* cfg, int32_t B, const int32
     return MLA_QCACHE_ERR_ALIGN;
   const int64_t bytes = 4 * static_cast<int64_t>(B);  // heads of a sequence read the lists while the first stores its length
   const Span lens = span_of(seq_lens, bytes), pages = span_of(pool, n_pages * kv4_page_bytes(cfg));
-  const Span in[4] = {span_of(kept, bytes * max_kept), span_of(n_kept, bytes), span_of(tree_base, bytes), span_of(page_table, bytes * max_pages)};
+  const Span in[5] = {span_of(kept, bytes * max_kept), span_of(n_kept, bytes), span_of(tree_base, bytes), span_of(page_table, bytes * max_pages),
+                      span_of(err_word, 4)};
   for (const Span& x : in)
     if (overlap(lens, x) || overlap(pages, x)) return MLA_QCACHE_ERR_SHAPE;
   if (overlap(lens, pages)) return MLA_QCACHE_ERR_SHAPE;

@@ -47,6 +47,7 @@ int check(mlaq::VerifyParams& p, const uint64_t* tree_mask, int32_t mask_words, 
                       span_of(p.u_accept, p.u_accept ? 4 * rows : 0),
                       span_of(p.u_sample, p.u_sample ? 4 * static_cast<int64_t>(p.B) : 0)};
   for (int i = 0; i < 3; ++i) {
+    if (overlap(out[i], span_of(p.err, 4))) return MLA_QCACHE_ERR_SHAPE;
     for (const Span& x : in)
       if (overlap(out[i], x)) return MLA_QCACHE_ERR_SHAPE;
     for (int j = 0; j < i; ++j)
@@ -125,7 +126,8 @@ int mla_qcache_tree_mask(int32_t B, int32_t n_rows, const int32_t* parents, cons
   if (!parents || !cu_rows || !mask || !err_word) return MLA_QCACHE_ERR_NULL;
   if (!aligned(parents, 4) || !aligned(cu_rows, 4) || !aligned(mask, 8) || !aligned(err_word, 4)) return MLA_QCACHE_ERR_ALIGN;
   const Span out = span_of(mask, 8 * static_cast<int64_t>(n_rows) * mask_words);
-  if (overlap(out, span_of(parents, 4 * static_cast<int64_t>(n_rows))) || overlap(out, span_of(cu_rows, 4 * (static_cast<int64_t>(B) + 1))))
+  if (overlap(out, span_of(parents, 4 * static_cast<int64_t>(n_rows))) || overlap(out, span_of(cu_rows, 4 * (static_cast<int64_t>(B) + 1))) ||
+      overlap(out, span_of(err_word, 4)))
     return MLA_QCACHE_ERR_SHAPE;
   mlaq::TreeMaskParams p{};
   p.parents = parents;
