@@ -59,11 +59,10 @@ struct LatentAppendParams {
 };
 cudaError_t launch_latent_append(const LatentAppendParams& p, cudaStream_t stream);
 
-// What the kernel that joins the parts of cut items has to know, one place for each CTA: the item which it begins (parts 0: none) and
-// which of its two parts it stored.
+// An item that several CTAs took: what the kernel that joins its parts has to know. One place for each CTA, that of the item which
+// it begins; parts 0: none. A part whose sum is negative is not there (its CTA's wait ran out).
 struct Kv4Joined {
   int h, rb, parts, r0, rows;  // kv head, row block, its parts, the sequence's first row, rows (of all heads of the group)
-  int stored;                  // bit 1: the part of the item that it begins, bit 0: the one of an earlier item
 };
 struct Kv4AttnParams {
   HeadView q;

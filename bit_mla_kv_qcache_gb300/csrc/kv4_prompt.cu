@@ -43,21 +43,19 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnPar
   auto slot_of = [&](int i) { return static_cast<size_t>(2 * (c0 + i) + (i == 0 ? 1 : 0)); };  // of the CTA's two: the item that it begins
   const Kv4Joined it = p.joined[c0];
   float2 ml[kPer];
-  bool held[kPer];  // the part was stored: a CTA whose wait ran out leaves its item as it is
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int i = lane + k * kLanes;
-    held[k] = c0 + i < static_cast<int>(gridDim.x) && (__ldcg(&p.joined[c0 + i].stored) >> (i == 0 ? 1 : 0) & 1);
     ml[k] = c0 + i < static_cast<int>(gridDim.x) ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(i) * R + row) : make_float2(kNoMax, 0.f);
   }
   if (it.parts < 2 || it.rb * R + row >= it.rows) return;  // (all lanes of the row)
   const int parts = min(min(it.parts, kMaxParts), static_cast<int>(gridDim.x) - c0);
   float M = kNoMax, L = 0.f;
-  bool whole = true;
+  bool whole = true;  // an item with a part that is not there stays as it is
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     if (lane + k * kLanes >= parts) ml[k] = make_float2(kNoMax, 0.f);
-    else whole &= held[k];
+    else whole &= !(ml[k].y < 0.f);
     M = fmaxf(M, ml[k].x);
   }
   if (!__all_sync(group, whole)) return;

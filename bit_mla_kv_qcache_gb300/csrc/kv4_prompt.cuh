@@ -1257,11 +1257,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             dst[e] = *reinterpret_cast<const float4*>(st + r2 * kRow + 16 * (ch ^ (r2 & 7)));
           }
           if (live) reinterpret_cast<float2*>(p.part_ml)[static_cast<size_t>(sg.part) * R + row] = make_float2(m, l);
-          if (tid == 0) {
-            const int stored = s_joined.stored | 1 << (sg.part & 1);
-            if (sg.c0 == static_cast<int>(blockIdx.x)) s_joined = Kv4Joined{sg.h, sg.rb, sg.parts, sg.r0, sg.n * p.G, stored};
-            else s_joined.stored = stored;
-          }
+          if (tid == 0 && sg.c0 == static_cast<int>(blockIdx.x)) s_joined = Kv4Joined{sg.h, sg.rb, sg.parts, sg.r0, sg.n * p.G};
         } else {
           uint32_t res[D / 2];
 #pragma unroll
@@ -1302,9 +1298,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   tc5::fence_before();
   __syncthreads();
   if (warp == 12) tc5::dealloc512(tmem);
-  if (line && tid == 0) {
-    if (s_abort) s_joined.stored = 0;  // some warp may have given up before it stored its rows
-    p.joined[blockIdx.x] = s_joined;
+  if (line && tid == 0) p.joined[blockIdx.x] = s_joined;
+  if (line && s_abort) {  // some warp may have given up before it stored its rows: neither part counts
+    float2* const ml = reinterpret_cast<float2*>(p.part_ml) + static_cast<size_t>(blockIdx.x) * 2 * R;
+    for (int i = tid; i < 2 * R; i += kThreads) ml[i] = make_float2(kNoMax, -1.f);
   }
   flags = __reduce_or_sync(0xffffffffu, flags);
   if (lane == 0 && flags) atomicOr(p.err, flags);

@@ -3,10 +3,10 @@
 
 #include "kv4.cuh"
 
-// joined [ctas][6]: kv head, row block, parts, first row, rows, parts stored (bits). Heads of D, one kv head, `G` query heads on it.
+// joined [ctas][5]: kv head, row block, parts, first row, rows. Heads of D, one kv head, `G` query heads on it.
 extern "C" int join_parts(int ctas, int rows, int D, int G, const float* part_o, const float* part_ml, const int32_t* joined, int f16,
                           void* out, float* lse, void* stream) {
-  static_assert(sizeof(mlaq::Kv4Joined) == 24, "as the test lays it out");
+  static_assert(sizeof(mlaq::Kv4Joined) == 20, "as the test lays it out");
   mlaq::Kv4AttnParams p{};
   p.part_o = const_cast<float*>(part_o);
   p.part_ml = const_cast<float*>(part_ml);

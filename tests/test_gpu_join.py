@@ -42,15 +42,16 @@ def test_items_with_a_part_that_is_missing_stay(join, D, rows, G, parts):
     slots = [2 * first + 1] + [2 * (first + i) for i in range(1, parts)]
 
     def run(missing):
-        joined = np.zeros((ctas, 6), np.int32)
-        joined[first, :5] = [0, 0, parts, 0, live]
-        joined[:, 5] = 3
-        for i in missing:  # the other bit stays: it is of another item
-            joined[first + i, 5] = 1 if i == 0 else 2
+        joined = np.zeros((ctas, 5), np.int32)
+        joined[first] = [0, 0, parts, 0, live]
+        marked = part_ml.clone()
+        marked[2 * first] = marked[slots[-1] + 1] = torch.tensor([-1e30, -1.0])  # of other items
+        for i in missing:
+            marked[slots[i]] = torch.tensor([-1e30, -1.0])
         out = torch.full((n, G, D), 7.0, dtype=torch.float16, device="cuda")
         lse = torch.full((n, G), 7.0, device="cuda")
         j = torch.tensor(joined, device="cuda")
-        assert join(ctas, rows, D, G, part_o.data_ptr(), part_ml.data_ptr(), j.data_ptr(), 1, out.data_ptr(), lse.data_ptr(),
+        assert join(ctas, rows, D, G, part_o.data_ptr(), marked.data_ptr(), j.data_ptr(), 1, out.data_ptr(), lse.data_ptr(),
                     torch.cuda.current_stream().cuda_stream) == 0
         torch.cuda.synchronize()
         return out.view(n * G, D), lse.view(n * G)
