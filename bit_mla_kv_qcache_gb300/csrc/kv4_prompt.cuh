@@ -38,7 +38,7 @@
 // bits.) The minimum enters as sixteen more channels: its value for each
 // group against the sum of the group's queries, in two FP16 parts. One stage of keys then has the room; its halves
 // (of the channels) fill and empty one by one. Taken when the log-sum-exp is asked for, and always with one tile of queries
-// of 128 channels, where it costs little (40 rows: 81 us, rounded keys 79).
+// of 128 channels, where it costs little (40 rows: 81 us, rounded keys 79), and beside weights in two parts (kSplit).
 //
 // Work: one CTA per item (sequence, kv head, row block), those that see the most tokens first (of trees the longest
 // sequences, up to 512 of them: 16 nodes of 64 sequences up to 8K 254 us in the order given, 231 by length); or items cut
@@ -1326,12 +1326,16 @@ cudaError_t launch_as(const Kv4AttnParams& p, int rows, int line, int ctas, cuda
 
 template <int D, int NG, bool kTree, bool kSplit>
 cudaError_t launch_many(const Kv4AttnParams& p, int rows, int line, int ctas, cudaStream_t stream) {
-  if (rows == 256)
-    return p.lse ? launch_as<D, NG, true, true, kTree, kSplit>(p, rows, line, ctas, stream) : launch_as<D, NG, false, true, kTree, kSplit>(p, rows, line, ctas, stream);
-  if constexpr (D == 64) {
-    if (!p.lse) return launch_as<D, NG, false, false, kTree, kSplit>(p, rows, line, ctas, stream);
+  // Keys rounded to FP16 where nothing asks for exact scores, but not beside weights in two parts: an FP16 output would be off by 4.6e-4
+  // in place of 2.8e-4 of it, and by more or less as a log-sum-exp is asked for.
+  if constexpr (!kSplit) {
+    if (rows == 256 && !p.lse) return launch_as<D, NG, false, true, kTree, false>(p, rows, line, ctas, stream);
+    if constexpr (D == 64) {
+      if (rows < 256 && !p.lse) return launch_as<D, NG, false, false, kTree, false>(p, rows, line, ctas, stream);
+    }
   }
-  return launch_as<D, NG, true, false, kTree, kSplit>(p, rows, line, ctas, stream);
+  return rows == 256 ? launch_as<D, NG, true, true, kTree, kSplit>(p, rows, line, ctas, stream)
+                     : launch_as<D, NG, true, false, kTree, kSplit>(p, rows, line, ctas, stream);
 }
 
 template <bool kTree, bool kSplit>

@@ -677,7 +677,7 @@ int mla_qcache_kv4_append_tree(const mla_qcache_kv4_config* cfg, int32_t dtype, 
  * Pages without a token in [base - window, base + 64 * mask_words) are not read with a window: their ids may be anything.
  * Numerics, workspace (mla_qcache_kv4_workspace_bytes for the same sizes) and capture as for mla_qcache_kv4_attn; its arithmetic of
  * few rows holds up to 128 rows where sequences, kv heads and the table's room are few, and above that the weights of FP16 outputs
- * enter in two FP16 parts.
+ * enter in two FP16 parts, beside keys that are exact with and without an lse.
  * Errors: as mla_qcache_kv4_attn; max_q > 64 * mask_words, mask_words not 1..4, outputs that overlap the masks or tree->base ->
  * MLA_QCACHE_ERR_SHAPE; tree or its mask NULL -> MLA_QCACHE_ERR_NULL.
  */

@@ -2,10 +2,10 @@
 weights' rounding and the output's own as the only ones that show, so that a second part that is missing, or beside the wrong
 token, lies outside the bound.
 
-Bound of an output, from the arithmetic: scores s off by 2 D 2^-24 |q|.|k| (float32 sums; also 2^-11 of it where keys are rounded to
-FP16), exponentials and their sums by 2^-20 and a 2^-24 for each token that counts, both in numerator and denominator; a
-weight's two parts leave 2^-22 of it, and 2^-32 of the largest; the products are summed in float32, a step of 2^-23 for each of the two
-parts of a token that counts; joining and rescaling 2^-20. Tokens of a weight below 2^-50 do not count. Rounded once to FP16."""
+Bound of an output, from the arithmetic: scores s off by 2 D 2^-24 |q|.|k| (float32 sums; keys are exact), exponentials and their sums by
+2^-20 and a 2^-24 for each token that counts, both in numerator and denominator; a weight's two parts leave 2^-22 of it, and 2^-32 of
+the largest; the products are summed in float32, a step of 2^-23 for each of the two parts of a token that counts; joining and rescaling
+2^-20. Tokens of a weight below 2^-50 do not count. Rounded once to FP16."""
 import math
 
 import numpy as np
@@ -48,7 +48,7 @@ def prepared(lens, sizes, near, wide, Hkv, G, D, group, P=16, seed=0):
     return c
 
 
-def statement(q, k, v, scale, ok, keys_rounded):
+def statement(q, k, v, scale, ok):
     """(output, its bound, the output with weights in one part, with the second parts one token off) of one sequence."""
     n, Hq, D = q.shape
     G, half = Hq // k.shape[0], 2.0 ** -11
@@ -66,7 +66,7 @@ def statement(q, k, v, scale, ok, keys_rounded):
             lost = w[~counts].sum()
             m, w = m[counts], w[counts]
             p, va = w / w.sum(), np.abs(vv[m])
-            e = (2 * D * 2.0 ** -24 + (2.0 ** -11 if keys_rounded else 0)) * mag[i, m] + 2.0 ** -20 + (len(m) + 1) * 2.0 ** -24
+            e = 2 * D * 2.0 ** -24 * mag[i, m] + 2.0 ** -20 + (len(m) + 1) * 2.0 ** -24
             pv, top = p @ va, va.max()
             out[i, h] = p @ vv[m]
             b = (p * e) @ va + (p @ e) * pv + (2.0 ** -22 + 2 * len(m) * 2.0 ** -23 + 2.0 ** -20) * pv
@@ -93,12 +93,11 @@ def test_weights_enter_in_two_parts(D, group, G, size, lse, cut):
     out, _ = c.run(lse=lse)
     torch.cuda.synchronize()
     assert int(c.err) == 0
-    keys_rounded = not lse and rows > (32 if D == 64 else 128)
     pool, r, told, moved, total = c.pool.cpu().numpy(), 0, 0, 0, 0
     for b, (T, n, base) in enumerate(zip(c.lens, c.new, c.base)):
         k, v, _, _ = ref.read_sequence(pool, c.table[b], T, c.Hkv, D, group, c.P)
         ok = tr.seen(T, base, c.masks[b], c.words, 0)
-        want, bound, one, off = statement(c.q[r:r + n].double().cpu().numpy(), k, v, 1 / math.sqrt(D), ok, keys_rounded)
+        want, bound, one, off = statement(c.q[r:r + n].double().cpu().numpy(), k, v, 1 / math.sqrt(D), ok)
         far = np.abs(out[r:r + n].double().cpu().numpy() - want)
         assert (far <= bound).all(), f"sequence {b}: {(far - bound).max():.3e} beyond the bound ({(far / bound).max():.2f} of it)"
         told += (np.abs(one - want) > bound).sum()
@@ -106,3 +105,15 @@ def test_weights_enter_in_two_parts(D, group, G, size, lse, cut):
         total += want.size
         r += n
     assert told > total / 50 and moved > total / 50  # what the bound would not let pass
+
+
+@pytest.mark.parametrize("D,group,G,size", [(128, 128, 8, 20), (128, 32, 8, 40), (64, 64, 7, 9), (64, 32, 16, 20), (64, 64, 8, 5), (128, 64, 8, 14)])
+@pytest.mark.parametrize("wide", [True, False])
+def test_fp16_outputs_do_not_go_by_the_log_sum_exp(D, group, G, size, wide):
+    """Keys are exact whether it is asked for or not."""
+    c = Tree([700 + size, 90 + size, size], [size, size, size], Hkv=2, G=G, D=D, group=group, P=16, dtype="fp16", seed=size)
+    if wide:
+        c.table = np.ascontiguousarray(np.concatenate([c.table, np.full((3, 2 ** 20 // c.P), 10 ** 6, np.int32)], 1))
+    (a, _), (b, _) = c.run(lse=True), c.run(lse=False)
+    torch.cuda.synchronize()
+    assert int(c.err) == 0 and torch.equal(a, b)
