@@ -15,7 +15,7 @@ int kv4_decode_rows(int B, int Hkv, int max_q, int G, int64_t max_tokens, int nu
 // Trees of 33 to 128 rows stay here where their blocks of eight are few and short: the kernel for many rows starts and ends for ~18 us.
 // Here and there, 8 kv heads, D = 128: 40 rows of one sequence, 1K tokens 12.0 and 22.6 us, 8K 19.4 and 22.9, 16K 29.2 and 27.3; 64 rows
 // of one, 4K 18.1 and 21.9, 8K 26.2 and 23.2; of four, 1K 16.6 and 23.6, 2K 24.0 and 22.7; 128 rows of one, 2K 18.1 and 24.7, 4K 26.2 and
-// 25.4. 56 rows on 2 heads, D = 64: one sequence of 16K 14.0 and 22.3, four of 8K 18.2 and 20.4, eight of 4K 20.1 and 19.7.
+// 25.4 (of these the bound leaves 40 rows at 8K, 64 at 8K, four times 64 at 2K and 128 at 4K to the other). 56 rows on 2 heads, D = 64: one sequence of 16K 14.0 and 22.3, four of 8K 18.2 and 20.4, eight of 4K 20.1 and 19.7.
 bool kv4_tree_stays(int B, int Hkv, int max_q, int G, int64_t max_tokens, int D, int num_sms) {
   const int64_t rows = static_cast<int64_t>(max_q) * G, items = (rows + 7) / 8 * B * Hkv;
   return rows <= 128 && items <= kv4_decode_ctas(num_sms) && items * max_tokens * D <= (9 << 22);
