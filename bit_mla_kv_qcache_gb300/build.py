@@ -26,7 +26,9 @@ SOURCES = {  # file -> extra flags
     "abi_kv4.cu": [],
     "kv4_append.cu": ["-fmad=false"],  # as the writer
     "kv4_attn.cu": [],
+    "kv4_attn_f16.cu": [],
     "kv4_attn_tree.cu": [],
+    "kv4_attn_tree_f16.cu": [],
     "kv4_prompt.cu": [],
     "kv4_prompt_tree.cu": [],
     "kv4_prompt_tree_f16.cu": [],

@@ -92,7 +92,9 @@ int kv4_decode_rows(int B, int Hkv, int max_q, int G, int64_t max_tokens, int nu
 int kv4_decode_ctas(int num_sms);
 size_t kv4_decode_workspace_bytes(int rows, int D, int num_sms);
 cudaError_t launch_kv4_decode(const Kv4AttnParams& p, int D, int n_groups, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv4_decode_f16(const Kv4AttnParams& p, int D, int n_groups, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv4_decode_tree(const Kv4AttnParams& p, int D, int n_groups, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv4_decode_tree_f16(const Kv4AttnParams& p, int D, int n_groups, int num_sms, cudaStream_t stream);
 
 // Tokens base + kept[i] of a sequence move to base + i, i < n_kept, and its length becomes base + n_kept.
 struct Kv4KeepParams {

@@ -27,7 +27,7 @@ size_t kv4_decode_workspace_bytes(int rows, int D, int num_sms) {
 }
 
 cudaError_t launch_kv4_decode(const Kv4AttnParams& p, int D, int n_groups, int num_sms, cudaStream_t stream) {
-  return launch_decode_kernel<false>(p, D, n_groups, num_sms, stream);
+  return p.f16 ? launch_kv4_decode_f16(p, D, n_groups, num_sms, stream) : launch_decode_kernel<false, false>(p, D, n_groups, num_sms, stream);
 }
 
 }  // namespace mlaq

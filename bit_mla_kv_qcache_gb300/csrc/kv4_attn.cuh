@@ -12,6 +12,11 @@
 // values. For FP16 rows 7.5 times the sum of the errors is put back, which leaves them multiplied by n - 7.5 (error of the output
 // 5.1e-4 -> 3.1e-4 of it, half of that its own rounding; 64 ragged sequences up to 16K 49.4 -> 51.9 us). A BF16 output's
 // own rounding, 1.7e-3, covers them.
+// The tensor cores' float32 sums round towards zero, and sums of w n are all positive, so that over long contexts, where values average
+// out, they ended up to 1.2e-3 of the output low (16 sequences of 60K, 32 rows; 6e-4 with eight). For FP16 rows the last eight tokens of a
+// tile therefore enter from the top of their levels, v = (min + 15 s) - (15 - n) s: their weights negative, their codes complemented by the
+// instruction that masks them. The sums stay about zero (error of these outputs 7.5e-4 and 5.4e-4 -> 2.6e-4 and 2.8e-4). A form of its own
+// for each type costs no time (ragged batch 51.7 and 51.5 us; with a flag that both look at 32 sequences of 8K in BF16 64.6 -> 68.3).
 //
 // A warp owns steps of 32 tokens, two tiles of 16: S^T[16 tokens x rows] = K q^T with the key codes as the A operand
 // (a lane's fragment is 16 contiguous bytes of the page), softmax on the accumulators, movmatrix
@@ -291,7 +296,7 @@ __device__ __forceinline__ void merge_parts(const Kv4AttnParams& p, const Place&
   }
 }
 
-template <int D, int NG, int NT, bool kTree>
+template <int D, int NG, int NT, bool kTree, bool kF16>
 __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kernel(const Kv4AttnParams p) {
   using Ge = Geom<D, NG, NT>;
   constexpr int R = 8 * NT, KW = D / 32, VW = D / 64, MT = D / 16;
@@ -523,7 +528,7 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
       float mx = 0.f;
 #pragma unroll
       for (int j = 0; j < KW; ++j) {
-        unpack8(qraw[nt][j], p.f16, x[j]);
+        unpack8(qraw[nt][j], kF16, x[j]);
 #pragma unroll
         for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(x[j][k]));
       }
@@ -730,10 +735,10 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
             for (int k = 0; k < NG; ++k) {
               const float2 v0 = half2_to_float2(num[r][0][k].y), v1 = half2_to_float2(num[r][1][k].y);
 #pragma unroll
-              for (int c = 0; c < 2; ++c) om[nt][c][k] += w[c] * v0.y + w[2 + c] * v1.y;
-              const float s0 = v0.x * wf, s1 = v1.x * wf;
+              for (int c = 0; c < 2; ++c) om[nt][c][k] += w[c] * v0.y + w[2 + c] * (kF16 ? fmaf(15.f, v1.x, v1.y) : v1.y);
+              const float s0 = v0.x * wf, s1 = v1.x * (kF16 ? -wf : wf);
               const uint32_t h0 = float2_to_half2(w[0] * s0, w[1] * s0), h1 = float2_to_half2(w[2] * s1, w[3] * s1);
-              if (p.f16) {  // codes are about 7.5 from zero, values are not: the weights' rounding errors times 7.5 are put back
+              if constexpr (kF16) {  // codes are about 7.5 from zero, values are not: the weights' rounding errors times 7.5 are put back
                 const float2 r0 = half2_to_float2(h0), r1 = half2_to_float2(h1);
                 om[nt][0][k] += mid * (fmaf(w[0], s0, -r0.x) + fmaf(w[2], s1, -r1.x));
                 om[nt][1][k] += mid * (fmaf(w[1], s0, -r0.y) + fmaf(w[3], s1, -r1.y));
@@ -743,6 +748,7 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
             }
           }
         // ---- readout
+        constexpr uint32_t flip = kF16 ? ~0u : 0u;
 #pragma unroll
         for (int r = 0; r < PT; ++r) {
           no_loads_across();
@@ -756,8 +762,8 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
             for (int hi = 0; hi < 2; ++hi) {
               const int sh = 8 * hi;
               const uint32_t w0 = p0 >> sh, w1 = p1 >> sh, w2 = p2 >> sh, w3 = p3 >> sh;
-              const uint32_t a0w[4] = {w0 & 0x000F000Fu, w1 & 0x000F000Fu, w2 & 0x000F000Fu, w3 & 0x000F000Fu};
-              const uint32_t a1w[4] = {w0 & 0x00F000F0u, w1 & 0x00F000F0u, w2 & 0x00F000F0u, w3 & 0x00F000F0u};
+              const uint32_t a0w[4] = {w0 & 0x000F000Fu, w1 & 0x000F000Fu, (w2 ^ flip) & 0x000F000Fu, (w3 ^ flip) & 0x000F000Fu};
+              const uint32_t a1w[4] = {w0 & 0x00F000F0u, w1 & 0x00F000F0u, (w2 ^ flip) & 0x00F000F0u, (w3 ^ flip) & 0x00F000F0u};
               const int j = 4 * u + 2 * hi;
               constexpr int kPer = MT / NG;  // 16-channel blocks per group
 #pragma unroll
@@ -877,7 +883,7 @@ __global__ void __launch_bounds__(Geom<D, NG, NT>::kThreads, 2) kv4_decode_kerne
   if (lane == 0 && flags) atomicOr(p.err, flags);
 }
 
-template <int D, int NG, int NT, bool kTree>
+template <int D, int NG, int NT, bool kTree, bool kF16>
 cudaError_t launch_rows(const Kv4AttnParams& p, int ctas, cudaStream_t stream) {
   using Ge = Geom<D, NG, NT>;
   static bool attr_done[64] = {};
@@ -886,28 +892,28 @@ cudaError_t launch_rows(const Kv4AttnParams& p, int ctas, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_done[dev]) {
-    e = cudaFuncSetAttribute(kv4_decode_kernel<D, NG, NT, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ge::kSmem);
+    e = cudaFuncSetAttribute(kv4_decode_kernel<D, NG, NT, kTree, kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ge::kSmem);
     if (e != cudaSuccess) return e;
     attr_done[dev] = true;
   }
-  kv4_decode_kernel<D, NG, NT, kTree><<<ctas, Ge::kThreads, Ge::kSmem, stream>>>(p);
+  kv4_decode_kernel<D, NG, NT, kTree, kF16><<<ctas, Ge::kThreads, Ge::kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
-// One instance for each head size, group count and rows of an item.
-template <int D, int NG, bool kTree>
+// One instance for each head size, group count, rows of an item and type.
+template <int D, int NG, bool kTree, bool kF16>
 cudaError_t launch_few(const Kv4AttnParams& p, int rows, int ctas, cudaStream_t stream) {
-  return rows == 8 ? launch_rows<D, NG, 1, kTree>(p, ctas, stream) : launch_rows<D, NG, 2, kTree>(p, ctas, stream);
+  return rows == 8 ? launch_rows<D, NG, 1, kTree, kF16>(p, ctas, stream) : launch_rows<D, NG, 2, kTree, kF16>(p, ctas, stream);
 }
-template <bool kTree>
+template <bool kTree, bool kF16>
 cudaError_t launch_decode_kernel(const Kv4AttnParams& p, int D, int n_groups, int num_sms, cudaStream_t stream) {
   const int rows = kv4_decode_rows(p.B, p.Hkv, p.max_q, p.G, static_cast<int64_t>(p.max_pages) * p.P, num_sms), ctas = kv4_decode_ctas(num_sms);
   if (D == 128) {
-    if (n_groups == 1) return launch_few<128, 1, kTree>(p, rows, ctas, stream);
-    if (n_groups == 2) return launch_few<128, 2, kTree>(p, rows, ctas, stream);
-    return launch_few<128, 4, kTree>(p, rows, ctas, stream);
+    if (n_groups == 1) return launch_few<128, 1, kTree, kF16>(p, rows, ctas, stream);
+    if (n_groups == 2) return launch_few<128, 2, kTree, kF16>(p, rows, ctas, stream);
+    return launch_few<128, 4, kTree, kF16>(p, rows, ctas, stream);
   }
-  return n_groups == 1 ? launch_few<64, 1, kTree>(p, rows, ctas, stream) : launch_few<64, 2, kTree>(p, rows, ctas, stream);
+  return n_groups == 1 ? launch_few<64, 1, kTree, kF16>(p, rows, ctas, stream) : launch_few<64, 2, kTree, kF16>(p, rows, ctas, stream);
 }
 
 }  // namespace

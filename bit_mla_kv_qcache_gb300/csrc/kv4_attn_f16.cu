@@ -1,0 +1,10 @@
+// As kv4_attn.cu, for FP16 rows.
+#include "kv4_attn.cuh"
+
+namespace mlaq {
+
+cudaError_t launch_kv4_decode_f16(const Kv4AttnParams& p, int D, int n_groups, int num_sms, cudaStream_t stream) {
+  return launch_decode_kernel<false, true>(p, D, n_groups, num_sms, stream);
+}
+
+}  // namespace mlaq
