@@ -1,4 +1,4 @@
-// Attention over the 4-bit grouped-query cache for few query rows per kv head: rows of a sequence's last positions.
+// Attention over the 4-bit grouped-query cache for few query rows per kv head: rows of a sequence's last positions, BF16.
 #include "kv4_attn.cuh"
 
 namespace mlaq {

@@ -1,4 +1,4 @@
-// Attention over the 4-bit grouped-query cache for few query rows per kv head: nodes of trees of drafted tokens.
+// Attention over the 4-bit grouped-query cache for few query rows per kv head: nodes of trees of drafted tokens, BF16.
 #include "kv4_attn.cuh"
 
 namespace mlaq {
